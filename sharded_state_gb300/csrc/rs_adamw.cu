@@ -25,6 +25,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "adamw.cuh"
 #include "device_utils.cuh"
 #include "internal.h"
 
@@ -34,28 +35,11 @@ struct RankPtrs {
     const void* p[SS_MAX_WORLD];
 };
 
-// AdamW coefficients, computed once per call on the host in double and
-// rounded to fp32.
-struct AdamCoef {
-    float decay;         // 1 - lr * wd
-    float b1, omb1;      // beta1, 1 - beta1
-    float b2, omb2;      // beta2, 1 - beta2
-    float step_size;     // lr / (1 - beta1^t)
-    float inv_sqrt_bc2;  // 1 / sqrt(1 - beta2^t)
-    float eps;
-};
+using ss::AdamCoef;
+using ss::adamw_elem;
+using ss::make_coef;
 
 constexpr int kThreads = 256;
-
-// AdamW update of one element, in fp32.
-__device__ __forceinline__ void adamw_elem(float g, float& theta, float& m, float& v,
-                                           const AdamCoef& c) {
-    theta = __fmul_rn(theta, c.decay);
-    m = __fmaf_rn(c.b1, m, __fmul_rn(c.omb1, g));
-    v = __fmaf_rn(c.b2, v, __fmul_rn(c.omb2, __fmul_rn(g, g)));
-    float denom = __fmaf_rn(__fsqrt_rn(v), c.inv_sqrt_bc2, c.eps);
-    theta = __fmaf_rn(-c.step_size, __fdiv_rn(m, denom), theta);
-}
 
 // ---------------------------------------------------------------------------
 // bf16 gradients / shards: 8 elements per 128-bit vector
@@ -384,24 +368,6 @@ int grid_for(int64_t nvec) {
     const int64_t want = (nvec + kThreads - 1) / kThreads;
     const int64_t cap = 0x7FFFFFFF;
     return (int)(want < cap ? (want > 0 ? want : 1) : cap);
-}
-
-AdamCoef make_coef(const ss_adamw* hp) {
-    AdamCoef c;
-    std::memset(&c, 0, sizeof c);
-    if (!hp) return c;
-    const double t = (double)hp->step;
-    const double bc1 = 1.0 - std::pow(hp->beta1, t);
-    const double bc2 = 1.0 - std::pow(hp->beta2, t);
-    c.decay = (float)(1.0 - hp->lr * hp->weight_decay);
-    c.b1 = (float)hp->beta1;
-    c.omb1 = (float)(1.0 - hp->beta1);
-    c.b2 = (float)hp->beta2;
-    c.omb2 = (float)(1.0 - hp->beta2);
-    c.step_size = (float)(hp->lr / bc1);
-    c.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(bc2));
-    c.eps = (float)hp->eps;
-    return c;
 }
 
 }  // namespace

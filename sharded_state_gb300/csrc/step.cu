@@ -39,6 +39,7 @@
 #include <utility>
 #include <vector>
 
+#include "adamw.cuh"
 #include "device_utils.cuh"
 #include "internal.h"
 #include "segmap.cuh"
@@ -68,18 +69,9 @@ using PtrTabSmall = PtrTabT<kTabSmall>;
 // Launches of at most this many vectors with a table that fits kTabSmall slots
 // take the small form of the flat kernel.
 constexpr int64_t kSmallVecs = (int64_t)2 * 3 * 152 * 256;
-struct AdamCoef {
-    float decay, b1, omb1, b2, omb2, step_size, inv_sqrt_bc2, eps;
-};
-
-__device__ __forceinline__ void adamw_elem(float g, float& theta, float& m, float& v,
-                                           const AdamCoef& c) {
-    theta = __fmul_rn(theta, c.decay);
-    m = __fmaf_rn(c.b1, m, __fmul_rn(c.omb1, g));
-    v = __fmaf_rn(c.b2, v, __fmul_rn(c.omb2, __fmul_rn(g, g)));
-    float denom = __fmaf_rn(__fsqrt_rn(v), c.inv_sqrt_bc2, c.eps);
-    theta = __fmaf_rn(-c.step_size, __fdiv_rn(m, denom), theta);
-}
+using ss::AdamCoef;
+using ss::adamw_elem;
+using ss::make_coef;
 
 // Kernel arguments that do not change within a launch.
 struct StepArgs {
@@ -975,22 +967,6 @@ auto pick_flat_any(int N) {
         case 16: return fused_step_flat_any_kernel<16, SMALL>;
         default: return fused_step_flat_any_kernel<0, SMALL>;
     }
-}
-
-AdamCoef make_coef(const ss_adamw* hp) {
-    AdamCoef c;
-    const double t = (double)hp->step;
-    const double bc1 = 1.0 - std::pow(hp->beta1, t);
-    const double bc2 = 1.0 - std::pow(hp->beta2, t);
-    c.decay = (float)(1.0 - hp->lr * hp->weight_decay);
-    c.b1 = (float)hp->beta1;
-    c.omb1 = (float)(1.0 - hp->beta1);
-    c.b2 = (float)hp->beta2;
-    c.omb2 = (float)(1.0 - hp->beta2);
-    c.step_size = (float)(hp->lr / bc1);
-    c.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(bc2));
-    c.eps = (float)hp->eps;
-    return c;
 }
 
 }  // namespace
