@@ -425,6 +425,88 @@ int ddp_bucket_assign(int num_tensors, const int64_t* numels, int elem_bytes,
                       size_t bucket_cap_bytes, int* bucket_of);
 
 /* ---------------------------------------------------------------------- */
+/* gradient norm and clipping                                              */
+/* ---------------------------------------------------------------------- */
+
+/* Workspace the calls of this section take: device memory, 16-byte aligned,
+ * with no contents expected or kept.  Calls that may overlap on the GPU need
+ * one each. */
+#define SS_NORM_WORKSPACE_BYTES (4u * 1024u * 1024u)
+
+/*
+ * Global norm of a list of tensors:
+ *   norm_out[0] = n = sqrt(sum over every element of every tensor of x^2)
+ *   norm_out[1] = 1
+ * Squares and partial sums are fp32, their sum over the CTAs fp64 in a fixed
+ * order: the same inputs give the same bits.  NaN and infinities come through
+ * (a square passes fp32 from |x| = 1.8e19 on); an empty list has norm 0.
+ *   numels      HOST array [num_tensors], each >= 0.
+ *   elem_bytes  HOST array [num_tensors]: 2 (bf16) or 4 (fp32), in any mixture.
+ *   grads       HOST array [num_tensors] of device pointers to contiguous
+ *               tensors, aligned to their element size; those of empty tensors
+ *               are not looked at.
+ *   norm_out    device, 2 floats.
+ * Errors: SS_EINVAL, SS_EALIGN, SS_EOVERFLOW, SS_ECUDA.
+ */
+int ss_grad_norm(int num_tensors, const int64_t* numels, const int* elem_bytes,
+                 const void* const* grads, float* norm_out, void* workspace, size_t workspace_bytes,
+                 ss_stream_t stream);
+
+/*
+ * The same norm, and every tensor scaled by the clipping factor:
+ *   norm_out[1] = c = min(1, max_norm / (n + 1e-6))   (NaN where n is)
+ *   out[k] = c * grads[k], in fp32, rounded once to the tensor's type
+ *   out         HOST array [num_tensors] of device pointers, or NULL for in
+ *               place.  Each is its own input's address or overlaps no input
+ *               and no other output; any element alignment.
+ *   max_norm    >= 0; +infinity never clips.
+ * In place, nothing is written when c is 1.
+ * Errors: as ss_grad_norm.
+ */
+int ss_clip_grads(int num_tensors, const int64_t* numels, const int* elem_bytes, void* const* grads,
+                  void* const* out, double max_norm, float* norm_out, void* workspace,
+                  size_t workspace_bytes, ss_stream_t stream);
+
+/*
+ * Reduce-scatter of N virtual ranks' gradients with the sum of the result's
+ * squares: what a sharded step does per group while gradients arrive, before
+ * the norm over all groups is known.
+ *   reduced_grad[f] = g = (G_0[f] + ... + G_{N-1}[f]) / N, bit for bit the g of
+ *                     fsdp_reduce_scatter_adamw
+ *   *sq_out         = sum of g^2 over the selected range (pads hold zero
+ *                     gradients and add nothing); 0 for an empty one
+ *   rank_grads    HOST array [N] of packed gradient buffers of the plan dtype,
+ *                 16-byte aligned.
+ *   reduced_grad  total_numel floats, 16-byte aligned.
+ *   sq_out        device, 1 double.
+ *   group         -1 = every group, else one group index.
+ * Errors: SS_EINVAL, SS_EALIGN, SS_EOVERFLOW, SS_ENODEVICE, SS_ECUDA.
+ */
+int fsdp_reduce_scatter_norm(const ss_plan* plan, const void* const* rank_grads, float* reduced_grad,
+                             double* sq_out, void* workspace, size_t workspace_bytes, int group,
+                             ss_stream_t stream);
+
+/*
+ * AdamW on the clipped reduced gradient of the selected range:
+ *   n = sqrt(sum of sq_sums), c = min(1, max_norm / (n + 1e-6)); norm_out = {n, c}
+ *   g = c * reduced_grad[f], then AdamW exactly as fsdp_reduce_scatter_adamw
+ * With c = 1 the state and shards are bit for bit what fsdp_reduce_scatter_adamw
+ * gives.
+ *   sq_sums       device, num_sums doubles, summed in order: the sq_out of
+ *                 every group (and of other plans whose gradients the norm
+ *                 spans).
+ *   max_norm      >= 0; +infinity never clips.
+ *   master        nullable: the recipe without fp32 master weights.
+ *   norm_out      device, 2 floats.
+ * The other arguments are fsdp_reduce_scatter_adamw's; bf16 and fp32 plans.
+ * Errors: SS_EINVAL, SS_EALIGN, SS_EOVERFLOW, SS_ENODEVICE, SS_ECUDA.
+ */
+int fsdp_clip_adamw(const ss_plan* plan, const float* reduced_grad, const double* sq_sums, int num_sums,
+                    double max_norm, float* master, float* exp_avg, float* exp_avg_sq,
+                    void* param_shards, const ss_adamw* hp, float* norm_out, int group,
+                    ss_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
 /* diagnostics                                                             */
 /* ---------------------------------------------------------------------- */
 

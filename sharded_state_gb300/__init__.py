@@ -27,6 +27,7 @@ SS_ECUDA = -5
 SS_ENODEVICE = -6
 SS_ESCRATCH = -7
 SS_DDP_NOALLOC_TABLE_BYTES = 256 * 1024
+SS_NORM_WORKSPACE_BYTES = 4 * 1024 * 1024
 
 SS_FLAT_ORIG_FALSE = 0
 SS_FLAT_ORIG_TRUE = 1
@@ -41,7 +42,8 @@ EXPORTED = ("fsdp_plan_create", "fsdp_plan_layout", "fsdp_plan_info", "fsdp_plan
             "fsdp_reduce_scatter_adamw", "fsdp_all_gather_unpack", "ddp_bucket_pack_average",
             "ddp_bucket_assign", "ss_strerror", "ss_last_cuda_error", "ss_version",
             "ss_launch_count", "ddp_bucket_pack_average_noalloc", "fsdp_sharded_step",
-            "fsdp_reduce_scatter_accumulate", "fsdp_plan_validate")
+            "fsdp_reduce_scatter_accumulate", "fsdp_plan_validate", "ss_grad_norm", "ss_clip_grads",
+            "fsdp_reduce_scatter_norm", "fsdp_clip_adamw")
 
 
 class ShardStateError(RuntimeError):
@@ -111,6 +113,12 @@ def _load() -> ctypes.CDLL:
         "fsdp_sharded_step": ([vp, ctypes.POINTER(_Step), i32, vp], i32),
         "fsdp_reduce_scatter_accumulate": ([vp, vpp, vp, i32, i32, vp, vp, vp, vp,
                                             ctypes.POINTER(AdamW), vp, i32, vp], i32),
+        "ss_grad_norm": ([i32, i64p, ctypes.POINTER(i32), vpp, vp, vp, ctypes.c_size_t, vp], i32),
+        "ss_clip_grads": ([i32, i64p, ctypes.POINTER(i32), vpp, vpp, ctypes.c_double, vp, vp,
+                           ctypes.c_size_t, vp], i32),
+        "fsdp_reduce_scatter_norm": ([vp, vpp, vp, vp, vp, ctypes.c_size_t, i32, vp], i32),
+        "fsdp_clip_adamw": ([vp, vp, vp, i32, ctypes.c_double, vp, vp, vp, vp, ctypes.POINTER(AdamW),
+                             vp, i32, vp], i32),
         "ss_strerror": ([i32], ctypes.c_char_p),
         "ss_last_cuda_error": ([], i32),
         "ss_version": ([], ctypes.c_char_p),
@@ -441,3 +449,100 @@ def ddp_bucket_assign(numels: Sequence[int], elem_bytes: int, bucket_cap_bytes: 
     if nb < 0:
         _check("ddp_bucket_assign", nb)
     return [int(out[t]) for t in range(T)], int(nb)
+
+
+# ---------------------------------------------------------------------------
+# gradient norm and clipping
+# ---------------------------------------------------------------------------
+
+def _nbytes(t) -> int:
+    return int(t.numel()) * int(t.element_size())
+
+
+def _want(fn: str, t, dtype, what: str, numel: Optional[int] = None) -> None:
+    """The binding knows a tensor's type and size, which the C ABI cannot check."""
+    if t.dtype != dtype or not t.is_contiguous() or (numel is not None and t.numel() < numel):
+        raise ShardStateError(fn, SS_EINVAL, f"{what}: contiguous {dtype}"
+                              + (f", at least {numel} elements" if numel is not None else ""))
+
+
+def _grad_list(fn: str, grads: Sequence, out: Optional[Sequence]):
+    """numels, element sizes and pointers of a list of contiguous bf16 / fp32 tensors."""
+    import torch
+    for k, g in enumerate(grads):
+        if g.dtype not in (torch.bfloat16, torch.float32) or not g.is_contiguous():
+            raise ShardStateError(fn, SS_EINVAL, f"tensor {k}: contiguous bf16 or fp32 is wanted")
+    if out is not None:
+        if len(out) != len(grads):
+            raise ShardStateError(fn, SS_EINVAL, "out: one tensor for each gradient is wanted")
+        for k, (g, o) in enumerate(zip(grads, out)):
+            if o.dtype != g.dtype or o.numel() != g.numel() or not o.is_contiguous():
+                raise ShardStateError(fn, SS_EINVAL, f"out {k}: its gradient's type and size are wanted")
+    eb = (ctypes.c_int * max(1, len(grads)))(*[g.element_size() for g in grads])
+    return (len(grads), _i64_array([g.numel() for g in grads]), eb, _ptr_array(grads),
+            _ptr_array(out) if out is not None else None)
+
+
+def ss_grad_norm(grads: Sequence, norm_out, workspace, stream=None) -> None:
+    """norm_out (2 floats on the device) = {global norm of the tensors, 1}."""
+    import torch
+    _want("ss_grad_norm", norm_out, torch.float32, "norm_out", 2)
+    n, numels, eb, ptrs, _ = _grad_list("ss_grad_norm", grads, None)
+    _check("ss_grad_norm", _lib.ss_grad_norm(n, numels, eb, ptrs, _addr(norm_out), _addr(workspace),
+                                             _nbytes(workspace), _stream(stream)))
+
+
+def ss_clip_grads(grads: Sequence, max_norm: float, norm_out, workspace, out: Optional[Sequence] = None,
+                  stream=None) -> None:
+    """Scale the tensors (into `out`, or in place) by min(1, max_norm / (norm + 1e-6));
+    norm_out = {global norm, that factor}."""
+    GradClip(grads, max_norm, norm_out, workspace, out=out, stream=_stream(stream))()
+
+
+class GradClip:
+    """ss_clip_grads with every argument marshalled once, for a loop whose
+    gradients stay in place; called with nothing, it clips on `stream` (by
+    default the stream that is current at the call).  The tensors must stay
+    alive as long as the object is used."""
+
+    def __init__(self, grads: Sequence, max_norm: float, norm_out, workspace,
+                 out: Optional[Sequence] = None, stream=None):
+        import torch
+        _want("ss_clip_grads", norm_out, torch.float32, "norm_out", 2)
+        n, numels, eb, ptrs, outs = _grad_list("ss_clip_grads", grads, out)
+        self._args = (n, numels, eb, ptrs, outs, ctypes.c_double(max_norm),
+                      ctypes.c_void_p(_addr(norm_out)), ctypes.c_void_p(_addr(workspace)),
+                      ctypes.c_size_t(_nbytes(workspace)))
+        self._keep = (norm_out, workspace)
+        self._stream = None if stream is None else _stream(stream)
+        self._fn = _lib.ss_clip_grads
+
+    def __call__(self) -> None:
+        stream = _stream(None) if self._stream is None else self._stream
+        status = self._fn(*self._args, stream)
+        if status != SS_OK:
+            _check("ss_clip_grads", status)
+
+
+def fsdp_reduce_scatter_norm(plan: Plan, rank_grads: Sequence, reduced_grad, sq_out, workspace,
+                             group: int = -1, stream=None) -> None:
+    """reduced_grad = the ranks' mean; sq_out (1 fp64 element) = its sum of squares."""
+    import torch
+    _want("fsdp_reduce_scatter_norm", sq_out, torch.float64, "sq_out", 1)
+    _check("fsdp_reduce_scatter_norm", _lib.fsdp_reduce_scatter_norm(
+        plan, _ptr_array(rank_grads), _addr(reduced_grad), _addr(sq_out), _addr(workspace),
+        _nbytes(workspace), group, _stream(stream)))
+
+
+def fsdp_clip_adamw(plan: Plan, reduced_grad, sq_sums, max_norm: float, master, exp_avg, exp_avg_sq,
+                    param_shards, hp: AdamW, norm_out, group: int = -1, stream=None) -> None:
+    """AdamW on reduced_grad scaled by min(1, max_norm / (norm + 1e-6)), the norm
+    being the root of the sum of sq_sums (fp64, one element per
+    fsdp_reduce_scatter_norm call the norm spans); norm_out = {norm, factor}."""
+    import torch
+    _want("fsdp_clip_adamw", sq_sums, torch.float64, "sq_sums", 1)
+    _want("fsdp_clip_adamw", norm_out, torch.float32, "norm_out", 2)
+    _check("fsdp_clip_adamw", _lib.fsdp_clip_adamw(
+        plan, _addr(reduced_grad), _addr(sq_sums), int(sq_sums.numel()), max_norm, _addr(master),
+        _addr(exp_avg), _addr(exp_avg_sq), _addr(param_shards), ctypes.byref(hp), _addr(norm_out), group,
+        _stream(stream)))
