@@ -425,6 +425,65 @@ int ddp_bucket_assign(int num_tensors, const int64_t* numels, int elem_bytes,
                       size_t bucket_cap_bytes, int* bucket_of);
 
 /* ---------------------------------------------------------------------- */
+/* the loss at the head of the model                                       */
+/* ---------------------------------------------------------------------- */
+
+enum { SS_LOSS_MEAN = 0, SS_LOSS_SUM = 1 };
+
+/* ss_linear_ce_workspace flags. */
+#define SS_CE_GRADIENT 1u     /* the call writes d_hidden or d_weight */
+#define SS_CE_STAGE_WEIGHT 2u /* weight rows not 16-byte aligned (assumed when hidden_size % 8 != 0) */
+
+/*
+ * Softmax cross entropy of a linear head, and its gradients, with no logits
+ * kept.  With l_tv = <hidden_t, weight_v>, over the tokens t whose target y_t
+ * is not ignore_index:
+ *   loss_t = log(sum_v exp(l_tv)) - l_t,y_t
+ *   loss   = their sum, or their mean (0 when no token counts)
+ *   d_hidden, d_weight = grad_scale * the gradient of loss
+ * Ignored tokens have a token loss and a d_hidden row of 0, whatever their
+ * hidden row holds; a target outside [0, vocab_size) that is not ignore_index
+ * makes its token's loss, and so the loss, NaN.
+ *
+ * All matrices are bf16, row-major with a row stride in elements (>= the row's
+ * length) and any element alignment; products accumulate and statistics are
+ * held in fp32, the logits' exponentials are rounded to bf16 once on their way
+ * into the gradients.  Weight rows on 16-byte boundaries (an aligned address
+ * and a stride that is a multiple of 8) are read in place, others are copied to
+ * the workspace first.  The same inputs give the same bits.
+ */
+typedef struct {
+    int64_t num_tokens;   /* T >= 0 */
+    int64_t hidden_size;  /* D >= 1 */
+    int64_t vocab_size;   /* V >= 1 */
+    const void* hidden;   /* [T, D] */
+    int64_t hidden_stride;
+    const void* weight;   /* [V, D] */
+    int64_t weight_stride;
+    const int64_t* targets; /* device [T] */
+    int64_t ignore_index;
+    int reduction;          /* SS_LOSS_MEAN or SS_LOSS_SUM */
+    double grad_scale;      /* finite: the gradient of the objective by the loss */
+    float* loss_out;        /* device, 1 float */
+    float* token_loss_out;  /* nullable: device [T] */
+    void* d_hidden;         /* nullable: [T, D] */
+    int64_t d_hidden_stride;
+    void* d_weight;         /* nullable: [V, D] */
+    int64_t d_weight_stride;
+    void* workspace;        /* 256-byte aligned; no contents expected or kept */
+    size_t workspace_bytes;
+} ss_linear_ce;
+
+/* Bytes of workspace ss_linear_cross_entropy takes for these sizes on the
+ * current device. */
+int ss_linear_ce_workspace(int64_t num_tokens, int64_t hidden_size, int64_t vocab_size, unsigned flags,
+                           size_t* bytes_out);
+
+/* Errors: SS_EINVAL, SS_EALIGN, SS_EOVERFLOW (sizes above 2^28, or strides
+ * beyond 64-bit offsets), SS_ECUDA. */
+int ss_linear_cross_entropy(const ss_linear_ce* args, ss_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
 /* gradient norm and clipping                                              */
 /* ---------------------------------------------------------------------- */
 

@@ -33,6 +33,10 @@ SS_FLAT_ORIG_FALSE = 0
 SS_FLAT_ORIG_TRUE = 1
 SS_PER_PARAM_DIM0 = 2
 SS_PLAN_HOST_ONLY = 1
+SS_LOSS_MEAN = 0
+SS_LOSS_SUM = 1
+SS_CE_GRADIENT = 1
+SS_CE_STAGE_WEIGHT = 2
 SS_MAX_WORLD = 64
 SS_MAX_REPLICAS = 64
 
@@ -43,7 +47,8 @@ EXPORTED = ("fsdp_plan_create", "fsdp_plan_layout", "fsdp_plan_info", "fsdp_plan
             "ddp_bucket_assign", "ss_strerror", "ss_last_cuda_error", "ss_version",
             "ss_launch_count", "ddp_bucket_pack_average_noalloc", "fsdp_sharded_step",
             "fsdp_reduce_scatter_accumulate", "fsdp_plan_validate", "ss_grad_norm", "ss_clip_grads",
-            "fsdp_reduce_scatter_norm", "fsdp_clip_adamw")
+            "fsdp_reduce_scatter_norm", "fsdp_clip_adamw", "ss_linear_ce_workspace",
+            "ss_linear_cross_entropy")
 
 
 class ShardStateError(RuntimeError):
@@ -84,6 +89,19 @@ class _Step(ctypes.Structure):
                 ("params_out", ctypes.c_void_p), ("n_out", ctypes.c_int)]
 
 
+class _LinearCE(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int64), ("hidden_size", ctypes.c_int64),
+                ("vocab_size", ctypes.c_int64), ("hidden", ctypes.c_void_p),
+                ("hidden_stride", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("weight_stride", ctypes.c_int64), ("targets", ctypes.c_void_p),
+                ("ignore_index", ctypes.c_int64), ("reduction", ctypes.c_int),
+                ("grad_scale", ctypes.c_double), ("loss_out", ctypes.c_void_p),
+                ("token_loss_out", ctypes.c_void_p), ("d_hidden", ctypes.c_void_p),
+                ("d_hidden_stride", ctypes.c_int64), ("d_weight", ctypes.c_void_p),
+                ("d_weight_stride", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python sharded_state_gb300/build.py` "
@@ -119,6 +137,8 @@ def _load() -> ctypes.CDLL:
         "fsdp_reduce_scatter_norm": ([vp, vpp, vp, vp, vp, ctypes.c_size_t, i32, vp], i32),
         "fsdp_clip_adamw": ([vp, vp, vp, i32, ctypes.c_double, vp, vp, vp, vp, ctypes.POINTER(AdamW),
                              vp, i32, vp], i32),
+        "ss_linear_ce_workspace": ([i64, i64, i64, ctypes.c_uint, ctypes.POINTER(ctypes.c_size_t)], i32),
+        "ss_linear_cross_entropy": ([ctypes.POINTER(_LinearCE), vp], i32),
         "ss_strerror": ([i32], ctypes.c_char_p),
         "ss_last_cuda_error": ([], i32),
         "ss_version": ([], ctypes.c_char_p),
@@ -546,3 +566,60 @@ def fsdp_clip_adamw(plan: Plan, reduced_grad, sq_sums, max_norm: float, master, 
         plan, _addr(reduced_grad), _addr(sq_sums), int(sq_sums.numel()), max_norm, _addr(master),
         _addr(exp_avg), _addr(exp_avg_sq), _addr(param_shards), ctypes.byref(hp), _addr(norm_out), group,
         _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# the loss at the head of the model
+# ---------------------------------------------------------------------------
+
+def ss_linear_ce_workspace(num_tokens: int, hidden_size: int, vocab_size: int, gradient: bool,
+                           stage_weight: bool = False) -> int:
+    """Bytes of workspace ss_linear_cross_entropy takes: with `gradient`, to write
+    d_hidden or d_weight; with `stage_weight`, for a weight whose rows do not
+    start on 16-byte boundaries (assumed when hidden_size % 8 != 0)."""
+    out = ctypes.c_size_t()
+    flags = (SS_CE_GRADIENT if gradient else 0) | (SS_CE_STAGE_WEIGHT if stage_weight else 0)
+    _check("ss_linear_ce_workspace", _lib.ss_linear_ce_workspace(num_tokens, hidden_size, vocab_size, flags,
+                                                                 ctypes.byref(out)))
+    return out.value
+
+
+def _matrix(fn: str, t, what: str, rows: int, cols: int):
+    """Address and row stride of a bf16 matrix (NULL, 0 for None)."""
+    import torch
+    if t is None:
+        return None, 0
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or tuple(t.shape) != (rows, cols) or \
+            (cols > 1 and t.stride(1) != 1):
+        raise ShardStateError(fn, SS_EINVAL, f"{what}: bf16 [{rows}, {cols}] with unit column stride is wanted")
+    return _addr(t), max(int(t.stride(0)), cols) if rows <= 1 else int(t.stride(0))
+
+
+def ss_linear_cross_entropy(hidden, weight, targets, loss_out, workspace, token_loss_out=None, d_hidden=None,
+                            d_weight=None, ignore_index: int = -100, reduction: str = "mean",
+                            grad_scale: float = 1.0, stream=None) -> None:
+    """Cross entropy of softmax(hidden @ weight.T) against targets, with no logits
+    kept: hidden [T, D] and weight [V, D] bf16 (rows may be strided), targets [T]
+    int64 -> loss_out (1 float; "mean" or "sum" over the targets that are not
+    ignore_index), token_loss_out [T], and grad_scale times the gradients in
+    d_hidden [T, D] and d_weight [V, D]; the last three are optional."""
+    import torch
+    fn = "ss_linear_cross_entropy"
+    if hidden.dim() != 2 or weight.dim() != 2:
+        raise ShardStateError(fn, SS_EINVAL, "hidden and weight: matrices are wanted")
+    T, D = hidden.shape
+    V = weight.shape[0]
+    if reduction not in ("mean", "sum"):
+        raise ShardStateError(fn, SS_EINVAL, "reduction: mean or sum")
+    _want(fn, targets, torch.int64, "targets", T)
+    _want(fn, loss_out, torch.float32, "loss_out", 1)
+    if token_loss_out is not None:
+        _want(fn, token_loss_out, torch.float32, "token_loss_out", T)
+    h, ldh = _matrix(fn, hidden, "hidden", T, D)
+    w, ldw = _matrix(fn, weight, "weight", V, D)
+    dh, ld_dh = _matrix(fn, d_hidden, "d_hidden", T, D)
+    dw, ld_dw = _matrix(fn, d_weight, "d_weight", V, D)
+    args = _LinearCE(T, D, V, h, ldh, w, ldw, _addr(targets), ignore_index,
+                     SS_LOSS_MEAN if reduction == "mean" else SS_LOSS_SUM, grad_scale, _addr(loss_out),
+                     _addr(token_loss_out), dh, ld_dh, dw, ld_dw, _addr(workspace), _nbytes(workspace))
+    _check(fn, _lib.ss_linear_cross_entropy(ctypes.byref(args), _stream(stream)))

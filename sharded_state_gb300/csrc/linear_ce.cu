@@ -1,0 +1,818 @@
+// linear_ce.cu -- softmax cross entropy of a linear head over a large
+// vocabulary, and its gradients, without keeping the logits.
+//
+//   l_tv = <h_t, w_v>          lse_t = log sum_v exp(l_tv)
+//   loss_t = lse_t - l_t,y(t)  over the tokens whose target is not ignored
+//   P_tv = exp(l_tv - lse_t) - [v = y(t)]
+//   dH = scale * P W           dW = scale * P^T H
+//
+// The tokens that count are gathered first, so that ignored ones cost nothing
+// and whatever their rows hold (NaN, infinities) stays out of every product.
+// Then four matrix products carry the work, 2TVD flops each:
+//
+//   statistics  H W^T a tile at a time; of each tile's row only the maximum's
+//               exponent and the sum of exponentials leave the SM
+//   for each piece of the vocabulary (as much of P as the workspace holds):
+//     probability  H W^T again, P written in bf16
+//     head         dW of the piece = P^T H
+//     hidden       dH += P W of the piece
+//
+// P in bf16 is the one rounding between inputs and outputs beside their own:
+// the tensor cores take bf16 operands, and the error it leaves (at most 2^-8 of
+// each term, independent) is the size of the outputs' own rounding.  Logits,
+// statistics, and every sum are fp32; what is combined across tiles, fp64.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "device_utils.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+
+namespace {
+
+namespace tc = ss::tc;
+
+constexpr int kTile = 256;        // rows and columns of a CTA pair's tile
+constexpr int kHalf = 128;        // each CTA's rows of A, of B, and of the accumulator
+constexpr int kBlockK = 64;       // k of one stage: 128 bytes of bf16
+constexpr int kStages = 6;
+constexpr int kStageBytes = 2 * kHalf * kBlockK * 2;  // A and B of one CTA
+constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+constexpr int kEpilogueWarps = 4;
+constexpr int kGemmThreads = 32 * (4 + kEpilogueWarps);
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLn2 = 0.6931471805599453;
+
+// What the gather leaves for the kernels after it, at the workspace's start.
+struct Header {
+    int live;     // tokens that count
+    int failed;   // a wait ran out somewhere
+    float scale;  // of both gradients
+    int reserved;
+};
+
+enum Mode { kStatistics, kProbability, kHead, kHidden };
+
+struct GemmArgs {
+    Header* header;
+    int n_tiles;  // column tiles
+    int m_tiles;  // row tiles (kHead; the token modes take theirs from header->live)
+    int splits;   // of k (kHead, kHidden)
+    int k;        // elements of k (kHead: the tokens that count)
+    int v0;       // first vocabulary row of the piece
+    int vocab;
+    // kStatistics
+    float2* stats;        // [n_tiles][rows]: exponent of the tile's maximum, sum of exponentials
+    float* target_logit;  // [rows]
+    const int* target;    // [rows]
+    int rows;             // allocated token rows
+    // kProbability
+    const float* lse2;  // [rows], base 2
+    uint16_t* p;        // [rows][ldp]
+    int ldp;
+    // kHead, kHidden: into fp32 partials [splits][part_rows][part_ld] or, where NULL, into out
+    float* part;
+    int64_t part_split;  // elements between two splits
+    int part_ld;
+    int add;             // partials already hold the earlier pieces
+    uint16_t* out;
+    int64_t out_ld;
+    const int* row_map;  // output row of each row (NULL: itself, from v0)
+    int m_rows;          // rows that exist (kHead)
+    int cols;            // columns that exist
+};
+
+// This thread's row: exponentials of 32 logits (columns from col of the tile's
+// row) added to (m, s), m an integer exponent at or above every logit so far.
+__device__ __forceinline__ void add_logits(const float (&l)[32], float& m, float& s) {
+    float top = l[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) top = fmaxf(top, l[i]);
+    const float up = fmaxf(m, ceilf(top * kLog2e));
+    // nothing but -inf so far: any finite exponent gives the zeros it should
+    const float at = up == -INFINITY ? 0.f : up;
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        a += exp2f(fmaf(l[i], kLog2e, -at));
+        b += exp2f(fmaf(l[i + 1], kLog2e, -at));
+    }
+    s = (m == -INFINITY ? 0.f : s * exp2f(m - at)) + (a + b);
+    m = up;
+}
+
+// One persistent CTA pair takes output tiles of 256 x 256, its first CTA the
+// upper 128 rows.  Warp 0 loads (one thread), warp 1 of the first CTA issues the
+// products, warps 4.. read finished accumulators from tensor memory while the
+// next tile's products go to the other half of it.
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+               const GemmArgs g) {
+    constexpr bool kTokenRows = MODE != kHead;
+    constexpr int kAMn = MODE == kHead, kBMn = MODE == kHead || MODE == kHidden;
+    extern __shared__ unsigned char raw[];
+    __shared__ uint64_t bars[2 * kStages + 4];
+    __shared__ uint32_t tmem_base;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_ctarank();
+    const uint32_t smem = (tc::smem_addr(raw) + 1023u) & ~1023u;
+    const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
+    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(full + 8 * i, 1);
+            tc::mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(acc_full + 8 * i, 1);
+            tc::mbar_init(acc_empty + 8 * i, 2 * kEpilogueWarps);
+        }
+        tc::mbar_init_fence();
+        tc::prefetch_map(&map_a);
+        tc::prefetch_map(&map_b);
+    }
+    if (warp == 2) tc::tmem_alloc(tc::smem_addr(&tmem_base), 512);
+    tc::fence_before();
+    tc::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = tmem_base;
+
+    const int live = g.header->live;
+    const int m_tiles = kTokenRows ? (live + kTile - 1) / kTile : g.m_tiles;
+    const int kblocks = ((MODE == kHead ? live : g.k) + kBlockK - 1) / kBlockK;
+    const int per_split = (kblocks + g.splits - 1) / g.splits;
+    const int mn = m_tiles * g.n_tiles;
+    const int tiles = mn * g.splits;
+    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+
+    // the k blocks of a tile's split
+    auto k_range = [&](int t, int& kb, int& ke) {
+        const int s = t / mn;
+        kb = s * per_split < kblocks ? s * per_split : kblocks;
+        ke = kb + per_split < kblocks ? kb + per_split : kblocks;
+    };
+
+    bool ok = true;
+    if (warp == 0 && lane == 0) {
+        int it = 0;
+        for (int t = first; t < tiles && ok; t += stride) {
+            const int m = (t % mn) % m_tiles, n = (t % mn) / m_tiles;
+            int kb, ke;
+            k_range(t, kb, ke);
+            const int am = m * kTile + (int)rank * kHalf;
+            const int bn = n * kTile + (int)rank * kHalf;
+            for (int k = kb; k < ke && ok; ++k, ++it) {
+                const int st = it % kStages;
+                const uint32_t a = smem + st * kStageBytes, b = a + kHalf * kBlockK * 2;
+                ok = tc::mbar_wait(empty + 8 * st, ((it / kStages) & 1) ^ 1);
+                if (!ok) break;
+                const uint32_t bar = tc::map_to_rank(full + 8 * st, 0);
+                if (rank == 0) tc::mbar_expect_tx(full + 8 * st, 2 * kStageBytes);
+                if (kAMn) {
+                    tc::tma_load_2d(a, &map_a, am, k * kBlockK, bar);
+                    tc::tma_load_2d(a + 8192, &map_a, am + 64, k * kBlockK, bar);
+                } else {
+                    tc::tma_load_2d(a, &map_a, k * kBlockK, am, bar);
+                }
+                if (kBMn) {
+                    const int y = (MODE == kHidden ? g.v0 : 0) + k * kBlockK;
+                    tc::tma_load_2d(b, &map_b, bn, y, bar);
+                    tc::tma_load_2d(b + 8192, &map_b, bn + 64, y, bar);
+                } else {
+                    tc::tma_load_2d(b, &map_b, k * kBlockK, g.v0 + bn, bar);
+                }
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        constexpr uint32_t idesc = tc::instr_desc(kTile, kTile, kAMn, kBMn);
+        int it = 0, j = 0;
+        for (int t = first; t < tiles && ok; t += stride, ++j) {
+            int kb, ke;
+            k_range(t, kb, ke);
+            const uint32_t d = tmem + (j & 1) * kTile;
+            ok = tc::mbar_wait(acc_empty + 8 * (j & 1), ((j >> 1) & 1) ^ 1);
+            if (!ok) break;
+            tc::fence_after();
+            for (int k = kb; k < ke; ++k, ++it) {
+                const int st = it % kStages;
+                ok = tc::mbar_wait(full + 8 * st, (it / kStages) & 1);
+                if (!ok) break;
+                tc::fence_after();
+                const uint32_t a = smem + st * kStageBytes, b = a + kHalf * kBlockK * 2;
+                // K-major: 16 k are 32 bytes of every row; MN-major: two 8-column groups
+                const uint64_t da = kAMn ? tc::operand_desc(a, 8192, 1024) : tc::operand_desc(a, 16, 1024);
+                const uint64_t db = kBMn ? tc::operand_desc(b, 8192, 1024) : tc::operand_desc(b, 16, 1024);
+#pragma unroll
+                for (int i = 0; i < kBlockK / 16; ++i)
+                    tc::mma_pair(d, da + i * ((kAMn ? 2048 : 32) >> 4), db + i * ((kBMn ? 2048 : 32) >> 4), idesc,
+                                 k > kb || i > 0);
+                tc::commit_pair(empty + 8 * st);
+            }
+            tc::commit_pair(acc_full + 8 * (j & 1));
+        }
+    } else if (warp >= 4) {
+        const int quad = warp & 3;
+        const uint32_t acc_empty0 = tc::map_to_rank(acc_empty, 0);
+        int j = 0;
+        for (int t = first; t < tiles && ok; t += stride, ++j) {
+            const int m = (t % mn) % m_tiles, n = (t % mn) / m_tiles, s = t / mn;
+            int kb, ke;
+            k_range(t, kb, ke);
+            const int row = m * kTile + (int)rank * kHalf + quad * 32 + lane;
+            const uint32_t d = tmem + (j & 1) * kTile + ((uint32_t)quad << 21);
+            ok = tc::mbar_wait(acc_full + 8 * (j & 1), (j >> 1) & 1);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc::fence_after();
+            if (MODE == kStatistics) {
+                const int y = row < live ? g.target[row] - (g.v0 + n * kTile) : -1;  // column of the target
+                const int left = g.vocab - (g.v0 + n * kTile);  // columns that exist
+                float top = -INFINITY, sum = 0.f, hit = 0.f;
+                for (int c = 0; c < kTile && c < left; c += 32) {
+                    float l[32];
+                    __syncwarp();
+                    tc::tmem_ld32(d + c, l);
+                    if (c + 32 > left) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) l[i] = c + i < left ? l[i] : -INFINITY;
+                    }
+                    if (y >= c && y < c + 32) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) hit = c + i == y ? l[i] : hit;
+                    }
+                    add_logits(l, top, sum);
+                }
+                if (row < live) {
+                    g.stats[(int64_t)n * g.rows + row] = make_float2(top, sum);
+                    if (y >= 0 && y < kTile && y < left) g.target_logit[row] = hit;
+                }
+            } else if (MODE == kProbability) {
+                const int y = row < live ? g.target[row] - (g.v0 + n * kTile) : -1;
+                const int left = g.vocab - (g.v0 + n * kTile);
+                const float lse2 = row < live ? g.lse2[row] : 0.f;
+                uint16_t* o = g.p + (int64_t)row * g.ldp + n * kTile;
+                for (int c = 0; c < kTile; c += 32) {
+                    float l[32];
+                    __syncwarp();
+                    tc::tmem_ld32(d + c, l);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        l[i] = exp2f(fmaf(l[i], kLog2e, -lse2));
+                        if (row >= live || c + i >= left) l[i] = 0.f;
+                    }
+                    if (y >= c && y < c + 32) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) l[i] -= c + i == y ? 1.f : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        *reinterpret_cast<uint4*>(o + c + i) =
+                            make_uint4(ss::pack_bf16x2(l[i], l[i + 1]), ss::pack_bf16x2(l[i + 2], l[i + 3]),
+                                       ss::pack_bf16x2(l[i + 4], l[i + 5]), ss::pack_bf16x2(l[i + 6], l[i + 7]));
+                }
+            } else {
+                const int limit = kTokenRows ? live : g.m_rows;
+                const float scale = g.header->scale;
+                const int64_t orow = row < limit ? (g.row_map ? g.row_map[row] : (int64_t)g.v0 + row) : 0;
+                for (int c = 0; c < kTile && n * kTile + c < g.cols; c += 32) {
+                    float x[32];
+                    __syncwarp();
+                    tc::tmem_ld32(d + c, x);
+                    if (kb == ke) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                    }
+                    const int col = n * kTile + c, left = g.cols - col;
+                    if (row >= limit) {
+                        // a row past the end: the warp still reads together
+                    } else if (g.part) {
+                        float* o = g.part + s * g.part_split + (int64_t)row * g.part_ld + col;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            if (i < left) {  // part_ld is a multiple of 4
+                                float4 v = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                                if (g.add) {
+                                    const float4 w = *reinterpret_cast<const float4*>(o + i);
+                                    v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+                                }
+                                *reinterpret_cast<float4*>(o + i) = v;
+                            }
+                        }
+                    } else {
+                        uint16_t* o = g.out + orow * g.out_ld + col;
+                        if (left >= 32 && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8)
+                                *reinterpret_cast<uint4*>(o + i) = make_uint4(
+                                    ss::pack_bf16x2(scale * x[i], scale * x[i + 1]),
+                                    ss::pack_bf16x2(scale * x[i + 2], scale * x[i + 3]),
+                                    ss::pack_bf16x2(scale * x[i + 4], scale * x[i + 5]),
+                                    ss::pack_bf16x2(scale * x[i + 6], scale * x[i + 7]));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < left) o[i] = ss::f32_to_bf16(scale * x[i]);
+                        }
+                    }
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(acc_empty0 + 8 * (j & 1));
+        }
+    }
+    if (!ok) {
+        g.header->failed = 1;
+        __nanosleep(1000000);  // the copies in flight land before the CTA goes
+    }
+    __syncwarp();
+    tc::fence_before();
+    tc::cluster_sync();
+    tc::fence_after();
+    if (warp == 2) tc::tmem_free(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// around the products
+// ---------------------------------------------------------------------------
+
+constexpr int kThreads = 256;
+constexpr int kGatherRows = 32;  // tokens per CTA
+
+// 8 elements from element 8j of a row of D bf16 at any element alignment,
+// zeros past its end.
+__device__ __forceinline__ uint4 row_vec(const uint16_t* row, int j, int D) {
+    if (8 * j + 8 <= D) return ss::ld_any16(row + 8 * j);
+    uint32_t w[4] = {0, 0, 0, 0};
+    for (int i = 8 * j; i < D; ++i) w[(i & 7) >> 1] |= (uint32_t)row[i] << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+struct GatherArgs {
+    Header* header;
+    const int64_t* targets;
+    int64_t ignore;
+    int T, D, Dp, vocab;
+    const uint16_t* hidden;
+    int64_t ld;
+    uint16_t* h;          // [rows][Dp]
+    int* row;             // [rows]: token of each gathered row
+    int* target;          // [rows]
+    float* target_logit;  // [rows], NaN until its tile writes it
+    float* token_loss;    // nullable
+    uint16_t* d_hidden;   // nullable
+    int64_t d_ld;
+    float grad_scale;
+    int mean;
+};
+
+// CTA b places tokens [32 b, 32 b + 32): how many of the tokens before count
+// (read again by every CTA: T * T / 8 bytes in all, from L2), then its own
+// rows, gathered or, where ignored, zeroed in the outputs.  The last CTA knows
+// the total; it zeroes the rows up to the next whole k block.
+__global__ void __launch_bounds__(kThreads) ce_gather_kernel(const GatherArgs a) {
+    __shared__ int part[kThreads / 32];
+    __shared__ int place[kGatherRows];
+    __shared__ int total;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t0 = blockIdx.x * kGatherRows;
+    int before = 0;
+    for (int t = threadIdx.x; t < t0; t += kThreads) before += a.targets[t] != a.ignore;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) before += __shfl_down_sync(0xFFFFFFFFu, before, d);
+    if (lane == 0) part[warp] = before;
+    __syncthreads();
+    if (warp == 0) {
+        int sum = 0;
+        for (int i = 0; i < kThreads / 32; ++i) sum += part[i];
+        const int t = t0 + lane;
+        const int64_t y = t < a.T ? a.targets[t] : a.ignore;
+        const bool counts = t < a.T && y != a.ignore;
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, counts);
+        const int at = sum + __popc(mask & ((1u << lane) - 1));
+        place[lane] = counts ? at : -1;
+        if (counts) {
+            a.row[at] = t;
+            a.target[at] = y >= 0 && y < a.vocab ? (int)y : -1;
+            a.target_logit[at] = NAN;
+        } else if (t < a.T && a.token_loss) {
+            a.token_loss[t] = 0.f;
+        }
+        if (lane == 0) total = sum + __popc(mask);
+    }
+    __syncthreads();
+    const int vecs = a.Dp / 8;
+    for (int i = warp; i < kGatherRows && t0 + i < a.T; i += kThreads / 32) {
+        const int at = place[i];
+        if (at >= 0) {
+            const uint16_t* src = a.hidden + (int64_t)(t0 + i) * a.ld;
+            uint4* dst = reinterpret_cast<uint4*>(a.h + (int64_t)at * a.Dp);
+            for (int j = lane; j < vecs; j += 32) dst[j] = row_vec(src, j, a.D);
+        } else if (a.d_hidden) {
+            uint16_t* dst = a.d_hidden + (int64_t)(t0 + i) * a.d_ld;
+            for (int j = lane; j < a.D; j += 32) dst[j] = 0;
+        }
+    }
+    if (blockIdx.x == gridDim.x - 1) {
+        const int live = total;
+        const int end = (live + kBlockK - 1) / kBlockK * kBlockK;
+        for (int64_t j = threadIdx.x; j < (int64_t)(end - live) * vecs; j += kThreads)
+            reinterpret_cast<uint4*>(a.h + (int64_t)live * a.Dp)[j] = make_uint4(0, 0, 0, 0);
+        if (threadIdx.x == 0) {
+            a.header->live = live;
+            a.header->failed = 0;
+            a.header->scale = a.mean ? (live > 0 ? a.grad_scale / (float)live : 0.f) : a.grad_scale;
+        }
+    }
+}
+
+// Rows of a weight whose rows do not start on 16-byte boundaries, copied to
+// rows that do: one warp per row.
+__global__ void __launch_bounds__(kThreads)
+ce_stage_kernel(const uint16_t* __restrict__ w, int64_t ld, int V, int D, int Dp, uint16_t* __restrict__ out) {
+    const int64_t v = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (v >= V) return;
+    const uint16_t* src = w + v * ld;
+    uint4* dst = reinterpret_cast<uint4*>(out + v * Dp);
+    for (int j = threadIdx.x & 31; j < Dp / 8; j += 32) dst[j] = row_vec(src, j, D);
+}
+
+constexpr int kLossRows = 32;  // rows per CTA, 8 threads each
+
+// The tiles' statistics of a row to its log-sum-exp and loss; the CTA's losses
+// to one fp64 partial.
+__global__ void __launch_bounds__(kThreads)
+ce_loss_rows_kernel(const Header* __restrict__ header, const float2* __restrict__ stats, int n_tiles, int rows,
+                    const float* __restrict__ target_logit, const int* __restrict__ row_map,
+                    float* __restrict__ lse2, float* __restrict__ token_loss, double* __restrict__ partials) {
+    __shared__ float top_s[8][kLossRows];
+    __shared__ float sum_s[8][kLossRows];
+    const int r = threadIdx.x & (kLossRows - 1), slice = threadIdx.x / kLossRows;
+    const int row = blockIdx.x * kLossRows + r;
+    const bool lives = row < header->live;
+    float top = -INFINITY, sum = 0.f;
+    if (lives) {
+        for (int n = slice; n < n_tiles; n += 8) {
+            const float2 v = stats[(int64_t)n * rows + row];
+            const float up = fmaxf(top, v.x);
+            const float at = up == -INFINITY ? 0.f : up;
+            sum = (top == -INFINITY ? 0.f : sum * exp2f(top - at)) + (v.x == -INFINITY ? v.y : v.y * exp2f(v.x - at));
+            top = up;
+        }
+    }
+    top_s[slice][r] = top;
+    sum_s[slice][r] = sum;
+    __syncthreads();
+    if (slice == 0) {
+        double loss = 0.0;
+        if (lives) {
+            for (int i = 1; i < 8; ++i) top = fmaxf(top, top_s[i][r]);
+            const float at = top == -INFINITY ? 0.f : top;
+            sum = 0.f;
+            for (int i = 0; i < 8; ++i)
+                sum += top_s[i][r] == -INFINITY ? sum_s[i][r] : sum_s[i][r] * exp2f(top_s[i][r] - at);
+            lse2[row] = at + log2f(sum);
+            loss = (double)at * kLn2 + (double)logf(sum) - (double)target_logit[row];
+            if (token_loss) token_loss[row_map[row]] = (float)loss;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) loss += __shfl_down_sync(0xFFFFFFFFu, loss, d);
+        if (r == 0) partials[blockIdx.x] = loss;
+    }
+}
+
+// The loss: the partials' sum in order, over the tokens that count for a mean
+// (0 when there are none); NaN where a product did not finish.
+__global__ void __launch_bounds__(kThreads)
+ce_loss_kernel(const Header* __restrict__ header, const double* __restrict__ partials, int n, int mean,
+               float* __restrict__ loss) {
+    __shared__ double part[kThreads / 32];
+    double s = 0.0;
+    for (int i = threadIdx.x; i < n; i += kThreads) s += partials[i];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, d);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = 0.0;
+        for (int i = 0; i < kThreads / 32; ++i) s += part[i];
+        if (mean && header->live > 0) s /= header->live;
+        *loss = header->failed ? NAN : (float)s;
+    }
+}
+
+// out = bf16(scale * sum of the splits' partials), rows through row_map.
+__global__ void __launch_bounds__(kThreads)
+ce_join_kernel(const Header* __restrict__ header, const float* __restrict__ part, int splits, int64_t part_split,
+               int part_ld, int rows, int cols, uint16_t* __restrict__ out, int64_t out_ld,
+               const int* __restrict__ row_map) {
+    const int limit = row_map ? header->live : rows;
+    const int vecs = part_ld / 4;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t row = i / vecs;
+    const int col = (int)(i % vecs) * 4;
+    if (row >= limit) return;
+    const float* p = part + row * part_ld + col;
+    float4 s = *reinterpret_cast<const float4*>(p);
+    for (int k = 1; k < splits; ++k) {
+        const float4 x = *reinterpret_cast<const float4*>(p + k * part_split);
+        s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+    }
+    const float c = header->scale;
+    uint16_t* o = out + (row_map ? (int64_t)row_map[row] : row) * out_ld + col;
+    const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (col + e < cols) o[e] = ss::f32_to_bf16(c * v[e]);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// Splits of k that keep the pairs busy, by the clocks of each choice: a k block
+// of a 256 x 256 tile takes a pair 512, and a tile's fp32 partial, written and
+// read once, 512 KB at about 3500 bytes a clock.
+int choose_splits(int64_t tiles, int64_t kblocks, int pairs) {
+    int best = 1;
+    double least = 1e30;
+    for (int s = 1; s <= 32 && (s == 1 || s * 4 <= kblocks); ++s) {
+        const double rounds = (double)((tiles * s + pairs - 1) / pairs);
+        const double cost = rounds * (double)((kblocks + s - 1) / s) * 512 + (s > 1 ? tiles * s * 150.0 : 0.0);
+        if (cost < least) least = cost, best = s;
+    }
+    return best;
+}
+
+// Where everything lies in the workspace.
+struct Layout {
+    int64_t T, D, V, Dp, rows, n_tiles, piece, pieces;
+    int hidden_splits, head_splits;
+    bool grad, stage;
+    int64_t row, target, target_logit, lse2, partials, stats, h, w, p, hidden_part, head_part, bytes;
+};
+
+constexpr int64_t kPieceBytes = 128ll << 20;  // of P: what stays near the 129 MB L2
+
+Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int pairs) {
+    Layout l = {};
+    l.T = T, l.D = D, l.V = V, l.grad = grad, l.stage = stage;
+    l.Dp = up(D, 8);
+    l.rows = up(T, kTile);
+    l.n_tiles = up(V, kTile) / kTile;
+    int64_t at = 256;  // the header
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += up(bytes, 256);
+        return here;
+    };
+    l.row = take(l.rows * 4);
+    l.target = take(l.rows * 4);
+    l.target_logit = take(l.rows * 4);
+    l.lse2 = take(l.rows * 4);
+    l.partials = take(l.rows / kLossRows * 8);
+    l.stats = take(l.n_tiles * l.rows * 8);
+    l.h = take(l.rows * l.Dp * 2);
+    if (stage) l.w = take(V * l.Dp * 2);
+    if (grad) {
+        const int64_t fit = kPieceBytes / (l.rows * 2) / kTile * kTile;
+        l.piece = fit < kTile ? kTile : fit;
+        l.pieces = (l.n_tiles * kTile + l.piece - 1) / l.piece;
+        l.piece = (l.n_tiles + l.pieces - 1) / l.pieces * kTile;  // even pieces
+        l.p = take(l.rows * l.piece * 2);
+        const int64_t d_tiles = up(D, kTile) / kTile;
+        l.hidden_splits = choose_splits(l.rows / kTile * d_tiles, l.piece / kBlockK, pairs);
+        l.head_splits = choose_splits(l.piece / kTile * d_tiles, l.rows / kBlockK, pairs);
+        const int64_t ld = up(D, 4);
+        if (l.hidden_splits > 1 || l.pieces > 1) l.hidden_part = take(l.hidden_splits * l.rows * ld * 4);
+        if (l.head_splits > 1) l.head_part = take(l.head_splits * l.piece * ld * 4);
+    }
+    l.bytes = at;
+    return l;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// A [rows][cols] bf16 matrix of row stride ld, in boxes of 64 columns and
+// box_rows rows, out-of-range elements read as zero.
+int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    const EncodeTiled fn = encoder();
+    if (!fn) return ss::cuda_fail(cudaErrorNotSupported);
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SS_OK : ss::cuda_fail(cudaErrorInvalidValue);
+}
+
+template <int MODE>
+int launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& g, int64_t tiles, cudaStream_t st) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(ce_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return ss::cuda_fail(e);
+    const int64_t pairs = ss::num_sms() / 2;
+    ce_gemm_kernel<MODE><<<(int)(2 * (tiles < pairs ? tiles : pairs)), kGemmThreads, kSmemBytes, st>>>(a, b, g);
+    return ss::check_launch();
+}
+
+constexpr int64_t kMaxSize = 1 << 28;  // tokens, hidden, vocabulary: 32-bit tile coordinates
+
+bool valid_sizes(int64_t T, int64_t D, int64_t V) { return T >= 0 && D >= 1 && V >= 1; }
+
+bool rows_aligned(const void* p, int64_t ld) { return ss::aligned(p, 16) && ld % 8 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+int ss_linear_ce_workspace(int64_t num_tokens, int64_t hidden_size, int64_t vocab_size, unsigned flags,
+                           size_t* bytes_out) {
+    if (!bytes_out || !valid_sizes(num_tokens, hidden_size, vocab_size)) return SS_EINVAL;
+    if (flags & ~(SS_CE_GRADIENT | SS_CE_STAGE_WEIGHT)) return SS_EINVAL;
+    if (num_tokens > kMaxSize || hidden_size > kMaxSize || vocab_size > kMaxSize) return SS_EOVERFLOW;
+    const bool stage = (flags & SS_CE_STAGE_WEIGHT) || hidden_size % 8 != 0;
+    *bytes_out = (size_t)plan_layout(num_tokens, hidden_size, vocab_size, flags & SS_CE_GRADIENT, stage,
+                                     ss::num_sms() / 2)
+                     .bytes;
+    return SS_OK;
+}
+
+int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
+    if (!a || !valid_sizes(a->num_tokens, a->hidden_size, a->vocab_size)) return SS_EINVAL;
+    const int64_t T = a->num_tokens, D = a->hidden_size, V = a->vocab_size;
+    if (T > kMaxSize || D > kMaxSize || V > kMaxSize) return SS_EOVERFLOW;
+    if ((T > 0 && (!a->hidden || !a->targets)) || !a->weight || !a->loss_out || !a->workspace) return SS_EINVAL;
+    if (a->reduction != SS_LOSS_MEAN && a->reduction != SS_LOSS_SUM) return SS_EINVAL;
+    if (!std::isfinite(a->grad_scale)) return SS_EINVAL;
+    const bool grad = a->d_hidden || a->d_weight;
+    if (a->hidden_stride < D || a->weight_stride < D || (a->d_hidden && a->d_hidden_stride < D) ||
+        (a->d_weight && a->d_weight_stride < D))
+        return SS_EINVAL;
+    const int64_t most = INT64_MAX / 8;
+    if (a->weight_stride > most / V || (T > 0 && a->hidden_stride > most / T) ||
+        (a->d_weight && a->d_weight_stride > most / V) || (a->d_hidden && T > 0 && a->d_hidden_stride > most / T))
+        return SS_EOVERFLOW;
+    if (!ss::aligned(a->hidden, 2) || !ss::aligned(a->weight, 2) || !ss::aligned(a->d_hidden, 2) ||
+        !ss::aligned(a->d_weight, 2) || !ss::aligned(a->targets, 8) || !ss::aligned(a->loss_out, 4) ||
+        !ss::aligned(a->token_loss_out, 4) || !ss::aligned(a->workspace, 256))
+        return SS_EALIGN;
+    const bool stage = !rows_aligned(a->weight, a->weight_stride);
+    const int pairs = ss::num_sms() / 2;
+    const Layout l = plan_layout(T, D, V, grad, stage || D % 8 != 0, pairs);
+    if (a->workspace_bytes < (size_t)l.bytes) return SS_EINVAL;
+
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    unsigned char* ws = static_cast<unsigned char*>(a->workspace);
+    Header* header = reinterpret_cast<Header*>(ws);
+    int* row = reinterpret_cast<int*>(ws + l.row);
+    int* target = reinterpret_cast<int*>(ws + l.target);
+    float* target_logit = reinterpret_cast<float*>(ws + l.target_logit);
+    float* lse2 = reinterpret_cast<float*>(ws + l.lse2);
+    double* partials = reinterpret_cast<double*>(ws + l.partials);
+    uint16_t* h = reinterpret_cast<uint16_t*>(ws + l.h);
+    const int mean = a->reduction == SS_LOSS_MEAN;
+
+    GatherArgs ga = {header, a->targets, a->ignore_index, (int)T, (int)D, (int)l.Dp, (int)V,
+                     static_cast<const uint16_t*>(a->hidden), a->hidden_stride, h, row, target, target_logit,
+                     a->token_loss_out, static_cast<uint16_t*>(a->d_hidden), a->d_hidden_stride,
+                     (float)a->grad_scale, mean};
+    ce_gather_kernel<<<(int)((T > 0 ? T + kGatherRows - 1 : kGatherRows) / kGatherRows), kThreads, 0, st>>>(ga);
+    if (int rc = ss::check_launch()) return rc;
+
+    const uint16_t* w = static_cast<const uint16_t*>(a->weight);
+    int64_t ldw = a->weight_stride;
+    if (stage) {
+        uint16_t* staged = reinterpret_cast<uint16_t*>(ws + l.w);
+        const int64_t per = kThreads / 32;
+        ce_stage_kernel<<<(int)((V + per - 1) / per), kThreads, 0, st>>>(w, ldw, (int)V, (int)D, (int)l.Dp, staged);
+        if (int rc = ss::check_launch()) return rc;
+        w = staged;
+        ldw = l.Dp;
+    }
+
+    GemmArgs g = {};
+    g.header = header;
+    g.splits = 1;
+    g.k = (int)D;
+    g.vocab = (int)V;
+    g.rows = (int)l.rows;
+    g.target = target;
+    const int loss_blocks = (int)(l.rows / kLossRows);
+    CUtensorMap h_k, w_k;
+    if (T > 0) {
+        if (int rc = make_map(&h_k, h, l.rows, D, l.Dp, kHalf)) return rc;
+        if (int rc = make_map(&w_k, w, V, D, ldw, kHalf)) return rc;
+        GemmArgs s = g;
+        s.n_tiles = (int)l.n_tiles;
+        s.stats = reinterpret_cast<float2*>(ws + l.stats);
+        s.target_logit = target_logit;
+        if (int rc = launch_gemm<kStatistics>(h_k, w_k, s, l.rows / kTile * l.n_tiles, st)) return rc;
+        ce_loss_rows_kernel<<<loss_blocks, kThreads, 0, st>>>(header, s.stats, s.n_tiles, s.rows, target_logit, row,
+                                                              lse2, a->token_loss_out, partials);
+        if (int rc = ss::check_launch()) return rc;
+    }
+
+    if (grad) {
+        CUtensorMap p_k, p_mn, h_mn, w_mn;
+        uint16_t* p = reinterpret_cast<uint16_t*>(ws + l.p);
+        const int64_t ld = up(D, 4), d_tiles = up(D, kTile) / kTile;
+        if (T > 0) {
+            if (int rc = make_map(&p_k, p, l.rows, l.piece, l.piece, kHalf)) return rc;
+            if (int rc = make_map(&p_mn, p, l.rows, l.piece, l.piece, kBlockK)) return rc;
+            if (int rc = make_map(&h_mn, h, l.rows, D, l.Dp, kBlockK)) return rc;
+            if (int rc = make_map(&w_mn, w, V, D, ldw, kBlockK)) return rc;
+        }
+        if (T == 0 && a->d_weight) {
+            const cudaError_t e =
+                cudaMemset2DAsync(a->d_weight, (size_t)a->d_weight_stride * 2, 0, (size_t)D * 2, (size_t)V, st);
+            if (e != cudaSuccess) return ss::cuda_fail(e);
+        }
+        for (int64_t i = 0; T > 0 && i < l.pieces; ++i) {
+            const int64_t v0 = i * l.piece;
+            const int64_t tiles_v = (V - v0 < l.piece ? up(V - v0, kTile) : l.piece) / kTile;
+            GemmArgs q = g;
+            q.v0 = (int)v0;
+            q.n_tiles = (int)tiles_v;
+            q.lse2 = lse2;
+            q.p = p;
+            q.ldp = (int)l.piece;
+            if (int rc = launch_gemm<kProbability>(h_k, w_k, q, l.rows / kTile * tiles_v, st)) return rc;
+            const int64_t rows_v = V - v0 < l.piece ? V - v0 : l.piece;
+            if (a->d_weight) {
+                GemmArgs d = g;
+                d.v0 = (int)v0;
+                d.m_tiles = (int)tiles_v;
+                d.m_rows = (int)rows_v;
+                d.n_tiles = (int)d_tiles;
+                d.cols = (int)D;
+                d.splits = l.head_splits;
+                d.part = l.head_part ? reinterpret_cast<float*>(ws + l.head_part) : nullptr;
+                d.part_split = l.piece * ld;
+                d.part_ld = (int)ld;
+                d.out = static_cast<uint16_t*>(a->d_weight);
+                d.out_ld = a->d_weight_stride;
+                if (int rc = launch_gemm<kHead>(p_mn, h_mn, d, tiles_v * d_tiles * d.splits, st)) return rc;
+                if (d.part) {
+                    const int64_t blocks = (rows_v * (ld / 4) + kThreads - 1) / kThreads;
+                    ce_join_kernel<<<(int)blocks, kThreads, 0, st>>>(
+                        header, d.part, d.splits, d.part_split, d.part_ld, (int)rows_v, (int)D,
+                        d.out + v0 * d.out_ld, d.out_ld, nullptr);
+                    if (int rc = ss::check_launch()) return rc;
+                }
+            }
+            if (a->d_hidden) {
+                GemmArgs d = g;
+                d.v0 = (int)v0;
+                d.k = (int)(tiles_v * kTile);
+                d.n_tiles = (int)d_tiles;
+                d.cols = (int)D;
+                d.splits = l.hidden_splits;
+                d.part = l.hidden_part ? reinterpret_cast<float*>(ws + l.hidden_part) : nullptr;
+                d.part_split = l.rows * ld;
+                d.part_ld = (int)ld;
+                d.add = i > 0;
+                d.out = static_cast<uint16_t*>(a->d_hidden);
+                d.out_ld = a->d_hidden_stride;
+                d.row_map = row;
+                if (int rc = launch_gemm<kHidden>(p_k, w_mn, d, l.rows / kTile * d_tiles * d.splits, st)) return rc;
+                if (d.part && i == l.pieces - 1) {
+                    const int64_t blocks = (l.rows * (ld / 4) + kThreads - 1) / kThreads;
+                    ce_join_kernel<<<(int)blocks, kThreads, 0, st>>>(header, d.part, d.splits, d.part_split, d.part_ld,
+                                                                     (int)l.rows, (int)D, d.out, d.out_ld, row);
+                    if (int rc = ss::check_launch()) return rc;
+                }
+            }
+        }
+    }
+    ce_loss_kernel<<<1, kThreads, 0, st>>>(header, partials, T > 0 ? loss_blocks : 0, mean, a->loss_out);
+    return ss::check_launch();
+}
+
+}  // extern "C"
