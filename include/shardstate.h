@@ -443,7 +443,7 @@ enum { SS_LOSS_MEAN = 0, SS_LOSS_SUM = 1 };
  *   d_hidden, d_weight = grad_scale * the gradient of loss
  * Ignored tokens have a token loss and a d_hidden row of 0, whatever their
  * hidden row holds; a target outside [0, vocab_size) that is not ignore_index
- * makes its token's loss, and so the loss, NaN.
+ * makes its token's loss NaN, and with it the loss and the gradients.
  *
  * All matrices are bf16, row-major with a row stride in elements (>= the row's
  * length) and any element alignment; products accumulate and statistics are

@@ -50,9 +50,9 @@ constexpr double kLn2 = 0.6931471805599453;
 
 // What the gather leaves for the kernels after it, at the workspace's start.
 struct Header {
-    int live;     // tokens that count
-    int failed;   // a wait ran out somewhere
-    float scale;  // of both gradients
+    int live;      // tokens that count
+    float scale;   // of both gradients
+    int finished;  // CTAs of the loss kernel that are done
     int reserved;
 };
 
@@ -66,14 +66,14 @@ struct GemmArgs {
     int k;        // elements of k (kHead: the tokens that count)
     int v0;       // first vocabulary row of the piece
     int vocab;
+    float* loss;  // NaN goes there when a wait runs out
     // kStatistics
-    float2* stats;        // [n_tiles][rows]: exponent of the tile's maximum, sum of exponentials
-    float* target_logit;  // [rows]
-    const int* target;    // [rows]
-    int rows;             // allocated token rows
+    float2* stats;      // [n_tiles][rows]: exponent of the tile's maximum, sum of exponentials
+    const int* target;  // [rows]
+    int rows;           // allocated token rows
     // kProbability
-    const float* lse2;  // [rows], base 2
-    uint16_t* p;        // [rows][ldp]
+    const float2* row_loss;  // [rows]: log-sum-exp in base 2, the target's p - 1
+    uint16_t* p;             // [rows][ldp]
     int ldp;
     // kHead, kHidden: into fp32 partials [splits][part_rows][part_ld] or, where NULL, into out
     float* part;
@@ -86,6 +86,12 @@ struct GemmArgs {
     int m_rows;          // rows that exist (kHead)
     int cols;            // columns that exist
 };
+
+// Every kernel of a call but its first is launched while the one before still
+// runs: it lets its own successor launch, sets itself up, and waits for the one
+// before to be done before it reads or writes anything.
+__device__ __forceinline__ void launch_after() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // This thread's row: exponentials of 32 logits (columns from col of the tile's
 // row) added to (m, s), m an integer exponent at or above every logit so far.
@@ -117,9 +123,11 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     constexpr bool kTokenRows = MODE != kHead;
     constexpr int kAMn = MODE == kHead, kBMn = MODE == kHead || MODE == kHidden;
     extern __shared__ unsigned char raw[];
+    __shared__ __align__(16) float turn[(MODE == kHead || MODE == kHidden) ? kEpilogueWarps : 1][32 * 32];
     __shared__ uint64_t bars[2 * kStages + 4];
     __shared__ uint32_t tmem_base;
 
+    launch_after();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_ctarank();
     const uint32_t smem = (tc::smem_addr(raw) + 1023u) & ~1023u;
@@ -144,6 +152,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     tc::cluster_sync();
     tc::fence_after();
     const uint32_t tmem = tmem_base;
+    wait_before();
 
     const int live = g.header->live;
     const int m_tiles = kTokenRows ? (live + kTile - 1) / kTile : g.m_tiles;
@@ -153,6 +162,16 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     const int tiles = mn * g.splits;
     const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
+    // Token products run down the tokens first: the hidden states stay in L2 and
+    // the weight is read once.  The gradients run along the hidden size first: a
+    // panel of P is read by the pairs that need it at about the same time.
+    auto place = [&](int t, int& m, int& n) {
+        const int i = t % mn;
+        if (MODE == kStatistics || MODE == kProbability)
+            m = i % m_tiles, n = i / m_tiles;
+        else
+            m = i / g.n_tiles, n = i % g.n_tiles;
+    };
     // the k blocks of a tile's split
     auto k_range = [&](int t, int& kb, int& ke) {
         const int s = t / mn;
@@ -164,8 +183,8 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     if (warp == 0 && lane == 0) {
         int it = 0;
         for (int t = first; t < tiles && ok; t += stride) {
-            const int m = (t % mn) % m_tiles, n = (t % mn) / m_tiles;
-            int kb, ke;
+            int m, n, kb, ke;
+            place(t, m, n);
             k_range(t, kb, ke);
             const int am = m * kTile + (int)rank * kHalf;
             const int bn = n * kTile + (int)rank * kHalf;
@@ -223,8 +242,9 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const uint32_t acc_empty0 = tc::map_to_rank(acc_empty, 0);
         int j = 0;
         for (int t = first; t < tiles && ok; t += stride, ++j) {
-            const int m = (t % mn) % m_tiles, n = (t % mn) / m_tiles, s = t / mn;
-            int kb, ke;
+            const int s = t / mn;
+            int m, n, kb, ke;
+            place(t, m, n);
             k_range(t, kb, ke);
             const int row = m * kTile + (int)rank * kHalf + quad * 32 + lane;
             const uint32_t d = tmem + (j & 1) * kTile + ((uint32_t)quad << 21);
@@ -233,9 +253,10 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             if (!ok) break;
             tc::fence_after();
             if (MODE == kStatistics) {
+                // the target's own exponential is left out: it is added from a logit of its own
                 const int y = row < live ? g.target[row] - (g.v0 + n * kTile) : -1;  // column of the target
                 const int left = g.vocab - (g.v0 + n * kTile);  // columns that exist
-                float top = -INFINITY, sum = 0.f, hit = 0.f;
+                float top = -INFINITY, sum = 0.f;
                 for (int c = 0; c < kTile && c < left; c += 32) {
                     float l[32];
                     __syncwarp();
@@ -246,18 +267,16 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
                     if (y >= c && y < c + 32) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) hit = c + i == y ? l[i] : hit;
+                        for (int i = 0; i < 32; ++i) l[i] = c + i == y ? -INFINITY : l[i];
                     }
                     add_logits(l, top, sum);
                 }
-                if (row < live) {
-                    g.stats[(int64_t)n * g.rows + row] = make_float2(top, sum);
-                    if (y >= 0 && y < kTile && y < left) g.target_logit[row] = hit;
-                }
+                if (row < live) g.stats[(int64_t)n * g.rows + row] = make_float2(top, sum);
             } else if (MODE == kProbability) {
                 const int y = row < live ? g.target[row] - (g.v0 + n * kTile) : -1;
                 const int left = g.vocab - (g.v0 + n * kTile);
-                const float lse2 = row < live ? g.lse2[row] : 0.f;
+                const float2 rl = row < live ? g.row_loss[row] : make_float2(0.f, 0.f);
+                const float lse2 = rl.x;
                 uint16_t* o = g.p + (int64_t)row * g.ldp + n * kTile;
                 for (int c = 0; c < kTile; c += 32) {
                     float l[32];
@@ -270,7 +289,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
                     if (y >= c && y < c + 32) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) l[i] -= c + i == y ? 1.f : 0.f;
+                        for (int i = 0; i < 32; ++i) l[i] = c + i == y ? rl.y : l[i];
                     }
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
@@ -279,9 +298,13 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                                        ss::pack_bf16x2(l[i + 4], l[i + 5]), ss::pack_bf16x2(l[i + 6], l[i + 7]));
                 }
             } else {
+                // 32 x 32 values at a time through shared memory (16-byte groups of row r at
+                // group ^ (r & 7), free of bank conflicts both ways), so that a row's go out together
                 const int limit = kTokenRows ? live : g.m_rows;
+                const int row0 = row - lane;
                 const float scale = g.header->scale;
-                const int64_t orow = row < limit ? (g.row_map ? g.row_map[row] : (int64_t)g.v0 + row) : 0;
+                float* mine = turn[warp - 4];
+                const bool wide = (reinterpret_cast<uintptr_t>(g.out) & 7u) == 0 && (g.out_ld & 3) == 0;
                 for (int c = 0; c < kTile && n * kTile + c < g.cols; c += 32) {
                     float x[32];
                     __syncwarp();
@@ -290,36 +313,46 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] = 0.f;
                     }
-                    const int col = n * kTile + c, left = g.cols - col;
-                    if (row >= limit) {
-                        // a row past the end: the warp still reads together
-                    } else if (g.part) {
-                        float* o = g.part + s * g.part_split + (int64_t)row * g.part_ld + col;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            if (i < left) {  // part_ld is a multiple of 4
-                                float4 v = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<float4*>(mine + lane * 32 + 4 * (i ^ (lane & 7))) =
+                            make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    __syncwarp();
+                    const int col = n * kTile + c, left = g.cols - col;
+                    if (g.part || wide) {  // 8 lanes a row, 4 columns a lane
+                        const int k = lane & 7;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 4 * i + (lane >> 3);
+                            if (row0 + r >= limit || 4 * k >= left) continue;
+                            float4 v = *reinterpret_cast<const float4*>(mine + r * 32 + 4 * (k ^ (r & 7)));
+                            if (g.part) {  // part_ld is a multiple of 4
+                                float* o = g.part + s * g.part_split + (int64_t)(row0 + r) * g.part_ld + col + 4 * k;
                                 if (g.add) {
-                                    const float4 w = *reinterpret_cast<const float4*>(o + i);
+                                    const float4 w = *reinterpret_cast<const float4*>(o);
                                     v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
                                 }
-                                *reinterpret_cast<float4*>(o + i) = v;
+                                *reinterpret_cast<float4*>(o) = v;
+                            } else {
+                                const int64_t orow = g.row_map ? g.row_map[row0 + r] : (int64_t)g.v0 + row0 + r;
+                                uint16_t* o = g.out + orow * g.out_ld + col + 4 * k;
+                                if (4 * k + 4 <= left) {
+                                    *reinterpret_cast<uint2*>(o) =
+                                        make_uint2(ss::pack_bf16x2(scale * v.x, scale * v.y),
+                                                   ss::pack_bf16x2(scale * v.z, scale * v.w));
+                                } else {
+                                    o[0] = ss::f32_to_bf16(scale * v.x);
+                                    if (4 * k + 1 < left) o[1] = ss::f32_to_bf16(scale * v.y);
+                                    if (4 * k + 2 < left) o[2] = ss::f32_to_bf16(scale * v.z);
+                                }
                             }
                         }
-                    } else {
-                        uint16_t* o = g.out + orow * g.out_ld + col;
-                        if (left >= 32 && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 8)
-                                *reinterpret_cast<uint4*>(o + i) = make_uint4(
-                                    ss::pack_bf16x2(scale * x[i], scale * x[i + 1]),
-                                    ss::pack_bf16x2(scale * x[i + 2], scale * x[i + 3]),
-                                    ss::pack_bf16x2(scale * x[i + 4], scale * x[i + 5]),
-                                    ss::pack_bf16x2(scale * x[i + 6], scale * x[i + 7]));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i < left) o[i] = ss::f32_to_bf16(scale * x[i]);
+                    } else {  // a row at a time, a column a lane
+                        for (int r = 0; r < 32 && row0 + r < limit; ++r) {
+                            const int64_t orow = g.row_map ? g.row_map[row0 + r] : (int64_t)g.v0 + row0 + r;
+                            if (lane < left)
+                                g.out[orow * g.out_ld + col + lane] =
+                                    ss::f32_to_bf16(scale * mine[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)]);
                         }
                     }
                 }
@@ -330,7 +363,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         }
     }
     if (!ok) {
-        g.header->failed = 1;
+        *g.loss = NAN;
         __nanosleep(1000000);  // the copies in flight land before the CTA goes
     }
     __syncwarp();
@@ -345,7 +378,8 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 // ---------------------------------------------------------------------------
 
 constexpr int kThreads = 256;
-constexpr int kGatherRows = 32;  // tokens per CTA
+constexpr int kGatherThreads = 1024;
+constexpr int kGatherRows = 32;  // tokens per CTA, one per warp
 
 // 8 elements from element 8j of a row of D bf16 at any element alignment,
 // zeros past its end.
@@ -356,6 +390,17 @@ __device__ __forceinline__ uint4 row_vec(const uint16_t* row, int j, int D) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+__device__ __forceinline__ float dot_bf16(uint4 a, uint4 b, float s) {
+    s = fmaf(ss::bf16_lo(a.x), ss::bf16_lo(b.x), s);
+    s = fmaf(ss::bf16_hi(a.x), ss::bf16_hi(b.x), s);
+    s = fmaf(ss::bf16_lo(a.y), ss::bf16_lo(b.y), s);
+    s = fmaf(ss::bf16_hi(a.y), ss::bf16_hi(b.y), s);
+    s = fmaf(ss::bf16_lo(a.z), ss::bf16_lo(b.z), s);
+    s = fmaf(ss::bf16_hi(a.z), ss::bf16_hi(b.z), s);
+    s = fmaf(ss::bf16_lo(a.w), ss::bf16_lo(b.w), s);
+    return fmaf(ss::bf16_hi(a.w), ss::bf16_hi(b.w), s);
+}
+
 struct GatherArgs {
     Header* header;
     const int64_t* targets;
@@ -363,10 +408,12 @@ struct GatherArgs {
     int T, D, Dp, vocab;
     const uint16_t* hidden;
     int64_t ld;
+    const uint16_t* weight;
+    int64_t ldw;
     uint16_t* h;          // [rows][Dp]
     int* row;             // [rows]: token of each gathered row
     int* target;          // [rows]
-    float* target_logit;  // [rows], NaN until its tile writes it
+    float* target_logit;  // [rows]
     float* token_loss;    // nullable
     uint16_t* d_hidden;   // nullable
     int64_t d_ld;
@@ -376,23 +423,26 @@ struct GatherArgs {
 
 // CTA b places tokens [32 b, 32 b + 32): how many of the tokens before count
 // (read again by every CTA: T * T / 8 bytes in all, from L2), then its own
-// rows, gathered or, where ignored, zeroed in the outputs.  The last CTA knows
-// the total; it zeroes the rows up to the next whole k block.
-__global__ void __launch_bounds__(kThreads) ce_gather_kernel(const GatherArgs a) {
-    __shared__ int part[kThreads / 32];
+// rows, one per warp: gathered together with the logit of their target, or,
+// where ignored, zeroed in the outputs.  The tensor cores' sums drop bits in one
+// direction, and the target's logit is the one that grows large, so it gets
+// a sum of its own, in fp32 by 256 partial sums.  The last CTA knows the total; it
+// zeroes the rows up to the next whole k block.
+__global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherArgs a) {
+    launch_after();
+    __shared__ int part[kGatherThreads / 32];
     __shared__ int place[kGatherRows];
     __shared__ int total;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * kGatherRows;
     int before = 0;
-    for (int t = threadIdx.x; t < t0; t += kThreads) before += a.targets[t] != a.ignore;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) before += __shfl_down_sync(0xFFFFFFFFu, before, d);
+#pragma unroll 4
+    for (int t = threadIdx.x; t < t0; t += kGatherThreads) before += a.targets[t] != a.ignore;
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
     if (lane == 0) part[warp] = before;
     __syncthreads();
     if (warp == 0) {
-        int sum = 0;
-        for (int i = 0; i < kThreads / 32; ++i) sum += part[i];
+        const int sum = __reduce_add_sync(0xFFFFFFFFu, part[lane]);
         const int t = t0 + lane;
         const int64_t y = t < a.T ? a.targets[t] : a.ignore;
         const bool counts = t < a.T && y != a.ignore;
@@ -402,7 +452,6 @@ __global__ void __launch_bounds__(kThreads) ce_gather_kernel(const GatherArgs a)
         if (counts) {
             a.row[at] = t;
             a.target[at] = y >= 0 && y < a.vocab ? (int)y : -1;
-            a.target_logit[at] = NAN;
         } else if (t < a.T && a.token_loss) {
             a.token_loss[t] = 0.f;
         }
@@ -410,25 +459,35 @@ __global__ void __launch_bounds__(kThreads) ce_gather_kernel(const GatherArgs a)
     }
     __syncthreads();
     const int vecs = a.Dp / 8;
-    for (int i = warp; i < kGatherRows && t0 + i < a.T; i += kThreads / 32) {
-        const int at = place[i];
-        if (at >= 0) {
-            const uint16_t* src = a.hidden + (int64_t)(t0 + i) * a.ld;
-            uint4* dst = reinterpret_cast<uint4*>(a.h + (int64_t)at * a.Dp);
-            for (int j = lane; j < vecs; j += 32) dst[j] = row_vec(src, j, a.D);
-        } else if (a.d_hidden) {
-            uint16_t* dst = a.d_hidden + (int64_t)(t0 + i) * a.d_ld;
-            for (int j = lane; j < a.D; j += 32) dst[j] = 0;
+    const int t = t0 + warp, at = place[warp];
+    if (at >= 0) {
+        const uint16_t* src = a.hidden + (int64_t)t * a.ld;
+        uint4* dst = reinterpret_cast<uint4*>(a.h + (int64_t)at * a.Dp);
+        const int64_t y = a.targets[t];
+        const bool known = y >= 0 && y < a.vocab;
+        const uint16_t* w = a.weight + (known ? y : 0) * a.ldw;
+        float s = 0.f;
+#pragma unroll 4
+        for (int j = lane; j < vecs; j += 32) {
+            const uint4 x = row_vec(src, j, a.D);
+            dst[j] = x;
+            s += dot_bf16(x, row_vec(w, j, a.D), 0.f);
         }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        if (lane == 0) a.target_logit[at] = known ? s : NAN;
+    } else if (t < a.T && a.d_hidden) {
+        uint16_t* dst = a.d_hidden + (int64_t)t * a.d_ld;
+        for (int j = lane; j < a.D; j += 32) dst[j] = 0;
     }
     if (blockIdx.x == gridDim.x - 1) {
         const int live = total;
         const int end = (live + kBlockK - 1) / kBlockK * kBlockK;
-        for (int64_t j = threadIdx.x; j < (int64_t)(end - live) * vecs; j += kThreads)
+        for (int64_t j = threadIdx.x; j < (int64_t)(end - live) * vecs; j += kGatherThreads)
             reinterpret_cast<uint4*>(a.h + (int64_t)live * a.Dp)[j] = make_uint4(0, 0, 0, 0);
         if (threadIdx.x == 0) {
             a.header->live = live;
-            a.header->failed = 0;
+            a.header->finished = 0;
             a.header->scale = a.mean ? (live > 0 ? a.grad_scale / (float)live : 0.f) : a.grad_scale;
         }
     }
@@ -438,6 +497,8 @@ __global__ void __launch_bounds__(kThreads) ce_gather_kernel(const GatherArgs a)
 // rows that do: one warp per row.
 __global__ void __launch_bounds__(kThreads)
 ce_stage_kernel(const uint16_t* __restrict__ w, int64_t ld, int V, int D, int Dp, uint16_t* __restrict__ out) {
+    launch_after();
+    wait_before();
     const int64_t v = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     if (v >= V) return;
     const uint16_t* src = w + v * ld;
@@ -445,27 +506,48 @@ ce_stage_kernel(const uint16_t* __restrict__ w, int64_t ld, int V, int D, int Dp
     for (int j = threadIdx.x & 31; j < Dp / 8; j += 32) dst[j] = row_vec(src, j, D);
 }
 
-constexpr int kLossRows = 32;  // rows per CTA, 8 threads each
+constexpr int kLossThreads = 1024;
+constexpr int kLossRows = 32;  // rows per CTA, 32 threads each
+constexpr int kLossSlices = kLossThreads / kLossRows;
 
-// The tiles' statistics of a row to its log-sum-exp and loss; the CTA's losses
-// to one fp64 partial.
-__global__ void __launch_bounds__(kThreads)
-ce_loss_rows_kernel(const Header* __restrict__ header, const float2* __restrict__ stats, int n_tiles, int rows,
-                    const float* __restrict__ target_logit, const int* __restrict__ row_map,
-                    float* __restrict__ lse2, float* __restrict__ token_loss, double* __restrict__ partials) {
-    __shared__ float top_s[8][kLossRows];
-    __shared__ float sum_s[8][kLossRows];
+// The tiles' statistics of a row to its loss.  With r = sum over every other
+// class of exp(l - l_target): loss = log(1 + r), log-sum-exp = l_target + loss and
+// the target's p - 1 = -r / (1 + r), none of which cancels where the target holds
+// almost all of the mass.  The CTA's losses go to one fp64 partial; the last CTA
+// to finish sums the partials, in order, to the loss: over the tokens that count
+// for a mean, 0 when there are none.
+__global__ void __launch_bounds__(kLossThreads)
+ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, int rows,
+               const float* __restrict__ target_logit, const int* __restrict__ row_map,
+               float2* __restrict__ row_loss, float* __restrict__ token_loss, double* __restrict__ partials,
+               int mean, float* __restrict__ loss_out) {
+    launch_after();
+    __shared__ float top_s[kLossSlices][kLossRows];
+    __shared__ float sum_s[kLossSlices][kLossRows + 1];
+    __shared__ double loss_s[32];
+    __shared__ bool last;
     const int r = threadIdx.x & (kLossRows - 1), slice = threadIdx.x / kLossRows;
     const int row = blockIdx.x * kLossRows + r;
-    const bool lives = row < header->live;
+    wait_before();
+    const int live = header->live;
     float top = -INFINITY, sum = 0.f;
-    if (lives) {
-        for (int n = slice; n < n_tiles; n += 8) {
+    auto add = [](float& m, float& s, float m2, float s2) {  // exponents are whole numbers: exact
+        const float up = fmaxf(m, m2);
+        s = (m == up ? s : s * exp2f(m - up)) + (m2 == up ? s2 : s2 * exp2f(m2 - up));
+        m = up;
+    };
+    if (row < live) {
+        int n = slice;
+        for (; n + 3 * kLossSlices < n_tiles; n += 4 * kLossSlices) {
+            float2 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = stats[(int64_t)(n + i * kLossSlices) * rows + row];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) add(top, sum, v[i].x, v[i].y);
+        }
+        for (; n < n_tiles; n += kLossSlices) {
             const float2 v = stats[(int64_t)n * rows + row];
-            const float up = fmaxf(top, v.x);
-            const float at = up == -INFINITY ? 0.f : up;
-            sum = (top == -INFINITY ? 0.f : sum * exp2f(top - at)) + (v.x == -INFINITY ? v.y : v.y * exp2f(v.x - at));
-            top = up;
+            add(top, sum, v.x, v.y);
         }
     }
     top_s[slice][r] = top;
@@ -473,47 +555,48 @@ ce_loss_rows_kernel(const Header* __restrict__ header, const float2* __restrict_
     __syncthreads();
     if (slice == 0) {
         double loss = 0.0;
-        if (lives) {
-            for (int i = 1; i < 8; ++i) top = fmaxf(top, top_s[i][r]);
-            const float at = top == -INFINITY ? 0.f : top;
-            sum = 0.f;
-            for (int i = 0; i < 8; ++i)
-                sum += top_s[i][r] == -INFINITY ? sum_s[i][r] : sum_s[i][r] * exp2f(top_s[i][r] - at);
-            lse2[row] = at + log2f(sum);
-            loss = (double)at * kLn2 + (double)logf(sum) - (double)target_logit[row];
-            if (token_loss) token_loss[row_map[row]] = (float)loss;
+        if (row < live) {
+            for (int i = 1; i < kLossSlices; ++i) add(top, sum, top_s[i][r], sum_s[i][r]);
+            const float hit = target_logit[row];
+            // log of r; a lone class has r = 0
+            const float d = (float)((double)top * kLn2 + (double)logf(sum) - (double)hit);
+            const float rest = expf(-fabsf(d));
+            const float l = (d > 0.f ? d : 0.f) + log1pf(rest);
+            row_loss[row] = make_float2((hit + l) * kLog2e, -(d > 0.f ? 1.f : rest) / (1.f + rest));
+            if (token_loss) token_loss[row_map[row]] = l;
+            loss = (double)l;
         }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) loss += __shfl_down_sync(0xFFFFFFFFu, loss, d);
-        if (r == 0) partials[blockIdx.x] = loss;
+        for (int k = 16; k > 0; k >>= 1) loss += __shfl_down_sync(0xFFFFFFFFu, loss, k);
+        if (r == 0) {
+            partials[blockIdx.x] = loss;
+            __threadfence();
+            last = atomicAdd(&header->finished, 1) == (int)gridDim.x - 1;
+        }
     }
-}
-
-// The loss: the partials' sum in order, over the tokens that count for a mean
-// (0 when there are none); NaN where a product did not finish.
-__global__ void __launch_bounds__(kThreads)
-ce_loss_kernel(const Header* __restrict__ header, const double* __restrict__ partials, int n, int mean,
-               float* __restrict__ loss) {
-    __shared__ double part[kThreads / 32];
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
     double s = 0.0;
-    for (int i = threadIdx.x; i < n; i += kThreads) s += partials[i];
+    for (int i = threadIdx.x; i < (int)gridDim.x; i += kLossThreads) s += __ldcg(partials + i);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, d);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    for (int k = 16; k > 0; k >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, k);
+    if ((threadIdx.x & 31) == 0) loss_s[threadIdx.x >> 5] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
         s = 0.0;
-        for (int i = 0; i < kThreads / 32; ++i) s += part[i];
-        if (mean && header->live > 0) s /= header->live;
-        *loss = header->failed ? NAN : (float)s;
+        for (int i = 0; i < 32; ++i) s += loss_s[i];
+        *loss_out = (float)(mean && live > 0 ? s / live : s);
     }
 }
 
 // out = bf16(scale * sum of the splits' partials), rows through row_map.
 __global__ void __launch_bounds__(kThreads)
-ce_join_kernel(const Header* __restrict__ header, const float* __restrict__ part, int splits, int64_t part_split,
+ce_join_kernel(const Header* __restrict__ header, const float* part, int splits, int64_t part_split,
                int part_ld, int rows, int cols, uint16_t* __restrict__ out, int64_t out_ld,
                const int* __restrict__ row_map) {
+    launch_after();
+    wait_before();
     const int limit = row_map ? header->live : rows;
     const int vecs = part_ld / 4;
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -559,10 +642,10 @@ struct Layout {
     int64_t T, D, V, Dp, rows, n_tiles, piece, pieces;
     int hidden_splits, head_splits;
     bool grad, stage;
-    int64_t row, target, target_logit, lse2, partials, stats, h, w, p, hidden_part, head_part, bytes;
+    int64_t row, target, target_logit, row_loss, partials, stats, h, w, p, hidden_part, head_part, bytes;
 };
 
-constexpr int64_t kPieceBytes = 128ll << 20;  // of P: what stays near the 129 MB L2
+constexpr int64_t kPieceBytes = 256ll << 20;  // of P
 
 Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int pairs) {
     Layout l = {};
@@ -579,7 +662,7 @@ Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int p
     l.row = take(l.rows * 4);
     l.target = take(l.rows * 4);
     l.target_logit = take(l.rows * 4);
-    l.lse2 = take(l.rows * 4);
+    l.row_loss = take(l.rows * 8);
     l.partials = take(l.rows / kLossRows * 8);
     l.stats = take(l.n_tiles * l.rows * 8);
     l.h = take(l.rows * l.Dp * 2);
@@ -632,14 +715,31 @@ int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int
     return r == CUDA_SUCCESS ? SS_OK : ss::cuda_fail(cudaErrorInvalidValue);
 }
 
+// Launch with programmatic stream serialisation (see launch_after).
+template <class... P, class... A>
+int launch(void (*kernel)(P...), int64_t grid, int threads, int smem, cudaStream_t st, A... args) {
+    if (grid > INT32_MAX) return SS_EOVERFLOW;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    return e == cudaSuccess ? ss::check_launch() : ss::cuda_fail(e);
+}
+
 template <int MODE>
 int launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& g, int64_t tiles, cudaStream_t st) {
     const cudaError_t e =
         cudaFuncSetAttribute(ce_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return ss::cuda_fail(e);
     const int64_t pairs = ss::num_sms() / 2;
-    ce_gemm_kernel<MODE><<<(int)(2 * (tiles < pairs ? tiles : pairs)), kGemmThreads, kSmemBytes, st>>>(a, b, g);
-    return ss::check_launch();
+    return launch(ce_gemm_kernel<MODE>, 2 * (tiles < pairs ? tiles : pairs), kGemmThreads, kSmemBytes, st, a, b, g);
 }
 
 constexpr int64_t kMaxSize = 1 << 28;  // tokens, hidden, vocabulary: 32-bit tile coordinates
@@ -694,16 +794,16 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
     int* row = reinterpret_cast<int*>(ws + l.row);
     int* target = reinterpret_cast<int*>(ws + l.target);
     float* target_logit = reinterpret_cast<float*>(ws + l.target_logit);
-    float* lse2 = reinterpret_cast<float*>(ws + l.lse2);
+    float2* row_loss = reinterpret_cast<float2*>(ws + l.row_loss);
     double* partials = reinterpret_cast<double*>(ws + l.partials);
     uint16_t* h = reinterpret_cast<uint16_t*>(ws + l.h);
     const int mean = a->reduction == SS_LOSS_MEAN;
 
     GatherArgs ga = {header, a->targets, a->ignore_index, (int)T, (int)D, (int)l.Dp, (int)V,
-                     static_cast<const uint16_t*>(a->hidden), a->hidden_stride, h, row, target, target_logit,
-                     a->token_loss_out, static_cast<uint16_t*>(a->d_hidden), a->d_hidden_stride,
-                     (float)a->grad_scale, mean};
-    ce_gather_kernel<<<(int)((T > 0 ? T + kGatherRows - 1 : kGatherRows) / kGatherRows), kThreads, 0, st>>>(ga);
+                     static_cast<const uint16_t*>(a->hidden), a->hidden_stride, static_cast<const uint16_t*>(a->weight),
+                     a->weight_stride, h, row, target, target_logit, a->token_loss_out,
+                     static_cast<uint16_t*>(a->d_hidden), a->d_hidden_stride, (float)a->grad_scale, mean};
+    ce_gather_kernel<<<(int)((T > 0 ? T + kGatherRows - 1 : kGatherRows) / kGatherRows), kGatherThreads, 0, st>>>(ga);
     if (int rc = ss::check_launch()) return rc;
 
     const uint16_t* w = static_cast<const uint16_t*>(a->weight);
@@ -711,8 +811,7 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
     if (stage) {
         uint16_t* staged = reinterpret_cast<uint16_t*>(ws + l.w);
         const int64_t per = kThreads / 32;
-        ce_stage_kernel<<<(int)((V + per - 1) / per), kThreads, 0, st>>>(w, ldw, (int)V, (int)D, (int)l.Dp, staged);
-        if (int rc = ss::check_launch()) return rc;
+        if (int rc = launch(ce_stage_kernel, (V + per - 1) / per, kThreads, 0, st, w, ldw, V, D, l.Dp, staged)) return rc;
         w = staged;
         ldw = l.Dp;
     }
@@ -724,7 +823,7 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
     g.vocab = (int)V;
     g.rows = (int)l.rows;
     g.target = target;
-    const int loss_blocks = (int)(l.rows / kLossRows);
+    g.loss = a->loss_out;
     CUtensorMap h_k, w_k;
     if (T > 0) {
         if (int rc = make_map(&h_k, h, l.rows, D, l.Dp, kHalf)) return rc;
@@ -732,12 +831,13 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
         GemmArgs s = g;
         s.n_tiles = (int)l.n_tiles;
         s.stats = reinterpret_cast<float2*>(ws + l.stats);
-        s.target_logit = target_logit;
         if (int rc = launch_gemm<kStatistics>(h_k, w_k, s, l.rows / kTile * l.n_tiles, st)) return rc;
-        ce_loss_rows_kernel<<<loss_blocks, kThreads, 0, st>>>(header, s.stats, s.n_tiles, s.rows, target_logit, row,
-                                                              lse2, a->token_loss_out, partials);
-        if (int rc = ss::check_launch()) return rc;
+        g.stats = s.stats;
     }
+    if (int rc = launch(ce_loss_kernel, T > 0 ? (T + kLossRows - 1) / kLossRows : 1, kLossThreads, 0, st, header, g.stats,
+                        (int)l.n_tiles, (int)l.rows, target_logit, row, row_loss, a->token_loss_out, partials, mean,
+                        a->loss_out))
+        return rc;
 
     if (grad) {
         CUtensorMap p_k, p_mn, h_mn, w_mn;
@@ -760,7 +860,7 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
             GemmArgs q = g;
             q.v0 = (int)v0;
             q.n_tiles = (int)tiles_v;
-            q.lse2 = lse2;
+            q.row_loss = row_loss;
             q.p = p;
             q.ldp = (int)l.piece;
             if (int rc = launch_gemm<kProbability>(h_k, w_k, q, l.rows / kTile * tiles_v, st)) return rc;
@@ -781,10 +881,9 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
                 if (int rc = launch_gemm<kHead>(p_mn, h_mn, d, tiles_v * d_tiles * d.splits, st)) return rc;
                 if (d.part) {
                     const int64_t blocks = (rows_v * (ld / 4) + kThreads - 1) / kThreads;
-                    ce_join_kernel<<<(int)blocks, kThreads, 0, st>>>(
-                        header, d.part, d.splits, d.part_split, d.part_ld, (int)rows_v, (int)D,
-                        d.out + v0 * d.out_ld, d.out_ld, nullptr);
-                    if (int rc = ss::check_launch()) return rc;
+                    if (int rc = launch(ce_join_kernel, blocks, kThreads, 0, st, header, d.part, d.splits, d.part_split,
+                                        d.part_ld, (int)rows_v, (int)D, d.out + v0 * d.out_ld, d.out_ld, nullptr))
+                        return rc;
                 }
             }
             if (a->d_hidden) {
@@ -804,15 +903,14 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
                 if (int rc = launch_gemm<kHidden>(p_k, w_mn, d, l.rows / kTile * d_tiles * d.splits, st)) return rc;
                 if (d.part && i == l.pieces - 1) {
                     const int64_t blocks = (l.rows * (ld / 4) + kThreads - 1) / kThreads;
-                    ce_join_kernel<<<(int)blocks, kThreads, 0, st>>>(header, d.part, d.splits, d.part_split, d.part_ld,
-                                                                     (int)l.rows, (int)D, d.out, d.out_ld, row);
-                    if (int rc = ss::check_launch()) return rc;
+                    if (int rc = launch(ce_join_kernel, blocks, kThreads, 0, st, header, d.part, d.splits, d.part_split,
+                                        d.part_ld, (int)l.rows, (int)D, d.out, d.out_ld, row))
+                        return rc;
                 }
             }
         }
     }
-    ce_loss_kernel<<<1, kThreads, 0, st>>>(header, partials, T > 0 ? loss_blocks : 0, mean, a->loss_out);
-    return ss::check_launch();
+    return SS_OK;
 }
 
 }  // extern "C"
