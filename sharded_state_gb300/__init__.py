@@ -206,6 +206,17 @@ def _ptr_array(xs: Sequence) -> ctypes.Array:
     return arr
 
 
+def _current_stream() -> int:
+    """The current stream's handle.  torch's own accessor of the raw handle, where it
+    has one, costs a sixth of building a Stream object (0.5 against 2.9 us on a Grace
+    core), which shows beside launches of a few microseconds."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return int(torch.cuda.current_stream().cuda_stream)
+    return int(raw(torch.cuda.current_device()))
+
+
 def _i64_array(xs: Sequence[int]):
     arr = (ctypes.c_int64 * max(1, len(xs)))()
     for k, x in enumerate(xs):
@@ -215,8 +226,7 @@ def _i64_array(xs: Sequence[int]):
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)

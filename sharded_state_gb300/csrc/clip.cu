@@ -14,7 +14,12 @@
 //           does not depend on which CTA ran first;
 //   pass 2  every element is scaled by the factor.
 //
-// All of it is bound by HBM: 2 flops per 2 bytes read.
+// A list small enough for one cluster of CTAs takes a single launch: the data stay
+// in registers between the passes, and the CTAs' sums meet in one another's
+// shared memory.
+//
+// All of it is bound by HBM (2 flops per 2 bytes read), or, where there is
+// little of it, by launches.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,6 +29,8 @@
 #include "adamw.cuh"
 #include "device_utils.cuh"
 #include "internal.h"
+#include "launch.cuh"
+#include "segmap.cuh"
 
 namespace {
 
@@ -33,6 +40,7 @@ constexpr int kThreads = 256;
 constexpr int kVecs = 4;                         // 16-byte blocks per thread of a tile
 constexpr int kTileBlocks = kThreads * kVecs;    // 16 KiB: a tile is one of these, or more (list_rounds)
 constexpr int kTab = 512;                        // tensors per launch
+constexpr int kTabSmall = 16;                    // of the one-cluster form (a short parameter block)
 constexpr double kEps = 1e-6;                    // added to the norm in the factor's denominator
 constexpr int kFoldSpan = 8192;                  // partials summed by one CTA of the first fold
 
@@ -44,13 +52,15 @@ static_assert((kMaxPartials * 4) % 16 == 0, "the first fold's doubles are aligne
 
 // The tensors of one launch: start, first tile and element count of each
 // (elements are negated for fp32).
-struct ListTab {
-    const unsigned char* in[kTab];
-    unsigned char* out[kTab];
-    int64_t n[kTab];
-    int first[kTab + 1];
+template <int S>
+struct ListTabT {
+    const unsigned char* in[S];
+    unsigned char* out[S];
+    int64_t n[S];
+    int first[S + 1];
     int count;
 };
+using ListTab = ListTabT<kTab>;
 
 struct RankPtrs {
     const void* p[SS_MAX_WORLD];
@@ -121,6 +131,7 @@ __device__ __forceinline__ T block_sum(T s) {
 // same 16 bytes as one of its own, and are masked out.
 __global__ void __launch_bounds__(kThreads)
 list_square_kernel(const __grid_constant__ ListTab tab, int rounds, float* __restrict__ partials) {
+    ss::launch_after();
     const int tile = blockIdx.x;
     const int k = find_tensor(tab.first, tab.count, tile);
     const unsigned char* p = tab.in[k];
@@ -157,6 +168,8 @@ list_square_kernel(const __grid_constant__ ListTab tab, int rounds, float* __res
 // First fold, for many partials: CTA b sums partials [b * kFoldSpan, ...).
 __global__ void __launch_bounds__(kThreads)
 fold_kernel(const float* __restrict__ partials, int64_t n, double* __restrict__ sums) {
+    ss::launch_after();
+    ss::wait_before();
     const int64_t a = (int64_t)blockIdx.x * kFoldSpan;
     const int64_t b = a + kFoldSpan < n ? a + kFoldSpan : n;
     double s = 0.0;
@@ -165,21 +178,30 @@ fold_kernel(const float* __restrict__ partials, int64_t n, double* __restrict__ 
     if (threadIdx.x == 0) sums[blockIdx.x] = s;
 }
 
-// The norm and the factor of a sum of squares.  A NaN norm gives a NaN factor
-// (min would drop it).
+// The norm and the factor of a sum of squares, in fp32 where the sum is in its
+// range (fp64 roots and quotients take hundreds of clocks).  A NaN norm gives a
+// NaN factor (min would drop it).
 __device__ __forceinline__ void write_norm(double sq, double max_norm, float* norm_out) {
-    const double norm = sqrt(sq);
-    const double c = max_norm / (norm + kEps);
-    norm_out[0] = (float)norm;
-    norm_out[1] = c >= 1.0 ? 1.0f : (float)c;
+    float norm, c;
+    if (sq > 1e-30 && sq < 1e38) {
+        norm = __fsqrt_rn((float)sq);
+        c = __fdiv_rn((float)max_norm, norm + (float)kEps);
+    } else {
+        const double n = sqrt(sq);
+        norm = (float)n;
+        c = (float)(max_norm / (n + kEps));
+    }
+    norm_out[0] = norm;
+    norm_out[1] = c >= 1.0f ? 1.0f : c;
 }
 
-// Last fold, one CTA: the sum of n values, as it is (sq_out) or as norm and
+// Last fold, one CTA: the sum of n partials, as it is (sq_out) or as norm and
 // factor (norm_out); either may be NULL.
 template <class T>
 __global__ void __launch_bounds__(kThreads)
-finish_kernel(const T* __restrict__ v, int64_t n, double max_norm, double* __restrict__ sq_out,
-              float* __restrict__ norm_out) {
+finish_kernel(const T* v, int64_t n, double max_norm, double* sq_out, float* norm_out) {
+    ss::launch_after();
+    ss::wait_before();
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < n; i += kThreads) s += (double)v[i];
     s = block_sum(s);
@@ -187,6 +209,24 @@ finish_kernel(const T* __restrict__ v, int64_t n, double max_norm, double* __res
         if (sq_out) *sq_out = s;
         if (norm_out) write_norm(s, max_norm, norm_out);
     }
+}
+
+// Sum of n doubles by one warp, the same in every lane and whichever kernel asks.
+__device__ __forceinline__ double sum_sums(const double* sq, int n) {
+    double s = 0.0;
+    for (int i = threadIdx.x & 31; i < n; i += 32) s += sq[i];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    return s;
+}
+
+// Norm and factor of the sums of a sharded step; one warp.  Its successor may
+// start when this one's own predecessors are done, and has the factor to wait for.
+__global__ void norm_kernel(const double* sq, int n, double max_norm, float* norm_out) {
+    ss::wait_before();
+    ss::launch_after();
+    const double s = sum_sums(sq, n);
+    if (threadIdx.x == 0) write_norm(s, max_norm, norm_out);
 }
 
 __device__ __forceinline__ uint4 scale_bf16(uint4 w, float c) {
@@ -214,10 +254,29 @@ __device__ __forceinline__ uint4 ld_rw_u4(const void* p) {
 // Pass 2 over a list: one tile of a tensor's output, in aligned 16-byte blocks
 // of the output; an input at another offset is realigned in registers, and the
 // blocks at the tensor's ends go element by element.  In place with a factor of
-// 1 there is nothing to write.
+// 1 there is nothing to write.  SELF: every CTA folds the (few) partials itself,
+// the first one writes the result down.
+template <bool SELF>
 __global__ void __launch_bounds__(kThreads)
-list_scale_kernel(const __grid_constant__ ListTab tab, int rounds, const float* __restrict__ norm) {
-    const float c = norm[1];
+list_scale_kernel(const __grid_constant__ ListTab tab, int rounds, const float* partials, int n_partials,
+                  double max_norm, float* norm) {
+    ss::launch_after();
+    ss::wait_before();
+    float c;
+    if (SELF) {
+        __shared__ float result[2];
+        double sum = 0.0;
+        for (int i = threadIdx.x; i < n_partials; i += kThreads) sum += (double)partials[i];
+        sum = block_sum(sum);
+        if (threadIdx.x == 0) {
+            write_norm(sum, max_norm, result);
+            if (blockIdx.x == 0) norm[0] = result[0], norm[1] = result[1];
+        }
+        __syncthreads();
+        c = result[1];
+    } else {
+        c = norm[1];
+    }
     const int tile = blockIdx.x;
     const int k = find_tensor(tab.first, tab.count, tile);
     const unsigned char* in = tab.in[k];
@@ -255,6 +314,112 @@ list_scale_kernel(const __grid_constant__ ListTab tab, int rounds, const float* 
 }
 
 // ---------------------------------------------------------------------------
+// a list in one cluster
+// ---------------------------------------------------------------------------
+
+constexpr int kClusterMax = 8;                          // the portable size
+constexpr int kSmallRounds = 2;                         // 4 KiB tiles of a CTA, held in registers
+constexpr int kSmallTiles = kClusterMax * kSmallRounds;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Sum over a cluster of one fp32 value per CTA (thread 0's), in rank order and
+// in fp64, the same in every thread of every CTA.  All threads take part, and
+// call cluster_wait() before they leave: their CTA's value may still be read.
+__device__ __forceinline__ double cluster_sum(float s) {
+    __shared__ float mine;
+    if (threadIdx.x == 0) mine = s;
+    cluster_arrive();
+    cluster_wait();
+    const int n = (int)cluster_size(), lane = threadIdx.x & 31;
+    float x = 0.f;
+    if (lane < n) {
+        uint32_t at = (uint32_t)__cvta_generic_to_shared(&mine);
+        asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(lane));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+    }
+    __syncwarp();
+    cluster_arrive();
+    double sum = 0.0;
+    for (int i = 0; i < n; ++i) sum += (double)__shfl_sync(0xFFFFFFFFu, x, i);
+    return sum;
+}
+
+// Norm, and (scale) clipping, of a list in one launch.  CTA r of R takes tiles r,
+// r + R, ... of 256 aligned 16-byte blocks of the outputs; every load goes out
+// before the first square, and the values stay in registers until they are scaled.
+__global__ void __launch_bounds__(kThreads)
+list_small_kernel(const __grid_constant__ ListTabT<kTabSmall> tab, double max_norm, int scale, float* norm_out) {
+    const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
+    const int tiles = tab.first[tab.count];
+    uint4 w[kSmallRounds];
+    int at_k[kSmallRounds];
+#pragma unroll
+    for (int i = 0; i < kSmallRounds; ++i) {
+        const int tile = rank + i * ranks;
+        w[i] = make_uint4(0, 0, 0, 0);
+        at_k[i] = 0;
+        if (tile >= tiles) continue;
+        const int k = find_tensor(tab.first, tab.count, tile);
+        at_k[i] = k;
+        const unsigned char* in = tab.in[k];
+        const int64_t n = tab.n[k], bytes = n < 0 ? -n * 4 : n * 2;
+        const int lead = (int)(reinterpret_cast<uintptr_t>(tab.out[k]) & 15u);
+        const int64_t at = 16 * ((int64_t)(tile - tab.first[k]) * kThreads + threadIdx.x) - lead;
+        if (at >= 0 && at + 16 <= bytes) {
+            w[i] = (reinterpret_cast<uintptr_t>(in + at) & 15u) == 0 ? ld_rw_u4(in + at) : ss::ld_any16(in + at);
+        } else if (at < bytes) {
+            uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int b = 0; b < 16; b += 2)
+                if (at + b >= 0 && at + b < bytes)
+                    v[b >> 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(in + at + b) << (8 * (b & 2));
+            w[i] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSmallRounds; ++i)
+        s = tab.n[at_k[i]] < 0 ? square_sum_f32(w[i], s) : square_sum_bf16(w[i], s);
+    const double sq = cluster_sum(block_sum(s));
+    float result[2];
+    write_norm(sq, max_norm, result);
+    if (threadIdx.x == 0 && rank == 0) norm_out[0] = result[0], norm_out[1] = result[1];
+    const float c = result[1];
+#pragma unroll
+    for (int i = 0; i < kSmallRounds; ++i) {
+        const int tile = rank + i * ranks;
+        if (!scale || tile >= tiles) continue;
+        const int k = at_k[i];
+        unsigned char* out = tab.out[k];
+        if (c == 1.0f && tab.in[k] == out) continue;
+        const int64_t n = tab.n[k], bytes = n < 0 ? -n * 4 : n * 2;
+        const int lead = (int)(reinterpret_cast<uintptr_t>(out) & 15u);
+        const int64_t at = 16 * ((int64_t)(tile - tab.first[k]) * kThreads + threadIdx.x) - lead;
+        const uint4 v = n < 0 ? scale_f32(w[i], c) : scale_bf16(w[i], c);
+        if (at >= 0 && at + 16 <= bytes)
+            *reinterpret_cast<uint4*>(out + at) = v;
+        else if (at < bytes)
+            ss::st_bytes(out + at, v, at < 0 ? (int)-at : 0, bytes - at < 16 ? (int)(bytes - at) : 16);
+    }
+    __syncwarp();
+    cluster_wait();
+}
+
+// ---------------------------------------------------------------------------
 // the sharded form
 // ---------------------------------------------------------------------------
 
@@ -275,22 +440,34 @@ __device__ __forceinline__ void widen(uint4 w, float (&x)[16 / EB]) {
     }
 }
 
-// Reduce-scatter of one vector per thread and iteration: g = (G_0 + ... +
-// G_{N-1}) / N in rank order, written, and the CTA's sum of g^2 as one partial.
-// Pads hold zero gradients and add nothing.  CTA b takes `rounds` consecutive
-// rounds of kThreads vectors (one, unless the partials would not fit).
-template <int NR, int EB>
+// A plan range as whole vectors and the elements left at its two ends (fewer
+// than 16 in all), which one CTA's first warp takes one by one.
+struct Split {
+    int64_t vbeg, nvec, a0, a1, b0, b1;
+    // the element of an edge thread, -1 for none
+    __device__ __forceinline__ int64_t edge(int t) const {
+        return t < a1 - a0 ? a0 + t : t - (a1 - a0) < b1 - b0 ? b0 + (t - (a1 - a0)) : -1;
+    }
+};
+
+// Reduce-scatter of one vector per thread and round: g = (G_0 + ... + G_{N-1}) / N
+// in rank order, written, and the CTA's sum of g^2 as one partial; CLUSTER: the
+// whole grid is one cluster, which sums the partials itself.  Pads hold zero
+// gradients and add nothing.  CTA b takes `rounds` consecutive rounds of kThreads
+// vectors (one, unless the partials would not fit).
+template <int NR, int EB, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads)
-rs_square_kernel(RankPtrs grads, int N, int64_t vbeg, int64_t nvec, int rounds, float* __restrict__ gout,
-                 float* __restrict__ partials) {
+rs_square_kernel(RankPtrs grads, int N, Split sp, int rounds, float* __restrict__ gout,
+                 float* __restrict__ partials, double* __restrict__ sq_out) {
+    ss::launch_after();
     constexpr int E = Vec<EB>::n;
     const int n = NR > 0 ? NR : N;
     const float fN = (float)n;
     float sq = 0.f;
     for (int it = 0; it < rounds; ++it) {
         const int64_t q = ((int64_t)blockIdx.x * rounds + it) * kThreads + threadIdx.x;
-        if (q >= nvec) break;
-        const int64_t at = (vbeg + q * E) * EB;  // byte offset of the vector
+        if (q >= sp.nvec) break;
+        const int64_t at = (sp.vbeg + q * E) * EB;  // byte offset of the vector
         constexpr int kW = NR > 0 ? NR : 8;
         uint4 w[kW];
 #pragma unroll
@@ -326,114 +503,120 @@ rs_square_kernel(RankPtrs grads, int N, int64_t vbeg, int64_t nvec, int rounds, 
             s[e] = __fdiv_rn(s[e], fN);
             sq = fmaf(s[e], s[e], sq);
         }
-        float* o = gout + vbeg + q * E;
+        float* o = gout + sp.vbeg + q * E;
 #pragma unroll
         for (int e = 0; e < E; e += 4) ss::st_stream_f4(o + e, make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]));
     }
-    sq = block_sum(sq);
-    if (threadIdx.x == 0) partials[blockIdx.x] = sq;
-}
-
-// The elements of a group's range outside whole vectors, fewer than 16, as the
-// kernel above; one warp.
-__global__ void rs_square_edge_kernel(RankPtrs grads, int N, int eb, int64_t a0, int64_t a1, int64_t b0,
-                                      int64_t b1, float* gout, float* partial) {
-    const int64_t k = threadIdx.x, na = a1 - a0;
-    const int64_t f = k < na ? a0 + k : b0 + (k - na);
-    float sq = 0.f;
-    if (k < na || k - na < b1 - b0) {
+    const int64_t f = blockIdx.x == gridDim.x - 1 ? sp.edge(threadIdx.x) : -1;
+    if (f >= 0) {
         float s = 0.f;
-        for (int r = 0; r < N; ++r) {
-            const float x = eb == 2 ? ss::bf16_to_f32(static_cast<const uint16_t*>(grads.p[r])[f])
+        for (int r = 0; r < n; ++r) {
+            const float x = EB == 2 ? ss::bf16_to_f32(static_cast<const uint16_t*>(grads.p[r])[f])
                                     : static_cast<const float*>(grads.p[r])[f];
             s = r == 0 ? x : __fadd_rn(s, x);
         }
-        s = __fdiv_rn(s, (float)N);
+        s = __fdiv_rn(s, fN);
         gout[f] = s;
-        sq = s * s;
+        sq = fmaf(s, s, sq);
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sq += __shfl_down_sync(0xFFFFFFFFu, sq, d);
-    if (threadIdx.x == 0) *partial = sq;
+    sq = block_sum(sq);
+    if (CLUSTER) {
+        const double sum = cluster_sum(sq);
+        if (threadIdx.x == 0 && blockIdx.x == 0) *sq_out = sum;
+        __syncwarp();
+        cluster_wait();
+    } else if (threadIdx.x == 0) {
+        partials[blockIdx.x] = sq;
+    }
 }
 
 // AdamW on the clipped reduced gradient, one vector of plan elements per
-// thread.  MASTER == false: theta is the shard itself (no fp32 master).
-template <int EB, bool MASTER>
+// thread.  MASTER == false: theta is the shard itself (no fp32 master).  SELF:
+// every CTA works the factor out of the sums (CTA 0 writes it down), else
+// norm_kernel has done it.
+template <int EB, bool MASTER, bool SELF>
 __global__ void __launch_bounds__(kThreads)
-clip_adamw_kernel(const float* __restrict__ reduced, const float* __restrict__ norm, int64_t vbeg,
-                  int64_t nvec, float* __restrict__ master, float* __restrict__ exp_avg,
+clip_adamw_kernel(const float* __restrict__ reduced, const double* sq, int num_sums, double max_norm, float* norm,
+                  Split sp, float* __restrict__ master, float* __restrict__ exp_avg,
                   float* __restrict__ exp_avg_sq, unsigned char* __restrict__ shards, AdamCoef c) {
     constexpr int E = Vec<EB>::n;
     const int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (q >= nvec) return;
-    const int64_t f = vbeg + q * E;
+    const int64_t f = sp.vbeg + q * E;
+    const bool whole = q < sp.nvec;
     float4 g[E / 4], t[E / 4], m[E / 4], v[E / 4];
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-        const uint4 w = ss::ld_stream_u4(reduced + f + 4 * i);
-        g[i] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
-        if (MASTER) t[i] = ss::ld_rw_f4(master + f + 4 * i);
-        m[i] = ss::ld_rw_f4(exp_avg + f + 4 * i);
-        v[i] = ss::ld_rw_f4(exp_avg_sq + f + 4 * i);
-    }
-    if (!MASTER) {
-        float x[E];
-        widen<EB>(ld_rw_u4(shards + f * EB), x);
+        for (int i = 0; i < E / 4; ++i) {
+            const uint4 w = ss::ld_stream_u4(reduced + f + 4 * i);
+            g[i] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+            if (MASTER) t[i] = ss::ld_rw_f4(master + f + 4 * i);
+            m[i] = ss::ld_rw_f4(exp_avg + f + 4 * i);
+            v[i] = ss::ld_rw_f4(exp_avg_sq + f + 4 * i);
+        }
+        if (!MASTER) {
+            float x[E];
+            widen<EB>(ld_rw_u4(shards + f * EB), x);
 #pragma unroll
-        for (int i = 0; i < E / 4; ++i) t[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            for (int i = 0; i < E / 4; ++i) t[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        }
     }
-    const float clip = norm[1];
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-        ss::adamw_elem(__fmul_rn(g[i].x, clip), t[i].x, m[i].x, v[i].x, c);
-        ss::adamw_elem(__fmul_rn(g[i].y, clip), t[i].y, m[i].y, v[i].y, c);
-        ss::adamw_elem(__fmul_rn(g[i].z, clip), t[i].z, m[i].z, v[i].z, c);
-        ss::adamw_elem(__fmul_rn(g[i].w, clip), t[i].w, m[i].w, v[i].w, c);
-        if (MASTER) ss::st_stream_f4(master + f + 4 * i, t[i]);
-        ss::st_stream_f4(exp_avg + f + 4 * i, m[i]);
-        ss::st_stream_f4(exp_avg_sq + f + 4 * i, v[i]);
-    }
-    uint4 p;
-    if constexpr (EB == 2) {
-        p = make_uint4(ss::pack_bf16x2(t[0].x, t[0].y), ss::pack_bf16x2(t[0].z, t[0].w),
-                       ss::pack_bf16x2(t[1].x, t[1].y), ss::pack_bf16x2(t[1].z, t[1].w));
+    float clip;
+    if (SELF) {
+        __shared__ float result[2];
+        if (threadIdx.x < 32) {
+            const double s = sum_sums(sq, num_sums);
+            if (threadIdx.x == 0) {
+                write_norm(s, max_norm, result);
+                if (blockIdx.x == 0) norm[0] = result[0], norm[1] = result[1];
+            }
+        }
+        __syncthreads();
+        clip = result[1];
     } else {
-        p = make_uint4(__float_as_uint(t[0].x), __float_as_uint(t[0].y), __float_as_uint(t[0].z),
-                       __float_as_uint(t[0].w));
+        ss::wait_before();
+        clip = norm[1];
     }
-    ss::st_stream_u4(shards + f * EB, p);
-}
-
-__global__ void clip_adamw_edge_kernel(const float* reduced, const float* norm, int eb, int64_t a0, int64_t a1,
-                                       int64_t b0, int64_t b1, float* master, float* exp_avg,
-                                       float* exp_avg_sq, void* shards, AdamCoef c) {
-    const int64_t k = threadIdx.x, na = a1 - a0;
-    if (k >= na && k - na >= b1 - b0) return;
-    const int64_t f = k < na ? a0 + k : b0 + (k - na);
-    float th = master ? master[f]
-                      : (eb == 2 ? ss::bf16_to_f32(static_cast<const uint16_t*>(shards)[f])
-                                 : static_cast<const float*>(shards)[f]);
-    float m = exp_avg[f], v = exp_avg_sq[f];
-    ss::adamw_elem(__fmul_rn(reduced[f], norm[1]), th, m, v, c);
-    if (master) master[f] = th;
-    exp_avg[f] = m;
-    exp_avg_sq[f] = v;
-    if (eb == 2)
-        static_cast<uint16_t*>(shards)[f] = ss::f32_to_bf16(th);
-    else
-        static_cast<float*>(shards)[f] = th;
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+            ss::adamw_elem(__fmul_rn(g[i].x, clip), t[i].x, m[i].x, v[i].x, c);
+            ss::adamw_elem(__fmul_rn(g[i].y, clip), t[i].y, m[i].y, v[i].y, c);
+            ss::adamw_elem(__fmul_rn(g[i].z, clip), t[i].z, m[i].z, v[i].z, c);
+            ss::adamw_elem(__fmul_rn(g[i].w, clip), t[i].w, m[i].w, v[i].w, c);
+            if (MASTER) ss::st_stream_f4(master + f + 4 * i, t[i]);
+            ss::st_stream_f4(exp_avg + f + 4 * i, m[i]);
+            ss::st_stream_f4(exp_avg_sq + f + 4 * i, v[i]);
+        }
+        uint4 p;
+        if constexpr (EB == 2) {
+            p = make_uint4(ss::pack_bf16x2(t[0].x, t[0].y), ss::pack_bf16x2(t[0].z, t[0].w),
+                           ss::pack_bf16x2(t[1].x, t[1].y), ss::pack_bf16x2(t[1].z, t[1].w));
+        } else {
+            p = make_uint4(__float_as_uint(t[0].x), __float_as_uint(t[0].y), __float_as_uint(t[0].z),
+                           __float_as_uint(t[0].w));
+        }
+        ss::st_stream_u4(shards + f * EB, p);
+    }
+    const int64_t x = blockIdx.x == gridDim.x - 1 ? sp.edge(threadIdx.x) : -1;
+    if (x >= 0) {
+        uint16_t* s16 = reinterpret_cast<uint16_t*>(shards);
+        float* s32 = reinterpret_cast<float*>(shards);
+        float th = MASTER ? master[x] : EB == 2 ? ss::bf16_to_f32(s16[x]) : s32[x];
+        float m1 = exp_avg[x], v1 = exp_avg_sq[x];
+        ss::adamw_elem(__fmul_rn(reduced[x], clip), th, m1, v1, c);
+        if (MASTER) master[x] = th;
+        exp_avg[x] = m1;
+        exp_avg_sq[x] = v1;
+        if (EB == 2)
+            s16[x] = ss::f32_to_bf16(th);
+        else
+            s32[x] = th;
+    }
 }
 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-
-// A plan range as whole vectors and what is left at its two ends.
-struct Split {
-    int64_t vbeg, nvec, a0, a1, b0, b1;
-    bool edges() const { return a1 > a0 || b1 > b0; }
-};
 
 Split split_range(int64_t lo, int64_t hi, int e) {
     Split s;
@@ -452,16 +635,12 @@ Split split_range(int64_t lo, int64_t hi, int e) {
 // n fp32 partials at the workspace's start to one sum, norm and factor.
 int fold(void* workspace, int64_t n, double max_norm, double* sq_out, float* norm_out, cudaStream_t st) {
     float* partials = static_cast<float*>(workspace);
-    if (n <= kFoldSpan) {
-        finish_kernel<float><<<1, kThreads, 0, st>>>(partials, n, max_norm, sq_out, norm_out);
-        return ss::check_launch();
-    }
+    if (n <= kFoldSpan)
+        return ss::launch(finish_kernel<float>, 1, kThreads, 0, 0, true, st, partials, n, max_norm, sq_out, norm_out);
     double* sums = reinterpret_cast<double*>(partials + kMaxPartials);
-    const int blocks = (int)((n + kFoldSpan - 1) / kFoldSpan);
-    fold_kernel<<<blocks, kThreads, 0, st>>>(partials, n, sums);
-    if (int rc = ss::check_launch()) return rc;
-    finish_kernel<double><<<1, kThreads, 0, st>>>(sums, blocks, max_norm, sq_out, norm_out);
-    return ss::check_launch();
+    const int64_t blocks = (n + kFoldSpan - 1) / kFoldSpan;
+    if (int rc = ss::launch(fold_kernel, blocks, kThreads, 0, 0, true, st, partials, n, sums)) return rc;
+    return ss::launch(finish_kernel<double>, 1, kThreads, 0, 0, true, st, sums, blocks, max_norm, sq_out, norm_out);
 }
 
 int check_workspace(const void* workspace, size_t bytes) {
@@ -528,32 +707,90 @@ int for_tables(int num_tensors, const int64_t* numels, const int* elem_bytes, co
     return SS_OK;
 }
 
-int list_norm(int num_tensors, const int64_t* numels, const int* elem_bytes, const void* const* grads,
-              int rounds, double max_norm, float* norm_out, void* workspace, cudaStream_t st) {
-    float* partials = static_cast<float*>(workspace);
-    int64_t n = 0;
-    int rc = for_tables(num_tensors, numels, elem_bytes, grads, nullptr, false, rounds, [&](const ListTab& tab) {
-        const int tiles = tab.first[tab.count];
-        list_square_kernel<<<tiles, kThreads, 0, st>>>(tab, rounds, partials + n);
-        n += tiles;
-        return ss::check_launch();
-    });
-    return rc ? rc : fold(workspace, n, max_norm, nullptr, norm_out, st);
+int cluster_for(int64_t ctas) {
+    int c = 1;
+    while (c < kClusterMax && c < ctas) c *= 2;
+    return c;
 }
 
-template <int EB>
+// The whole call in one launch, where the list fits a cluster: kNotSmall if not.
+constexpr int kNotSmall = 1;
+
+int list_small(int num_tensors, const int64_t* numels, const int* elem_bytes, const void* const* grads,
+               void* const* out, bool scale, double max_norm, float* norm_out, cudaStream_t st) {
+    ListTabT<kTabSmall> tab;
+    tab.count = 0;
+    tab.first[0] = 0;
+    tab.n[0] = 0;
+    for (int k = 0; k < num_tensors; ++k) {
+        if (numels[k] == 0) continue;
+        if (tab.count == kTabSmall) return kNotSmall;
+        const int j = tab.count;
+        tab.in[j] = static_cast<const unsigned char*>(grads[k]);
+        tab.out[j] = static_cast<unsigned char*>(out ? out[k] : const_cast<void*>(grads[k]));
+        tab.n[j] = elem_bytes[k] == 4 ? -numels[k] : numels[k];
+        const int64_t blocks =
+            ((int64_t)(reinterpret_cast<uintptr_t>(tab.out[j]) & 15u) + numels[k] * elem_bytes[k] + 15) / 16;
+        const int64_t tiles = tab.first[j] + (blocks + kThreads - 1) / kThreads;
+        if (tiles > kSmallTiles) return kNotSmall;
+        tab.first[j + 1] = (int)tiles;
+        tab.count = j + 1;
+    }
+    const int cluster = cluster_for(tab.first[tab.count]);
+    return ss::launch(list_small_kernel, cluster, kThreads, 0, cluster, false, st, tab, max_norm, scale ? 1 : 0, norm_out);
+}
+
+// Partials up to which the second pass folds them itself, in every CTA.
+constexpr int64_t kSelfPartials = 1024;
+
+int list_call(int num_tensors, const int64_t* numels, const int* elem_bytes, const void* const* grads,
+              void* const* out, bool scale, double max_norm, float* norm_out, void* workspace, cudaStream_t st) {
+    int rc = list_small(num_tensors, numels, elem_bytes, grads, out, scale, max_norm, norm_out, st);
+    if (rc != kNotSmall) return rc;
+    const int rounds = list_rounds(num_tensors, numels, elem_bytes, grads);
+    if (rounds == 0) return SS_EOVERFLOW;
+    float* partials = static_cast<float*>(workspace);
+    int64_t n = 0;
+    rc = for_tables(num_tensors, numels, elem_bytes, grads, nullptr, false, rounds, [&](const ListTab& tab) {
+        const int tiles = tab.first[tab.count];
+        const int rc1 = ss::launch(list_square_kernel, tiles, kThreads, 0, 0, false, st, tab, rounds, partials + n);
+        n += tiles;
+        return rc1;
+    });
+    if (rc) return rc;
+    const bool self = scale && n <= kSelfPartials;
+    if (!self)
+        if ((rc = fold(workspace, n, max_norm, nullptr, norm_out, st))) return rc;
+    if (!scale) return SS_OK;
+    return for_tables(num_tensors, numels, elem_bytes, grads, out, true, rounds, [&](const ListTab& tab) {
+        return ss::launch(self ? list_scale_kernel<true> : list_scale_kernel<false>, tab.first[tab.count], kThreads, 0, 0,
+                          true, st, tab, rounds, partials, (int)n, max_norm, norm_out);
+    });
+}
+
+template <int EB, bool CLUSTER>
 auto pick_square(int N) {
     switch (N) {
-        case 1: return rs_square_kernel<1, EB>;
-        case 2: return rs_square_kernel<2, EB>;
-        case 3: return rs_square_kernel<3, EB>;
-        case 4: return rs_square_kernel<4, EB>;
-        case 5: return rs_square_kernel<5, EB>;
-        case 6: return rs_square_kernel<6, EB>;
-        case 7: return rs_square_kernel<7, EB>;
-        case 8: return rs_square_kernel<8, EB>;
-        default: return rs_square_kernel<0, EB>;
+        case 1: return rs_square_kernel<1, EB, CLUSTER>;
+        case 2: return rs_square_kernel<2, EB, CLUSTER>;
+        case 3: return rs_square_kernel<3, EB, CLUSTER>;
+        case 4: return rs_square_kernel<4, EB, CLUSTER>;
+        case 5: return rs_square_kernel<5, EB, CLUSTER>;
+        case 6: return rs_square_kernel<6, EB, CLUSTER>;
+        case 7: return rs_square_kernel<7, EB, CLUSTER>;
+        case 8: return rs_square_kernel<8, EB, CLUSTER>;
+        default: return rs_square_kernel<0, EB, CLUSTER>;
     }
+}
+
+// CTAs up to which clip_adamw_kernel works its factor out itself: some 100 fp64
+// instructions a CTA, free next to a launch's latency but not next to a long stream.
+constexpr int64_t kSelfGrid = 2 * 152;
+
+template <bool SELF>
+auto pick_adamw(int eb, bool master) {
+    return eb == 2 ? (master ? clip_adamw_kernel<2, true, SELF> : clip_adamw_kernel<2, false, SELF>)
+                   : (master ? clip_adamw_kernel<4, true, SELF> : clip_adamw_kernel<4, false, SELF>);
 }
 
 }  // namespace
@@ -566,9 +803,7 @@ int ss_grad_norm(int num_tensors, const int64_t* numels, const int* elem_bytes, 
     if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
     if (!ss::aligned(norm_out, 4)) return SS_EALIGN;
     if (int rc = check_list(num_tensors, numels, elem_bytes, grads, nullptr)) return rc;
-    const int rounds = list_rounds(num_tensors, numels, elem_bytes, grads);
-    if (rounds == 0) return SS_EOVERFLOW;
-    return list_norm(num_tensors, numels, elem_bytes, grads, rounds, INFINITY, norm_out, workspace,
+    return list_call(num_tensors, numels, elem_bytes, grads, nullptr, false, INFINITY, norm_out, workspace,
                      reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -579,15 +814,8 @@ int ss_clip_grads(int num_tensors, const int64_t* numels, const int* elem_bytes,
     if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
     if (!ss::aligned(norm_out, 4)) return SS_EALIGN;
     if (int rc = check_list(num_tensors, numels, elem_bytes, grads, out)) return rc;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int rounds = list_rounds(num_tensors, numels, elem_bytes, grads);
-    if (rounds == 0) return SS_EOVERFLOW;
-    int rc = list_norm(num_tensors, numels, elem_bytes, grads, rounds, max_norm, norm_out, workspace, st);
-    if (rc) return rc;
-    return for_tables(num_tensors, numels, elem_bytes, grads, out, true, rounds, [&](const ListTab& tab) {
-        list_scale_kernel<<<tab.first[tab.count], kThreads, 0, st>>>(tab, rounds, norm_out);
-        return ss::check_launch();
-    });
+    return list_call(num_tensors, numels, elem_bytes, grads, out, true, max_norm, norm_out, workspace,
+                     reinterpret_cast<cudaStream_t>(stream));
 }
 
 int fsdp_reduce_scatter_norm(const ss_plan* plan, const void* const* rank_grads, float* reduced_grad,
@@ -609,24 +837,20 @@ int fsdp_reduce_scatter_norm(const ss_plan* plan, const void* const* rank_grads,
     if (!ss::aligned(reduced_grad, 16) || !ss::aligned(sq_out, 8)) return SS_EALIGN;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const Split s = split_range(lo, hi > lo ? hi : lo, 16 / plan->eb);
-    float* partials = static_cast<float*>(workspace);
-    int64_t n = 0;
-    if (s.nvec > 0) {
-        const int64_t span = kMaxPartials - 1;  // one partial is left for the edges
-        const int64_t per = (s.nvec + kThreads - 1) / kThreads;
-        const int64_t rounds = (per + span - 1) / span;
-        if (rounds > INT32_MAX) return SS_EOVERFLOW;
-        n = (per + rounds - 1) / rounds;
-        auto fn = plan->eb == 2 ? pick_square<2>(plan->N) : pick_square<4>(plan->N);
-        fn<<<(int)n, kThreads, 0, st>>>(rp, plan->N, s.vbeg, s.nvec, (int)rounds, reduced_grad, partials);
-        if (int rc = ss::check_launch()) return rc;
+    const int64_t per = s.nvec > 0 ? (s.nvec + kThreads - 1) / kThreads : 1;  // CTA rounds
+    if (per <= 2 * kClusterMax) {
+        auto fn = plan->eb == 2 ? pick_square<2, true>(plan->N) : pick_square<4, true>(plan->N);
+        const int cluster = cluster_for(per);
+        return ss::launch(fn, cluster, kThreads, 0, cluster, false, st, rp, plan->N, s,
+                          (int)((per + cluster - 1) / cluster), reduced_grad, nullptr, sq_out);
     }
-    if (s.edges()) {
-        rs_square_edge_kernel<<<1, 32, 0, st>>>(rp, plan->N, plan->eb, s.a0, s.a1, s.b0, s.b1, reduced_grad,
-                                                partials + n);
-        if (int rc = ss::check_launch()) return rc;
-        ++n;
-    }
+    const int64_t rounds = (per + kMaxPartials - 1) / kMaxPartials;
+    if (rounds > INT32_MAX) return SS_EOVERFLOW;
+    const int64_t n = (per + rounds - 1) / rounds;
+    auto fn = plan->eb == 2 ? pick_square<2, false>(plan->N) : pick_square<4, false>(plan->N);
+    if (int rc = ss::launch(fn, n, kThreads, 0, 0, false, st, rp, plan->N, s, (int)rounds, reduced_grad,
+                            static_cast<float*>(workspace), nullptr))
+        return rc;
     return fold(workspace, n, INFINITY, sq_out, nullptr, st);
 }
 
@@ -646,26 +870,16 @@ int fsdp_clip_adamw(const ss_plan* plan, const float* reduced_grad, const double
         if (b && !ss::aligned(b, 16)) return SS_EALIGN;
     if (!ss::aligned(sq_sums, 8) || !ss::aligned(norm_out, 4)) return SS_EALIGN;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    finish_kernel<double><<<1, kThreads, 0, st>>>(sq_sums, num_sums, max_norm, nullptr, norm_out);
-    if (int rc = ss::check_launch()) return rc;
-    if (hi <= lo) return SS_OK;
     const AdamCoef c = ss::make_coef(hp);
-    const Split s = split_range(lo, hi, 16 / plan->eb);
-    if (s.nvec > 0) {
-        const int64_t grid = (s.nvec + kThreads - 1) / kThreads;
-        if (grid > INT32_MAX) return SS_EOVERFLOW;
-        auto fn = plan->eb == 2 ? (master ? clip_adamw_kernel<2, true> : clip_adamw_kernel<2, false>)
-                                : (master ? clip_adamw_kernel<4, true> : clip_adamw_kernel<4, false>);
-        fn<<<(int)grid, kThreads, 0, st>>>(reduced_grad, norm_out, s.vbeg, s.nvec, master, exp_avg, exp_avg_sq,
-                                           static_cast<unsigned char*>(param_shards), c);
-        if (int rc = ss::check_launch()) return rc;
-    }
-    if (s.edges()) {
-        clip_adamw_edge_kernel<<<1, 32, 0, st>>>(reduced_grad, norm_out, plan->eb, s.a0, s.a1, s.b0, s.b1,
-                                                 master, exp_avg, exp_avg_sq, param_shards, c);
-        return ss::check_launch();
-    }
-    return SS_OK;
+    const Split s = split_range(lo, hi > lo ? hi : lo, 16 / plan->eb);
+    const int64_t grid = s.nvec > 0 ? (s.nvec + kThreads - 1) / kThreads : 1;
+    unsigned char* shards = static_cast<unsigned char*>(param_shards);
+    if (grid <= kSelfGrid)
+        return ss::launch(pick_adamw<true>(plan->eb, master), grid, kThreads, 0, 0, false, st, reduced_grad, sq_sums,
+                          num_sums, max_norm, norm_out, s, master, exp_avg, exp_avg_sq, shards, c);
+    if (int rc = ss::launch(norm_kernel, 1, 32, 0, 0, true, st, sq_sums, num_sums, max_norm, norm_out)) return rc;
+    return ss::launch(pick_adamw<false>(plan->eb, master), grid, kThreads, 0, 0, true, st, reduced_grad, sq_sums,
+                      num_sums, max_norm, norm_out, s, master, exp_avg, exp_avg_sq, shards, c);
 }
 
 }  // extern "C"

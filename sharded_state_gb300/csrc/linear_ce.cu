@@ -25,11 +25,13 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
 #include "device_utils.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "tcgen05.cuh"
 
 namespace {
@@ -87,11 +89,8 @@ struct GemmArgs {
     int cols;            // columns that exist
 };
 
-// Every kernel of a call but its first is launched while the one before still
-// runs: it lets its own successor launch, sets itself up, and waits for the one
-// before to be done before it reads or writes anything.
-__device__ __forceinline__ void launch_after() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+using ss::launch_after;
+using ss::wait_before;
 
 // This thread's row: exponentials of 32 logits (columns from col of the tile's
 // row) added to (m, s), m an integer exponent at or above every logit so far.
@@ -378,8 +377,8 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 // ---------------------------------------------------------------------------
 
 constexpr int kThreads = 256;
-constexpr int kGatherThreads = 1024;
-constexpr int kGatherRows = 32;  // tokens per CTA, one per warp
+constexpr int kGatherRows = 16;  // tokens per CTA, one per warp
+constexpr int kGatherThreads = 32 * kGatherRows;
 
 // 8 elements from element 8j of a row of D bf16 at any element alignment,
 // zeros past its end.
@@ -421,8 +420,8 @@ struct GatherArgs {
     int mean;
 };
 
-// CTA b places tokens [32 b, 32 b + 32): how many of the tokens before count
-// (read again by every CTA: T * T / 8 bytes in all, from L2), then its own
+// CTA b places tokens [16 b, 16 b + 16): how many of the tokens before count
+// (read again by every CTA: T * T / 4 bytes in all, from L2), then its own
 // rows, one per warp: gathered together with the logit of their target, or,
 // where ignored, zeroed in the outputs.  The tensor cores' sums drop bits in one
 // direction, and the target's logit is the one that grows large, so it gets
@@ -430,8 +429,8 @@ struct GatherArgs {
 // zeroes the rows up to the next whole k block.
 __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherArgs a) {
     launch_after();
-    __shared__ int part[kGatherThreads / 32];
-    __shared__ int place[kGatherRows];
+    __shared__ int part[32];
+    __shared__ int place[32];
     __shared__ int total;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * kGatherRows;
@@ -442,17 +441,18 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherA
     if (lane == 0) part[warp] = before;
     __syncthreads();
     if (warp == 0) {
-        const int sum = __reduce_add_sync(0xFFFFFFFFu, part[lane]);
+        const int sum = __reduce_add_sync(0xFFFFFFFFu, lane < kGatherRows ? part[lane] : 0);
         const int t = t0 + lane;
-        const int64_t y = t < a.T ? a.targets[t] : a.ignore;
-        const bool counts = t < a.T && y != a.ignore;
+        const bool here = lane < kGatherRows && t < a.T;
+        const int64_t y = here ? a.targets[t] : a.ignore;
+        const bool counts = here && y != a.ignore;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, counts);
         const int at = sum + __popc(mask & ((1u << lane) - 1));
         place[lane] = counts ? at : -1;
         if (counts) {
             a.row[at] = t;
             a.target[at] = y >= 0 && y < a.vocab ? (int)y : -1;
-        } else if (t < a.T && a.token_loss) {
+        } else if (here && a.token_loss) {
             a.token_loss[t] = 0.f;
         }
         if (lane == 0) total = sum + __popc(mask);
@@ -506,6 +506,117 @@ ce_stage_kernel(const uint16_t* __restrict__ w, int64_t ld, int V, int D, int Dp
     for (int j = threadIdx.x & 31; j < Dp / 8; j += 32) dst[j] = row_vec(src, j, D);
 }
 
+// ---------------------------------------------------------------------------
+// statistics of a few tokens
+// ---------------------------------------------------------------------------
+
+// With a handful of tokens the weight's one read is all the time there is: dot
+// products on the CUDA cores, 4 weight rows of a warp at a time (16 loads in flight
+// a lane), against the tokens in shared memory.
+constexpr int kFewTokens = 4;
+constexpr int kFewRows = 4;
+constexpr int kFewSmem = 64 * 1024;  // of hidden states
+constexpr int kFewSlices = 1024;     // CTAs at most, each a slice of statistics
+
+// Statistics as the tile kernel leaves them, one slice per CTA: CTA b's warps
+// take groups of kFewRows rows, b's after those of the CTA before.
+template <int TOKENS>
+__global__ void __launch_bounds__(kThreads)
+ce_few_kernel(const Header* header, const uint16_t* __restrict__ h, int Dp, const uint16_t* __restrict__ w, int64_t ldw,
+              int V, const int* target, int rows, float2* stats) {
+    launch_after();
+    extern __shared__ __align__(16) unsigned char raw[];
+    uint4* hs = reinterpret_cast<uint4*>(raw);
+    __shared__ float top_s[kThreads / 32][kFewTokens];
+    __shared__ float sum_s[kThreads / 32][kFewTokens];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int vecs = Dp / 8;
+    wait_before();
+    const int live = header->live;
+    for (int i = threadIdx.x; i < TOKENS * vecs; i += kThreads)
+        hs[i] = i < live * vecs ? reinterpret_cast<const uint4*>(h)[i] : make_uint4(0, 0, 0, 0);
+    int y[TOKENS];
+#pragma unroll
+    for (int t = 0; t < TOKENS; ++t) y[t] = t < live ? target[t] : -1;
+    __syncthreads();
+    float top[TOKENS], sum[TOKENS];
+#pragma unroll
+    for (int t = 0; t < TOKENS; ++t) top[t] = -INFINITY, sum[t] = 0.f;
+    const int groups = (V + kFewRows - 1) / kFewRows;
+    for (int g = blockIdx.x * (kThreads / 32) + warp; g < groups; g += gridDim.x * (kThreads / 32)) {
+        const int v0 = g * kFewRows;
+        const uint4* wr[kFewRows];
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r)  // past the end: the last row again, left out below
+            wr[r] = reinterpret_cast<const uint4*>(w + (int64_t)(v0 + r < V ? v0 + r : V - 1) * ldw);
+        float acc[kFewRows][TOKENS];
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r)
+#pragma unroll
+            for (int t = 0; t < TOKENS; ++t) acc[r][t] = 0.f;
+        int j = lane;
+        for (; j + 96 < vecs; j += 128) {
+            uint4 x[4][kFewRows];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < kFewRows; ++r) x[i][r] = ss::ld_stream_u4(wr[r] + j + 32 * i);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int t = 0; t < TOKENS; ++t) {
+                    const uint4 hv = hs[t * vecs + j + 32 * i];
+#pragma unroll
+                    for (int r = 0; r < kFewRows; ++r) acc[r][t] = dot_bf16(x[i][r], hv, acc[r][t]);
+                }
+        }
+        for (; j < vecs; j += 32) {
+            uint4 x[kFewRows];
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) x[r] = ss::ld_stream_u4(wr[r] + j);
+#pragma unroll
+            for (int t = 0; t < TOKENS; ++t) {
+                const uint4 hv = hs[t * vecs + j];
+#pragma unroll
+                for (int r = 0; r < kFewRows; ++r) acc[r][t] = dot_bf16(x[r], hv, acc[r][t]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < TOKENS; ++t) {
+            float l[kFewRows], m = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) {
+                l[r] = acc[r][t];
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], d);
+                if (v0 + r >= V || v0 + r == y[t]) l[r] = -INFINITY;
+                m = fmaxf(m, l[r]);
+            }
+            const float up = fmaxf(top[t], ceilf(m * kLog2e));
+            const float at = up == -INFINITY ? 0.f : up;
+            float a = 0.f;
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) a += exp2f(fmaf(l[r], kLog2e, -at));
+            sum[t] = (top[t] == -INFINITY ? 0.f : sum[t] * exp2f(top[t] - at)) + a;
+            top[t] = up;
+        }
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int t = 0; t < TOKENS; ++t) top_s[warp][t] = top[t], sum_s[warp][t] = sum[t];
+    }
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t < TOKENS && t < live) {
+        float m = -INFINITY, s = 0.f;
+        for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, top_s[i][t]);
+        const float at = m == -INFINITY ? 0.f : m;
+        for (int i = 0; i < kThreads / 32; ++i)
+            s += top_s[i][t] == -INFINITY ? sum_s[i][t] : sum_s[i][t] * exp2f(top_s[i][t] - at);
+        stats[(int64_t)blockIdx.x * rows + t] = make_float2(m, s);
+    }
+}
+
 constexpr int kLossThreads = 1024;
 constexpr int kLossRows = 32;  // rows per CTA, 32 threads each
 constexpr int kLossSlices = kLossThreads / kLossRows;
@@ -522,58 +633,73 @@ ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, in
                float2* __restrict__ row_loss, float* __restrict__ token_loss, double* __restrict__ partials,
                int mean, float* __restrict__ loss_out) {
     launch_after();
-    __shared__ float top_s[kLossSlices][kLossRows];
+    __shared__ float top_s[kLossSlices][kLossRows + 1];
     __shared__ float sum_s[kLossSlices][kLossRows + 1];
-    __shared__ double loss_s[32];
+    __shared__ double loss_s[kLossRows];
     __shared__ bool last;
-    const int r = threadIdx.x & (kLossRows - 1), slice = threadIdx.x / kLossRows;
-    const int row = blockIdx.x * kLossRows + r;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_before();
     const int live = header->live;
-    float top = -INFINITY, sum = 0.f;
     auto add = [](float& m, float& s, float m2, float s2) {  // exponents are whole numbers: exact
         const float up = fmaxf(m, m2);
         s = (m == up ? s : s * exp2f(m - up)) + (m2 == up ? s2 : s2 * exp2f(m2 - up));
         m = up;
     };
-    if (row < live) {
-        int n = slice;
-        for (; n + 3 * kLossSlices < n_tiles; n += 4 * kLossSlices) {
-            float2 v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = stats[(int64_t)(n + i * kLossSlices) * rows + row];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) add(top, sum, v[i].x, v[i].y);
-        }
-        for (; n < n_tiles; n += kLossSlices) {
-            const float2 v = stats[(int64_t)n * rows + row];
-            add(top, sum, v.x, v.y);
-        }
-    }
-    top_s[slice][r] = top;
-    sum_s[slice][r] = sum;
-    __syncthreads();
-    if (slice == 0) {
-        double loss = 0.0;
+    {  // rows side by side (lane), a warp's slice of the tiles
+        const int row = blockIdx.x * kLossRows + lane;
+        float top = -INFINITY, sum = 0.f;
         if (row < live) {
-            for (int i = 1; i < kLossSlices; ++i) add(top, sum, top_s[i][r], sum_s[i][r]);
-            const float hit = target_logit[row];
+            int n = warp;
+            for (; n < n_tiles; n += 8 * kLossSlices) {
+                float2 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = n + i * kLossSlices < n_tiles ? stats[(int64_t)(n + i * kLossSlices) * rows + row]
+                                                         : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) add(top, sum, v[i].x, v[i].y);
+            }
+        }
+        top_s[warp][lane] = top;
+        sum_s[warp][lane] = sum;
+    }
+    const int row = blockIdx.x * kLossRows + warp;  // from here on a warp's row, a lane's slice
+    const float hit = row < live ? target_logit[row] : 0.f;
+    const int token = row < live ? row_map[row] : 0;
+    __syncthreads();
+    float top = top_s[lane][warp], sum = sum_s[lane][warp];
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1)
+        add(top, sum, __shfl_xor_sync(0xFFFFFFFFu, top, k), __shfl_xor_sync(0xFFFFFFFFu, sum, k));
+    if (lane == 0) {
+        float l = 0.f;
+        if (row < live) {
             // log of r; a lone class has r = 0
             const float d = (float)((double)top * kLn2 + (double)logf(sum) - (double)hit);
             const float rest = expf(-fabsf(d));
-            const float l = (d > 0.f ? d : 0.f) + log1pf(rest);
+            l = (d > 0.f ? d : 0.f) + log1pf(rest);
             row_loss[row] = make_float2((hit + l) * kLog2e, -(d > 0.f ? 1.f : rest) / (1.f + rest));
-            if (token_loss) token_loss[row_map[row]] = l;
-            loss = (double)l;
+            if (token_loss) token_loss[token] = l;
         }
+        loss_s[warp] = (double)l;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        double loss = loss_s[lane];
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) loss += __shfl_down_sync(0xFFFFFFFFu, loss, k);
-        if (r == 0) {
-            partials[blockIdx.x] = loss;
-            __threadfence();
-            last = atomicAdd(&header->finished, 1) == (int)gridDim.x - 1;
+        if (lane == 0) {
+            last = true;
+            if (gridDim.x > 1) {
+                partials[blockIdx.x] = loss;
+                __threadfence();
+                last = atomicAdd(&header->finished, 1) == (int)gridDim.x - 1;
+            } else {
+                *loss_out = (float)(mean && live > 0 ? loss / live : loss);
+            }
         }
     }
+    if (gridDim.x == 1) return;
     __syncthreads();
     if (!last) return;
     __threadfence();
@@ -581,12 +707,13 @@ ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, in
     for (int i = threadIdx.x; i < (int)gridDim.x; i += kLossThreads) s += __ldcg(partials + i);
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, k);
-    if ((threadIdx.x & 31) == 0) loss_s[threadIdx.x >> 5] = s;
+    if (lane == 0) loss_s[warp] = s;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        s = 0.0;
-        for (int i = 0; i < 32; ++i) s += loss_s[i];
-        *loss_out = (float)(mean && live > 0 ? s / live : s);
+    if (warp == 0) {
+        s = loss_s[lane];
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, k);
+        if (lane == 0) *loss_out = (float)(mean && live > 0 ? s / live : s);
     }
 }
 
@@ -639,7 +766,8 @@ int choose_splits(int64_t tiles, int64_t kblocks, int pairs) {
 
 // Where everything lies in the workspace.
 struct Layout {
-    int64_t T, D, V, Dp, rows, n_tiles, piece, pieces;
+    int64_t T, D, V, Dp, rows, n_tiles, slices, piece, pieces;
+    bool few;  // tokens: the dot-product kernel
     int hidden_splits, head_splits;
     bool grad, stage;
     int64_t row, target, target_logit, row_loss, partials, stats, h, w, p, hidden_part, head_part, bytes;
@@ -653,6 +781,9 @@ Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int p
     l.Dp = up(D, 8);
     l.rows = up(T, kTile);
     l.n_tiles = up(V, kTile) / kTile;
+    l.few = T <= kFewTokens && kFewTokens * l.Dp * 2 <= kFewSmem;
+    const int64_t few_ctas = (V + kFewRows * (kThreads / 32) - 1) / (kFewRows * (kThreads / 32));
+    l.slices = !l.few ? l.n_tiles : few_ctas < kFewSlices ? few_ctas : kFewSlices;
     int64_t at = 256;  // the header
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -664,7 +795,7 @@ Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int p
     l.target_logit = take(l.rows * 4);
     l.row_loss = take(l.rows * 8);
     l.partials = take(l.rows / kLossRows * 8);
-    l.stats = take(l.n_tiles * l.rows * 8);
+    l.stats = take(l.slices * l.rows * 8);
     l.h = take(l.rows * l.Dp * 2);
     if (stage) l.w = take(V * l.Dp * 2);
     if (grad) {
@@ -715,29 +846,38 @@ int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int
     return r == CUDA_SUCCESS ? SS_OK : ss::cuda_fail(cudaErrorInvalidValue);
 }
 
-// Launch with programmatic stream serialisation (see launch_after).
-template <class... P, class... A>
-int launch(void (*kernel)(P...), int64_t grid, int threads, int smem, cudaStream_t st, A... args) {
-    if (grid > INT32_MAX) return SS_EOVERFLOW;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1] = {};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-    return e == cudaSuccess ? ss::check_launch() : ss::cuda_fail(e);
+// Launch chained to the kernel before it (see launch_after).
+template <class K, class... A>
+int launch(K kernel, int64_t grid, int threads, int smem, cudaStream_t st, A&&... args) {
+    return ss::launch(kernel, grid, threads, smem, 0, true, st, args...);
+}
+
+// Raises a kernel's limit of dynamic shared memory, once for each device.
+int allow_smem(std::atomic<uint64_t>& ready, const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return ss::cuda_fail(e);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (ready.load(std::memory_order_acquire) & bit) return SS_OK;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return ss::cuda_fail(e);
+    if (dev < 64) ready.fetch_or(bit, std::memory_order_release);
+    return SS_OK;
+}
+
+template <int TOKENS>
+int launch_few(const GemmArgs& g, const uint16_t* h, int64_t Dp, const uint16_t* w, int64_t ldw, int64_t slices,
+               cudaStream_t st) {
+    static std::atomic<uint64_t> ready{0};
+    if (int rc = allow_smem(ready, reinterpret_cast<const void*>(ce_few_kernel<TOKENS>), kFewSmem)) return rc;
+    return launch(ce_few_kernel<TOKENS>, slices, kThreads, (int)(TOKENS * Dp * 2), st, g.header, h, (int)Dp, w, ldw,
+                  g.vocab, g.target, g.rows, g.stats);
 }
 
 template <int MODE>
 int launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& g, int64_t tiles, cudaStream_t st) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(ce_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return ss::cuda_fail(e);
+    static std::atomic<uint64_t> ready{0};  // devices whose limit has been raised
+    if (int rc = allow_smem(ready, reinterpret_cast<const void*>(ce_gemm_kernel<MODE>), kSmemBytes)) return rc;
     const int64_t pairs = ss::num_sms() / 2;
     return launch(ce_gemm_kernel<MODE>, 2 * (tiles < pairs ? tiles : pairs), kGemmThreads, kSmemBytes, st, a, b, g);
 }
@@ -831,11 +971,18 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
         GemmArgs s = g;
         s.n_tiles = (int)l.n_tiles;
         s.stats = reinterpret_cast<float2*>(ws + l.stats);
-        if (int rc = launch_gemm<kStatistics>(h_k, w_k, s, l.rows / kTile * l.n_tiles, st)) return rc;
         g.stats = s.stats;
+        if (l.few) {
+            const int rc = T == 1   ? launch_few<1>(s, h, l.Dp, w, ldw, l.slices, st)
+                           : T == 2 ? launch_few<2>(s, h, l.Dp, w, ldw, l.slices, st)
+                                    : launch_few<kFewTokens>(s, h, l.Dp, w, ldw, l.slices, st);
+            if (rc) return rc;
+        } else if (int rc = launch_gemm<kStatistics>(h_k, w_k, s, l.rows / kTile * l.n_tiles, st)) {
+            return rc;
+        }
     }
     if (int rc = launch(ce_loss_kernel, T > 0 ? (T + kLossRows - 1) / kLossRows : 1, kLossThreads, 0, st, header, g.stats,
-                        (int)l.n_tiles, (int)l.rows, target_logit, row, row_loss, a->token_loss_out, partials, mean,
+                        (int)l.slices, (int)l.rows, target_logit, row, row_loss, a->token_loss_out, partials, mean,
                         a->loss_out))
         return rc;
 
