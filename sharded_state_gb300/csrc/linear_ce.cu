@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -44,11 +45,13 @@ constexpr int kBlockK = 64;       // k of one stage: 128 bytes of bf16
 constexpr int kStages = 6;
 constexpr int kStageBytes = 2 * kHalf * kBlockK * 2;  // A and B of one CTA
 constexpr int kSmemBytes = kStages * kStageBytes + 1024;
-constexpr int kEpilogueWarps = 4;
+constexpr int kEpilogueWarps = 8;      // two for each 32 rows, half of the columns each
+constexpr int kColumns = kTile / 2;    // of a warp
 constexpr int kGemmThreads = 32 * (4 + kEpilogueWarps);
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr double kLn2 = 0.6931471805599453;
+constexpr float kLn2High = 0.693145751953125f;                               // 16 bits
+constexpr float kLn2Low = (float)(0.6931471805599453 - 0.693145751953125);
 
 // What the gather leaves for the kernels after it, at the workspace's start.
 struct Header {
@@ -58,39 +61,60 @@ struct Header {
     int reserved;
 };
 
-enum Mode { kStatistics, kProbability, kHead, kHidden };
+// The products, by what is done with a 256 x 256 tile of them.
+enum Product { kStatistics, kProbability, kHead, kHidden };
 
-struct GemmArgs {
-    Header* header;
+// One product of a launch.
+struct Work {
+    int product;
     int n_tiles;  // column tiles
-    int m_tiles;  // row tiles (kHead; the token modes take theirs from header->live)
+    int m_tiles;  // row tiles (kHead; the others have token rows: header->live)
     int splits;   // of k (kHead, kHidden)
     int k;        // elements of k (kHead: the tokens that count)
     int v0;       // first vocabulary row of the piece
-    int vocab;
-    float* loss;  // NaN goes there when a wait runs out
-    // kStatistics
-    float2* stats;      // [n_tiles][rows]: exponent of the tile's maximum, sum of exponentials
-    const int* target;  // [rows]
-    int rows;           // allocated token rows
-    // kProbability
-    const float2* row_loss;  // [rows]: log-sum-exp in base 2, the target's p - 1
-    uint16_t* p;             // [rows][ldp]
-    int ldp;
-    // kHead, kHidden: into fp32 partials [splits][part_rows][part_ld] or, where NULL, into out
+    // kHead, kHidden: into fp32 partials [splits][rows][part_ld], or, where NULL, into out
     float* part;
     int64_t part_split;  // elements between two splits
     int part_ld;
     int add;             // partials already hold the earlier pieces
     uint16_t* out;
     int64_t out_ld;
-    const int* row_map;  // output row of each row (NULL: itself, from v0)
     int m_rows;          // rows that exist (kHead)
     int cols;            // columns that exist
+    uint16_t* p;         // kProbability: [rows][ldp]
+    int ldp;
+};
+
+constexpr int kMaxWork = 3;
+
+struct GemmArgs {
+    Header* header;
+    int* next;  // tiles handed out beyond the first of each pair, 0 at the launch
+    int vocab;
+    int rows;   // allocated token rows
+    float* loss;  // NaN goes there when a wait runs out
+    const int* target;       // [rows]
+    const int* token;        // [rows]: output row of each row (kHidden)
+    const float2* row_loss;  // [rows]: log-sum-exp in base 2, the target's p - 1 (kProbability)
+    float2* stats;           // [2 n_tiles][rows], each half tile's: exponent of the maximum, sum of exponentials (kStatistics)
+    int count;               // products, the ones with the longest tiles first
+    Work work[kMaxWork];
+};
+
+// The operands of each product.
+struct Maps {
+    CUtensorMap a[kMaxWork], b[kMaxWork];
 };
 
 using ss::launch_after;
 using ss::wait_before;
+
+// 2^x: one instruction, good to 2 ulp, results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // This thread's row: exponentials of 32 logits (columns from col of the tile's
 // row) added to (m, s), m an integer exponent at or above every logit so far.
@@ -104,26 +128,65 @@ __device__ __forceinline__ void add_logits(const float (&l)[32], float& m, float
     float a = 0.f, b = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-        a += exp2f(fmaf(l[i], kLog2e, -at));
-        b += exp2f(fmaf(l[i + 1], kLog2e, -at));
+        a += ex2(fmaf(l[i], kLog2e, -at));
+        b += ex2(fmaf(l[i + 1], kLog2e, -at));
     }
-    s = (m == -INFINITY ? 0.f : s * exp2f(m - at)) + (a + b);
+    s = (m == -INFINITY ? 0.f : s * ex2(m - at)) + (a + b);
     m = up;
 }
+
+// A tile of a launch: which product (-1: there is none left), where, and its
+// split's k blocks.
+struct __align__(16) Tile {
+    int w, m, n, s, kb, ke, pad[2];
+};
+
+// Tiles are numbered product after product.  Token products run down the tokens
+// first: the hidden states stay in L2 and the weight is read once.  The gradients
+// run along the hidden size first: a panel of P is read by the pairs that need it
+// at about the same time.
+__device__ __forceinline__ Tile find_tile(const GemmArgs& g, int live, int id) {
+    Tile t = {};
+    for (int w = 0; w < g.count; ++w) {
+        const Work& x = g.work[w];
+        const int m_tiles = x.product == kHead ? x.m_tiles : (live + kTile - 1) / kTile;
+        const int mn = m_tiles * x.n_tiles, tiles = mn * x.splits;
+        if (id >= tiles) {
+            id -= tiles;
+            continue;
+        }
+        const int kblocks = ((x.product == kHead ? live : x.k) + kBlockK - 1) / kBlockK;
+        const int per = (kblocks + x.splits - 1) / x.splits;
+        t.w = w;
+        t.s = id / mn;
+        id -= t.s * mn;
+        if (x.product <= kProbability)
+            t.m = id % m_tiles, t.n = id / m_tiles;
+        else
+            t.m = id / x.n_tiles, t.n = id % x.n_tiles;
+        t.kb = min(t.s * per, kblocks);
+        t.ke = min(t.kb + per, kblocks);
+        return t;
+    }
+    t.w = -1;
+    return t;
+}
+
+constexpr int kQueue = 4;  // tiles handed out ahead
 
 // One persistent CTA pair takes output tiles of 256 x 256, its first CTA the
 // upper 128 rows.  Warp 0 loads (one thread), warp 1 of the first CTA issues the
 // products, warps 4.. read finished accumulators from tensor memory while the
-// next tile's products go to the other half of it.
-template <int MODE>
+// next tile's products go to the other half of it.  Warp 3 of the first CTA hands
+// out tiles: a pair's first by its number, then whichever is next of the launch, so
+// that products with tiles of different lengths share a launch and the pairs end
+// together.  A tile's result does not depend on who computes it.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
-ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-               const GemmArgs g) {
-    constexpr bool kTokenRows = MODE != kHead;
-    constexpr int kAMn = MODE == kHead, kBMn = MODE == kHead || MODE == kHidden;
+ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmArgs g) {
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(16) float turn[(MODE == kHead || MODE == kHidden) ? kEpilogueWarps : 1][32 * 32];
-    __shared__ uint64_t bars[2 * kStages + 4];
+    __shared__ __align__(16) float turn[kEpilogueWarps][32 * 32];
+    __shared__ uint64_t bars[2 * kStages + 4 + 2 * kQueue];
+    __shared__ Tile queue[kQueue];
     __shared__ uint32_t tmem_base;
 
     launch_after();
@@ -132,6 +195,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     const uint32_t smem = (tc::smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
     const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16;
+    const uint32_t queue_full = acc_empty + 16, queue_empty = queue_full + 8 * kQueue;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -142,9 +206,15 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             tc::mbar_init(acc_full + 8 * i, 1);
             tc::mbar_init(acc_empty + 8 * i, 2 * kEpilogueWarps);
         }
+        for (int i = 0; i < kQueue; ++i) {
+            tc::mbar_init(queue_full + 8 * i, 1);
+            tc::mbar_init(queue_empty + 8 * i, 2 + 1 + 2 * kEpilogueWarps);  // loaders, issuer, epilogues
+        }
         tc::mbar_init_fence();
-        tc::prefetch_map(&map_a);
-        tc::prefetch_map(&map_b);
+        for (int w = 0; w < g.count; ++w) {
+            tc::prefetch_map(&maps.a[w]);
+            tc::prefetch_map(&maps.b[w]);
+        }
     }
     if (warp == 2) tc::tmem_alloc(tc::smem_addr(&tmem_base), 512);
     tc::fence_before();
@@ -154,187 +224,201 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     wait_before();
 
     const int live = g.header->live;
-    const int m_tiles = kTokenRows ? (live + kTile - 1) / kTile : g.m_tiles;
-    const int kblocks = ((MODE == kHead ? live : g.k) + kBlockK - 1) / kBlockK;
-    const int per_split = (kblocks + g.splits - 1) / g.splits;
-    const int mn = m_tiles * g.n_tiles;
-    const int tiles = mn * g.splits;
-    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
-
-    // Token products run down the tokens first: the hidden states stay in L2 and
-    // the weight is read once.  The gradients run along the hidden size first: a
-    // panel of P is read by the pairs that need it at about the same time.
-    auto place = [&](int t, int& m, int& n) {
-        const int i = t % mn;
-        if (MODE == kStatistics || MODE == kProbability)
-            m = i % m_tiles, n = i / m_tiles;
-        else
-            m = i / g.n_tiles, n = i % g.n_tiles;
-    };
-    // the k blocks of a tile's split
-    auto k_range = [&](int t, int& kb, int& ke) {
-        const int s = t / mn;
-        kb = s * per_split < kblocks ? s * per_split : kblocks;
-        ke = kb + per_split < kblocks ? kb + per_split : kblocks;
-    };
-
+    const int first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     bool ok = true;
+
+    // The pair's j-th tile, read by a whole warp or by one thread.
+    auto take_tile = [&](int j) {
+        const int slot = j % kQueue;
+        Tile t;
+        ok = tc::mbar_wait(queue_full + 8 * slot, (j / kQueue) & 1);
+        const int4 x = *reinterpret_cast<const int4*>(queue + slot);
+        const int2 y = *reinterpret_cast<const int2*>(&queue[slot].kb);
+        t.w = x.x, t.m = x.y, t.n = x.z, t.s = x.w, t.kb = y.x, t.ke = y.y;
+        return t;
+    };
+    auto tile_taken = [&](int j) {  // one thread
+        tc::mbar_arrive_cluster(tc::map_to_rank(queue_empty + 8 * (j % kQueue), 0));
+    };
+
     if (warp == 0 && lane == 0) {
         int it = 0;
-        for (int t = first; t < tiles && ok; t += stride) {
-            int m, n, kb, ke;
-            place(t, m, n);
-            k_range(t, kb, ke);
-            const int am = m * kTile + (int)rank * kHalf;
-            const int bn = n * kTile + (int)rank * kHalf;
-            for (int k = kb; k < ke && ok; ++k, ++it) {
+        for (int j = 0;; ++j) {
+            const Tile t = take_tile(j);
+            if (!ok || t.w < 0) break;
+            tile_taken(j);
+            const Work& x = g.work[t.w];
+            const CUtensorMap *map_a = &maps.a[t.w], *map_b = &maps.b[t.w];
+            const bool a_mn = x.product == kHead, b_mn = x.product >= kHead;
+            const int am = t.m * kTile + (int)rank * kHalf;
+            const int bn = t.n * kTile + (int)rank * kHalf + (b_mn ? 0 : x.v0);
+            const int bk = x.product == kHidden ? x.v0 : 0;
+            for (int k = t.kb; k < t.ke; ++k, ++it) {
                 const int st = it % kStages;
                 const uint32_t a = smem + st * kStageBytes, b = a + kHalf * kBlockK * 2;
                 ok = tc::mbar_wait(empty + 8 * st, ((it / kStages) & 1) ^ 1);
                 if (!ok) break;
                 const uint32_t bar = tc::map_to_rank(full + 8 * st, 0);
                 if (rank == 0) tc::mbar_expect_tx(full + 8 * st, 2 * kStageBytes);
-                if (kAMn) {
-                    tc::tma_load_2d(a, &map_a, am, k * kBlockK, bar);
-                    tc::tma_load_2d(a + 8192, &map_a, am + 64, k * kBlockK, bar);
+                if (a_mn) {
+                    tc::tma_load_2d(a, map_a, am, k * kBlockK, bar);
+                    tc::tma_load_2d(a + 8192, map_a, am + 64, k * kBlockK, bar);
                 } else {
-                    tc::tma_load_2d(a, &map_a, k * kBlockK, am, bar);
+                    tc::tma_load_2d(a, map_a, k * kBlockK, am, bar);
                 }
-                if (kBMn) {
-                    const int y = (MODE == kHidden ? g.v0 : 0) + k * kBlockK;
-                    tc::tma_load_2d(b, &map_b, bn, y, bar);
-                    tc::tma_load_2d(b + 8192, &map_b, bn + 64, y, bar);
+                if (b_mn) {
+                    tc::tma_load_2d(b, map_b, bn, bk + k * kBlockK, bar);
+                    tc::tma_load_2d(b + 8192, map_b, bn + 64, bk + k * kBlockK, bar);
                 } else {
-                    tc::tma_load_2d(b, &map_b, k * kBlockK, g.v0 + bn, bar);
+                    tc::tma_load_2d(b, map_b, k * kBlockK, bn, bar);
                 }
             }
+            if (!ok) break;
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {
-        constexpr uint32_t idesc = tc::instr_desc(kTile, kTile, kAMn, kBMn);
-        int it = 0, j = 0;
-        for (int t = first; t < tiles && ok; t += stride, ++j) {
-            int kb, ke;
-            k_range(t, kb, ke);
+        int it = 0;
+        for (int j = 0;; ++j) {
+            const Tile t = take_tile(j);
+            if (!ok || t.w < 0) break;
+            tile_taken(j);
+            const int product = g.work[t.w].product;
+            const bool a_mn = product == kHead, b_mn = product >= kHead;
+            const uint32_t idesc = tc::instr_desc(kTile, kTile, a_mn, b_mn);
+            // K-major: 16 k are 32 bytes of every row; MN-major: two 8-column groups
+            const uint32_t a_lbo = a_mn ? 8192 : 16, b_lbo = b_mn ? 8192 : 16;
+            const uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
             const uint32_t d = tmem + (j & 1) * kTile;
             ok = tc::mbar_wait(acc_empty + 8 * (j & 1), ((j >> 1) & 1) ^ 1);
             if (!ok) break;
             tc::fence_after();
-            for (int k = kb; k < ke; ++k, ++it) {
+            for (int k = t.kb; k < t.ke; ++k, ++it) {
                 const int st = it % kStages;
                 ok = tc::mbar_wait(full + 8 * st, (it / kStages) & 1);
                 if (!ok) break;
                 tc::fence_after();
                 const uint32_t a = smem + st * kStageBytes, b = a + kHalf * kBlockK * 2;
-                // K-major: 16 k are 32 bytes of every row; MN-major: two 8-column groups
-                const uint64_t da = kAMn ? tc::operand_desc(a, 8192, 1024) : tc::operand_desc(a, 16, 1024);
-                const uint64_t db = kBMn ? tc::operand_desc(b, 8192, 1024) : tc::operand_desc(b, 16, 1024);
+                const uint64_t da = tc::operand_desc(a, a_lbo, 1024), db = tc::operand_desc(b, b_lbo, 1024);
 #pragma unroll
                 for (int i = 0; i < kBlockK / 16; ++i)
-                    tc::mma_pair(d, da + i * ((kAMn ? 2048 : 32) >> 4), db + i * ((kBMn ? 2048 : 32) >> 4), idesc,
-                                 k > kb || i > 0);
+                    tc::mma_pair(d, da + i * a_step, db + i * b_step, idesc, k > t.kb || i > 0);
                 tc::commit_pair(empty + 8 * st);
             }
+            if (!ok) break;
             tc::commit_pair(acc_full + 8 * (j & 1));
         }
+    } else if (warp == 3 && lane == 0 && rank == 0) {
+        for (int j = 0;; ++j) {
+            const int slot = j % kQueue;
+            ok = tc::mbar_wait(queue_empty + 8 * slot, ((j / kQueue) & 1) ^ 1);
+            if (!ok) break;
+            const Tile t = find_tile(g, live, j == 0 ? first : pairs + atomicAdd(g.next, 1));
+            for (uint32_t r = 0; r < 2; ++r) {
+                const uint32_t at = tc::map_to_rank(tc::smem_addr(queue + slot), r);
+                tc::st_cluster(at, t.w, t.m, t.n, t.s);
+                tc::st_cluster(at + 16, t.kb, t.ke, 0, 0);
+                tc::mbar_arrive_cluster(tc::map_to_rank(queue_full + 8 * slot, r));
+            }
+            if (t.w < 0) break;
+        }
     } else if (warp >= 4) {
-        const int quad = warp & 3;
+        const int quad = warp & 3, half = (warp - 4) >> 2;
         const uint32_t acc_empty0 = tc::map_to_rank(acc_empty, 0);
-        int j = 0;
-        for (int t = first; t < tiles && ok; t += stride, ++j) {
-            const int s = t / mn;
-            int m, n, kb, ke;
-            place(t, m, n);
-            k_range(t, kb, ke);
-            const int row = m * kTile + (int)rank * kHalf + quad * 32 + lane;
-            const uint32_t d = tmem + (j & 1) * kTile + ((uint32_t)quad << 21);
+        const float scale = g.header->scale;
+        for (int j = 0;; ++j) {
+            const Tile t = take_tile(j);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok || t.w < 0) break;
+            if (lane == 0) tile_taken(j);
+            const Work& x = g.work[t.w];
+            const int row0 = t.m * kTile + (int)rank * kHalf + quad * 32, row = row0 + lane;
+            const int col0 = t.n * kTile + half * kColumns;
+            const uint32_t d = tmem + (j & 1) * kTile + half * kColumns + ((uint32_t)quad << 21);
             ok = tc::mbar_wait(acc_full + 8 * (j & 1), (j >> 1) & 1);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc::fence_after();
-            if (MODE == kStatistics) {
-                // the target's own exponential is left out: it is added from a logit of its own
-                const int y = row < live ? g.target[row] - (g.v0 + n * kTile) : -1;  // column of the target
-                const int left = g.vocab - (g.v0 + n * kTile);  // columns that exist
-                float top = -INFINITY, sum = 0.f;
-                for (int c = 0; c < kTile && c < left; c += 32) {
-                    float l[32];
-                    __syncwarp();
-                    tc::tmem_ld32(d + c, l);
-                    if (c + 32 > left) {
+            if (x.product <= kProbability) {
+                const int y = row < live ? g.target[row] - (x.v0 + col0) : -1;  // column of the target
+                const int left = g.vocab - (x.v0 + col0);                       // columns that exist
+                if (x.product == kStatistics) {
+                    // the target's own exponential is left out: it is added from a logit of its own
+                    float top = -INFINITY, sum = 0.f;
+                    for (int c = 0; c < kColumns && c < left; c += 32) {
+                        float l[32];
+                        __syncwarp();
+                        tc::tmem_ld32(d + c, l);
+                        if (c + 32 > left) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) l[i] = c + i < left ? l[i] : -INFINITY;
+                            for (int i = 0; i < 32; ++i) l[i] = c + i < left ? l[i] : -INFINITY;
+                        }
+                        if (y >= c && y < c + 32) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) l[i] = c + i == y ? -INFINITY : l[i];
+                        }
+                        add_logits(l, top, sum);
                     }
-                    if (y >= c && y < c + 32) {
+                    if (row < live) g.stats[(int64_t)(2 * t.n + half) * g.rows + row] = make_float2(top, sum);
+                } else {
+                    const float2 rl = row < live ? g.row_loss[row] : make_float2(0.f, 0.f);
+                    uint16_t* o = x.p + (int64_t)row * x.ldp + col0;
+                    for (int c = 0; c < kColumns; c += 32) {
+                        float l[32];
+                        __syncwarp();
+                        tc::tmem_ld32(d + c, l);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) l[i] = c + i == y ? -INFINITY : l[i];
+                        for (int i = 0; i < 32; ++i) {
+                            l[i] = ex2(fmaf(l[i], kLog2e, -rl.x));
+                            if (row >= live || c + i >= left) l[i] = 0.f;
+                        }
+                        if (y >= c && y < c + 32) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) l[i] = c + i == y ? rl.y : l[i];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            *reinterpret_cast<uint4*>(o + c + i) =
+                                make_uint4(ss::pack_bf16x2(l[i], l[i + 1]), ss::pack_bf16x2(l[i + 2], l[i + 3]),
+                                           ss::pack_bf16x2(l[i + 4], l[i + 5]), ss::pack_bf16x2(l[i + 6], l[i + 7]));
                     }
-                    add_logits(l, top, sum);
-                }
-                if (row < live) g.stats[(int64_t)n * g.rows + row] = make_float2(top, sum);
-            } else if (MODE == kProbability) {
-                const int y = row < live ? g.target[row] - (g.v0 + n * kTile) : -1;
-                const int left = g.vocab - (g.v0 + n * kTile);
-                const float2 rl = row < live ? g.row_loss[row] : make_float2(0.f, 0.f);
-                const float lse2 = rl.x;
-                uint16_t* o = g.p + (int64_t)row * g.ldp + n * kTile;
-                for (int c = 0; c < kTile; c += 32) {
-                    float l[32];
-                    __syncwarp();
-                    tc::tmem_ld32(d + c, l);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        l[i] = exp2f(fmaf(l[i], kLog2e, -lse2));
-                        if (row >= live || c + i >= left) l[i] = 0.f;
-                    }
-                    if (y >= c && y < c + 32) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) l[i] = c + i == y ? rl.y : l[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        *reinterpret_cast<uint4*>(o + c + i) =
-                            make_uint4(ss::pack_bf16x2(l[i], l[i + 1]), ss::pack_bf16x2(l[i + 2], l[i + 3]),
-                                       ss::pack_bf16x2(l[i + 4], l[i + 5]), ss::pack_bf16x2(l[i + 6], l[i + 7]));
                 }
             } else {
                 // 32 x 32 values at a time through shared memory (16-byte groups of row r at
                 // group ^ (r & 7), free of bank conflicts both ways), so that a row's go out together
-                const int limit = kTokenRows ? live : g.m_rows;
-                const int row0 = row - lane;
-                const float scale = g.header->scale;
+                const int limit = x.product == kHidden ? live : x.m_rows;
+                const int* token = x.product == kHidden ? g.token : nullptr;
                 float* mine = turn[warp - 4];
-                const bool wide = (reinterpret_cast<uintptr_t>(g.out) & 7u) == 0 && (g.out_ld & 3) == 0;
-                for (int c = 0; c < kTile && n * kTile + c < g.cols; c += 32) {
-                    float x[32];
+                const bool wide = (reinterpret_cast<uintptr_t>(x.out) & 7u) == 0 && (x.out_ld & 3) == 0;
+                for (int c = 0; c < kColumns && col0 + c < x.cols; c += 32) {
+                    float v32[32];
                     __syncwarp();
-                    tc::tmem_ld32(d + c, x);
-                    if (kb == ke) {
+                    tc::tmem_ld32(d + c, v32);
+                    if (t.kb == t.ke) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                        for (int i = 0; i < 32; ++i) v32[i] = 0.f;
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         *reinterpret_cast<float4*>(mine + lane * 32 + 4 * (i ^ (lane & 7))) =
-                            make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                            make_float4(v32[4 * i], v32[4 * i + 1], v32[4 * i + 2], v32[4 * i + 3]);
                     __syncwarp();
-                    const int col = n * kTile + c, left = g.cols - col;
-                    if (g.part || wide) {  // 8 lanes a row, 4 columns a lane
+                    const int col = col0 + c, left = x.cols - col;
+                    if (x.part || wide) {  // 8 lanes a row, 4 columns a lane
                         const int k = lane & 7;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int r = 4 * i + (lane >> 3);
                             if (row0 + r >= limit || 4 * k >= left) continue;
                             float4 v = *reinterpret_cast<const float4*>(mine + r * 32 + 4 * (k ^ (r & 7)));
-                            if (g.part) {  // part_ld is a multiple of 4
-                                float* o = g.part + s * g.part_split + (int64_t)(row0 + r) * g.part_ld + col + 4 * k;
-                                if (g.add) {
+                            if (x.part) {  // part_ld is a multiple of 4
+                                float* o = x.part + t.s * x.part_split + (int64_t)(row0 + r) * x.part_ld + col + 4 * k;
+                                if (x.add) {
                                     const float4 w = *reinterpret_cast<const float4*>(o);
                                     v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
                                 }
                                 *reinterpret_cast<float4*>(o) = v;
                             } else {
-                                const int64_t orow = g.row_map ? g.row_map[row0 + r] : (int64_t)g.v0 + row0 + r;
-                                uint16_t* o = g.out + orow * g.out_ld + col + 4 * k;
+                                const int64_t orow = token ? token[row0 + r] : (int64_t)x.v0 + row0 + r;
+                                uint16_t* o = x.out + orow * x.out_ld + col + 4 * k;
                                 if (4 * k + 4 <= left) {
                                     *reinterpret_cast<uint2*>(o) =
                                         make_uint2(ss::pack_bf16x2(scale * v.x, scale * v.y),
@@ -348,9 +432,9 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                         }
                     } else {  // a row at a time, a column a lane
                         for (int r = 0; r < 32 && row0 + r < limit; ++r) {
-                            const int64_t orow = g.row_map ? g.row_map[row0 + r] : (int64_t)g.v0 + row0 + r;
+                            const int64_t orow = token ? token[row0 + r] : (int64_t)x.v0 + row0 + r;
                             if (lane < left)
-                                g.out[orow * g.out_ld + col + lane] =
+                                x.out[orow * x.out_ld + col + lane] =
                                     ss::f32_to_bf16(scale * mine[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)]);
                         }
                     }
@@ -377,7 +461,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 // ---------------------------------------------------------------------------
 
 constexpr int kThreads = 256;
-constexpr int kGatherRows = 16;  // tokens per CTA, one per warp
+constexpr int kGatherRows = 8;  // tokens per CTA, one per warp
 constexpr int kGatherThreads = 32 * kGatherRows;
 
 // 8 elements from element 8j of a row of D bf16 at any element alignment,
@@ -418,15 +502,16 @@ struct GatherArgs {
     int64_t d_ld;
     float grad_scale;
     int mean;
+    int* counters;  // of the launches' tiles
+    int n_counters;
 };
 
-// CTA b places tokens [16 b, 16 b + 16): how many of the tokens before count
-// (read again by every CTA: T * T / 4 bytes in all, from L2), then its own
+// CTA b places tokens [8 b, 8 b + 8): how many of the tokens before count
+// (read again by every CTA: T * T / 2 bytes in all, from L2), then its own
 // rows, one per warp: gathered together with the logit of their target, or,
 // where ignored, zeroed in the outputs.  The tensor cores' sums drop bits in one
 // direction, and the target's logit is the one that grows large, so it gets
-// a sum of its own, in fp32 by 256 partial sums.  The last CTA knows the total; it
-// zeroes the rows up to the next whole k block.
+// a sum of its own, in fp32 by 256 partial sums.  The last CTA knows the total.
 __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherArgs a) {
     launch_after();
     __shared__ int part[32];
@@ -434,9 +519,20 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherA
     __shared__ int total;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * kGatherRows;
+    const int t = t0 + warp;
+    const int64_t y = t < a.T ? a.targets[t] : a.ignore;
+    const bool known = y >= 0 && y < a.vocab;
+    const uint16_t* src = a.hidden + (int64_t)t * a.ld;
+    const uint16_t* w = a.weight + (known ? y : 0) * a.ldw;
+    if (y != a.ignore) {  // both rows on their way to L2 while the tokens before are counted
+        for (int j = 64 * lane; j < a.D; j += 64 * 32) {
+            ss::prefetch_l2(src + j);
+            ss::prefetch_l2(w + j);
+        }
+    }
     int before = 0;
-#pragma unroll 4
-    for (int t = threadIdx.x; t < t0; t += kGatherThreads) before += a.targets[t] != a.ignore;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < t0; i += kGatherThreads) before += a.targets[i] != a.ignore;
     before = __reduce_add_sync(0xFFFFFFFFu, before);
     if (lane == 0) part[warp] = before;
     __syncthreads();
@@ -445,7 +541,7 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherA
         const int t = t0 + lane;
         const bool here = lane < kGatherRows && t < a.T;
         const int64_t y = here ? a.targets[t] : a.ignore;
-        const bool counts = here && y != a.ignore;
+        const bool counts = y != a.ignore;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, counts);
         const int at = sum + __popc(mask & ((1u << lane) - 1));
         place[lane] = counts ? at : -1;
@@ -459,13 +555,9 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherA
     }
     __syncthreads();
     const int vecs = a.Dp / 8;
-    const int t = t0 + warp, at = place[warp];
+    const int at = place[warp];
     if (at >= 0) {
-        const uint16_t* src = a.hidden + (int64_t)t * a.ld;
         uint4* dst = reinterpret_cast<uint4*>(a.h + (int64_t)at * a.Dp);
-        const int64_t y = a.targets[t];
-        const bool known = y >= 0 && y < a.vocab;
-        const uint16_t* w = a.weight + (known ? y : 0) * a.ldw;
         float s = 0.f;
 #pragma unroll 4
         for (int j = lane; j < vecs; j += 32) {
@@ -481,11 +573,9 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherA
         for (int j = lane; j < a.D; j += 32) dst[j] = 0;
     }
     if (blockIdx.x == gridDim.x - 1) {
-        const int live = total;
-        const int end = (live + kBlockK - 1) / kBlockK * kBlockK;
-        for (int64_t j = threadIdx.x; j < (int64_t)(end - live) * vecs; j += kGatherThreads)
-            reinterpret_cast<uint4*>(a.h + (int64_t)live * a.Dp)[j] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < a.n_counters; i += kGatherThreads) a.counters[i] = 0;
         if (threadIdx.x == 0) {
+            const int live = total;
             a.header->live = live;
             a.header->finished = 0;
             a.header->scale = a.mean ? (live > 0 ? a.grad_scale / (float)live : 0.f) : a.grad_scale;
@@ -523,7 +613,7 @@ constexpr int kFewSlices = 1024;     // CTAs at most, each a slice of statistics
 template <int TOKENS>
 __global__ void __launch_bounds__(kThreads)
 ce_few_kernel(const Header* header, const uint16_t* __restrict__ h, int Dp, const uint16_t* __restrict__ w, int64_t ldw,
-              int V, const int* target, int rows, float2* stats) {
+              int V, int staged, const int* target, int rows, float2* stats) {
     launch_after();
     extern __shared__ __align__(16) unsigned char raw[];
     uint4* hs = reinterpret_cast<uint4*>(raw);
@@ -531,7 +621,24 @@ ce_few_kernel(const Header* header, const uint16_t* __restrict__ h, int Dp, cons
     __shared__ float sum_s[kThreads / 32][kFewTokens];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int vecs = Dp / 8;
-    wait_before();
+    const int groups = (V + kFewRows - 1) / kFewRows;
+    int g = blockIdx.x * (kThreads / 32) + warp;
+    uint4 x[4][kFewRows];
+    auto load = [&](int g, int j) {
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r) {  // past the end: the last row again, left out below
+            const int v = g * kFewRows + r < V ? g * kFewRows + r : V - 1;
+            const uint4* p = reinterpret_cast<const uint4*>(w + (int64_t)v * ldw);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (j + 32 * i < vecs) x[i][r] = ss::ld_stream_u4(p + j + 32 * i);
+        }
+    };
+    // a weight that no kernel of this call has written is read before the wait
+    if (staged) wait_before();
+    bool loaded = g < groups && lane < vecs;
+    if (loaded) load(g, lane);
+    if (!staged) wait_before();
     const int live = header->live;
     for (int i = threadIdx.x; i < TOKENS * vecs; i += kThreads)
         hs[i] = i < live * vecs ? reinterpret_cast<const uint4*>(h)[i] : make_uint4(0, 0, 0, 0);
@@ -542,45 +649,28 @@ ce_few_kernel(const Header* header, const uint16_t* __restrict__ h, int Dp, cons
     float top[TOKENS], sum[TOKENS];
 #pragma unroll
     for (int t = 0; t < TOKENS; ++t) top[t] = -INFINITY, sum[t] = 0.f;
-    const int groups = (V + kFewRows - 1) / kFewRows;
-    for (int g = blockIdx.x * (kThreads / 32) + warp; g < groups; g += gridDim.x * (kThreads / 32)) {
+    for (; g < groups; g += gridDim.x * (kThreads / 32)) {
         const int v0 = g * kFewRows;
-        const uint4* wr[kFewRows];
-#pragma unroll
-        for (int r = 0; r < kFewRows; ++r)  // past the end: the last row again, left out below
-            wr[r] = reinterpret_cast<const uint4*>(w + (int64_t)(v0 + r < V ? v0 + r : V - 1) * ldw);
         float acc[kFewRows][TOKENS];
 #pragma unroll
         for (int r = 0; r < kFewRows; ++r)
 #pragma unroll
             for (int t = 0; t < TOKENS; ++t) acc[r][t] = 0.f;
-        int j = lane;
-        for (; j + 96 < vecs; j += 128) {
-            uint4 x[4][kFewRows];
+        for (int j = lane; j < vecs; j += 128) {
+            if (j != lane || !loaded) load(g, j);
+            loaded = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int r = 0; r < kFewRows; ++r) x[i][r] = ss::ld_stream_u4(wr[r] + j + 32 * i);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                if (j + 32 * i >= vecs) continue;
 #pragma unroll
                 for (int t = 0; t < TOKENS; ++t) {
                     const uint4 hv = hs[t * vecs + j + 32 * i];
 #pragma unroll
                     for (int r = 0; r < kFewRows; ++r) acc[r][t] = dot_bf16(x[i][r], hv, acc[r][t]);
                 }
-        }
-        for (; j < vecs; j += 32) {
-            uint4 x[kFewRows];
-#pragma unroll
-            for (int r = 0; r < kFewRows; ++r) x[r] = ss::ld_stream_u4(wr[r] + j);
-#pragma unroll
-            for (int t = 0; t < TOKENS; ++t) {
-                const uint4 hv = hs[t * vecs + j];
-#pragma unroll
-                for (int r = 0; r < kFewRows; ++r) acc[r][t] = dot_bf16(x[r], hv, acc[r][t]);
             }
         }
+        __syncwarp();
 #pragma unroll
         for (int t = 0; t < TOKENS; ++t) {
             float l[kFewRows], m = -INFINITY;
@@ -596,8 +686,8 @@ ce_few_kernel(const Header* header, const uint16_t* __restrict__ h, int Dp, cons
             const float at = up == -INFINITY ? 0.f : up;
             float a = 0.f;
 #pragma unroll
-            for (int r = 0; r < kFewRows; ++r) a += exp2f(fmaf(l[r], kLog2e, -at));
-            sum[t] = (top[t] == -INFINITY ? 0.f : sum[t] * exp2f(top[t] - at)) + a;
+            for (int r = 0; r < kFewRows; ++r) a += ex2(fmaf(l[r], kLog2e, -at));
+            sum[t] = (top[t] == -INFINITY ? 0.f : sum[t] * ex2(top[t] - at)) + a;
             top[t] = up;
         }
     }
@@ -612,26 +702,27 @@ ce_few_kernel(const Header* header, const uint16_t* __restrict__ h, int Dp, cons
         for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, top_s[i][t]);
         const float at = m == -INFINITY ? 0.f : m;
         for (int i = 0; i < kThreads / 32; ++i)
-            s += top_s[i][t] == -INFINITY ? sum_s[i][t] : sum_s[i][t] * exp2f(top_s[i][t] - at);
+            s += top_s[i][t] == -INFINITY ? sum_s[i][t] : sum_s[i][t] * ex2(top_s[i][t] - at);
         stats[(int64_t)blockIdx.x * rows + t] = make_float2(m, s);
     }
 }
 
-constexpr int kLossThreads = 1024;
-constexpr int kLossRows = 32;  // rows per CTA, 32 threads each
-constexpr int kLossSlices = kLossThreads / kLossRows;
+constexpr int kLossThreads = 256;
+constexpr int kLossRows = kLossThreads / 32;  // rows per CTA, 32 threads each
+constexpr int kLossSlices = 32;
 
 // The tiles' statistics of a row to its loss.  With r = sum over every other
 // class of exp(l - l_target): loss = log(1 + r), log-sum-exp = l_target + loss and
 // the target's p - 1 = -r / (1 + r), none of which cancels where the target holds
 // almost all of the mass.  The CTA's losses go to one fp64 partial; the last CTA
 // to finish sums the partials, in order, to the loss: over the tokens that count
-// for a mean, 0 when there are none.
+// for a mean, 0 when there are none.  For the gradients (h), the gathered hidden
+// states are zeroed from the last row to the next whole k block.
 __global__ void __launch_bounds__(kLossThreads)
 ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, int rows,
                const float* __restrict__ target_logit, const int* __restrict__ row_map,
                float2* __restrict__ row_loss, float* __restrict__ token_loss, double* __restrict__ partials,
-               int mean, float* __restrict__ loss_out) {
+               int mean, float* __restrict__ loss_out, uint16_t* h, int Dp) {
     launch_after();
     __shared__ float top_s[kLossSlices][kLossRows + 1];
     __shared__ float sum_s[kLossSlices][kLossRows + 1];
@@ -642,14 +733,15 @@ ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, in
     const int live = header->live;
     auto add = [](float& m, float& s, float m2, float s2) {  // exponents are whole numbers: exact
         const float up = fmaxf(m, m2);
-        s = (m == up ? s : s * exp2f(m - up)) + (m2 == up ? s2 : s2 * exp2f(m2 - up));
+        s = (m == up ? s : s * ex2(m - up)) + (m2 == up ? s2 : s2 * ex2(m2 - up));
         m = up;
     };
-    {  // rows side by side (lane), a warp's slice of the tiles
-        const int row = blockIdx.x * kLossRows + lane;
+    {  // rows side by side, a thread's slice of the tiles
+        const int r = threadIdx.x % kLossRows, slice = threadIdx.x / kLossRows;
+        const int row = blockIdx.x * kLossRows + r;
         float top = -INFINITY, sum = 0.f;
         if (row < live) {
-            int n = warp;
+            int n = slice;
             for (; n < n_tiles; n += 8 * kLossSlices) {
                 float2 v[8];
 #pragma unroll
@@ -660,10 +752,12 @@ ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, in
                 for (int i = 0; i < 8; ++i) add(top, sum, v[i].x, v[i].y);
             }
         }
-        top_s[warp][lane] = top;
-        sum_s[warp][lane] = sum;
+        top_s[slice][r] = top;
+        sum_s[slice][r] = sum;
     }
     const int row = blockIdx.x * kLossRows + warp;  // from here on a warp's row, a lane's slice
+    if (h && row >= live && row < (live + kBlockK - 1) / kBlockK * kBlockK)
+        for (int j = lane; j < Dp / 8; j += 32) reinterpret_cast<uint4*>(h + (int64_t)row * Dp)[j] = make_uint4(0, 0, 0, 0);
     const float hit = row < live ? target_logit[row] : 0.f;
     const int token = row < live ? row_map[row] : 0;
     __syncthreads();
@@ -674,8 +768,9 @@ ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, in
     if (lane == 0) {
         float l = 0.f;
         if (row < live) {
-            // log of r; a lone class has r = 0
-            const float d = (float)((double)top * kLn2 + (double)logf(sum) - (double)hit);
+            // log of r, the whole exponent's ln 2 in two parts (the first exact); a lone class has r = 0
+            const float d = top == -INFINITY ? (sum == 0.f ? top : sum)
+                                             : fmaf(top, kLn2High, -hit) + fmaf(top, kLn2Low, logf(sum));
             const float rest = expf(-fabsf(d));
             l = (d > 0.f ? d : 0.f) + log1pf(rest);
             row_loss[row] = make_float2((hit + l) * kLog2e, -(d > 0.f ? 1.f : rest) / (1.f + rest));
@@ -685,9 +780,9 @@ ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, in
     }
     __syncthreads();
     if (warp == 0) {
-        double loss = loss_s[lane];
+        double loss = lane < kLossRows ? loss_s[lane] : 0.0;
 #pragma unroll
-        for (int k = 16; k > 0; k >>= 1) loss += __shfl_down_sync(0xFFFFFFFFu, loss, k);
+        for (int k = kLossRows / 2; k > 0; k >>= 1) loss += __shfl_down_sync(0xFFFFFFFFu, loss, k);
         if (lane == 0) {
             last = true;
             if (gridDim.x > 1) {
@@ -710,9 +805,9 @@ ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, in
     if (lane == 0) loss_s[warp] = s;
     __syncthreads();
     if (warp == 0) {
-        s = loss_s[lane];
+        s = lane < kLossRows ? loss_s[lane] : 0.0;
 #pragma unroll
-        for (int k = 16; k > 0; k >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, k);
+        for (int k = kLossRows / 2; k > 0; k >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, k);
         if (lane == 0) *loss_out = (float)(mean && live > 0 ? s / live : s);
     }
 }
@@ -770,10 +865,11 @@ struct Layout {
     bool few;  // tokens: the dot-product kernel
     int hidden_splits, head_splits;
     bool grad, stage;
-    int64_t row, target, target_logit, row_loss, partials, stats, h, w, p, hidden_part, head_part, bytes;
+    int64_t counters, n_counters;
+    int64_t row, target, target_logit, row_loss, partials, stats, h, w, p[2], hidden_part, head_part, bytes;
 };
 
-constexpr int64_t kPieceBytes = 256ll << 20;  // of P
+constexpr int64_t kPieceBytes = 256ll << 20;  // of P, one buffer of two
 
 Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int pairs) {
     Layout l = {};
@@ -783,7 +879,7 @@ Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int p
     l.n_tiles = up(V, kTile) / kTile;
     l.few = T <= kFewTokens && kFewTokens * l.Dp * 2 <= kFewSmem;
     const int64_t few_ctas = (V + kFewRows * (kThreads / 32) - 1) / (kFewRows * (kThreads / 32));
-    l.slices = !l.few ? l.n_tiles : few_ctas < kFewSlices ? few_ctas : kFewSlices;
+    l.slices = !l.few ? 2 * l.n_tiles : few_ctas < kFewSlices ? few_ctas : kFewSlices;
     int64_t at = 256;  // the header
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -795,15 +891,20 @@ Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int p
     l.target_logit = take(l.rows * 4);
     l.row_loss = take(l.rows * 8);
     l.partials = take(l.rows / kLossRows * 8);
+    if (grad) {
+        const int64_t fit = kPieceBytes / (l.rows > 0 ? l.rows * 2 : 2) / kTile * kTile;
+        l.piece = fit < kTile ? kTile : fit;
+        l.pieces = (l.n_tiles * kTile + l.piece - 1) / l.piece;
+        l.piece = (l.n_tiles + l.pieces - 1) / l.pieces * kTile;  // even pieces
+    }
+    l.n_counters = 2 + l.pieces;
+    l.counters = take(l.n_counters * 4);
     l.stats = take(l.slices * l.rows * 8);
     l.h = take(l.rows * l.Dp * 2);
     if (stage) l.w = take(V * l.Dp * 2);
     if (grad) {
-        const int64_t fit = kPieceBytes / (l.rows * 2) / kTile * kTile;
-        l.piece = fit < kTile ? kTile : fit;
-        l.pieces = (l.n_tiles * kTile + l.piece - 1) / l.piece;
-        l.piece = (l.n_tiles + l.pieces - 1) / l.pieces * kTile;  // even pieces
-        l.p = take(l.rows * l.piece * 2);
+        l.p[0] = take(l.rows * l.piece * 2);
+        l.p[1] = l.pieces > 1 ? take(l.rows * l.piece * 2) : l.p[0];
         const int64_t d_tiles = up(D, kTile) / kTile;
         l.hidden_splits = choose_splits(l.rows / kTile * d_tiles, l.piece / kBlockK, pairs);
         l.head_splits = choose_splits(l.piece / kTile * d_tiles, l.rows / kBlockK, pairs);
@@ -866,20 +967,21 @@ int allow_smem(std::atomic<uint64_t>& ready, const void* kernel, int bytes) {
 }
 
 template <int TOKENS>
-int launch_few(const GemmArgs& g, const uint16_t* h, int64_t Dp, const uint16_t* w, int64_t ldw, int64_t slices,
-               cudaStream_t st) {
+int launch_few(const GemmArgs& g, const uint16_t* h, int64_t Dp, const uint16_t* w, int64_t ldw, bool staged,
+               int64_t slices, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
     if (int rc = allow_smem(ready, reinterpret_cast<const void*>(ce_few_kernel<TOKENS>), kFewSmem)) return rc;
     return launch(ce_few_kernel<TOKENS>, slices, kThreads, (int)(TOKENS * Dp * 2), st, g.header, h, (int)Dp, w, ldw,
-                  g.vocab, g.target, g.rows, g.stats);
+                  g.vocab, staged ? 1 : 0, g.target, g.rows, g.stats);
 }
 
-template <int MODE>
-int launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& g, int64_t tiles, cudaStream_t st) {
-    static std::atomic<uint64_t> ready{0};  // devices whose limit has been raised
-    if (int rc = allow_smem(ready, reinterpret_cast<const void*>(ce_gemm_kernel<MODE>), kSmemBytes)) return rc;
+int launch_gemm(const Maps& maps, GemmArgs& g, int64_t tiles, cudaStream_t st) {
+    static std::atomic<uint64_t> ready{0};
+    if (int rc = allow_smem(ready, reinterpret_cast<const void*>(ce_gemm_kernel), kSmemBytes)) return rc;
     const int64_t pairs = ss::num_sms() / 2;
-    return launch(ce_gemm_kernel<MODE>, 2 * (tiles < pairs ? tiles : pairs), kGemmThreads, kSmemBytes, st, a, b, g);
+    const int rc = launch(ce_gemm_kernel, 2 * (tiles < pairs ? tiles : pairs), kGemmThreads, kSmemBytes, st, maps, g);
+    ++g.next;
+    return rc;
 }
 
 constexpr int64_t kMaxSize = 1 << 28;  // tokens, hidden, vocabulary: 32-bit tile coordinates
@@ -937,12 +1039,14 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
     float2* row_loss = reinterpret_cast<float2*>(ws + l.row_loss);
     double* partials = reinterpret_cast<double*>(ws + l.partials);
     uint16_t* h = reinterpret_cast<uint16_t*>(ws + l.h);
+    int* counters = reinterpret_cast<int*>(ws + l.counters);
     const int mean = a->reduction == SS_LOSS_MEAN;
 
     GatherArgs ga = {header, a->targets, a->ignore_index, (int)T, (int)D, (int)l.Dp, (int)V,
                      static_cast<const uint16_t*>(a->hidden), a->hidden_stride, static_cast<const uint16_t*>(a->weight),
                      a->weight_stride, h, row, target, target_logit, a->token_loss_out,
-                     static_cast<uint16_t*>(a->d_hidden), a->d_hidden_stride, (float)a->grad_scale, mean};
+                     static_cast<uint16_t*>(a->d_hidden), a->d_hidden_stride, (float)a->grad_scale, mean, counters,
+                     (int)l.n_counters};
     ce_gather_kernel<<<(int)((T > 0 ? T + kGatherRows - 1 : kGatherRows) / kGatherRows), kGatherThreads, 0, st>>>(ga);
     if (int rc = ss::check_launch()) return rc;
 
@@ -958,104 +1062,138 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
 
     GemmArgs g = {};
     g.header = header;
-    g.splits = 1;
-    g.k = (int)D;
+    g.next = counters;
     g.vocab = (int)V;
     g.rows = (int)l.rows;
     g.target = target;
+    g.token = row;
+    g.row_loss = row_loss;
     g.loss = a->loss_out;
+    g.stats = reinterpret_cast<float2*>(ws + l.stats);
     CUtensorMap h_k, w_k;
+    const int64_t m_tiles = l.rows / kTile;
     if (T > 0) {
         if (int rc = make_map(&h_k, h, l.rows, D, l.Dp, kHalf)) return rc;
         if (int rc = make_map(&w_k, w, V, D, ldw, kHalf)) return rc;
-        GemmArgs s = g;
-        s.n_tiles = (int)l.n_tiles;
-        s.stats = reinterpret_cast<float2*>(ws + l.stats);
-        g.stats = s.stats;
         if (l.few) {
-            const int rc = T == 1   ? launch_few<1>(s, h, l.Dp, w, ldw, l.slices, st)
-                           : T == 2 ? launch_few<2>(s, h, l.Dp, w, ldw, l.slices, st)
-                                    : launch_few<kFewTokens>(s, h, l.Dp, w, ldw, l.slices, st);
+            const int rc = T == 1   ? launch_few<1>(g, h, l.Dp, w, ldw, stage, l.slices, st)
+                           : T == 2 ? launch_few<2>(g, h, l.Dp, w, ldw, stage, l.slices, st)
+                                    : launch_few<kFewTokens>(g, h, l.Dp, w, ldw, stage, l.slices, st);
             if (rc) return rc;
-        } else if (int rc = launch_gemm<kStatistics>(h_k, w_k, s, l.rows / kTile * l.n_tiles, st)) {
-            return rc;
+        } else {
+            Maps maps;
+            maps.a[0] = h_k, maps.b[0] = w_k;
+            Work& x = g.work[0];
+            x.product = kStatistics;
+            x.n_tiles = (int)l.n_tiles;
+            x.splits = 1;
+            x.k = (int)D;
+            g.count = 1;
+            if (int rc = launch_gemm(maps, g, m_tiles * l.n_tiles, st)) return rc;
         }
     }
-    if (int rc = launch(ce_loss_kernel, T > 0 ? (T + kLossRows - 1) / kLossRows : 1, kLossThreads, 0, st, header, g.stats,
+    if (int rc = launch(ce_loss_kernel, T > 0 ? up(T, grad ? kBlockK : kLossRows) / kLossRows : 1, kLossThreads, 0, st, header, g.stats,
                         (int)l.slices, (int)l.rows, target_logit, row, row_loss, a->token_loss_out, partials, mean,
-                        a->loss_out))
+                        a->loss_out, grad ? h : nullptr, (int)l.Dp))
         return rc;
+    if (!grad) return SS_OK;
+    if (T == 0) {
+        if (!a->d_weight) return SS_OK;
+        const cudaError_t e =
+            cudaMemset2DAsync(a->d_weight, (size_t)a->d_weight_stride * 2, 0, (size_t)D * 2, (size_t)V, st);
+        return e == cudaSuccess ? SS_OK : ss::cuda_fail(e);
+    }
 
-    if (grad) {
-        CUtensorMap p_k, p_mn, h_mn, w_mn;
-        uint16_t* p = reinterpret_cast<uint16_t*>(ws + l.p);
-        const int64_t ld = up(D, 4), d_tiles = up(D, kTile) / kTile;
-        if (T > 0) {
-            if (int rc = make_map(&p_k, p, l.rows, l.piece, l.piece, kHalf)) return rc;
-            if (int rc = make_map(&p_mn, p, l.rows, l.piece, l.piece, kBlockK)) return rc;
-            if (int rc = make_map(&h_mn, h, l.rows, D, l.Dp, kBlockK)) return rc;
-            if (int rc = make_map(&w_mn, w, V, D, ldw, kBlockK)) return rc;
-        }
-        if (T == 0 && a->d_weight) {
-            const cudaError_t e =
-                cudaMemset2DAsync(a->d_weight, (size_t)a->d_weight_stride * 2, 0, (size_t)D * 2, (size_t)V, st);
-            if (e != cudaSuccess) return ss::cuda_fail(e);
-        }
-        for (int64_t i = 0; T > 0 && i < l.pieces; ++i) {
-            const int64_t v0 = i * l.piece;
-            const int64_t tiles_v = (V - v0 < l.piece ? up(V - v0, kTile) : l.piece) / kTile;
-            GemmArgs q = g;
-            q.v0 = (int)v0;
-            q.n_tiles = (int)tiles_v;
-            q.row_loss = row_loss;
-            q.p = p;
-            q.ldp = (int)l.piece;
-            if (int rc = launch_gemm<kProbability>(h_k, w_k, q, l.rows / kTile * tiles_v, st)) return rc;
-            const int64_t rows_v = V - v0 < l.piece ? V - v0 : l.piece;
-            if (a->d_weight) {
-                GemmArgs d = g;
-                d.v0 = (int)v0;
-                d.m_tiles = (int)tiles_v;
-                d.m_rows = (int)rows_v;
-                d.n_tiles = (int)d_tiles;
-                d.cols = (int)D;
-                d.splits = l.head_splits;
-                d.part = l.head_part ? reinterpret_cast<float*>(ws + l.head_part) : nullptr;
-                d.part_split = l.piece * ld;
-                d.part_ld = (int)ld;
-                d.out = static_cast<uint16_t*>(a->d_weight);
-                d.out_ld = a->d_weight_stride;
-                if (int rc = launch_gemm<kHead>(p_mn, h_mn, d, tiles_v * d_tiles * d.splits, st)) return rc;
-                if (d.part) {
-                    const int64_t blocks = (rows_v * (ld / 4) + kThreads - 1) / kThreads;
-                    if (int rc = launch(ce_join_kernel, blocks, kThreads, 0, st, header, d.part, d.splits, d.part_split,
-                                        d.part_ld, (int)rows_v, (int)D, d.out + v0 * d.out_ld, d.out_ld, nullptr))
-                        return rc;
-                }
-            }
+    // Launch i: the gradients of piece i - 1 and the probabilities of piece i.
+    uint16_t* p[2] = {reinterpret_cast<uint16_t*>(ws + l.p[0]), reinterpret_cast<uint16_t*>(ws + l.p[1])};
+    CUtensorMap p_k[2], p_mn[2], h_mn, w_mn;
+    for (int i = 0; i < 2; ++i) {
+        if (int rc = make_map(&p_k[i], p[i], l.rows, l.piece, l.piece, kHalf)) return rc;
+        if (int rc = make_map(&p_mn[i], p[i], l.rows, l.piece, l.piece, kBlockK)) return rc;
+    }
+    if (int rc = make_map(&h_mn, h, l.rows, D, l.Dp, kBlockK)) return rc;
+    if (int rc = make_map(&w_mn, w, V, D, ldw, kBlockK)) return rc;
+    const int64_t ld = up(D, 4), d_tiles = up(D, kTile) / kTile;
+    for (int64_t i = 0; i <= l.pieces; ++i) {
+        struct {
+            Work work;
+            const CUtensorMap *a, *b;
+            int64_t tiles, blocks;
+        } list[kMaxWork];
+        int n = 0;
+        const int64_t v0 = (i - 1) * l.piece;  // of the piece whose gradients are taken
+        const int64_t rows_v = V - v0 < l.piece ? V - v0 : l.piece;
+        const int64_t tiles_v = up(rows_v, kTile) / kTile;
+        Work head = {};
+        if (i > 0) {
+            const int b = (int)((i - 1) & 1);
             if (a->d_hidden) {
-                GemmArgs d = g;
-                d.v0 = (int)v0;
-                d.k = (int)(tiles_v * kTile);
-                d.n_tiles = (int)d_tiles;
-                d.cols = (int)D;
-                d.splits = l.hidden_splits;
-                d.part = l.hidden_part ? reinterpret_cast<float*>(ws + l.hidden_part) : nullptr;
-                d.part_split = l.rows * ld;
-                d.part_ld = (int)ld;
-                d.add = i > 0;
-                d.out = static_cast<uint16_t*>(a->d_hidden);
-                d.out_ld = a->d_hidden_stride;
-                d.row_map = row;
-                if (int rc = launch_gemm<kHidden>(p_k, w_mn, d, l.rows / kTile * d_tiles * d.splits, st)) return rc;
-                if (d.part && i == l.pieces - 1) {
-                    const int64_t blocks = (l.rows * (ld / 4) + kThreads - 1) / kThreads;
-                    if (int rc = launch(ce_join_kernel, blocks, kThreads, 0, st, header, d.part, d.splits, d.part_split,
-                                        d.part_ld, (int)l.rows, (int)D, d.out, d.out_ld, row))
-                        return rc;
-                }
+                Work x = {};
+                x.product = kHidden;
+                x.n_tiles = (int)d_tiles;
+                x.splits = l.hidden_splits;
+                x.k = (int)(tiles_v * kTile);
+                x.v0 = (int)v0;
+                x.part = l.hidden_part ? reinterpret_cast<float*>(ws + l.hidden_part) : nullptr;
+                x.part_split = l.rows * ld;
+                x.part_ld = (int)ld;
+                x.add = i > 1;
+                x.out = static_cast<uint16_t*>(a->d_hidden);
+                x.out_ld = a->d_hidden_stride;
+                x.cols = (int)D;
+                list[n++] = {x, &p_k[b], &w_mn, m_tiles * d_tiles * x.splits, tiles_v * kTile / kBlockK / x.splits};
+            }
+            if (a->d_weight) {
+                head.product = kHead;
+                head.m_tiles = (int)tiles_v;
+                head.n_tiles = (int)d_tiles;
+                head.splits = l.head_splits;
+                head.v0 = (int)v0;
+                head.part = l.head_part ? reinterpret_cast<float*>(ws + l.head_part) : nullptr;
+                head.part_split = l.piece * ld;
+                head.part_ld = (int)ld;
+                head.out = static_cast<uint16_t*>(a->d_weight);
+                head.out_ld = a->d_weight_stride;
+                head.m_rows = (int)rows_v;
+                head.cols = (int)D;
+                list[n++] = {head, &p_mn[b], &h_mn, tiles_v * d_tiles * head.splits, l.rows / kBlockK / head.splits};
             }
         }
+        if (i < l.pieces) {
+            Work x = {};
+            const int64_t left = l.n_tiles - i * (l.piece / kTile);
+            x.product = kProbability;
+            x.n_tiles = (int)(left < l.piece / kTile ? left : l.piece / kTile);
+            x.splits = 1;
+            x.k = (int)D;
+            x.v0 = (int)(i * l.piece);
+            x.p = p[i & 1];
+            x.ldp = (int)l.piece;
+            list[n++] = {x, &h_k, &w_k, m_tiles * x.n_tiles, up(D, kBlockK) / kBlockK};
+        }
+        std::stable_sort(list, list + n, [](const auto& x, const auto& y) { return x.blocks > y.blocks; });
+        Maps maps;
+        int64_t tiles = 0;
+        for (int k = 0; k < n; ++k) {
+            g.work[k] = list[k].work;
+            maps.a[k] = *list[k].a, maps.b[k] = *list[k].b;
+            tiles += list[k].tiles;
+        }
+        g.count = n;
+        if (tiles > INT32_MAX - 1024) return SS_EOVERFLOW;
+        if (int rc = launch_gemm(maps, g, tiles, st)) return rc;
+        if (head.part) {
+            const int64_t blocks = (rows_v * (ld / 4) + kThreads - 1) / kThreads;
+            if (int rc = launch(ce_join_kernel, blocks, kThreads, 0, st, header, head.part, head.splits, head.part_split,
+                                head.part_ld, (int)rows_v, (int)D, head.out + v0 * head.out_ld, head.out_ld, nullptr))
+                return rc;
+        }
+    }
+    if (a->d_hidden && l.hidden_part) {
+        const int64_t blocks = (l.rows * (ld / 4) + kThreads - 1) / kThreads;
+        return launch(ce_join_kernel, blocks, kThreads, 0, st, header, reinterpret_cast<float*>(ws + l.hidden_part),
+                      l.hidden_splits, l.rows * ld, (int)ld, (int)l.rows, (int)D, static_cast<uint16_t*>(a->d_hidden),
+                      a->d_hidden_stride, row);
     }
     return SS_OK;
 }
