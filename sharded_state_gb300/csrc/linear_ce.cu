@@ -93,6 +93,9 @@ struct GemmArgs {
     int vocab;
     int rows;   // allocated token rows
     float* loss;  // NaN goes there when a wait runs out
+    const double* partials;  // this launch sums them to the loss (NULL: it does not)
+    int n_partials;
+    int mean;
     const int* target;       // [rows]
     const int* token;        // [rows]: output row of each row (kHidden)
     const float2* row_loss;  // [rows]: log-sum-exp in base 2, the target's p - 1 (kProbability)
@@ -133,6 +136,18 @@ __device__ __forceinline__ void add_logits(const float (&l)[32], float& m, float
     }
     s = (m == -INFINITY ? 0.f : s * ex2(m - at)) + (a + b);
     m = up;
+}
+
+// The loss, by one warp: the partials' sum in a fixed order, over the tokens that
+// count for a mean, 0 when there are none.
+__device__ __forceinline__ void sum_losses(const double* partials, int n, int live, int mean, float* loss) {
+    const int lane = threadIdx.x & 31;
+    double s = 0.0;
+#pragma unroll 8
+    for (int i = lane; i < n; i += 32) s += __ldcg(partials + i);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, k);
+    if (lane == 0) *loss = (float)(mean && live > 0 ? s / live : s);
 }
 
 // A tile of a launch: which product (-1: there is none left), where, and its
@@ -320,6 +335,8 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
             }
             if (t.w < 0) break;
         }
+    } else if (warp == 3 && rank == 1 && first == 0 && g.partials) {
+        sum_losses(g.partials, g.n_partials, live, g.mean, g.loss);
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const uint32_t acc_empty0 = tc::map_to_rank(acc_empty, 0);
@@ -506,25 +523,23 @@ struct GatherArgs {
     int n_counters;
 };
 
-// CTA b places tokens [8 b, 8 b + 8): how many of the tokens before count
-// (read again by every CTA: T * T / 2 bytes in all, from L2), then its own
+// Block b places tokens [8 b, 8 b + 8): how many of the tokens before count
+// (read again by every block: T * T / 2 bytes in all, from L2), then its own
 // rows, one per warp: gathered together with the logit of their target, or,
 // where ignored, zeroed in the outputs.  The tensor cores' sums drop bits in one
 // direction, and the target's logit is the one that grows large, so it gets
-// a sum of its own, in fp32 by 256 partial sums.  The last CTA knows the total.
-__global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherArgs a) {
-    launch_after();
-    __shared__ int part[32];
-    __shared__ int place[32];
-    __shared__ int total;
+// a sum of its own, in fp32 by 256 partial sums.  The last block knows the total.
+__device__ __forceinline__ void gather_block(const GatherArgs& a, int block, bool last) {
+    __shared__ int part[kGatherRows];
+    __shared__ int flag[kGatherRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t0 = blockIdx.x * kGatherRows;
+    const int t0 = block * kGatherRows;
     const int t = t0 + warp;
     const int64_t y = t < a.T ? a.targets[t] : a.ignore;
-    const bool known = y >= 0 && y < a.vocab;
+    const bool counts = y != a.ignore, known = y >= 0 && y < a.vocab;
     const uint16_t* src = a.hidden + (int64_t)t * a.ld;
     const uint16_t* w = a.weight + (known ? y : 0) * a.ldw;
-    if (y != a.ignore) {  // both rows on their way to L2 while the tokens before are counted
+    if (counts) {  // both rows on their way to L2 while the tokens before are counted
         for (int j = 64 * lane; j < a.D; j += 64 * 32) {
             ss::prefetch_l2(src + j);
             ss::prefetch_l2(w + j);
@@ -534,29 +549,13 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherA
 #pragma unroll 8
     for (int i = threadIdx.x; i < t0; i += kGatherThreads) before += a.targets[i] != a.ignore;
     before = __reduce_add_sync(0xFFFFFFFFu, before);
-    if (lane == 0) part[warp] = before;
+    if (lane == 0) part[warp] = before, flag[warp] = counts;
     __syncthreads();
-    if (warp == 0) {
-        const int sum = __reduce_add_sync(0xFFFFFFFFu, lane < kGatherRows ? part[lane] : 0);
-        const int t = t0 + lane;
-        const bool here = lane < kGatherRows && t < a.T;
-        const int64_t y = here ? a.targets[t] : a.ignore;
-        const bool counts = y != a.ignore;
-        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, counts);
-        const int at = sum + __popc(mask & ((1u << lane) - 1));
-        place[lane] = counts ? at : -1;
-        if (counts) {
-            a.row[at] = t;
-            a.target[at] = y >= 0 && y < a.vocab ? (int)y : -1;
-        } else if (here && a.token_loss) {
-            a.token_loss[t] = 0.f;
-        }
-        if (lane == 0) total = sum + __popc(mask);
-    }
-    __syncthreads();
+    const int sum = __reduce_add_sync(0xFFFFFFFFu, lane < kGatherRows ? part[lane] : 0);
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, lane < kGatherRows && flag[lane]);
     const int vecs = a.Dp / 8;
-    const int at = place[warp];
-    if (at >= 0) {
+    if (counts) {
+        const int at = sum + __popc(mask & ((1u << warp) - 1));
         uint4* dst = reinterpret_cast<uint4*>(a.h + (int64_t)at * a.Dp);
         float s = 0.f;
 #pragma unroll 4
@@ -567,15 +566,22 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherA
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-        if (lane == 0) a.target_logit[at] = known ? s : NAN;
-    } else if (t < a.T && a.d_hidden) {
-        uint16_t* dst = a.d_hidden + (int64_t)t * a.d_ld;
-        for (int j = lane; j < a.D; j += 32) dst[j] = 0;
+        if (lane == 0) {
+            a.row[at] = t;
+            a.target[at] = known ? (int)y : -1;
+            a.target_logit[at] = known ? s : NAN;
+        }
+    } else if (t < a.T) {
+        if (lane == 0 && a.token_loss) a.token_loss[t] = 0.f;
+        if (a.d_hidden) {
+            uint16_t* dst = a.d_hidden + (int64_t)t * a.d_ld;
+            for (int j = lane; j < a.D; j += 32) dst[j] = 0;
+        }
     }
-    if (blockIdx.x == gridDim.x - 1) {
+    if (last) {
         for (int i = threadIdx.x; i < a.n_counters; i += kGatherThreads) a.counters[i] = 0;
         if (threadIdx.x == 0) {
-            const int live = total;
+            const int live = sum + __popc(mask);
             a.header->live = live;
             a.header->finished = 0;
             a.header->scale = a.mean ? (live > 0 ? a.grad_scale / (float)live : 0.f) : a.grad_scale;
@@ -583,17 +589,25 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherA
     }
 }
 
+__global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherArgs a) {
+    launch_after();
+    gather_block(a, blockIdx.x, blockIdx.x == gridDim.x - 1);
+}
+
 // Rows of a weight whose rows do not start on 16-byte boundaries, copied to
-// rows that do: one warp per row.
+// rows that do: one warp per row.  It needs nothing of the kernel before it, and
+// only ends after it, for the kernels behind both.
 __global__ void __launch_bounds__(kThreads)
 ce_stage_kernel(const uint16_t* __restrict__ w, int64_t ld, int V, int D, int Dp, uint16_t* __restrict__ out) {
     launch_after();
-    wait_before();
     const int64_t v = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (v >= V) return;
-    const uint16_t* src = w + v * ld;
-    uint4* dst = reinterpret_cast<uint4*>(out + v * Dp);
-    for (int j = threadIdx.x & 31; j < Dp / 8; j += 32) dst[j] = row_vec(src, j, D);
+    if (v < V) {
+        const uint16_t* src = w + v * ld;
+        uint4* dst = reinterpret_cast<uint4*>(out + v * Dp);
+#pragma unroll 4
+        for (int j = threadIdx.x & 31; j < Dp / 8; j += 32) dst[j] = row_vec(src, j, D);
+    }
+    wait_before();
 }
 
 // ---------------------------------------------------------------------------
@@ -609,18 +623,24 @@ constexpr int kFewSmem = 64 * 1024;  // of hidden states
 constexpr int kFewSlices = 1024;     // CTAs at most, each a slice of statistics
 
 // Statistics as the tile kernel leaves them, one slice per CTA: CTA b's warps
-// take groups of kFewRows rows, b's after those of the CTA before.
+// take groups of kFewRows rows, b's after those of the CTA before.  The CTAs pick
+// the tokens that count out themselves; one more CTA does the gather's work for
+// the kernels behind.  staged: the weight is a kernel's before this one.
 template <int TOKENS>
 __global__ void __launch_bounds__(kThreads)
-ce_few_kernel(const Header* header, const uint16_t* __restrict__ h, int Dp, const uint16_t* __restrict__ w, int64_t ldw,
-              int V, int staged, const int* target, int rows, float2* stats) {
+ce_few_kernel(const GatherArgs a, const uint16_t* __restrict__ w, int64_t ldw, int staged, int rows, float2* stats) {
     launch_after();
+    if (staged) wait_before();
+    if (blockIdx.x == gridDim.x - 1) {
+        gather_block(a, 0, true);
+        return;
+    }
     extern __shared__ __align__(16) unsigned char raw[];
     uint4* hs = reinterpret_cast<uint4*>(raw);
     __shared__ float top_s[kThreads / 32][kFewTokens];
     __shared__ float sum_s[kThreads / 32][kFewTokens];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int vecs = Dp / 8;
+    const int vecs = a.Dp / 8, V = a.vocab, slices = gridDim.x - 1;
     const int groups = (V + kFewRows - 1) / kFewRows;
     int g = blockIdx.x * (kThreads / 32) + warp;
     uint4 x[4][kFewRows];
@@ -634,22 +654,32 @@ ce_few_kernel(const Header* header, const uint16_t* __restrict__ h, int Dp, cons
                 if (j + 32 * i < vecs) x[i][r] = ss::ld_stream_u4(p + j + 32 * i);
         }
     };
-    // a weight that no kernel of this call has written is read before the wait
-    if (staged) wait_before();
-    bool loaded = g < groups && lane < vecs;
+    bool loaded = g < groups && lane < vecs;  // the first loads go out before the tokens are known
     if (loaded) load(g, lane);
-    if (!staged) wait_before();
-    const int live = header->live;
-    for (int i = threadIdx.x; i < TOKENS * vecs; i += kThreads)
-        hs[i] = i < live * vecs ? reinterpret_cast<const uint4*>(h)[i] : make_uint4(0, 0, 0, 0);
-    int y[TOKENS];
+    int y[TOKENS], from[TOKENS], live = 0;  // target and token of each row
 #pragma unroll
-    for (int t = 0; t < TOKENS; ++t) y[t] = t < live ? target[t] : -1;
+    for (int t = 0; t < TOKENS; ++t) y[t] = -1, from[t] = -1;
+#pragma unroll
+    for (int t = 0; t < TOKENS; ++t) {
+        const int64_t target = t < a.T ? a.targets[t] : a.ignore;
+        if (target == a.ignore) continue;
+#pragma unroll
+        for (int i = 0; i < TOKENS; ++i) {
+            if (i != live) continue;
+            y[i] = target >= 0 && target < V ? (int)target : -1;
+            from[i] = t;
+        }
+        ++live;
+    }
+#pragma unroll
+    for (int t = 0; t < TOKENS; ++t)
+        for (int j = threadIdx.x; j < vecs; j += kThreads)
+            hs[t * vecs + j] = from[t] >= 0 ? row_vec(a.hidden + from[t] * a.ld, j, a.D) : make_uint4(0, 0, 0, 0);
     __syncthreads();
     float top[TOKENS], sum[TOKENS];
 #pragma unroll
     for (int t = 0; t < TOKENS; ++t) top[t] = -INFINITY, sum[t] = 0.f;
-    for (; g < groups; g += gridDim.x * (kThreads / 32)) {
+    for (; g < groups; g += slices * (kThreads / 32)) {
         const int v0 = g * kFewRows;
         float acc[kFewRows][TOKENS];
 #pragma unroll
@@ -714,9 +744,9 @@ constexpr int kLossSlices = 32;
 // The tiles' statistics of a row to its loss.  With r = sum over every other
 // class of exp(l - l_target): loss = log(1 + r), log-sum-exp = l_target + loss and
 // the target's p - 1 = -r / (1 + r), none of which cancels where the target holds
-// almost all of the mass.  The CTA's losses go to one fp64 partial; the last CTA
-// to finish sums the partials, in order, to the loss: over the tokens that count
-// for a mean, 0 when there are none.  For the gradients (h), the gathered hidden
+// almost all of the mass.  The CTA's losses go to one fp64 partial.  With no
+// gradient to follow, the last CTA to finish sums the partials (sum_losses); else
+// the next launch does, off the gradients' path, and h is given: the gathered hidden
 // states are zeroed from the last row to the next whole k block.
 __global__ void __launch_bounds__(kLossThreads)
 ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, int rows,
@@ -727,7 +757,6 @@ ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, in
     __shared__ float top_s[kLossSlices][kLossRows + 1];
     __shared__ float sum_s[kLossSlices][kLossRows + 1];
     __shared__ double loss_s[kLossRows];
-    __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_before();
     const int live = header->live;
@@ -783,32 +812,19 @@ ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, in
         double loss = lane < kLossRows ? loss_s[lane] : 0.0;
 #pragma unroll
         for (int k = kLossRows / 2; k > 0; k >>= 1) loss += __shfl_down_sync(0xFFFFFFFFu, loss, k);
-        if (lane == 0) {
-            last = true;
-            if (gridDim.x > 1) {
-                partials[blockIdx.x] = loss;
+        if (lane == 0) partials[blockIdx.x] = loss;
+        if (h) return;
+        int last = 1;
+        if (gridDim.x > 1) {
+            if (lane == 0) {
                 __threadfence();
                 last = atomicAdd(&header->finished, 1) == (int)gridDim.x - 1;
-            } else {
-                *loss_out = (float)(mean && live > 0 ? loss / live : loss);
+                __threadfence();
             }
+            last = __shfl_sync(0xFFFFFFFFu, last, 0);
         }
-    }
-    if (gridDim.x == 1) return;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    double s = 0.0;
-    for (int i = threadIdx.x; i < (int)gridDim.x; i += kLossThreads) s += __ldcg(partials + i);
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, k);
-    if (lane == 0) loss_s[warp] = s;
-    __syncthreads();
-    if (warp == 0) {
-        s = lane < kLossRows ? loss_s[lane] : 0.0;
-#pragma unroll
-        for (int k = kLossRows / 2; k > 0; k >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, k);
-        if (lane == 0) *loss_out = (float)(mean && live > 0 ? s / live : s);
+        __syncwarp();
+        if (last) sum_losses(partials, gridDim.x, live, mean, loss_out);
     }
 }
 
@@ -877,7 +893,7 @@ Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int p
     l.Dp = up(D, 8);
     l.rows = up(T, kTile);
     l.n_tiles = up(V, kTile) / kTile;
-    l.few = T <= kFewTokens && kFewTokens * l.Dp * 2 <= kFewSmem;
+    l.few = T > 0 && T <= kFewTokens && kFewTokens * l.Dp * 2 <= kFewSmem;
     const int64_t few_ctas = (V + kFewRows * (kThreads / 32) - 1) / (kFewRows * (kThreads / 32));
     l.slices = !l.few ? 2 * l.n_tiles : few_ctas < kFewSlices ? few_ctas : kFewSlices;
     int64_t at = 256;  // the header
@@ -967,12 +983,12 @@ int allow_smem(std::atomic<uint64_t>& ready, const void* kernel, int bytes) {
 }
 
 template <int TOKENS>
-int launch_few(const GemmArgs& g, const uint16_t* h, int64_t Dp, const uint16_t* w, int64_t ldw, bool staged,
-               int64_t slices, cudaStream_t st) {
+int launch_few(const GatherArgs& a, const uint16_t* w, int64_t ldw, bool staged, int64_t slices, int64_t rows,
+               float2* stats, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
     if (int rc = allow_smem(ready, reinterpret_cast<const void*>(ce_few_kernel<TOKENS>), kFewSmem)) return rc;
-    return launch(ce_few_kernel<TOKENS>, slices, kThreads, (int)(TOKENS * Dp * 2), st, g.header, h, (int)Dp, w, ldw,
-                  g.vocab, staged ? 1 : 0, g.target, g.rows, g.stats);
+    return ss::launch(ce_few_kernel<TOKENS>, slices + 1, kThreads, TOKENS * a.Dp * 2, 0, staged, st, a, w, ldw,
+                      staged ? 1 : 0, (int)rows, stats);
 }
 
 int launch_gemm(const Maps& maps, GemmArgs& g, int64_t tiles, cudaStream_t st) {
@@ -1047,15 +1063,18 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
                      a->weight_stride, h, row, target, target_logit, a->token_loss_out,
                      static_cast<uint16_t*>(a->d_hidden), a->d_hidden_stride, (float)a->grad_scale, mean, counters,
                      (int)l.n_counters};
-    ce_gather_kernel<<<(int)((T > 0 ? T + kGatherRows - 1 : kGatherRows) / kGatherRows), kGatherThreads, 0, st>>>(ga);
-    if (int rc = ss::check_launch()) return rc;
+    if (!l.few)
+        if (int rc = ss::launch(ce_gather_kernel, T > 0 ? (T + kGatherRows - 1) / kGatherRows : 1, kGatherThreads, 0, 0,
+                                false, st, ga))
+            return rc;
 
     const uint16_t* w = static_cast<const uint16_t*>(a->weight);
     int64_t ldw = a->weight_stride;
     if (stage) {
         uint16_t* staged = reinterpret_cast<uint16_t*>(ws + l.w);
         const int64_t per = kThreads / 32;
-        if (int rc = launch(ce_stage_kernel, (V + per - 1) / per, kThreads, 0, st, w, ldw, V, D, l.Dp, staged)) return rc;
+        if (int rc = ss::launch(ce_stage_kernel, (V + per - 1) / per, kThreads, 0, 0, !l.few, st, w, ldw, V, D, l.Dp, staged))
+            return rc;
         w = staged;
         ldw = l.Dp;
     }
@@ -1076,9 +1095,9 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
         if (int rc = make_map(&h_k, h, l.rows, D, l.Dp, kHalf)) return rc;
         if (int rc = make_map(&w_k, w, V, D, ldw, kHalf)) return rc;
         if (l.few) {
-            const int rc = T == 1   ? launch_few<1>(g, h, l.Dp, w, ldw, stage, l.slices, st)
-                           : T == 2 ? launch_few<2>(g, h, l.Dp, w, ldw, stage, l.slices, st)
-                                    : launch_few<kFewTokens>(g, h, l.Dp, w, ldw, stage, l.slices, st);
+            const int rc = T == 1   ? launch_few<1>(ga, w, ldw, stage, l.slices, l.rows, g.stats, st)
+                           : T == 2 ? launch_few<2>(ga, w, ldw, stage, l.slices, l.rows, g.stats, st)
+                                    : launch_few<kFewTokens>(ga, w, ldw, stage, l.slices, l.rows, g.stats, st);
             if (rc) return rc;
         } else {
             Maps maps;
@@ -1092,9 +1111,10 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
             if (int rc = launch_gemm(maps, g, m_tiles * l.n_tiles, st)) return rc;
         }
     }
-    if (int rc = launch(ce_loss_kernel, T > 0 ? up(T, grad ? kBlockK : kLossRows) / kLossRows : 1, kLossThreads, 0, st, header, g.stats,
+    const int64_t loss_blocks = T > 0 ? up(T, grad ? kBlockK : kLossRows) / kLossRows : 1;
+    if (int rc = launch(ce_loss_kernel, loss_blocks, kLossThreads, 0, st, header, g.stats,
                         (int)l.slices, (int)l.rows, target_logit, row, row_loss, a->token_loss_out, partials, mean,
-                        a->loss_out, grad ? h : nullptr, (int)l.Dp))
+                        a->loss_out, grad && T > 0 ? h : nullptr, (int)l.Dp))
         return rc;
     if (!grad) return SS_OK;
     if (T == 0) {
@@ -1180,6 +1200,9 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
             tiles += list[k].tiles;
         }
         g.count = n;
+        g.partials = i == 0 ? partials : nullptr;
+        g.n_partials = (int)loss_blocks;
+        g.mean = mean;
         if (tiles > INT32_MAX - 1024) return SS_EOVERFLOW;
         if (int rc = launch_gemm(maps, g, tiles, st)) return rc;
         if (head.part) {
