@@ -187,7 +187,7 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& g, int live, int id) {
     return t;
 }
 
-constexpr int kQueue = 4;  // tiles handed out ahead
+constexpr int kQueue = 4;   // tiles handed out ahead
 
 // One persistent CTA pair takes output tiles of 256 x 256, its first CTA the
 // upper 128 rows.  Warp 0 loads (one thread), warp 1 of the first CTA issues the
