@@ -600,12 +600,41 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherA
 __global__ void __launch_bounds__(kThreads)
 ce_stage_kernel(const uint16_t* __restrict__ w, int64_t ld, int V, int D, int Dp, uint16_t* __restrict__ out) {
     launch_after();
+    const int lane = threadIdx.x & 31;
     const int64_t v = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (v < V) {
+    if (v < V) {  // a lane's aligned 16 bytes and its neighbour's make its vector
         const uint16_t* src = w + v * ld;
+        const int sh = (int)(reinterpret_cast<uintptr_t>(src) & 15u);
+        const unsigned char* base = reinterpret_cast<const unsigned char*>(src) - sh;
+        const int blocks = (sh + 2 * D + 15) / 16, vecs = Dp / 8;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
         uint4* dst = reinterpret_cast<uint4*>(out + v * Dp);
-#pragma unroll 4
-        for (int j = threadIdx.x & 31; j < Dp / 8; j += 32) dst[j] = row_vec(src, j, D);
+        for (int j0 = lane; j0 < vecs + lane; j0 += 128) {  // four loads of a lane before the first is used
+            uint4 x[4], e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = j0 + 32 * i;
+                x[i] = j < blocks ? ss::ld_stream_u4(base + 16 * j) : zero;
+                e[i] = lane == 31 && j + 1 < blocks ? ss::ld_stream_u4(base + 16 * (j + 1)) : zero;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = j0 + 32 * i;
+                uint4 y;
+                y.x = __shfl_down_sync(0xFFFFFFFFu, x[i].x, 1), y.y = __shfl_down_sync(0xFFFFFFFFu, x[i].y, 1);
+                y.z = __shfl_down_sync(0xFFFFFFFFu, x[i].z, 1), y.w = __shfl_down_sync(0xFFFFFFFFu, x[i].w, 1);
+                if (lane == 31) y = e[i];
+                uint4 r = sh ? ss::realign16(x[i], y, sh) : x[i];
+                if (8 * j + 8 > D) {  // zeros past the row's end
+                    uint32_t q[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (8 * j + k >= D) q[k >> 1] &= (k & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+                    r = make_uint4(q[0], q[1], q[2], q[3]);
+                }
+                if (j < vecs) dst[j] = r;
+            }
+        }
     }
     wait_before();
 }
@@ -615,12 +644,15 @@ ce_stage_kernel(const uint16_t* __restrict__ w, int64_t ld, int V, int D, int Dp
 // ---------------------------------------------------------------------------
 
 // With a handful of tokens the weight's one read is all the time there is: dot
-// products on the CUDA cores, 4 weight rows of a warp at a time (16 loads in flight
+// products on the CUDA cores, 2 weight rows of a warp at a time (8 loads in flight
 // a lane), against the tokens in shared memory.
+// Against the tile kernel, with vocabulary and hidden size 32000 x 2048, 32000 x 4096
+// and 5000 x 512: 1 or 2 tokens 31-33, 51-54 and 14 us (45, 70, 17), 3 or 4 tokens 43,
+// 73 and 14; from 5 on the tiles win.
 constexpr int kFewTokens = 4;
-constexpr int kFewRows = 4;
+constexpr int kFewRows = 2;
 constexpr int kFewSmem = 64 * 1024;  // of hidden states
-constexpr int kFewSlices = 1024;     // CTAs at most, each a slice of statistics
+constexpr int kFewCtas = 4;             // per SM at most, each a slice of statistics
 
 // Statistics as the tile kernel leaves them, one slice per CTA: CTA b's warps
 // take groups of kFewRows rows, b's after those of the CTA before.  The CTAs pick
@@ -701,6 +733,9 @@ ce_few_kernel(const GatherArgs a, const uint16_t* __restrict__ w, int64_t ldw, i
             }
         }
         __syncwarp();
+        const int next = g + slices * (kThreads / 32);  // its loads go out before this group's sums
+        loaded = next < groups && lane < vecs;
+        if (loaded) load(next, lane);
 #pragma unroll
         for (int t = 0; t < TOKENS; ++t) {
             float l[kFewRows], m = -INFINITY;
@@ -895,7 +930,7 @@ Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int p
     l.n_tiles = up(V, kTile) / kTile;
     l.few = T > 0 && T <= kFewTokens && kFewTokens * l.Dp * 2 <= kFewSmem;
     const int64_t few_ctas = (V + kFewRows * (kThreads / 32) - 1) / (kFewRows * (kThreads / 32));
-    l.slices = !l.few ? 2 * l.n_tiles : few_ctas < kFewSlices ? few_ctas : kFewSlices;
+    l.slices = !l.few ? 2 * l.n_tiles : few_ctas < 2 * pairs * kFewCtas ? few_ctas : 2 * pairs * kFewCtas;
     int64_t at = 256;  // the header
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
