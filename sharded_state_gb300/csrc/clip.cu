@@ -277,7 +277,7 @@ list_scale_kernel(const __grid_constant__ ListTab tab, int rounds, const float* 
     } else {
         c = norm[1];
     }
-    const int tile = blockIdx.x;
+    const int tile = gridDim.x - 1 - blockIdx.x;  // what pass 1 read last is in L2 still
     const int k = find_tensor(tab.first, tab.count, tile);
     const unsigned char* in = tab.in[k];
     unsigned char* out = tab.out[k];

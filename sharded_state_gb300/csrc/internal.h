@@ -120,6 +120,12 @@ inline int check_device(const ss_plan* p) {
     return dev == p->device ? SS_OK : SS_EINVAL;
 }
 
+// The one-launch form of ss_linear_cross_entropy with gradients (arguments already
+// checked), and the sizes that it takes: up to kSmallWork products T * D * V.
+constexpr int64_t kSmallWork = 1 << 20;
+bool linear_ce_fits_small(int64_t T, int64_t D, int64_t V);
+int linear_ce_small(const ss_linear_ce* a, cudaStream_t st);
+
 // Element range [lo, hi) of the packed buffers covered by `group` (-1 = all).
 inline bool group_range(const ss_plan* p, int group, int64_t* lo, int64_t* hi) {
     if (group < 0) {

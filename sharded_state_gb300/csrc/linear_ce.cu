@@ -1082,6 +1082,7 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
     if (a->workspace_bytes < (size_t)l.bytes) return SS_EINVAL;
 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (grad && ss::linear_ce_fits_small(T, D, V)) return ss::linear_ce_small(a, st);
     unsigned char* ws = static_cast<unsigned char*>(a->workspace);
     Header* header = reinterpret_cast<Header*>(ws);
     int* row = reinterpret_cast<int*>(ws + l.row);
