@@ -399,28 +399,25 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
                     }
                 }
             } else {
-                // 32 x 32 values at a time through shared memory (16-byte groups of row r at
-                // group ^ (r & 7), free of bank conflicts both ways), so that a row's go out together
+                // through shared memory (16-byte groups of row r at group ^ (r & 7), free of bank
+                // conflicts both ways), so that a row's values go out together
                 const int limit = x.product == kHidden ? live : x.m_rows;
                 const int* token = x.product == kHidden ? g.token : nullptr;
                 float* mine = turn[warp - 4];
                 const bool wide = (reinterpret_cast<uintptr_t>(x.out) & 7u) == 0 && (x.out_ld & 3) == 0;
-                for (int c = 0; c < kColumns && col0 + c < x.cols; c += 32) {
-                    float v32[32];
-                    __syncwarp();
-                    tc::tmem_ld32(d + c, v32);
-                    if (t.kb == t.ke) {
+                if (x.part || wide) {  // 32 columns at a time: 8 lanes a row, 4 columns a lane
+                    const int k = lane & 7;
+                    for (int c = 0; c < kColumns && col0 + c < x.cols; c += 32) {
+                        float v32[32];
+                        __syncwarp();
+                        tc::tmem_ld32(d + c, v32);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v32[i] = 0.f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<float4*>(mine + lane * 32 + 4 * (i ^ (lane & 7))) =
-                            make_float4(v32[4 * i], v32[4 * i + 1], v32[4 * i + 2], v32[4 * i + 3]);
-                    __syncwarp();
-                    const int col = col0 + c, left = x.cols - col;
-                    if (x.part || wide) {  // 8 lanes a row, 4 columns a lane
-                        const int k = lane & 7;
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<float4*>(mine + lane * 32 + 4 * (i ^ (lane & 7))) =
+                                t.kb == t.ke ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                             : make_float4(v32[4 * i], v32[4 * i + 1], v32[4 * i + 2], v32[4 * i + 3]);
+                        __syncwarp();
+                        const int col = col0 + c, left = x.cols - col;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int r = 4 * i + (lane >> 3);
@@ -447,12 +444,43 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
                                 }
                             }
                         }
-                    } else {  // a row at a time, a column a lane
-                        for (int r = 0; r < 32 && row0 + r < limit; ++r) {
+                    }
+                } else {  // rows at any element offset, 64 columns at a time: a row's words, one a lane
+                    uint32_t* words = reinterpret_cast<uint32_t*>(mine);
+                    for (int c = 0; c < kColumns && col0 + c < x.cols; c += 64) {
+                        __syncwarp();
+                        for (int h = 0; h < 2; ++h) {
+                            float v[32];
+                            tc::tmem_ld32(d + c + 32 * h, v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = t.kb == t.ke ? 0.f : scale * v[i];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<uint4*>(words + lane * 32 + 4 * ((4 * h + i) ^ (lane & 7))) =
+                                    make_uint4(ss::pack_bf16x2(v[8 * i], v[8 * i + 1]),
+                                               ss::pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                               ss::pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                                               ss::pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+                        }
+                        __syncwarp();
+                        const int col = col0 + c, left = x.cols - col;
+                        const int here = limit - row0 < 32 ? limit - row0 : 32;
+#pragma unroll 4
+                        for (int r = 0; r < here; ++r) {
                             const int64_t orow = token ? token[row0 + r] : (int64_t)x.v0 + row0 + r;
-                            if (lane < left)
-                                x.out[orow * x.out_ld + col + lane] =
-                                    ss::f32_to_bf16(scale * mine[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)]);
+                            uint16_t* o = x.out + orow * x.out_ld + col;
+                            const uint32_t w = words[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)];
+                            const int odd = (int)(reinterpret_cast<uintptr_t>(o) >> 1) & 1;
+                            // from an odd place the words are a column on: this one's upper half and
+                            // the next one's lower, and the first column goes by itself
+                            const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w, 1);
+                            const uint32_t u = odd ? __byte_perm(w, next, 0x5432) : w;
+                            const int at = 2 * lane + odd;
+                            if (at + 1 < left && at < 63)
+                                *reinterpret_cast<uint32_t*>(o + at) = u;
+                            else if (at < left)
+                                o[at] = (uint16_t)u;
+                            if (odd && lane == 0) o[0] = (uint16_t)w;
                         }
                     }
                 }
