@@ -953,7 +953,7 @@ constexpr int64_t kPieceBytes = 256ll << 20;  // of P, one buffer of two
 Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int pairs) {
     Layout l = {};
     l.T = T, l.D = D, l.V = V, l.grad = grad, l.stage = stage;
-    l.Dp = up(D, 8);
+    l.Dp = up(D, 16);  // rows on 32-byte sectors
     l.rows = up(T, kTile);
     l.n_tiles = up(V, kTile) / kTile;
     l.few = T > 0 && T <= kFewTokens && kFewTokens * l.Dp * 2 <= kFewSmem;
