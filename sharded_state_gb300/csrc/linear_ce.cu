@@ -246,7 +246,7 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
     auto take_tile = [&](int j) {
         const int slot = j % kQueue;
         Tile t;
-        ok = tc::mbar_wait(queue_full + 8 * slot, (j / kQueue) & 1);
+        ok = tc::mbar_wait<true>(queue_full + 8 * slot, (j / kQueue) & 1);
         const int4 x = *reinterpret_cast<const int4*>(queue + slot);
         const int2 y = *reinterpret_cast<const int2*>(&queue[slot].kb);
         t.w = x.x, t.m = x.y, t.n = x.z, t.s = x.w, t.kb = y.x, t.ke = y.y;
@@ -324,7 +324,7 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
     } else if (warp == 3 && lane == 0 && rank == 0) {
         for (int j = 0;; ++j) {
             const int slot = j % kQueue;
-            ok = tc::mbar_wait(queue_empty + 8 * slot, ((j / kQueue) & 1) ^ 1);
+            ok = tc::mbar_wait<true>(queue_empty + 8 * slot, ((j / kQueue) & 1) ^ 1);
             if (!ok) break;
             const Tile t = find_tile(g, live, j == 0 ? first : pairs + atomicAdd(g.next, 1));
             for (uint32_t r = 0; r < 2; ++r) {
@@ -906,6 +906,7 @@ ce_join_kernel(const Header* __restrict__ header, const float* part, int splits,
     if (row >= limit) return;
     const float* p = part + row * part_ld + col;
     float4 s = *reinterpret_cast<const float4*>(p);
+#pragma unroll 8
     for (int k = 1; k < splits; ++k) {
         const float4 x = *reinterpret_cast<const float4*>(p + k * part_split);
         s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
