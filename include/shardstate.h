@@ -15,7 +15,10 @@
  *   3. an all-gather returns the full parameters, read back out per
  *      parameter (fsdp_all_gather_unpack).
  * DDP's bucketed gradient all-reduce sits beside it
- * (ddp_bucket_pack_average).
+ * (ddp_bucket_pack_average), and so do the loss at the head of the model
+ * (ss_linear_cross_entropy) and the global gradient norm with clipping
+ * (ss_clip_grads; fsdp_reduce_scatter_norm and fsdp_clip_adamw for the
+ * sharded step).
  *
  * Conventions for every call:
  *   - Status: 0 (SS_OK) or a negative SS_E* code; ss_strerror() names it.
@@ -34,7 +37,8 @@
  *     arrays of device pointers; they are read during the call and may be
  *     reused as soon as it returns.
  *   - The arithmetic never traps: no device-side assert, no trap, and no
- *     kernel waits on another.
+ *     kernel waits on another.  Waits inside a kernel (for copies, products and
+ *     the other CTAs of a cluster) are bounded or end with the CTAs themselves.
  *
  * Element types: elem_bytes 2 = bf16 (gradients, parameters, shards),
  * elem_bytes 4 = fp32.  Optimizer state is always fp32.
@@ -498,7 +502,8 @@ int ss_linear_cross_entropy(const ss_linear_ce* args, ss_stream_t stream);
  *   norm_out[1] = 1
  * Squares and partial sums are fp32, their sum over the CTAs fp64 in a fixed
  * order: the same inputs give the same bits.  NaN and infinities come through
- * (a square passes fp32 from |x| = 1.8e19 on); an empty list has norm 0.
+ * (a square passes fp32 from |x| = 1.8e19 on, and vanishes below 2.6e-23); an
+ * empty list has norm 0.
  *   numels      HOST array [num_tensors], each >= 0.
  *   elem_bytes  HOST array [num_tensors]: 2 (bf16) or 4 (fp32), in any mixture.
  *   grads       HOST array [num_tensors] of device pointers to contiguous
@@ -551,7 +556,7 @@ int fsdp_reduce_scatter_norm(const ss_plan* plan, const void* const* rank_grads,
  *   g = c * reduced_grad[f], then AdamW exactly as fsdp_reduce_scatter_adamw
  * With c = 1 the state and shards are bit for bit what fsdp_reduce_scatter_adamw
  * gives.
- *   sq_sums       device, num_sums doubles, summed in order: the sq_out of
+ *   sq_sums       device, num_sums doubles, summed in a fixed order: the sq_out of
  *                 every group (and of other plans whose gradients the norm
  *                 spans).
  *   max_norm      >= 0; +infinity never clips.

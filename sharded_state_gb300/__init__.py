@@ -489,24 +489,23 @@ def _nbytes(t) -> int:
     return int(t.numel()) * int(t.element_size())
 
 
-def _want(fn: str, t, dtype, what: str, numel: Optional[int] = None) -> None:
-    """The binding knows a tensor's type and size, which the C ABI cannot check."""
-    if t.dtype != dtype or not t.is_contiguous() or (numel is not None and t.numel() < numel):
-        raise ShardStateError(fn, SS_EINVAL, f"{what}: contiguous {dtype}"
-                              + (f", at least {numel} elements" if numel is not None else ""))
+def _want(fn: str, t, dtype, what: str, numel: int = 0) -> None:
+    """The binding knows a tensor's place, type and size, which the C ABI cannot check."""
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or t.numel() < numel:
+        raise ShardStateError(fn, SS_EINVAL, f"{what}: contiguous {dtype} on the GPU, at least {numel} elements")
 
 
 def _grad_list(fn: str, grads: Sequence, out: Optional[Sequence]):
     """numels, element sizes and pointers of a list of contiguous bf16 / fp32 tensors."""
     import torch
     for k, g in enumerate(grads):
-        if g.dtype not in (torch.bfloat16, torch.float32) or not g.is_contiguous():
-            raise ShardStateError(fn, SS_EINVAL, f"tensor {k}: contiguous bf16 or fp32 is wanted")
+        if not g.is_cuda or g.dtype not in (torch.bfloat16, torch.float32) or not g.is_contiguous():
+            raise ShardStateError(fn, SS_EINVAL, f"tensor {k}: contiguous bf16 or fp32 on the GPU is wanted")
     if out is not None:
         if len(out) != len(grads):
             raise ShardStateError(fn, SS_EINVAL, "out: one tensor for each gradient is wanted")
         for k, (g, o) in enumerate(zip(grads, out)):
-            if o.dtype != g.dtype or o.numel() != g.numel() or not o.is_contiguous():
+            if not o.is_cuda or o.dtype != g.dtype or o.numel() != g.numel() or not o.is_contiguous():
                 raise ShardStateError(fn, SS_EINVAL, f"out {k}: its gradient's type and size are wanted")
     eb = (ctypes.c_int * max(1, len(grads)))(*[g.element_size() for g in grads])
     return (len(grads), _i64_array([g.numel() for g in grads]), eb, _ptr_array(grads),
@@ -517,6 +516,7 @@ def ss_grad_norm(grads: Sequence, norm_out, workspace, stream=None) -> None:
     """norm_out (2 floats on the device) = {global norm of the tensors, 1}."""
     import torch
     _want("ss_grad_norm", norm_out, torch.float32, "norm_out", 2)
+    _want("ss_grad_norm", workspace, workspace.dtype, "workspace")
     n, numels, eb, ptrs, _ = _grad_list("ss_grad_norm", grads, None)
     _check("ss_grad_norm", _lib.ss_grad_norm(n, numels, eb, ptrs, _addr(norm_out), _addr(workspace),
                                              _nbytes(workspace), _stream(stream)))
@@ -539,6 +539,7 @@ class GradClip:
                  out: Optional[Sequence] = None, stream=None):
         import torch
         _want("ss_clip_grads", norm_out, torch.float32, "norm_out", 2)
+        _want("ss_clip_grads", workspace, workspace.dtype, "workspace")
         n, numels, eb, ptrs, outs = _grad_list("ss_clip_grads", grads, out)
         self._args = (n, numels, eb, ptrs, outs, ctypes.c_double(max_norm),
                       ctypes.c_void_p(_addr(norm_out)), ctypes.c_void_p(_addr(workspace)),
@@ -559,6 +560,7 @@ def fsdp_reduce_scatter_norm(plan: Plan, rank_grads: Sequence, reduced_grad, sq_
     """reduced_grad = the ranks' mean; sq_out (1 fp64 element) = its sum of squares."""
     import torch
     _want("fsdp_reduce_scatter_norm", sq_out, torch.float64, "sq_out", 1)
+    _want("fsdp_reduce_scatter_norm", workspace, workspace.dtype, "workspace")
     _check("fsdp_reduce_scatter_norm", _lib.fsdp_reduce_scatter_norm(
         plan, _ptr_array(rank_grads), _addr(reduced_grad), _addr(sq_out), _addr(workspace),
         _nbytes(workspace), group, _stream(stream)))
@@ -599,9 +601,10 @@ def _matrix(fn: str, t, what: str, rows: int, cols: int):
     import torch
     if t is None:
         return None, 0
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or tuple(t.shape) != (rows, cols) or \
+    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 2 or tuple(t.shape) != (rows, cols) or \
             (cols > 1 and t.stride(1) != 1):
-        raise ShardStateError(fn, SS_EINVAL, f"{what}: bf16 [{rows}, {cols}] with unit column stride is wanted")
+        raise ShardStateError(fn, SS_EINVAL,
+                              f"{what}: bf16 [{rows}, {cols}] on the GPU with unit column stride is wanted")
     return _addr(t), max(int(t.stride(0)), cols) if rows <= 1 else int(t.stride(0))
 
 
@@ -623,6 +626,7 @@ def ss_linear_cross_entropy(hidden, weight, targets, loss_out, workspace, token_
         raise ShardStateError(fn, SS_EINVAL, "reduction: mean or sum")
     _want(fn, targets, torch.int64, "targets", T)
     _want(fn, loss_out, torch.float32, "loss_out", 1)
+    _want(fn, workspace, workspace.dtype, "workspace")
     if token_loss_out is not None:
         _want(fn, token_loss_out, torch.float32, "token_loss_out", T)
     h, ldh = _matrix(fn, hidden, "hidden", T, D)

@@ -157,6 +157,28 @@ def test_handle_and_stream(ss):
                 assert torch.equal(o, (t.float() * norm[1]).to(t.dtype))
 
 
+@gpu
+@pytest.mark.parametrize("name", ["tiny_mlp", "mixed", "large"])
+def test_captured(ss, name):
+    """A captured call replays on what the tensors hold by then."""
+    ts, _ = tensors(*LISTS[name])
+    outs = [torch.empty_like(t) for t in ts]
+    norm, ws = torch.empty(2, device="cuda"), workspace(ss)
+    stream = torch.cuda.Stream()
+    clip = ss.GradClip(ts, 0.1, norm, ws, out=outs, stream=stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        clip()
+    for t in ts:
+        t.mul_(2.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert abs(float(norm[0]) - norm64(ts)) <= NORM_RTOL * norm64(ts)
+    for t, o in zip(ts, outs):
+        assert torch.equal(o, (t.float() * norm[1]).to(t.dtype))
+
+
 # ---------------------------------------------------------------------------
 # the sharded step
 # ---------------------------------------------------------------------------
@@ -317,20 +339,21 @@ def status(ss, call):
 def test_refusals(ss):
     ts, _ = tensors([100], [BF], [0])
     norm, ws = torch.empty(2, device="cuda"), workspace(ss)
-    odd = torch.empty(101, dtype=torch.uint8, device="cuda")
-    launched = ss.ss_launch_count()
     for bad in (-1.0, math.nan):
         assert status(ss, lambda: ss.ss_clip_grads(ts, bad, norm, ws)) == ss.SS_EINVAL
     assert status(ss, lambda: ss.ss_clip_grads(ts, 1.0, norm, ws[:1024])) == ss.SS_EINVAL
     assert status(ss, lambda: ss.ss_clip_grads(ts, 1.0, norm[:1], ws)) == ss.SS_EINVAL
     assert status(ss, lambda: ss.ss_clip_grads([ts[0].half()], 1.0, norm, ws)) == ss.SS_EINVAL
+    assert status(ss, lambda: ss.ss_clip_grads([ts[0].cpu()], 1.0, norm, ws)) == ss.SS_EINVAL
+    assert status(ss, lambda: ss.ss_clip_grads(ts, 1.0, norm.cpu(), ws)) == ss.SS_EINVAL
+    assert status(ss, lambda: ss.ss_grad_norm(ts, norm, ws.cpu())) == ss.SS_EINVAL
     assert status(ss, lambda: ss.ss_clip_grads([ts[0][::2]], 1.0, norm, ws)) == ss.SS_EINVAL
     assert status(ss, lambda: ss.ss_clip_grads(ts, 1.0, norm, ws, out=[])) == ss.SS_EINVAL
     assert status(ss, lambda: ss.ss_clip_grads(ts, 1.0, norm, ws, out=[ts[0].float()])) == ss.SS_EINVAL
     big = torch.empty(ss.SS_NORM_WORKSPACE_BYTES + 16, dtype=torch.uint8, device="cuda")
     assert status(ss, lambda: ss.ss_grad_norm(ts, norm, big[8:])) == ss.SS_EALIGN
     s = Sharded(ss, "tiny")
-    launched = ss.ss_launch_count()
+    launched = ss.ss_launch_count()  # of refused calls: none
     red, sq = torch.empty(s.total + 4, device="cuda"), torch.empty(1, dtype=torch.float64, device="cuda")
     rs = lambda **k: ss.fsdp_reduce_scatter_norm(**{**dict(plan=s.plan, rank_grads=s.grads, reduced_grad=red,
                                                            sq_out=sq, workspace=ws), **k})
@@ -352,7 +375,6 @@ def test_refusals(ss):
     assert status(ss, lambda: ca(group=7)) == ss.SS_EINVAL
     assert status(ss, lambda: ca(sq_sums=sq[:0])) == ss.SS_EINVAL
     assert ss.ss_launch_count() == launched
-    del odd
 
 
 def test_refusals_on_the_host(ss):

@@ -211,6 +211,26 @@ def test_same_bits_twice_and_on_another_stream(ss):
 
 
 @gpu
+@pytest.mark.parametrize("T,V,D", [(3, 700, 72), (50, 128, 64), (300, 700, 100)])
+def test_captured(ss, T, V, D):
+    """A captured call (of each form) replays on what the inputs hold by then."""
+    c, other = Case(T, V, D, seed=1), Case(T, V, D, seed=2, mask="random")
+    c.run(ss)
+    stream = torch.cuda.Stream()
+    ws = torch.empty(ss.ss_linear_ce_workspace(T, D, V, True, stage_weight=True), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        ss.ss_linear_cross_entropy(c.h, c.w, c.y, c.loss, ws, token_loss_out=c.token_loss, d_hidden=c.dh,
+                                   d_weight=c.dw, stream=stream)
+    for a, b in ((c.h, other.h), (c.w, other.w), (c.y, other.y)):
+        a.copy_(b)
+    graph.replay()
+    torch.cuda.synchronize()
+    c.check()
+
+
+@gpu
 def test_workspace_used_again(ss):
     """Another call's leftovers in the workspace change nothing."""
     big, small = Case(600, 2000, 136, seed=1), Case(90, 700, 100, mask="random", seed=2)
@@ -332,10 +352,11 @@ def test_refusals_on_the_host(ss):
 @gpu
 def test_refusals_of_the_binding(ss):
     c = Case(10, 20, 16)
-    launched = ss.ss_launch_count()
+    launched = ss.ss_launch_count()  # of refused calls: none
     loss = torch.empty(1, device="cuda")
     ws = torch.empty(ss.ss_linear_ce_workspace(10, 16, 20, True), dtype=torch.uint8, device="cuda")
-    for kw in (dict(hidden=c.h.float()), dict(hidden=c.h[0]), dict(weight=c.w.t()), dict(targets=c.y.int()),
+    for kw in (dict(hidden=c.h.cpu()), dict(targets=c.y.cpu()), dict(loss_out=loss.cpu()), dict(workspace=ws.cpu()),
+               dict(hidden=c.h.float()), dict(hidden=c.h[0]), dict(weight=c.w.t()), dict(targets=c.y.int()),
                dict(targets=c.y[:9]), dict(loss_out=loss.double()), dict(reduction="none"), dict(d_hidden=c.w),
                dict(d_weight=c.h), dict(token_loss_out=torch.empty(9, device="cuda")), dict(workspace=ws[:256])):
         with pytest.raises(ss.ShardStateError) as e:
