@@ -210,11 +210,18 @@ def _current_stream() -> int:
     """The current stream's handle.  torch's own accessor of the raw handle, where it
     has one, costs a sixth of building a Stream object (0.5 against 2.9 us on a Grace
     core), which shows beside launches of a few microseconds."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
-        return int(torch.cuda.current_stream().cuda_stream)
-    return int(raw(torch.cuda.current_device()))
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        if raw is None or device is None:
+            return int(torch.cuda.current_stream().cuda_stream)
+        torch.cuda.init()
+        _raw_stream = lambda: raw(device())
+    return _raw_stream()
+
+
+_raw_stream = None
 
 
 def _i64_array(xs: Sequence[int]):
@@ -485,21 +492,35 @@ def ddp_bucket_assign(numels: Sequence[int], elem_bytes: int, bucket_cap_bytes: 
 # gradient norm and clipping
 # ---------------------------------------------------------------------------
 
-def _nbytes(t) -> int:
-    return int(t.numel()) * int(t.element_size())
-
-
-def _want(fn: str, t, dtype, what: str, numel: int = 0) -> None:
-    """The binding knows a tensor's place, type and size, which the C ABI cannot check."""
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or t.numel() < numel:
+def _want(fn: str, t, dtype: str, what: str, numel: int = 0) -> int:
+    """Address of a tensor whose place, type and size the C ABI cannot check."""
+    if not t.is_cuda or t.dtype != _dtype(dtype) or not t.is_contiguous() or t.numel() < numel:
         raise ShardStateError(fn, SS_EINVAL, f"{what}: contiguous {dtype} on the GPU, at least {numel} elements")
+    return t.data_ptr()
+
+
+def _workspace(fn: str, t):
+    """Address and bytes of a workspace tensor of any type."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ShardStateError(fn, SS_EINVAL, "workspace: a contiguous tensor on the GPU")
+    return t.data_ptr(), t.nbytes
+
+
+_dtypes = {}
+
+
+def _dtype(name: str):
+    if name not in _dtypes:
+        import torch
+        _dtypes[name] = getattr(torch, name)
+    return _dtypes[name]
 
 
 def _grad_list(fn: str, grads: Sequence, out: Optional[Sequence]):
     """numels, element sizes and pointers of a list of contiguous bf16 / fp32 tensors."""
-    import torch
+    kinds = (_dtype("bfloat16"), _dtype("float32"))
     for k, g in enumerate(grads):
-        if not g.is_cuda or g.dtype not in (torch.bfloat16, torch.float32) or not g.is_contiguous():
+        if not g.is_cuda or g.dtype not in kinds or not g.is_contiguous():
             raise ShardStateError(fn, SS_EINVAL, f"tensor {k}: contiguous bf16 or fp32 on the GPU is wanted")
     if out is not None:
         if len(out) != len(grads):
@@ -514,12 +535,11 @@ def _grad_list(fn: str, grads: Sequence, out: Optional[Sequence]):
 
 def ss_grad_norm(grads: Sequence, norm_out, workspace, stream=None) -> None:
     """norm_out (2 floats on the device) = {global norm of the tensors, 1}."""
-    import torch
-    _want("ss_grad_norm", norm_out, torch.float32, "norm_out", 2)
-    _want("ss_grad_norm", workspace, workspace.dtype, "workspace")
-    n, numels, eb, ptrs, _ = _grad_list("ss_grad_norm", grads, None)
-    _check("ss_grad_norm", _lib.ss_grad_norm(n, numels, eb, ptrs, _addr(norm_out), _addr(workspace),
-                                             _nbytes(workspace), _stream(stream)))
+    fn = "ss_grad_norm"
+    norm = _want(fn, norm_out, "float32", "norm_out", 2)
+    ws, nbytes = _workspace(fn, workspace)
+    n, numels, eb, ptrs, _ = _grad_list(fn, grads, None)
+    _check(fn, _lib.ss_grad_norm(n, numels, eb, ptrs, norm, ws, nbytes, _stream(stream)))
 
 
 def ss_clip_grads(grads: Sequence, max_norm: float, norm_out, workspace, out: Optional[Sequence] = None,
@@ -537,13 +557,12 @@ class GradClip:
 
     def __init__(self, grads: Sequence, max_norm: float, norm_out, workspace,
                  out: Optional[Sequence] = None, stream=None):
-        import torch
-        _want("ss_clip_grads", norm_out, torch.float32, "norm_out", 2)
-        _want("ss_clip_grads", workspace, workspace.dtype, "workspace")
-        n, numels, eb, ptrs, outs = _grad_list("ss_clip_grads", grads, out)
-        self._args = (n, numels, eb, ptrs, outs, ctypes.c_double(max_norm),
-                      ctypes.c_void_p(_addr(norm_out)), ctypes.c_void_p(_addr(workspace)),
-                      ctypes.c_size_t(_nbytes(workspace)))
+        fn = "ss_clip_grads"
+        norm = _want(fn, norm_out, "float32", "norm_out", 2)
+        ws, nbytes = _workspace(fn, workspace)
+        n, numels, eb, ptrs, outs = _grad_list(fn, grads, out)
+        self._args = (n, numels, eb, ptrs, outs, ctypes.c_double(max_norm), ctypes.c_void_p(norm),
+                      ctypes.c_void_p(ws), ctypes.c_size_t(nbytes))
         self._keep = (norm_out, workspace)
         self._stream = None if stream is None else _stream(stream)
         self._fn = _lib.ss_clip_grads
@@ -558,12 +577,11 @@ class GradClip:
 def fsdp_reduce_scatter_norm(plan: Plan, rank_grads: Sequence, reduced_grad, sq_out, workspace,
                              group: int = -1, stream=None) -> None:
     """reduced_grad = the ranks' mean; sq_out (1 fp64 element) = its sum of squares."""
-    import torch
-    _want("fsdp_reduce_scatter_norm", sq_out, torch.float64, "sq_out", 1)
-    _want("fsdp_reduce_scatter_norm", workspace, workspace.dtype, "workspace")
-    _check("fsdp_reduce_scatter_norm", _lib.fsdp_reduce_scatter_norm(
-        plan, _ptr_array(rank_grads), _addr(reduced_grad), _addr(sq_out), _addr(workspace),
-        _nbytes(workspace), group, _stream(stream)))
+    fn = "fsdp_reduce_scatter_norm"
+    sq = _want(fn, sq_out, "float64", "sq_out", 1)
+    ws, nbytes = _workspace(fn, workspace)
+    _check(fn, _lib.fsdp_reduce_scatter_norm(plan, _ptr_array(rank_grads), _addr(reduced_grad), sq, ws, nbytes,
+                                             group, _stream(stream)))
 
 
 def fsdp_clip_adamw(plan: Plan, reduced_grad, sq_sums, max_norm: float, master, exp_avg, exp_avg_sq,
@@ -571,13 +589,12 @@ def fsdp_clip_adamw(plan: Plan, reduced_grad, sq_sums, max_norm: float, master, 
     """AdamW on reduced_grad scaled by min(1, max_norm / (norm + 1e-6)), the norm
     being the root of the sum of sq_sums (fp64, one element per
     fsdp_reduce_scatter_norm call the norm spans); norm_out = {norm, factor}."""
-    import torch
-    _want("fsdp_clip_adamw", sq_sums, torch.float64, "sq_sums", 1)
-    _want("fsdp_clip_adamw", norm_out, torch.float32, "norm_out", 2)
-    _check("fsdp_clip_adamw", _lib.fsdp_clip_adamw(
-        plan, _addr(reduced_grad), _addr(sq_sums), int(sq_sums.numel()), max_norm, _addr(master),
-        _addr(exp_avg), _addr(exp_avg_sq), _addr(param_shards), ctypes.byref(hp), _addr(norm_out), group,
-        _stream(stream)))
+    fn = "fsdp_clip_adamw"
+    sq = _want(fn, sq_sums, "float64", "sq_sums", 1)
+    norm = _want(fn, norm_out, "float32", "norm_out", 2)
+    _check(fn, _lib.fsdp_clip_adamw(plan, _addr(reduced_grad), sq, sq_sums.numel(), max_norm, _addr(master),
+                                    _addr(exp_avg), _addr(exp_avg_sq), _addr(param_shards), ctypes.byref(hp), norm,
+                                    group, _stream(stream)))
 
 
 # ---------------------------------------------------------------------------
@@ -598,14 +615,13 @@ def ss_linear_ce_workspace(num_tokens: int, hidden_size: int, vocab_size: int, g
 
 def _matrix(fn: str, t, what: str, rows: int, cols: int):
     """Address and row stride of a bf16 matrix (NULL, 0 for None)."""
-    import torch
     if t is None:
         return None, 0
-    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 2 or tuple(t.shape) != (rows, cols) or \
-            (cols > 1 and t.stride(1) != 1):
+    if not t.is_cuda or t.dtype != _dtype("bfloat16") or t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1):
         raise ShardStateError(fn, SS_EINVAL,
                               f"{what}: bf16 [{rows}, {cols}] on the GPU with unit column stride is wanted")
-    return _addr(t), max(int(t.stride(0)), cols) if rows <= 1 else int(t.stride(0))
+    stride = t.stride(0)
+    return t.data_ptr(), stride if rows > 1 or stride > cols else cols
 
 
 def ss_linear_cross_entropy(hidden, weight, targets, loss_out, workspace, token_loss_out=None, d_hidden=None,
@@ -616,7 +632,6 @@ def ss_linear_cross_entropy(hidden, weight, targets, loss_out, workspace, token_
     int64 -> loss_out (1 float; "mean" or "sum" over the targets that are not
     ignore_index), token_loss_out [T], and grad_scale times the gradients in
     d_hidden [T, D] and d_weight [V, D]; the last three are optional."""
-    import torch
     fn = "ss_linear_cross_entropy"
     if hidden.dim() != 2 or weight.dim() != 2:
         raise ShardStateError(fn, SS_EINVAL, "hidden and weight: matrices are wanted")
@@ -624,16 +639,15 @@ def ss_linear_cross_entropy(hidden, weight, targets, loss_out, workspace, token_
     V = weight.shape[0]
     if reduction not in ("mean", "sum"):
         raise ShardStateError(fn, SS_EINVAL, "reduction: mean or sum")
-    _want(fn, targets, torch.int64, "targets", T)
-    _want(fn, loss_out, torch.float32, "loss_out", 1)
-    _want(fn, workspace, workspace.dtype, "workspace")
-    if token_loss_out is not None:
-        _want(fn, token_loss_out, torch.float32, "token_loss_out", T)
+    y = _want(fn, targets, "int64", "targets", T)
+    loss = _want(fn, loss_out, "float32", "loss_out", 1)
+    ws, nbytes = _workspace(fn, workspace)
+    token_loss = None if token_loss_out is None else _want(fn, token_loss_out, "float32", "token_loss_out", T)
     h, ldh = _matrix(fn, hidden, "hidden", T, D)
     w, ldw = _matrix(fn, weight, "weight", V, D)
     dh, ld_dh = _matrix(fn, d_hidden, "d_hidden", T, D)
     dw, ld_dw = _matrix(fn, d_weight, "d_weight", V, D)
-    args = _LinearCE(T, D, V, h, ldh, w, ldw, _addr(targets), ignore_index,
-                     SS_LOSS_MEAN if reduction == "mean" else SS_LOSS_SUM, grad_scale, _addr(loss_out),
-                     _addr(token_loss_out), dh, ld_dh, dw, ld_dw, _addr(workspace), _nbytes(workspace))
+    args = _LinearCE(T, D, V, h, ldh, w, ldw, y, ignore_index,
+                     SS_LOSS_MEAN if reduction == "mean" else SS_LOSS_SUM, grad_scale, loss, token_loss, dh, ld_dh, dw,
+                     ld_dw, ws, nbytes)
     _check(fn, _lib.ss_linear_cross_entropy(ctypes.byref(args), _stream(stream)))

@@ -9,11 +9,12 @@
 
 namespace ss {
 
-// Every kernel of a call but its first is launched while the one before still
-// runs: it lets its own successor launch, sets itself up, and waits for the one
-// before to be done before it reads or writes anything.  A kernel that waited is
-// done only after all before it, so the next one's wait covers them too.  In a
-// kernel without a programmatic predecessor the wait returns at once.
+// Kernels are launched while the one before them on the stream still runs (its
+// last CTAs, where it does not say otherwise): each lets its own successor launch,
+// sets itself up, and waits for the one before to be done before it reads or
+// writes anything.  A kernel that waited is done only after all before it, so the
+// next one's wait covers them too.  Without such a predecessor the wait returns at
+// once.
 __device__ __forceinline__ void launch_after() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -42,6 +43,23 @@ int launch(void (*kernel)(P...), int64_t grid, int threads, int smem, int cluste
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    return e == cudaSuccess ? check_launch() : cuda_fail(e);
+}
+
+// Launch of `grid` CTAs that may wait for one another (all resident at once, or
+// the launch fails).
+template <class... P, class... A>
+int launch_cooperative(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t st, A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1] = {};
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }

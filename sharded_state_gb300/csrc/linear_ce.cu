@@ -24,10 +24,10 @@
 // joining tiles rounds only sums; the tokens' losses are summed in fp64.
 //
 // Forming the logits twice makes it 8TVD flops for 6TVD, and nothing of size TV is
-// kept beyond a piece.  8192 tokens, 32000 x 2048, with gradients: 2660 us back to
-// back, 1610 TFLOP/s of the 8TVD, where a bare library product of such sizes
+// kept beyond a piece.  8192 tokens, 32000 x 2048, with gradients: 2670 us back to
+// back, 1600 TFLOP/s of the 8TVD, where a bare library product of such sizes
 // sustains 1724 under the card's power limit; 4096 tokens scored at hidden size
-// 4096: 632 us, 1700 TFLOP/s.
+// 4096: 636 us, 1690 TFLOP/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -635,15 +635,18 @@ __device__ __forceinline__ void gather_block(const GatherArgs& a, int block, boo
 }
 
 __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const GatherArgs a) {
-    launch_after();
+    wait_before();
+    launch_after();  // only now: ce_stage_kernel reads and writes before its own wait
     gather_block(a, blockIdx.x, blockIdx.x == gridDim.x - 1);
 }
 
 // Rows of a weight whose rows do not start on 16-byte boundaries, copied to
-// rows that do: one warp per row.  It needs nothing of the kernel before it, and
-// only ends after it, for the kernels behind both.
+// rows that do: one warp per row.  It needs nothing of the gather, and only ends
+// after it, for the kernels behind both; as the first kernel of a call it waits at once.
 __global__ void __launch_bounds__(kThreads)
-ce_stage_kernel(const uint16_t* __restrict__ w, int64_t ld, int V, int D, int Dp, uint16_t* __restrict__ out) {
+ce_stage_kernel(const uint16_t* __restrict__ w, int64_t ld, int V, int D, int Dp, int first,
+                uint16_t* __restrict__ out) {
+    if (first) wait_before();
     launch_after();
     const int lane = threadIdx.x & 31;
     const int64_t v = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -707,12 +710,12 @@ constexpr int kFewCtas = 4;             // per SM at most, each a slice of stati
 // Statistics as the tile kernel leaves them, one slice per CTA: CTA b's warps
 // take groups of kFewRows rows, b's after those of the CTA before.  The CTAs pick
 // the tokens that count out themselves; one more CTA does the gather's work for
-// the kernels behind.  staged: the weight is a kernel's before this one.
+// the kernels behind.
 template <int TOKENS>
 __global__ void __launch_bounds__(kThreads)
-ce_few_kernel(const GatherArgs a, const uint16_t* __restrict__ w, int64_t ldw, int staged, int rows, float2* stats) {
+ce_few_kernel(const GatherArgs a, const uint16_t* __restrict__ w, int64_t ldw, int rows, float2* stats) {
     launch_after();
-    if (staged) wait_before();
+    wait_before();
     if (blockIdx.x == gridDim.x - 1) {
         gather_block(a, 0, true);
         return;
@@ -1069,12 +1072,11 @@ int allow_smem(std::atomic<uint64_t>& ready, const void* kernel, int bytes) {
 }
 
 template <int TOKENS>
-int launch_few(const GatherArgs& a, const uint16_t* w, int64_t ldw, bool staged, int64_t slices, int64_t rows,
+int launch_few(const GatherArgs& a, const uint16_t* w, int64_t ldw, int64_t slices, int64_t rows,
                float2* stats, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
     if (int rc = allow_smem(ready, reinterpret_cast<const void*>(ce_few_kernel<TOKENS>), kFewSmem)) return rc;
-    return ss::launch(ce_few_kernel<TOKENS>, slices + 1, kThreads, TOKENS * a.Dp * 2, 0, staged, st, a, w, ldw,
-                      staged ? 1 : 0, (int)rows, stats);
+    return launch(ce_few_kernel<TOKENS>, slices + 1, kThreads, TOKENS * a.Dp * 2, st, a, w, ldw, (int)rows, stats);
 }
 
 int launch_gemm(const Maps& maps, GemmArgs& g, int64_t tiles, cudaStream_t st) {
@@ -1152,7 +1154,7 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
                      (int)l.n_counters};
     if (!l.few)
         if (int rc = ss::launch(ce_gather_kernel, T > 0 ? (T + kGatherRows - 1) / kGatherRows : 1, kGatherThreads, 0, 0,
-                                false, st, ga))
+                                true, st, ga))
             return rc;
 
     const uint16_t* w = static_cast<const uint16_t*>(a->weight);
@@ -1160,7 +1162,8 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
     if (stage) {
         uint16_t* staged = reinterpret_cast<uint16_t*>(ws + l.w);
         const int64_t per = kThreads / 32;
-        if (int rc = ss::launch(ce_stage_kernel, (V + per - 1) / per, kThreads, 0, 0, !l.few, st, w, ldw, V, D, l.Dp, staged))
+        if (int rc = ss::launch(ce_stage_kernel, (V + per - 1) / per, kThreads, 0, 0, true, st, w, ldw, V, D, l.Dp, l.few ? 1 : 0,
+                                staged))
             return rc;
         w = staged;
         ldw = l.Dp;
@@ -1182,9 +1185,9 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
         if (int rc = make_map(&h_k, h, l.rows, D, l.Dp, kHalf)) return rc;
         if (int rc = make_map(&w_k, w, V, D, ldw, kHalf)) return rc;
         if (l.few) {
-            const int rc = T == 1   ? launch_few<1>(ga, w, ldw, stage, l.slices, l.rows, g.stats, st)
-                           : T == 2 ? launch_few<2>(ga, w, ldw, stage, l.slices, l.rows, g.stats, st)
-                                    : launch_few<kFewTokens>(ga, w, ldw, stage, l.slices, l.rows, g.stats, st);
+            const int rc = T == 1   ? launch_few<1>(ga, w, ldw, l.slices, l.rows, g.stats, st)
+                           : T == 2 ? launch_few<2>(ga, w, ldw, l.slices, l.rows, g.stats, st)
+                                    : launch_few<kFewTokens>(ga, w, ldw, l.slices, l.rows, g.stats, st);
             if (rc) return rc;
         } else {
             Maps maps;
