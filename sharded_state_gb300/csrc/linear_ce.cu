@@ -566,10 +566,35 @@ struct GatherArgs {
     int mean;
     int* counters;  // of the launches' tiles
     int n_counters;
+    const int* chunk;  // tokens that count in each kChunk of them (NULL: count one by one)
 };
 
+// From so many tokens on, ce_count_kernel counts them by chunks first.  Counting one
+// by one reads T * T / 2 bytes from L2 in all: 130 MB for 16384 tokens, a few us, but
+// 0.5 TB for a million.
+constexpr int kChunk = 2048;
+constexpr int64_t kChunksFrom = 16384;
+
+__global__ void __launch_bounds__(kGatherThreads) ce_count_kernel(const int64_t* targets, int64_t ignore, int T, int* chunk) {
+    __shared__ int part[kGatherThreads / 32];
+    wait_before();
+    launch_after();
+    const int t0 = blockIdx.x * kChunk;
+    int n = 0;
+#pragma unroll
+    for (int i = threadIdx.x; i < kChunk; i += kGatherThreads) n += t0 + i < T && targets[t0 + i] != ignore;
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        n = 0;
+        for (int i = 0; i < kGatherThreads / 32; ++i) n += part[i];
+        chunk[blockIdx.x] = n;
+    }
+}
+
 // Block b places tokens [8 b, 8 b + 8): how many of the tokens before count
-// (read again by every block: T * T / 2 bytes in all, from L2), then its own
+// (by chunks where they have been counted; read again by every block), then its own
 // rows, one per warp: gathered together with the logit of their target, or,
 // where ignored, zeroed in the outputs.  The tensor cores' sums drop bits in one
 // direction, and the target's logit is the one that grows large, so it gets
@@ -591,8 +616,10 @@ __device__ __forceinline__ void gather_block(const GatherArgs& a, int block, boo
         }
     }
     int before = 0;
+    const int chunks = a.chunk ? t0 / kChunk : 0;
+    for (int i = threadIdx.x; i < chunks; i += kGatherThreads) before += a.chunk[i];
 #pragma unroll 8
-    for (int i = threadIdx.x; i < t0; i += kGatherThreads) before += a.targets[i] != a.ignore;
+    for (int i = chunks * kChunk + threadIdx.x; i < t0; i += kGatherThreads) before += a.targets[i] != a.ignore;
     before = __reduce_add_sync(0xFFFFFFFFu, before);
     if (lane == 0) part[warp] = before, flag[warp] = counts;
     __syncthreads();
@@ -970,7 +997,7 @@ struct Layout {
     bool few;  // tokens: the dot-product kernel
     int hidden_splits, head_splits;
     bool grad, stage;
-    int64_t counters, n_counters;
+    int64_t counters, n_counters, chunk;
     int64_t row, target, target_logit, row_loss, partials, stats, h, w, p[2], hidden_part, head_part, bytes;
 };
 
@@ -1004,6 +1031,7 @@ Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int p
     }
     l.n_counters = 2 + l.pieces;
     l.counters = take(l.n_counters * 4);
+    l.chunk = T >= kChunksFrom ? take(up(T, kChunk) / kChunk * 4) : 0;
     l.stats = take(l.slices * l.rows * 8);
     l.h = take(l.rows * l.Dp * 2);
     if (stage) l.w = take(V * l.Dp * 2);
@@ -1151,7 +1179,14 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
                      static_cast<const uint16_t*>(a->hidden), a->hidden_stride, static_cast<const uint16_t*>(a->weight),
                      a->weight_stride, h, row, target, target_logit, a->token_loss_out,
                      static_cast<uint16_t*>(a->d_hidden), a->d_hidden_stride, (float)a->grad_scale, mean, counters,
-                     (int)l.n_counters};
+                     (int)l.n_counters, nullptr};
+    if (l.chunk) {
+        int* chunk = reinterpret_cast<int*>(ws + l.chunk);
+        if (int rc = ss::launch(ce_count_kernel, up(T, kChunk) / kChunk, kGatherThreads, 0, 0, true, st, a->targets,
+                                a->ignore_index, T, chunk))
+            return rc;
+        ga.chunk = chunk;
+    }
     if (!l.few)
         if (int rc = ss::launch(ce_gather_kernel, T > 0 ? (T + kGatherRows - 1) / kGatherRows : 1, kGatherThreads, 0, 0,
                                 true, st, ga))

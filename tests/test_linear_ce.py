@@ -169,6 +169,14 @@ def test_pieces(ss):
 
 
 @gpu
+@pytest.mark.parametrize("T", [16384, 20001])
+@pytest.mark.parametrize("mask", ["none", "random", "first_half"])
+def test_many_tokens(ss, T, mask):
+    """So many tokens that those that count are counted by chunks first."""
+    Case(T, 130, 24, mask=mask, seed=6).run(ss).check()
+
+
+@gpu
 @pytest.mark.parametrize("std", [1e-3, 8.0])
 def test_flat_and_peaked(ss, std):
     """Nearly equal logits, and logits that put all the mass on one class (exponentials that underflow)."""
