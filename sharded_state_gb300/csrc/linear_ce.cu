@@ -40,6 +40,7 @@
 #include "device_utils.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "segmap.cuh"
 #include "tcgen05.cuh"
 
 namespace {
@@ -138,7 +139,10 @@ __device__ __forceinline__ float ex2(float x) {
 
 // This thread's row: exponentials of 32 logits (columns from col of the tile's
 // row) added to (m, s), m an integer exponent at or above every logit so far.
-__device__ __forceinline__ void add_logits(const float (&l)[32], float log2e, float& m, float& s) {
+__device__ __forceinline__ void add_logits(const uint32_t (&r)[32], float log2e, float& m, float& s) {
+    float l[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) l[i] = __uint_as_float(r[i]);
     float top = l[0];
 #pragma unroll
     for (int i = 1; i < 32; ++i) top = fmaxf(top, l[i]);
@@ -165,6 +169,21 @@ __device__ __forceinline__ void sum_losses(const double* partials, int n, int li
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, k);
     if (lane == 0) *loss = (float)(mean && live > 0 ? s / live : s);
+}
+
+// This lane's row, columns 32 h .. of 64, as bf16 words in its warp's shared memory.
+__device__ __forceinline__ void turn_words(uint32_t* words, int lane, int h, const uint32_t (&r)[32], float scale,
+                                           bool none) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = none ? 0u
+                        : ss::pack_bf16x2(scale * __uint_as_float(r[8 * i + 2 * e]),
+                                          scale * __uint_as_float(r[8 * i + 2 * e + 1]));
+        *reinterpret_cast<uint4*>(words + lane * 32 + 4 * ((4 * h + i) ^ (lane & 7))) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 
 // A tile of a launch: which product (-1: there is none left), where, and its
@@ -204,6 +223,15 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& g, int live, int id) {
     return t;
 }
 
+__device__ __forceinline__ int total_tiles(const GemmArgs& g, int live) {
+    int n = 0;
+    for (int w = 0; w < g.count; ++w) {
+        const Work& x = g.work[w];
+        n += (x.product == kHead ? x.m_tiles : (live + kTile - 1) / kTile) * x.n_tiles * x.splits;
+    }
+    return n;
+}
+
 constexpr int kQueue = 4;   // tiles handed out ahead
 
 // One persistent CTA pair takes output tiles of 256 x 256, its first CTA the
@@ -218,8 +246,8 @@ constexpr int kQueue = 4;   // tiles handed out ahead
 // which each CTA reads 32 KB, 64 bytes a clock, from L2; half the tile would need
 // half as much again.  Two accumulators fill tensor memory, and 6 stages what shared
 // memory the epilogues' turning leaves.  Tensor pipe active, by launch, at 2048
-// tokens, 32000 x 2048: statistics 75 % (153 us, 14 rounds of tiles for 13.2),
-// probabilities 71 % (167 us, and 131 MB written), both gradients 83 % (294 us).
+// tokens, 32000 x 2048: statistics 75 % (156 us, 14 rounds of tiles for 13.2),
+// probabilities 72 % (165 us, and 131 MB written), both gradients 85 % (281 us).
 // With 4 epilogue warps products of 16 k blocks waited for them (1021 ragged tokens
 // 274 -> 238 us with 8); a launch for each product left 7 to 16 % of the last rounds
 // empty.
@@ -269,18 +297,20 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
     const int first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     bool ok = true;
 
-    // The pair's j-th tile, read by a whole warp or by one thread.
+    // The pair's j-th tile, for a whole warp or for one thread: the first is worked
+    // out on the spot, the others come through the queue.
     auto take_tile = [&](int j) {
-        const int slot = j % kQueue;
+        if (j == 0) return find_tile(g, live, first);
+        const int slot = (j - 1) % kQueue;
         Tile t;
-        ok = tc::mbar_wait<true>(queue_full + 8 * slot, (j / kQueue) & 1);
+        ok = tc::mbar_wait(queue_full + 8 * slot, ((j - 1) / kQueue) & 1);
         const int4 x = *reinterpret_cast<const int4*>(queue + slot);
         const int2 y = *reinterpret_cast<const int2*>(&queue[slot].kb);
         t.w = x.x, t.m = x.y, t.n = x.z, t.s = x.w, t.kb = y.x, t.ke = y.y;
         return t;
     };
     auto tile_taken = [&](int j) {  // one thread
-        tc::mbar_arrive_cluster(tc::map_to_rank(queue_empty + 8 * (j % kQueue), 0));
+        if (j > 0) tc::mbar_arrive_cluster(tc::map_to_rank(queue_empty + 8 * ((j - 1) % kQueue), 0));
     };
 
     if (warp == 0 && lane == 0) {
@@ -349,16 +379,17 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
             tc::commit_pair(acc_full + 8 * (j & 1));
         }
     } else if (warp == 3 && lane == 0 && rank == 0) {
-        for (int j = 0;; ++j) {
+        for (int j = 0; first < total_tiles(g, live); ++j) {
             const int slot = j % kQueue;
             ok = tc::mbar_wait<true>(queue_empty + 8 * slot, ((j / kQueue) & 1) ^ 1);
             if (!ok) break;
-            const Tile t = find_tile(g, live, j == 0 ? first : pairs + atomicAdd(g.next, 1));
+            const Tile t = find_tile(g, live, pairs + atomicAdd(g.next, 1));
             for (uint32_t r = 0; r < 2; ++r) {
                 const uint32_t at = tc::map_to_rank(tc::smem_addr(queue + slot), r);
-                tc::st_cluster(at, t.w, t.m, t.n, t.s);
-                tc::st_cluster(at + 16, t.kb, t.ke, 0, 0);
-                tc::mbar_arrive_cluster(tc::map_to_rank(queue_full + 8 * slot, r));
+                const uint32_t bar = tc::map_to_rank(queue_full + 8 * slot, r);
+                tc::mbar_expect_tx_cluster(bar, sizeof(Tile));
+                tc::st_async(at, bar, t.w, t.m, t.n, t.s);
+                tc::st_async(at + 16, bar, t.kb, t.ke, 0, 0);
             }
             if (t.w < 0) break;
         }
@@ -381,137 +412,182 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc::fence_after();
+            // 32 columns at a time; but for the statistics, which are bound by their arithmetic and
+            // gain nothing, the next ones are on their way while these are worked on (292 x 6382 x
+            // 3584: 113.7 -> 103.8 us)
+            uint32_t r[2][32];
+            tc::tmem_ld32(d, r[0]);
             if (x.product <= kProbability) {
                 const int y = row < live ? g.target[row] - (x.v0 + col0) : -1;  // column of the target
                 const int left = g.vocab - (x.v0 + col0);                       // columns that exist
                 if (x.product == kStatistics) {
                     // the target's own exponential is left out: it is added from a logit of its own
                     float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
                     for (int c = 0; c < kColumns && c < left; c += 32) {
-                        float l[32];
                         __syncwarp();
-                        tc::tmem_ld32(d + c, l);
+                        if (c > 0) tc::tmem_ld32(d + c, r[0]);
+                        tc::tmem_wait(r[0]);
                         if (c + 32 > left) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) l[i] = c + i < left ? l[i] : -INFINITY;
+                            for (int i = 0; i < 32; ++i) r[0][i] = c + i < left ? r[0][i] : __float_as_uint(-INFINITY);
                         }
                         if (y >= c && y < c + 32) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) l[i] = c + i == y ? -INFINITY : l[i];
+                            for (int i = 0; i < 32; ++i) r[0][i] = c + i == y ? __float_as_uint(-INFINITY) : r[0][i];
                         }
-                        add_logits(l, g.log2e, top, sum);
+                        add_logits(r[0], g.log2e, top, sum);
                     }
                     if (row < live) g.stats[(int64_t)(2 * t.n + half) * g.rows + row] = make_float2(top, sum);
                 } else {
                     const float2 rl = row < live ? g.row_loss[row] : make_float2(0.f, 0.f);
                     uint16_t* o = x.p + (int64_t)row * x.ldp + col0;
-                    for (int c = 0; c < kColumns; c += 32) {
-                        float l[32];
-                        __syncwarp();
-                        tc::tmem_ld32(d + c, l);
+#pragma unroll 1
+                    for (int c = 0; c < kColumns; c += 64) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            l[i] = ex2(fmaf(l[i], g.log2e, -rl.x));
-                            if (row >= live || c + i >= left) l[i] = 0.f;
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = c + 32 * h;
+                            __syncwarp();
+                            tc::tmem_wait(r[h]);
+                            if (at + 32 < kColumns) tc::tmem_ld32(d + at + 32, r[h ^ 1]);
+                            uint32_t w[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                w[i] = ss::pack_bf16x2(ex2(fmaf(__uint_as_float(r[h][2 * i]), g.log2e, -rl.x)),
+                                                       ex2(fmaf(__uint_as_float(r[h][2 * i + 1]), g.log2e, -rl.x)));
+                            if (row >= live || at + 32 > left) {  // zeros where there is no token or no class
+                                const int have = row < live ? left - at : 0;
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    w[i] = 2 * i + 1 < have ? w[i] : 2 * i < have ? w[i] & 0xFFFFu : 0u;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<uint4*>(o + at + 8 * i) =
+                                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                         }
-                        if (y >= c && y < c + 32) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) l[i] = c + i == y ? rl.y : l[i];
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            *reinterpret_cast<uint4*>(o + c + i) =
-                                make_uint4(ss::pack_bf16x2(l[i], l[i + 1]), ss::pack_bf16x2(l[i + 2], l[i + 3]),
-                                           ss::pack_bf16x2(l[i + 4], l[i + 5]), ss::pack_bf16x2(l[i + 6], l[i + 7]));
                     }
+                    if (y >= 0 && y < kColumns && y < left) o[y] = ss::f32_to_bf16(rl.y);  // over its exponential
                 }
             } else {
-                // through shared memory (16-byte groups of row r at group ^ (r & 7), free of bank
+                // through shared memory (16-byte groups of row i at group ^ (i & 7), free of bank
                 // conflicts both ways), so that a row's values go out together
                 const int limit = x.product == kHidden ? live : x.m_rows;
                 const int* token = x.product == kHidden ? g.token : nullptr;
+                const bool none = t.kb == t.ke;  // no k: the accumulator holds something else
                 float* mine = turn[warp - 4];
-                const bool wide = (reinterpret_cast<uintptr_t>(x.out) & 7u) == 0 && (x.out_ld & 3) == 0;
-                if (x.part || wide) {  // 32 columns at a time: 8 lanes a row, 4 columns a lane
-                    const int k = lane & 7;
-                    for (int c = 0; c < kColumns && col0 + c < x.cols; c += 32) {
-                        float v32[32];
-                        __syncwarp();
-                        tc::tmem_ld32(d + c, v32);
+                uint32_t* words = reinterpret_cast<uint32_t*>(mine);
+                const int k = lane & 7;
+                if (x.part) {  // fp32, 32 columns at a time: 8 lanes a row, 4 columns a lane
+                    float* part = x.part + t.s * x.part_split + (int64_t)(row0 + (lane >> 3)) * x.part_ld + col0 + 4 * k;
+#pragma unroll 1
+                    for (int c = 0; c < kColumns && col0 + c < x.cols; c += 64) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<float4*>(mine + lane * 32 + 4 * (i ^ (lane & 7))) =
-                                t.kb == t.ke ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                             : make_float4(v32[4 * i], v32[4 * i + 1], v32[4 * i + 2], v32[4 * i + 3]);
-                        __syncwarp();
-                        const int col = col0 + c, left = x.cols - col;
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = c + 32 * h;
+                            __syncwarp();
+                            tc::tmem_wait(r[h]);
+                            if (at + 32 < kColumns) tc::tmem_ld32(d + at + 32, r[h ^ 1]);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 4 * i + (lane >> 3);
-                            if (row0 + r >= limit || 4 * k >= left) continue;
-                            float4 v = *reinterpret_cast<const float4*>(mine + r * 32 + 4 * (k ^ (r & 7)));
-                            if (x.part) {  // part_ld is a multiple of 4
-                                float* o = x.part + t.s * x.part_split + (int64_t)(row0 + r) * x.part_ld + col + 4 * k;
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<uint4*>(words + lane * 32 + 4 * (i ^ (lane & 7))) =
+                                    none ? make_uint4(0, 0, 0, 0)
+                                         : make_uint4(r[h][4 * i], r[h][4 * i + 1], r[h][4 * i + 2], r[h][4 * i + 3]);
+                            __syncwarp();
+                            if (col0 + at + 4 * k >= x.cols) continue;  // part_ld is a multiple of 4
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int q = 4 * i + (lane >> 3);
+                                if (row0 + q >= limit) continue;
+                                float4 v = *reinterpret_cast<const float4*>(mine + q * 32 + 4 * (k ^ (q & 7)));
+                                float4* o = reinterpret_cast<float4*>(part + (int64_t)(4 * i) * x.part_ld + at);
                                 if (x.add) {
-                                    const float4 w = *reinterpret_cast<const float4*>(o);
+                                    const float4 w = *o;
                                     v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
                                 }
-                                *reinterpret_cast<float4*>(o) = v;
-                            } else {
-                                const int64_t orow = token ? token[row0 + r] : (int64_t)x.v0 + row0 + r;
-                                uint16_t* o = x.out + orow * x.out_ld + col + 4 * k;
-                                if (4 * k + 4 <= left) {
-                                    *reinterpret_cast<uint2*>(o) =
-                                        make_uint2(ss::pack_bf16x2(scale * v.x, scale * v.y),
-                                                   ss::pack_bf16x2(scale * v.z, scale * v.w));
-                                } else {
-                                    o[0] = ss::f32_to_bf16(scale * v.x);
-                                    if (4 * k + 1 < left) o[1] = ss::f32_to_bf16(scale * v.y);
-                                    if (4 * k + 2 < left) o[2] = ss::f32_to_bf16(scale * v.z);
-                                }
+                                *o = v;
                             }
                         }
                     }
-                } else {  // rows at any element offset, 64 columns at a time: a row's words, one a lane
-                    uint32_t* words = reinterpret_cast<uint32_t*>(mine);
+                } else if ((reinterpret_cast<uintptr_t>(x.out) & 15u) == 0 && (x.out_ld & 7) == 0) {
+                    // bf16 rows on 16-byte boundaries, 64 columns at a time: 8 lanes a row, 16 bytes a lane
+#pragma unroll 1
                     for (int c = 0; c < kColumns && col0 + c < x.cols; c += 64) {
-                        __syncwarp();
+#pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            float v[32];
-                            tc::tmem_ld32(d + c + 32 * h, v);
+                            const int at = c + 32 * h;
+                            __syncwarp();
+                            tc::tmem_wait(r[h]);
+                            if (at + 32 < kColumns) tc::tmem_ld32(d + at + 32, r[h ^ 1]);
+                            turn_words(words, lane, h, r[h], scale, none);
+                        }
+                        __syncwarp();
+                        const int col = col0 + c + 8 * k, left = x.cols - col;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = t.kb == t.ke ? 0.f : scale * v[i];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                *reinterpret_cast<uint4*>(words + lane * 32 + 4 * ((4 * h + i) ^ (lane & 7))) =
-                                    make_uint4(ss::pack_bf16x2(v[8 * i], v[8 * i + 1]),
-                                               ss::pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                                               ss::pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
-                                               ss::pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+                        for (int i = 0; i < 8; ++i) {
+                            const int q = 4 * i + (lane >> 3);
+                            if (row0 + q >= limit || left <= 0) continue;
+                            const int64_t orow = token ? token[row0 + q] : (int64_t)x.v0 + row0 + q;
+                            uint16_t* o = x.out + orow * x.out_ld + col;
+                            const uint4 v = *reinterpret_cast<const uint4*>(words + q * 32 + 4 * (k ^ (q & 7)));
+                            if (left >= 8)
+                                *reinterpret_cast<uint4*>(o) = v;
+                            else
+                                ss::st_bytes(reinterpret_cast<unsigned char*>(o), v, 0, 2 * left);
+                        }
+                    }
+                } else {
+                    // bf16 rows at any element offset, 64 columns at a time.  Of a row's 128 bytes the 7
+                    // aligned blocks inside go out as such, put together from two groups, and the 8
+                    // elements before and after them one a lane; a row's last columns word by word.
+                    // (All of them word by word: 230 us where this takes 205, 604 of 1021 tokens, 32003 x 1001.)
+#pragma unroll 1
+                    for (int c = 0; c < kColumns && col0 + c < x.cols; c += 64) {
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            __syncwarp();
+                            if (c + h > 0) tc::tmem_ld32(d + c + 32 * h, r[0]);
+                            tc::tmem_wait(r[0]);
+                            turn_words(words, lane, h, r[0], scale, none);
                         }
                         __syncwarp();
                         const int col = col0 + c, left = x.cols - col;
-                        const int here = limit - row0 < 32 ? limit - row0 : 32;
+                        const int here = min(limit - row0, 32);
+                        if (left >= 64) {
 #pragma unroll 4
-                        for (int r = 0; r < here; ++r) {
-                            const int64_t orow = token ? token[row0 + r] : (int64_t)x.v0 + row0 + r;
-                            uint16_t* o = x.out + orow * x.out_ld + col;
-                            const uint32_t w = words[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)];
-                            const int odd = (int)(reinterpret_cast<uintptr_t>(o) >> 1) & 1;
-                            // from an odd place the words are a column on: this one's upper half and
-                            // the next one's lower, and the first column goes by itself
-                            const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w, 1);
-                            const uint32_t u = odd ? __byte_perm(w, next, 0x5432) : w;
-                            const int at = 2 * lane + odd;
-                            if (at + 1 < left && at < 63)
-                                *reinterpret_cast<uint32_t*>(o + at) = u;
-                            else if (at < left)
-                                o[at] = (uint16_t)u;
-                            if (odd && lane == 0) o[0] = (uint16_t)w;
+                            for (int i = 0; i < 8; ++i) {
+                                const int q = 4 * i + (lane >> 3);
+                                if (q >= here) continue;
+                                const int64_t orow = token ? token[row0 + q] : (int64_t)x.v0 + row0 + q;
+                                uint16_t* o = x.out + orow * x.out_ld + col;
+                                const int sh = (int)(reinterpret_cast<uintptr_t>(o) & 15u);
+                                const uint32_t* row_q = words + q * 32;
+                                const uint4 mine4 = *reinterpret_cast<const uint4*>(row_q + 4 * (k ^ (q & 7)));
+                                const uint4 next4 = *reinterpret_cast<const uint4*>(row_q + 4 * (min(k + 1, 7) ^ (q & 7)));
+                                if (sh == 0) {
+                                    *reinterpret_cast<uint4*>(o + 8 * k) = mine4;
+                                    continue;
+                                }
+                                if (k < 7)
+                                    *reinterpret_cast<uint4*>(o + 8 * k + 8 - sh / 2) = ss::realign16(mine4, next4, 16 - sh);
+                                const int e = 2 * k < 16 - sh ? k : 56 + k;  // before the blocks, or after
+                                const uint32_t w = row_q[4 * ((e >> 3) ^ (q & 7)) + ((e & 7) >> 1)];
+                                o[e] = (uint16_t)(e & 1 ? w >> 16 : w);
+                            }
+                        } else {
+                            for (int q = 0; q < here; ++q) {
+                                const int64_t orow = token ? token[row0 + q] : (int64_t)x.v0 + row0 + q;
+                                uint16_t* o = x.out + orow * x.out_ld + col;
+                                const uint32_t w = words[q * 32 + 4 * ((lane >> 2) ^ (q & 7)) + (lane & 3)];
+                                if (2 * lane < left) o[2 * lane] = (uint16_t)w;
+                                if (2 * lane + 1 < left) o[2 * lane + 1] = (uint16_t)(w >> 16);
+                            }
                         }
                     }
                 }
             }
+            __syncwarp();
+            tc::tmem_wait(r[0]);  // a load asked for and not used
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_cluster(acc_empty0 + 8 * (j & 1));
