@@ -632,6 +632,14 @@ __device__ __forceinline__ float dot_bf16(uint4 a, uint4 b, float s) {
     return fmaf(ss::bf16_hi(a.w), ss::bf16_hi(b.w), s);
 }
 
+// The first n (1 .. 7) of 8 elements, the others zero.
+__device__ __forceinline__ uint4 head_bf16(uint4 v, int n) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = 2 * i + 1 < n ? w[i] : 2 * i < n ? w[i] & 0xFFFFu : 0u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 struct GatherArgs {
     Header* header;
     const int64_t* targets;
@@ -838,7 +846,10 @@ ce_few_kernel(const GatherArgs a, const uint16_t* __restrict__ w, int64_t ldw, i
     __shared__ float top_s[kThreads / 32][kFewTokens];
     __shared__ float sum_s[kThreads / 32][kFewTokens];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int vecs = a.Dp / 8, V = a.vocab, slices = gridDim.x - 1;
+    // what lies between a row's end and the next one's start, or behind the last row, is
+    // not read, or masked where it shares 16 bytes with the row's end: it may be a NaN
+    const int vecs = (a.D + 7) / 8, V = a.vocab, slices = gridDim.x - 1;
+    const int cut = a.D % 8 ? vecs - 1 : -1;  // the vector to be masked
     const int groups = (V + kFewRows - 1) / kFewRows;
     int g = blockIdx.x * (kThreads / 32) + warp;
     uint4 x[4][kFewRows];
@@ -890,6 +901,10 @@ ce_few_kernel(const GatherArgs a, const uint16_t* __restrict__ w, int64_t ldw, i
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (j + 32 * i >= vecs) continue;
+                if (j + 32 * i == cut) {
+#pragma unroll
+                    for (int r = 0; r < kFewRows; ++r) x[i][r] = head_bf16(x[i][r], a.D % 8);
+                }
 #pragma unroll
                 for (int t = 0; t < TOKENS; ++t) {
                     const uint4 hv = hs[t * vecs + j + 32 * i];

@@ -205,6 +205,20 @@ def test_nan_comes_through(ss):
 
 
 @gpu
+@pytest.mark.parametrize("T,grad", [(1, False), (2, True), (3, False), (4, False), (4, True), (30, True), (150, False),
+                                    (150, True)])
+@pytest.mark.parametrize("D,extra", [(24, 0), (20, 4), (72, 0), (61, 3), (61, 0)])
+def test_nothing_beside_the_rows_is_read(ss, T, grad, D, extra):
+    """NaN between the rows and around the tensors, with rows on 16-byte boundaries and off."""
+    c = Case(T, 300, D, h_extra=extra, w_extra=extra)
+    for view, buf in ((c.h, c.hbuf), (c.w, c.wbuf)):
+        keep = view.clone()
+        buf.fill_(float("nan"))
+        view.copy_(keep)
+    c.run(ss, dh=grad, dw=grad).check()
+
+
+@gpu
 def test_same_bits_twice_and_on_another_stream(ss):
     c = Case(700, 3001, 136, mask="random")
     c.run(ss)
