@@ -632,14 +632,6 @@ __device__ __forceinline__ float dot_bf16(uint4 a, uint4 b, float s) {
     return fmaf(ss::bf16_hi(a.w), ss::bf16_hi(b.w), s);
 }
 
-// The first n (1 .. 7) of 8 elements, the others zero.
-__device__ __forceinline__ uint4 head_bf16(uint4 v, int n) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = 2 * i + 1 < n ? w[i] : 2 * i < n ? w[i] & 0xFFFFu : 0u;
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 struct GatherArgs {
     Header* header;
     const int64_t* targets;
@@ -813,26 +805,31 @@ ce_stage_kernel(const uint16_t* __restrict__ w, int64_t ld, int V, int D, int Dp
 // ---------------------------------------------------------------------------
 
 // With a handful of tokens the weight's one read is all the time there is: dot
-// products on the CUDA cores, 2 weight rows of a warp at a time (8 loads in flight
-// a lane), against the tokens in shared memory.
+// products on the CUDA cores against the tokens in shared memory, 8 loads in flight a
+// lane: of 2 weight rows, and from 3 tokens on, where shared memory is what is read
+// most (a token's vector once for all rows), of 4.
 // Against the tile kernel, with vocabulary and hidden size 32000 x 2048, 32000 x 4096
-// and 5000 x 512: 1 or 2 tokens 31-33, 51-54 and 14 us (45, 70, 17), 3 or 4 tokens 43,
-// 73 and 14; from 5 on the tiles win.
+// and 5000 x 512: 1 or 2 tokens 28-30, 49-52 and 11 us (42, 68, 14), 3 or 4 tokens 35,
+// 54 and 11; from 5 on the tiles win (42 against 42, 68 against 71 with dot products).
 constexpr int kFewTokens = 4;
-constexpr int kFewRows = 2;
+constexpr int kFewLoads = 8;
 constexpr int kFewSmem = 64 * 1024;  // of hidden states
-constexpr int kFewCtas = 4;             // per SM at most, each a slice of statistics
+constexpr int few_rows(int64_t tokens) { return tokens <= 2 ? 2 : 4; }
+// CTAs per SM at most, each a slice of statistics; their registers allow no more
+constexpr int few_ctas_per_sm(int64_t tokens) { return tokens <= 2 ? 4 : 2; }
 
 // Bound by the weight's read: 131 MB in 26 us at 32000 x 2048, 65 % of the DRAM's
-// rate; the launch's start and its last round are the rest.  4 CTAs of 8 warps an SM
-// measured 30.0 us a call, 2 CTAs 30.8, as many as there are rows 36.7; with 4 rows a
-// warp 30.8 to 35.9, with one 32.9 to 48.
+// rate; the launch's start and its last round are the rest.  One token: 4 CTAs of 8
+// warps an SM measured 28.2 us a call, 3 and 5 of them 29.5; one row a warp 29.2, 4 rows
+// 28.2 (20.5 for 19.7 at 50000 x 768), 16 loads in flight 28.7 to 35, loads through a
+// ring in shared memory, always 12 in flight, 31 to 35.  4 tokens: 2 rows a warp 41.1, 4
+// rows 35.1, 8 rows 55; as many CTAs as with one token 36.8.
 //
 // Statistics as the tile kernel leaves them, one slice per CTA: CTA b's warps
-// take groups of kFewRows rows, b's after those of the CTA before.  The CTAs pick
+// take groups of ROWS rows, b's after those of the CTA before.  The CTAs pick
 // the tokens that count out themselves; one more CTA does the gather's work for
 // the kernels behind.
-template <int TOKENS>
+template <int TOKENS, int ROWS>
 __global__ void __launch_bounds__(kThreads)
 ce_few_kernel(const GatherArgs a, const uint16_t* __restrict__ w, int64_t ldw, int rows, float2* stats) {
     launch_after();
@@ -846,20 +843,21 @@ ce_few_kernel(const GatherArgs a, const uint16_t* __restrict__ w, int64_t ldw, i
     __shared__ float top_s[kThreads / 32][kFewTokens];
     __shared__ float sum_s[kThreads / 32][kFewTokens];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // what lies between a row's end and the next one's start, or behind the last row, is
-    // not read, or masked where it shares 16 bytes with the row's end: it may be a NaN
-    const int vecs = (a.D + 7) / 8, V = a.vocab, slices = gridDim.x - 1;
-    const int cut = a.D % 8 ? vecs - 1 : -1;  // the vector to be masked
-    const int groups = (V + kFewRows - 1) / kFewRows;
+    // whole vectors of a row and the elements behind them, which go by themselves: what lies
+    // between a row's end and the next one's start, or behind the last row, may be a NaN
+    const int vecs = a.D / 8, rest = a.D % 8, ld_hs = (a.D + 7) / 8;
+    const int V = a.vocab, slices = gridDim.x - 1;
+    const int groups = (V + ROWS - 1) / ROWS;
     int g = blockIdx.x * (kThreads / 32) + warp;
-    uint4 x[4][kFewRows];
+    constexpr int U = kFewLoads / ROWS;  // of each row
+    uint4 x[U][ROWS];
     auto load = [&](int g, int j) {
 #pragma unroll
-        for (int r = 0; r < kFewRows; ++r) {  // past the end: the last row again, left out below
-            const int v = g * kFewRows + r < V ? g * kFewRows + r : V - 1;
+        for (int r = 0; r < ROWS; ++r) {  // past the end: the last row again, left out below
+            const int v = g * ROWS + r < V ? g * ROWS + r : V - 1;
             const uint4* p = reinterpret_cast<const uint4*>(w + (int64_t)v * ldw);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < U; ++i)
                 if (j + 32 * i < vecs) x[i][r] = ss::ld_stream_u4(p + j + 32 * i);
         }
     };
@@ -882,46 +880,51 @@ ce_few_kernel(const GatherArgs a, const uint16_t* __restrict__ w, int64_t ldw, i
     }
 #pragma unroll
     for (int t = 0; t < TOKENS; ++t)
-        for (int j = threadIdx.x; j < vecs; j += kThreads)
-            hs[t * vecs + j] = from[t] >= 0 ? row_vec(a.hidden + from[t] * a.ld, j, a.D) : make_uint4(0, 0, 0, 0);
+        for (int j = threadIdx.x; j < ld_hs; j += kThreads)
+            hs[t * ld_hs + j] = from[t] >= 0 ? row_vec(a.hidden + from[t] * a.ld, j, a.D) : make_uint4(0, 0, 0, 0);
     __syncthreads();
     float top[TOKENS], sum[TOKENS];
 #pragma unroll
     for (int t = 0; t < TOKENS; ++t) top[t] = -INFINITY, sum[t] = 0.f;
     for (; g < groups; g += slices * (kThreads / 32)) {
-        const int v0 = g * kFewRows;
-        float acc[kFewRows][TOKENS];
+        const int v0 = g * ROWS;
+        float acc[ROWS][TOKENS];
 #pragma unroll
-        for (int r = 0; r < kFewRows; ++r)
+        for (int r = 0; r < ROWS; ++r)
 #pragma unroll
             for (int t = 0; t < TOKENS; ++t) acc[r][t] = 0.f;
-        for (int j = lane; j < vecs; j += 128) {
+        for (int j = lane; j < vecs; j += 32 * U) {
             if (j != lane || !loaded) load(g, j);
             loaded = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < U; ++i) {
                 if (j + 32 * i >= vecs) continue;
-                if (j + 32 * i == cut) {
-#pragma unroll
-                    for (int r = 0; r < kFewRows; ++r) x[i][r] = head_bf16(x[i][r], a.D % 8);
-                }
 #pragma unroll
                 for (int t = 0; t < TOKENS; ++t) {
-                    const uint4 hv = hs[t * vecs + j + 32 * i];
+                    const uint4 hv = hs[t * ld_hs + j + 32 * i];
 #pragma unroll
-                    for (int r = 0; r < kFewRows; ++r) acc[r][t] = dot_bf16(x[i][r], hv, acc[r][t]);
+                    for (int r = 0; r < ROWS; ++r) acc[r][t] = dot_bf16(x[i][r], hv, acc[r][t]);
                 }
             }
         }
         __syncwarp();
+        if (lane < rest) {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(hs) + 8 * vecs + lane;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                const float wv = ss::bf16_to_f32(w[(int64_t)min(v0 + r, V - 1) * ldw + 8 * vecs + lane]);
+#pragma unroll
+                for (int t = 0; t < TOKENS; ++t) acc[r][t] = fmaf(wv, ss::bf16_to_f32(h[8 * t * ld_hs]), acc[r][t]);
+            }
+        }
         const int next = g + slices * (kThreads / 32);  // its loads go out before this group's sums
         loaded = next < groups && lane < vecs;
         if (loaded) load(next, lane);
 #pragma unroll
         for (int t = 0; t < TOKENS; ++t) {
-            float l[kFewRows], m = -INFINITY;
+            float l[ROWS], m = -INFINITY;
 #pragma unroll
-            for (int r = 0; r < kFewRows; ++r) {
+            for (int r = 0; r < ROWS; ++r) {
                 l[r] = acc[r][t];
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], d);
@@ -932,7 +935,7 @@ ce_few_kernel(const GatherArgs a, const uint16_t* __restrict__ w, int64_t ldw, i
             const float at = up == -INFINITY ? 0.f : up;
             float a = 0.f;
 #pragma unroll
-            for (int r = 0; r < kFewRows; ++r) a += ex2(fmaf(l[r], kLog2e, -at));
+            for (int r = 0; r < ROWS; ++r) a += ex2(fmaf(l[r], kLog2e, -at));
             sum[t] = (top[t] == -INFINITY ? 0.f : sum[t] * ex2(top[t] - at)) + a;
             top[t] = up;
         }
@@ -1111,8 +1114,9 @@ Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int p
     l.rows = up(T, kTile);
     l.n_tiles = up(V, kTile) / kTile;
     l.few = T > 0 && T <= kFewTokens && kFewTokens * l.Dp * 2 <= kFewSmem;
-    const int64_t few_ctas = (V + kFewRows * (kThreads / 32) - 1) / (kFewRows * (kThreads / 32));
-    l.slices = !l.few ? 2 * l.n_tiles : few_ctas < 2 * pairs * kFewCtas ? few_ctas : 2 * pairs * kFewCtas;
+    const int64_t per_cta = few_rows(T) * (kThreads / 32), few_ctas = (V + per_cta - 1) / per_cta;
+    const int64_t few_most = 2 * pairs * few_ctas_per_sm(T);
+    l.slices = !l.few ? 2 * l.n_tiles : few_ctas < few_most ? few_ctas : few_most;
     int64_t at = 256;  // the header
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -1204,8 +1208,9 @@ template <int TOKENS>
 int launch_few(const GatherArgs& a, const uint16_t* w, int64_t ldw, int64_t slices, int64_t rows,
                float2* stats, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
-    if (int rc = allow_smem(ready, reinterpret_cast<const void*>(ce_few_kernel<TOKENS>), kFewSmem)) return rc;
-    return launch(ce_few_kernel<TOKENS>, slices + 1, kThreads, TOKENS * a.Dp * 2, st, a, w, ldw, (int)rows, stats);
+    const auto kernel = ce_few_kernel<TOKENS, few_rows(TOKENS)>;
+    if (int rc = allow_smem(ready, reinterpret_cast<const void*>(kernel), kFewSmem)) return rc;
+    return launch(kernel, slices + 1, kThreads, TOKENS * a.Dp * 2, st, a, w, ldw, (int)rows, stats);
 }
 
 int launch_gemm(const Maps& maps, GemmArgs& g, int64_t tiles, cudaStream_t st) {
@@ -1324,6 +1329,7 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
         if (l.few) {
             const int rc = T == 1   ? launch_few<1>(ga, w, ldw, l.slices, l.rows, g.stats, st)
                            : T == 2 ? launch_few<2>(ga, w, ldw, l.slices, l.rows, g.stats, st)
+                           : T == 3 ? launch_few<3>(ga, w, ldw, l.slices, l.rows, g.stats, st)
                                     : launch_few<kFewTokens>(ga, w, ldw, l.slices, l.rows, g.stats, st);
             if (rc) return rc;
         } else {
