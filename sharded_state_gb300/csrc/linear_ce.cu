@@ -138,7 +138,8 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // This thread's row: exponentials of 32 logits (columns from col of the tile's
-// row) added to (m, s), m an integer exponent at or above every logit so far.
+// row) added to (m, s), m an integer exponent at or above every logit so far.  The
+// maximum passes over NaN, the sum does not: what it holds is never dropped.
 __device__ __forceinline__ void add_logits(const uint32_t (&r)[32], float log2e, float& m, float& s) {
     float l[32];
 #pragma unroll
@@ -155,7 +156,7 @@ __device__ __forceinline__ void add_logits(const uint32_t (&r)[32], float log2e,
         a += ex2(fmaf(l[i], log2e, -at));
         b += ex2(fmaf(l[i + 1], log2e, -at));
     }
-    s = (m == -INFINITY ? 0.f : s * ex2(m - at)) + (a + b);
+    s = (m == -INFINITY ? s : s * ex2(m - at)) + (a + b);  // at -inf s is 0, or the NaN of a logit
     m = up;
 }
 
@@ -936,7 +937,7 @@ ce_few_kernel(const GatherArgs a, const uint16_t* __restrict__ w, int64_t ldw, i
             float a = 0.f;
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) a += ex2(fmaf(l[r], kLog2e, -at));
-            sum[t] = (top[t] == -INFINITY ? 0.f : sum[t] * ex2(top[t] - at)) + a;
+            sum[t] = (top[t] == -INFINITY ? sum[t] : sum[t] * ex2(top[t] - at)) + a;  // as in add_logits
             top[t] = up;
         }
     }

@@ -205,6 +205,32 @@ def test_nan_comes_through(ss):
 
 
 @gpu
+@pytest.mark.parametrize("T,V,grad", [(1, 12003, False), (2, 12003, False), (2, 12003, True), (3, 20001, False),
+                                      (4, 20001, True), (40, 100, True), (40, 100, False), (300, 700, False),
+                                      (300, 700, True), (70, 3001, True)])
+@pytest.mark.parametrize("rows", ["pair", "four", "first_32", "second_half", "beside_the_target", "with_minus_infinities"])
+def test_nan_weight_rows_come_through(ss, T, V, grad, rows):
+    """A NaN in the head's weight makes every logit of its class NaN, and with it every token's loss (the definition's
+    sum holds that logit), wherever the class lies among those summed together and whatever follows it."""
+    c = Case(T, V, 72, seed=8)
+    c.y[:] = V - 2  # not one of the rows that are NaN
+    low, high = {"pair": (0, 2), "four": (0, 4), "first_32": (0, 32), "second_half": (128 % (V - 40), 128 % (V - 40) + 32),
+                 "beside_the_target": (6, 7), "with_minus_infinities": (0, 32)}[rows]
+    if rows == "beside_the_target":
+        c.y[:] = 7
+    if rows == "with_minus_infinities":
+        c.h.abs_()
+        c.w[low:high] = -math.inf
+        c.w[low + 1] = math.nan
+    else:
+        c.w[low:high] = math.nan
+    c.run(ss, dh=grad, dw=grad)
+    assert math.isnan(float(c.loss)) and bool(c.token_loss.isnan().all())
+    if grad:
+        assert bool(c.dh.isnan().all()) and bool(c.dw.isnan().all())
+
+
+@gpu
 @pytest.mark.parametrize("T,grad", [(1, False), (2, True), (3, False), (4, False), (4, True), (30, True), (150, False),
                                     (150, True)])
 @pytest.mark.parametrize("D,extra", [(24, 0), (20, 4), (72, 0), (61, 3), (61, 0)])
