@@ -447,7 +447,9 @@ enum { SS_LOSS_MEAN = 0, SS_LOSS_SUM = 1 };
  *   d_hidden, d_weight = grad_scale * the gradient of loss
  * Ignored tokens have a token loss and a d_hidden row of 0, whatever their
  * hidden row holds; a target outside [0, vocab_size) that is not ignore_index
- * makes its token's loss NaN, and with it the loss and the gradients.
+ * makes its token's loss NaN, and with it the loss and the gradients.  So does
+ * a logit of NaN or +infinity, of whichever class, and a token whose logits are
+ * all -infinity; a target's logit of -infinity is an infinite loss.
  *
  * All matrices are bf16, row-major with a row stride in elements (>= the row's
  * length) and any element alignment; products accumulate and statistics are

@@ -1018,11 +1018,15 @@ ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, in
         float l = 0.f;
         if (row < live) {
             // log of r, the whole exponent's ln 2 in two parts (the first exact); a lone class has r = 0
-            const float d = top == -INFINITY ? (sum == 0.f ? top : sum)
-                                             : fmaf(top, kLn2High, -hit) + fmaf(top, kLn2Low, logf(sum));
+            const float low = fmaf(top, kLn2Low, logf(sum));
+            float d = top == -INFINITY ? (sum == 0.f ? top : sum) : fmaf(top, kLn2High, -hit) + low;
+            // no loss without a target's logit, with one of +inf (inf - inf), or with nothing but -inf
+            if (!(hit < INFINITY) || (hit == -INFINITY && d == -INFINITY)) d = NAN;
             const float rest = expf(-fabsf(d));
             l = (d > 0.f ? d : 0.f) + log1pf(rest);
-            row_loss[row] = make_float2((hit + l) * kLog2e, -(d > 0.f ? 1.f : rest) / (1.f + rest));
+            // of a target at -inf the loss is infinite, and log-sum-exp what the other classes have
+            const float lse = hit == -INFINITY ? fmaf(top, kLn2High, low) : hit + l;
+            row_loss[row] = make_float2(lse * kLog2e, -(d > 0.f ? 1.f : rest) / (1.f + rest));
             if (token_loss) token_loss[token] = l;
         }
         loss_s[warp] = (double)l;

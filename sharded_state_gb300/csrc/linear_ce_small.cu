@@ -172,10 +172,14 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) ce_sma
         for (int r = 0; r < kCtas; ++r) sum += m[r] == -INFINITY ? s[r] : s[r] * expf(m[r] - at);
         if (target[tid] < 0) hit = NAN;
         // with r the other classes' mass over the target's: loss = log(1 + r), p - 1 = -r / (1 + r)
-        const float d = top == -INFINITY && sum == 0.f ? -INFINITY : (at - hit) + logf(sum);
+        float d = top == -INFINITY && sum == 0.f ? -INFINITY : (at - hit) + logf(sum);
+        // no loss without a target's logit, with one of +inf (inf - inf), or with nothing but -inf
+        if (!(hit < INFINITY) || (hit == -INFINITY && d == -INFINITY)) d = NAN;
         const float rest = expf(-fabsf(d));
         const float l = (d > 0.f ? d : 0.f) + log1pf(rest);
-        row_s[tid] = make_float2((hit + l) * kLog2e, -(d > 0.f ? 1.f : rest) / (1.f + rest));
+        // of a target at -inf the loss is infinite, and log-sum-exp what the other classes have
+        const float lse = hit == -INFINITY ? at + logf(sum) : hit + l;
+        row_s[tid] = make_float2(lse * kLog2e, -(d > 0.f ? 1.f : rest) / (1.f + rest));
         loss_s[tid] = l;
         if (rank == 0 && a.token_loss) a.token_loss[token[tid]] = l;
     }

@@ -230,6 +230,68 @@ def test_nan_weight_rows_come_through(ss, T, V, grad, rows):
         assert bool(c.dh.isnan().all()) and bool(c.dw.isnan().all())
 
 
+FORMS = [(1, 500, False), (2, 500, True), (4, 500, False), (4, 500, True), (40, 100, True), (40, 100, False),
+         (300, 700, False), (300, 700, True)]
+
+
+@gpu
+@pytest.mark.parametrize("T,V,grad", FORMS)
+def test_infinite_target_logit(ss, T, V, grad):
+    """A logit of +inf, here the target's own: its loss is inf - inf."""
+    c = Case(T, V, 72, seed=9)
+    c.h.abs_()
+    c.y[:] = 11
+    c.w[11] = math.inf
+    c.run(ss, dh=grad, dw=grad)
+    assert math.isnan(float(c.loss)) and bool(c.token_loss.isnan().all())
+    if grad:
+        assert bool(c.dh.isnan().all()) and bool(c.dw.isnan().all())
+
+
+@gpu
+@pytest.mark.parametrize("T,V,grad", FORMS)
+def test_target_logit_of_minus_infinity(ss, T, V, grad):
+    """A class whose logits are -inf is no part of any sum; where it is the target, the loss is infinite and P is the
+    other classes' softmax with -1 in its place."""
+    c = Case(T, V, 72, seed=9)
+    c.h.abs_()
+    c.y[c.y == 11] = 12
+    c.y[::2] = 11
+    c.w[11] = -math.inf
+    c.run(ss, dh=grad, dw=grad)
+    assert float(c.loss) == math.inf and bool((c.token_loss[::2] == math.inf).all())
+    h, w = c.h.double(), c.w.double()
+    w[11] = 0.0
+    logits = h @ w.t()
+    logits[:, 11] = -math.inf
+    want = torch.logsumexp(logits, 1) - logits.gather(1, c.y[:, None]).squeeze(1)
+    # dl as above: (72 / 16 + 2) * 2^-22 of a sum below 1000
+    assert bool(((c.token_loss[1::2].double() - want[1::2]).abs() <= 2e-3).all())
+    if grad:
+        p = torch.softmax(logits, 1)
+        p = (p - torch.nn.functional.one_hot(c.y, V)) / T
+        # two roundings to bf16, 2^-8 each, and 2e-3 of a p for its logit
+        assert bool(((c.dw.double() - p.t() @ h).abs() <= 0.012 * (p.abs().t() @ h) + 1e-36).all())
+
+
+@gpu
+@pytest.mark.parametrize("T,grad", [(1, False), (2, True), (4, True), (40, True), (40, False), (300, True)])
+def test_no_finite_logit(ss, T, grad):
+    """Every logit -inf, or the only class's NaN: no loss is defined.  A lone finite class has a loss of 0."""
+    for V, value in ((1, math.nan), (1, -math.inf), (70, -math.inf)):
+        c = Case(T, V, 72, seed=10)
+        c.h.abs_()
+        c.w[:] = value
+        c.run(ss, dh=grad, dw=grad)
+        assert math.isnan(float(c.loss)) and bool(c.token_loss.isnan().all()), (V, value)
+        if grad:
+            assert bool(c.dh.isnan().all()) and bool(c.dw.isnan().all()), (V, value)
+    c = Case(T, 1, 72, seed=10).run(ss, dh=grad, dw=grad)
+    assert float(c.loss) == 0.0 and bool((c.token_loss == 0).all())
+    if grad:
+        assert bool((c.dh == 0).all()) and bool((c.dw == 0).all())
+
+
 @gpu
 @pytest.mark.parametrize("T,grad", [(1, False), (2, True), (3, False), (4, False), (4, True), (30, True), (150, False),
                                     (150, True)])
