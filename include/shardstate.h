@@ -525,7 +525,7 @@ int ss_grad_norm(int num_tensors, const int64_t* numels, const int* elem_bytes,
  *   out         HOST array [num_tensors] of device pointers, or NULL for in
  *               place.  Each is its own input's address or overlaps no input
  *               and no other output; any element alignment.
- *   max_norm    >= 0; +infinity never clips.
+ *   max_norm    >= 0; +infinity never clips (c is 1 for an infinite norm too).
  * In place, nothing is written when c is 1.
  * Errors: as ss_grad_norm.
  */
@@ -561,7 +561,7 @@ int fsdp_reduce_scatter_norm(const ss_plan* plan, const void* const* rank_grads,
  *   sq_sums       device, num_sums doubles, summed in a fixed order: the sq_out of
  *                 every group (and of other plans whose gradients the norm
  *                 spans).
- *   max_norm      >= 0; +infinity never clips.
+ *   max_norm      >= 0; +infinity never clips (c is 1 for an infinite norm too).
  *   master        nullable: the recipe without fp32 master weights.
  *   norm_out      device, 2 floats.
  * The other arguments are fsdp_reduce_scatter_adamw's; bf16 and fp32 plans.

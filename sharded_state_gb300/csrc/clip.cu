@@ -5,7 +5,7 @@
 //   n = sqrt(sum over every element of x^2),  c = min(1, max_norm / (n + 1e-6)),
 //   x <- c * x
 // (c is NaN where n is; n is +inf once a square passes fp32, from |x| = 1.8e19
-// on, and c is then 0).  Nothing can be scaled before everything has been
+// on, and c is then 0; a max_norm of +inf never clips, whatever n is).  Nothing can be scaled before everything has been
 // read, so the work is two passes over the data with the factor between them:
 //
 //   pass 1  each CTA squares and sums its part of the elements in fp32 (at most
@@ -43,6 +43,7 @@ constexpr int kTileBlocks = kThreads * kVecs;    // 16 KiB: a tile is one of the
 constexpr int kTab = 512;                        // tensors per launch
 constexpr int kTabSmall = 16;                    // of the one-cluster form (a short parameter block)
 constexpr double kEps = 1e-6;                    // added to the norm in the factor's denominator
+constexpr double kNormOnly = -1.0;               // max_norm of a call that scales nothing: its factor is 1
 constexpr int kFoldSpan = 8192;                  // partials summed by one CTA of the first fold
 
 // The workspace: fp32 partials, then the doubles of a first fold.
@@ -183,7 +184,8 @@ fold_kernel(const float* __restrict__ partials, int64_t n, double* __restrict__ 
 
 // The norm and the factor of a sum of squares, in fp32 where the sum is in its
 // range (fp64 roots and quotients take hundreds of clocks).  A NaN norm gives a
-// NaN factor (min would drop it).
+// NaN factor (min would drop it); an infinite one is not divided into an infinite
+// max_norm.
 __device__ __forceinline__ void write_norm(double sq, double max_norm, float* norm_out) {
     float norm, c;
     if (sq > 1e-30 && sq < 1e38) {
@@ -194,8 +196,9 @@ __device__ __forceinline__ void write_norm(double sq, double max_norm, float* no
         norm = (float)n;
         c = (float)(max_norm / (n + kEps));
     }
+    const bool unclipped = max_norm < 0.0 || c >= 1.0f || (isinf(max_norm) && !isnan(norm));
     norm_out[0] = norm;
-    norm_out[1] = c >= 1.0f ? 1.0f : c;
+    norm_out[1] = unclipped ? 1.0f : c;
 }
 
 // Last fold, one CTA: the sum of n partials, as it is (sq_out) or as norm and
@@ -887,7 +890,7 @@ int ss_grad_norm(int num_tensors, const int64_t* numels, const int* elem_bytes, 
     if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
     if (!ss::aligned(norm_out, 4)) return SS_EALIGN;
     if (int rc = check_list(num_tensors, numels, elem_bytes, grads, nullptr)) return rc;
-    return list_call(num_tensors, numels, elem_bytes, grads, nullptr, false, INFINITY, norm_out, workspace,
+    return list_call(num_tensors, numels, elem_bytes, grads, nullptr, false, kNormOnly, norm_out, workspace,
                      reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -935,7 +938,7 @@ int fsdp_reduce_scatter_norm(const ss_plan* plan, const void* const* rank_grads,
     if (int rc = ss::launch(fn, n, kThreads, 0, 0, true, st, rp, plan->N, s, (int)rounds, reduced_grad,
                             static_cast<float*>(workspace), nullptr))
         return rc;
-    return fold(workspace, n, INFINITY, sq_out, nullptr, st);
+    return fold(workspace, n, kNormOnly, sq_out, nullptr, st);
 }
 
 int fsdp_clip_adamw(const ss_plan* plan, const float* reduced_grad, const double* sq_sums, int num_sums,

@@ -124,6 +124,44 @@ def test_not_finite(ss, bad, norm_is, factor_is):
         assert math.isnan(float(ts[0][512]))  # inf * 0
 
 
+FORM_LISTS = {"cluster": [1000, 77], "cooperative": [300_000, 77], "two_launches": [30_000_001, 77]}
+
+
+@gpu
+@pytest.mark.parametrize("bad", [math.inf, 3e38])
+@pytest.mark.parametrize("form", FORM_LISTS)
+def test_unlimited_with_an_infinite_norm(ss, form, bad):
+    """max_norm = +inf never clips: an infinite norm leaves every element as it is."""
+    ts, _ = tensors(FORM_LISTS[form], [F32, BF], [1, 3])
+    ts[0][512] = bad
+    was = [t.clone() for t in ts]
+    outs = [torch.empty_like(t) for t in ts]
+    norm = torch.empty(2, device="cuda")
+    ss.ss_clip_grads(ts, math.inf, norm, workspace(ss), out=outs)
+    assert norm.tolist() == [math.inf, 1.0]
+    for x, o in zip(was, outs):
+        assert torch.equal(x, o)
+    ss.ss_clip_grads(ts, math.inf, norm, workspace(ss))
+    for x, t in zip(was, ts):
+        assert torch.equal(x, t)
+    ts[0][512] = math.nan
+    ss.ss_clip_grads(ts, math.inf, norm, workspace(ss))
+    assert bool(norm.isnan().all()) and bool(ts[1].isnan().all())
+
+
+@gpu
+@pytest.mark.parametrize("bad", [math.nan, math.inf, 3e38])
+@pytest.mark.parametrize("form", FORM_LISTS)
+def test_norm_alone_not_finite(ss, form, bad):
+    """The norm alone has a factor of 1, whatever the norm."""
+    ts, _ = tensors(FORM_LISTS[form], [F32, BF], [1, 3])
+    ts[0][512] = bad
+    norm = torch.empty(2, device="cuda")
+    ss.ss_grad_norm(ts, norm, workspace(ss))
+    assert float(norm[1]) == 1.0
+    assert math.isnan(float(norm[0])) if math.isnan(bad) else float(norm[0]) == math.inf
+
+
 @gpu
 def test_zero_and_unlimited(ss):
     ts, _ = tensors([500], [BF], [1])
@@ -272,6 +310,24 @@ def test_unclipped_is_the_plain_step(ss, kind, with_master):
     assert float(a.norm[1]) == 1.0
     for x, y in zip(a.state(), b.state()):
         assert torch.equal(x, y)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["tiny", "flat_true_5_fp32"])
+def test_unlimited_step_with_an_infinite_norm(ss, kind):
+    """max_norm = +inf and a gradient whose square passes fp32: the plain step, bit for bit."""
+    a, b = Sharded(ss, kind), Sharded(ss, kind)
+    for s in (a, b):
+        s.grads[0][5] = 3e38
+    red, sq = torch.empty(a.total, device="cuda"), torch.empty(1, dtype=torch.float64, device="cuda")
+    hp = ss.adamw_params()
+    ss.fsdp_reduce_scatter_norm(a.plan, a.grads, red, sq, workspace(ss))
+    ss.fsdp_clip_adamw(a.plan, red, sq, math.inf, a.master, a.m, a.v, a.shards, hp, a.norm)
+    ss.fsdp_reduce_scatter_adamw(b.plan, b.grads, b.master, b.m, b.v, b.shards, hp)
+    assert a.norm.tolist() == [math.inf, 1.0]
+    for x, y in zip(a.state(), b.state()):
+        assert torch.equal(x, y)
+    assert bool(a.master.isfinite().any())
 
 
 @gpu
