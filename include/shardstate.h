@@ -457,6 +457,10 @@ enum { SS_LOSS_MEAN = 0, SS_LOSS_SUM = 1 };
  * into the gradients.  Weight rows on 16-byte boundaries (an aligned address
  * and a stride that is a multiple of 8) are read in place, others are copied to
  * the workspace first.  The same inputs give the same bits.
+ *
+ * Should a wait inside a kernel run out (two seconds; none does but by a fault of
+ * the device), the loss is NaN; where it was in the statistics, so are the token
+ * losses that count and the gradients, else the gradients are undefined.
  */
 typedef struct {
     int64_t num_tokens;   /* T >= 0 */
@@ -588,6 +592,13 @@ const char* ss_version(void);
 /* Number of kernels this library has launched in this process (all devices,
  * all threads), for accounting launches inside a timed region. */
 uint64_t ss_launch_count(void);
+
+/* For testing how a kernel that gives up is reported: this process's next
+ * ss_linear_cross_entropy call gets a wait that nothing ends, and that runs out,
+ * in its tensor-core launch number `launch` -- 0 forms the statistics, the ones
+ * from 1 on the gradients -- where the call makes that launch.  -1: none.
+ * Everything else of the launch runs as always.  Errors: SS_EINVAL. */
+int ss_linear_ce_expire_wait(int launch);
 
 #ifdef __cplusplus
 }

@@ -48,7 +48,7 @@ EXPORTED = ("fsdp_plan_create", "fsdp_plan_layout", "fsdp_plan_info", "fsdp_plan
             "ss_launch_count", "ddp_bucket_pack_average_noalloc", "fsdp_sharded_step",
             "fsdp_reduce_scatter_accumulate", "fsdp_plan_validate", "ss_grad_norm", "ss_clip_grads",
             "fsdp_reduce_scatter_norm", "fsdp_clip_adamw", "ss_linear_ce_workspace",
-            "ss_linear_cross_entropy")
+            "ss_linear_cross_entropy", "ss_linear_ce_expire_wait")
 
 
 class ShardStateError(RuntimeError):
@@ -139,6 +139,7 @@ def _load() -> ctypes.CDLL:
                              vp, i32, vp], i32),
         "ss_linear_ce_workspace": ([i64, i64, i64, ctypes.c_uint, ctypes.POINTER(ctypes.c_size_t)], i32),
         "ss_linear_cross_entropy": ([ctypes.POINTER(_LinearCE), vp], i32),
+        "ss_linear_ce_expire_wait": ([i32], i32),
         "ss_strerror": ([i32], ctypes.c_char_p),
         "ss_last_cuda_error": ([], i32),
         "ss_version": ([], ctypes.c_char_p),
@@ -622,6 +623,12 @@ def _matrix(fn: str, t, what: str, rows: int, cols: int):
                               f"{what}: bf16 [{rows}, {cols}] on the GPU with unit column stride is wanted")
     stride = t.stride(0)
     return t.data_ptr(), stride if rows > 1 or stride > cols else cols
+
+
+def ss_linear_ce_expire_wait(launch: int) -> None:
+    """Diagnostics: a wait of the next ss_linear_cross_entropy call runs out, in its tensor-core
+    launch number `launch` (0: the statistics, from 1 on the gradients; -1: none)."""
+    _check("ss_linear_ce_expire_wait", _lib.ss_linear_ce_expire_wait(launch))
 
 
 def ss_linear_cross_entropy(hidden, weight, targets, loss_out, workspace, token_loss_out=None, d_hidden=None,

@@ -75,7 +75,7 @@ struct Header {
     int live;      // tokens that count
     float scale;   // of both gradients
     int finished;  // CTAs of the loss kernel that are done
-    int reserved;
+    int failed;    // a wait of this call has run out: nothing behind it means anything
 };
 
 // The products, by what is done with a 256 x 256 tile of them.
@@ -110,10 +110,11 @@ struct GemmArgs {
     int vocab;
     int rows;   // allocated token rows
     float log2e;  // of logits as the products leave them (kDropped)
-    float* loss;  // NaN goes there when a wait runs out
+    float* loss;
     const double* partials;  // this launch sums them to the loss (NULL: it does not)
     int n_partials;
     int mean;
+    int expire;              // diagnostics: put in a wait that nothing ends
     const int* target;       // [rows]
     const int* token;        // [rows]: output row of each row (kHidden)
     const float2* row_loss;  // [rows]: log-sum-exp in base 2, the target's p - 1 (kProbability)
@@ -160,16 +161,30 @@ __device__ __forceinline__ void add_logits(const uint32_t (&r)[32], float log2e,
     m = up;
 }
 
+// A wait has run out: every loss from here on is NaN.  The flag first, then the loss,
+// as sum_losses may be writing it at this moment: whichever of the two fences comes
+// first, the last store is a NaN.
+__device__ __forceinline__ void give_up(Header* header, float* loss) {
+    *static_cast<volatile int*>(&header->failed) = 1;
+    __threadfence();
+    *static_cast<volatile float*>(loss) = NAN;
+}
+
 // The loss, by one warp: the partials' sum in a fixed order, over the tokens that
 // count for a mean, 0 when there are none.
-__device__ __forceinline__ void sum_losses(const double* partials, int n, int live, int mean, float* loss) {
+__device__ __forceinline__ void sum_losses(const Header* header, const double* partials, int n, int live, int mean,
+                                           float* loss) {
     const int lane = threadIdx.x & 31;
     double s = 0.0;
 #pragma unroll 8
     for (int i = lane; i < n; i += 32) s += __ldcg(partials + i);
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, k);
-    if (lane == 0) *loss = (float)(mean && live > 0 ? s / live : s);
+    if (lane == 0) {
+        *static_cast<volatile float*>(loss) = (float)(mean && live > 0 ? s / live : s);
+        __threadfence();
+        if (*static_cast<const volatile int*>(&header->failed)) *static_cast<volatile float*>(loss) = NAN;
+    }
 }
 
 // This lane's row, columns 32 h .. of 64, as bf16 words in its warp's shared memory.
@@ -256,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmArgs g) {
     extern __shared__ unsigned char raw[];
     __shared__ __align__(16) float turn[kEpilogueWarps][32 * 32];
-    __shared__ uint64_t bars[2 * kStages + 4 + 2 * kQueue];
+    __shared__ uint64_t bars[2 * kStages + 4 + 2 * kQueue + 1];
     __shared__ Tile queue[kQueue];
     __shared__ uint32_t tmem_base;
 
@@ -267,6 +282,7 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
     const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
     const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16;
     const uint32_t queue_full = acc_empty + 16, queue_empty = queue_full + 8 * kQueue;
+    const uint32_t never = queue_empty + 8 * kQueue;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -281,6 +297,7 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
             tc::mbar_init(queue_full + 8 * i, 1);
             tc::mbar_init(queue_empty + 8 * i, 2 + 1 + 2 * kEpilogueWarps);  // loaders, issuer, epilogues
         }
+        tc::mbar_init(never, 1);
         tc::mbar_init_fence();
         for (int w = 0; w < g.count; ++w) {
             tc::prefetch_map(&maps.a[w]);
@@ -379,6 +396,8 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
             if (!ok) break;
             tc::commit_pair(acc_full + 8 * (j & 1));
         }
+    } else if (warp == 2 && lane == 0 && first == 0 && rank == 0 && g.expire) {
+        ok = tc::mbar_wait(never, 0);
     } else if (warp == 3 && lane == 0 && rank == 0) {
         for (int j = 0; first < total_tiles(g, live); ++j) {
             const int slot = j % kQueue;
@@ -395,7 +414,7 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
             if (t.w < 0) break;
         }
     } else if (warp == 3 && rank == 1 && first == 0 && g.partials) {
-        sum_losses(g.partials, g.n_partials, live, g.mean, g.loss);
+        sum_losses(g.header, g.partials, g.n_partials, live, g.mean, g.loss);
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const uint32_t acc_empty0 = tc::map_to_rank(acc_empty, 0);
@@ -595,8 +614,11 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
         }
     }
     if (!ok) {
-        *g.loss = NAN;
-        __nanosleep(1000000);  // the copies in flight land before the CTA goes
+        give_up(g.header, g.loss);
+        // copies in flight land before the CTA goes: those that its other roles have asked for since (this
+        // one's own are two seconds old)
+        const uint64_t t0 = tc::global_ns();
+        while (tc::global_ns() - t0 < 1000000ull) __nanosleep(20000);
     }
     __syncwarp();
     tc::fence_before();
@@ -743,6 +765,7 @@ __device__ __forceinline__ void gather_block(const GatherArgs& a, int block, boo
             const int live = sum + __popc(mask);
             a.header->live = live;
             a.header->finished = 0;
+            a.header->failed = 0;
             a.header->scale = a.mean ? (live > 0 ? a.grad_scale / (float)live : 0.f) : a.grad_scale;
         }
     }
@@ -967,7 +990,8 @@ constexpr int kLossSlices = 32;
 // almost all of the mass.  The CTA's losses go to one fp64 partial.  With no
 // gradient to follow, the last CTA to finish sums the partials (sum_losses); else
 // the next launch does, off the gradients' path, and h is given: the gathered hidden
-// states are zeroed from the last row to the next whole k block.
+// states are zeroed from the last row to the next whole k block.  Where the statistics
+// gave up, every token's loss is NaN, and so are the gradients made of it.
 __global__ void __launch_bounds__(kLossThreads)
 ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, int rows,
                const float* __restrict__ target_logit, const int* __restrict__ row_map,
@@ -1007,7 +1031,7 @@ ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, in
     const int row = blockIdx.x * kLossRows + warp;  // from here on a warp's row, a lane's slice
     if (h && row >= live && row < (live + kBlockK - 1) / kBlockK * kBlockK)
         for (int j = lane; j < Dp / 8; j += 32) reinterpret_cast<uint4*>(h + (int64_t)row * Dp)[j] = make_uint4(0, 0, 0, 0);
-    const float hit = row < live ? target_logit[row] : 0.f;
+    const float hit = row >= live ? 0.f : header->failed ? NAN : target_logit[row];
     const int token = row < live ? row_map[row] : 0;
     __syncthreads();
     float top = top_s[lane][warp], sum = sum_s[lane][warp];
@@ -1048,7 +1072,7 @@ ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, in
             last = __shfl_sync(0xFFFFFFFFu, last, 0);
         }
         __syncwarp();
-        if (last) sum_losses(partials, gridDim.x, live, mean, loss_out);
+        if (last) sum_losses(header, partials, gridDim.x, live, mean, loss_out);
     }
 }
 
@@ -1227,6 +1251,9 @@ int launch_gemm(const Maps& maps, GemmArgs& g, int64_t tiles, cudaStream_t st) {
     return rc;
 }
 
+// The matrix launch of the next call that gets a wait which nothing ends (-1: none).
+std::atomic<int> g_expire{-1};
+
 constexpr int64_t kMaxSize = 1 << 28;  // tokens, hidden, vocabulary: 32-bit tile coordinates
 
 bool valid_sizes(int64_t T, int64_t D, int64_t V) { return T >= 0 && D >= 1 && V >= 1; }
@@ -1236,6 +1263,12 @@ bool rows_aligned(const void* p, int64_t ld) { return ss::aligned(p, 16) && ld %
 }  // namespace
 
 extern "C" {
+
+int ss_linear_ce_expire_wait(int launch) {
+    if (launch < -1) return SS_EINVAL;
+    g_expire.store(launch, std::memory_order_relaxed);
+    return SS_OK;
+}
 
 int ss_linear_ce_workspace(int64_t num_tokens, int64_t hidden_size, int64_t vocab_size, unsigned flags,
                            size_t* bytes_out) {
@@ -1272,6 +1305,8 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
     const int pairs = ss::num_sms() / 2;
     const Layout l = plan_layout(T, D, V, grad, stage || D % 8 != 0, pairs);
     if (a->workspace_bytes < (size_t)l.bytes) return SS_EINVAL;
+
+    const int expire = g_expire.exchange(-1, std::memory_order_relaxed);
 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (grad && ss::linear_ce_fits_small(T, D, V)) return ss::linear_ce_small(a, st);
@@ -1346,6 +1381,7 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
             x.splits = 1;
             x.k = (int)D;
             g.count = 1;
+            g.expire = expire == 0;
             if (int rc = launch_gemm(maps, g, m_tiles * l.n_tiles, st)) return rc;
         }
     }
@@ -1441,6 +1477,7 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
         g.partials = i == 0 ? partials : nullptr;
         g.n_partials = (int)loss_blocks;
         g.mean = mean;
+        g.expire = expire == i + 1;
         if (tiles > INT32_MAX - 1024) return SS_EOVERFLOW;
         if (int rc = launch_gemm(maps, g, tiles, st)) return rc;
         if (head.part) {

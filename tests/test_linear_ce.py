@@ -341,6 +341,24 @@ def test_captured(ss, T, V, D):
 
 
 @gpu
+@pytest.mark.parametrize("T,grad,launch,reduction", [(300, False, 0, "mean"), (20, False, 0, "sum"), (300, True, 0, "mean"),
+                                                     (300, True, 1, "sum"), (300, True, 2, "mean"), (3, True, 1, "mean")])
+def test_a_wait_that_runs_out(ss, T, grad, launch, reduction):
+    """One wait that nothing ends gives up by itself: the loss says so, the device stays usable, the next call is right."""
+    c = Case(T, 3000, 136, mask="random" if T > 3 else "none", seed=11)
+    ss.ss_linear_ce_expire_wait(launch)
+    c.run(ss, dh=grad, dw=grad, reduction=reduction)
+    assert math.isnan(float(c.loss))
+    away = c.y == c.ignore
+    assert bool((c.token_loss[away] == 0).all())
+    if launch == 0:
+        assert bool(c.token_loss[~away].isnan().all())
+        if grad:
+            assert bool(c.dh[~away].isnan().all()) and bool(c.dw.isnan().all())
+    c.run(ss, dh=grad, dw=grad, reduction=reduction).check(reduction)
+
+
+@gpu
 def test_workspace_used_again(ss):
     """Another call's leftovers in the workspace change nothing."""
     big, small = Case(600, 2000, 136, seed=1), Case(90, 700, 100, mask="random", seed=2)
@@ -457,6 +475,13 @@ def test_refusals_on_the_host(ss):
     for kw in (dict(num_tokens=1 << 40), dict(vocab_size=1 << 30), dict(weight_stride=1 << 60),
                dict(hidden_stride=1 << 62)):
         assert call(**kw) == ss.SS_EOVERFLOW, kw
+
+
+def test_expired_wait_is_for_one_launch(ss):
+    with pytest.raises(ss.ShardStateError) as e:
+        ss.ss_linear_ce_expire_wait(-2)
+    assert e.value.status == ss.SS_EINVAL
+    ss.ss_linear_ce_expire_wait(-1)
 
 
 @gpu
