@@ -423,6 +423,7 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
             const Tile t = take_tile(j);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok || t.w < 0) break;
+            __syncwarp();  // every lane's read of the queue before the slot is given back
             if (lane == 0) tile_taken(j);
             const Work& x = g.work[t.w];
             const int row0 = t.m * kTile + (int)rank * kHalf + quad * 32, row = row0 + lane;
