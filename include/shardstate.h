@@ -473,7 +473,7 @@ typedef struct {
     const int64_t* targets; /* device [T] */
     int64_t ignore_index;
     int reduction;          /* SS_LOSS_MEAN or SS_LOSS_SUM */
-    double grad_scale;      /* finite: the gradient of the objective by the loss */
+    double grad_scale;      /* finite in fp32: the gradient of the objective by the loss */
     float* loss_out;        /* device, 1 float */
     float* token_loss_out;  /* nullable: device [T] */
     void* d_hidden;         /* nullable: [T, D] */

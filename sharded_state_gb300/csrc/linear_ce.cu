@@ -1289,7 +1289,7 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
     if (T > kMaxSize || D > kMaxSize || V > kMaxSize) return SS_EOVERFLOW;
     if ((T > 0 && (!a->hidden || !a->targets)) || !a->weight || !a->loss_out || !a->workspace) return SS_EINVAL;
     if (a->reduction != SS_LOSS_MEAN && a->reduction != SS_LOSS_SUM) return SS_EINVAL;
-    if (!std::isfinite(a->grad_scale)) return SS_EINVAL;
+    if (!std::isfinite((float)a->grad_scale)) return SS_EINVAL;  // it is used in fp32
     const bool grad = a->d_hidden || a->d_weight;
     if (a->hidden_stride < D || a->weight_stride < D || (a->d_hidden && a->d_hidden_stride < D) ||
         (a->d_weight && a->d_weight_stride < D))

@@ -484,6 +484,15 @@ def test_expired_wait_is_for_one_launch(ss):
     ss.ss_linear_ce_expire_wait(-1)
 
 
+def test_scales_beyond_fp32_are_refused(ss):
+    """A finite scale that fp32 rounds to infinity would turn gradients of 0 to NaN."""
+    import ctypes
+    at = 1 << 20  # an address that is never touched: the workspace's is refused next
+    for scale, want in ((3.5e38, ss.SS_EINVAL), (-1e300, ss.SS_EINVAL), (3.4e38, ss.SS_EALIGN)):
+        a = ss._LinearCE(4, 64, 100, at, 64, at, 64, at, -100, 0, scale, at, None, at, 64, at, 64, at + 16, 1 << 30)
+        assert ss.lib().ss_linear_cross_entropy(ctypes.byref(a), None) == want
+
+
 @gpu
 def test_refusals_of_the_binding(ss):
     c = Case(10, 20, 16)
