@@ -60,12 +60,21 @@ constexpr int kGemmThreads = 32 * (4 + kEpilogueWarps);
 constexpr double kLog2eDouble = 1.4426950408889634;
 constexpr float kLog2e = (float)kLog2eDouble;
 // The tensor cores' accumulator drops what an add shifts out, towards zero, so a
-// logit comes out smaller by a part of itself that grows with the adds.  Measured
-// against 64 bits over hidden sizes 256 to 16384 and logits of scale 0.3 to 7.7, that
-// part is 1.47e-8 to 1.64e-8 for each 16 products; the logits' exponent makes it good.
-// Loss of 4096 tokens at hidden size 4096, relative error against 64 bits: 1.1e-6
-// without, 6e-8 with it (fp32 products: 5.9e-7).
+// logit comes out smaller by a part of itself that grows with the adds: half a unit
+// of the running sum's last place for each 16 products behind the ones that made it.
+// How large the part is depends on where along k a logit comes from.  Measured
+// against 64 bits, for each 16 products: 1.47e-8 to 1.64e-8 for random inputs (hidden
+// sizes 256 to 16384, logits of scale 0.3 to 7.7); with one dominant channel and noise,
+// 2.7e-8 to 4.1e-8 where the channel comes first, 1.3e-8 to 2.2e-8 in the middle,
+// nothing where it comes last; logits that grow evenly along k 1.3e-8 at 1024 and 3.5e-8
+// at 4096; products all of one sign that are tiny beside the sum, 1.9e-7.
+// The logits' exponent makes good a part near the middle of these, which leaves an
+// error of either sign where there was one of one sign; it holds for none of them
+// exactly, and is not raised beyond the hidden sizes that it was measured at.
+// Loss of 4096 random tokens at hidden size 4096, relative error against 64 bits:
+// 1.1e-6 without, 6e-8 with it (fp32 products: 5.9e-7).
 constexpr double kDropped = 1.55e-8;
+constexpr int64_t kDroppedUpTo = 16384;
 
 constexpr float kLn2High = 0.693145751953125f;                               // 16 bits
 constexpr float kLn2Low = (float)(0.6931471805599453 - 0.693145751953125);
@@ -1355,7 +1364,7 @@ int ss_linear_cross_entropy(const ss_linear_ce* a, ss_stream_t stream) {
     g.header = header;
     g.next = counters;
     g.vocab = (int)V;
-    g.log2e = (float)(kLog2eDouble * (1.0 + kDropped * (double)((D + 15) / 16)));
+    g.log2e = (float)(kLog2eDouble * (1.0 + kDropped * (double)((std::min(D, kDroppedUpTo) + 15) / 16)));
     g.rows = (int)l.rows;
     g.target = target;
     g.token = row;

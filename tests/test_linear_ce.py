@@ -306,6 +306,47 @@ def test_nothing_beside_the_rows_is_read(ss, T, grad, D, extra):
     c.run(ss, dh=grad, dw=grad).check()
 
 
+def dominant_channel(ss, D, at):
+    """Mean signed error, relative to the logit, of log-sum-exps that hang on one logit of about 37, which a single
+    channel of the hidden states makes and the others add noise to."""
+    T, V = 1024, 64
+    gen = torch.Generator("cuda").manual_seed(12 + at)
+    h = torch.randn(T, D, generator=gen, device="cuda") * 0.1
+    h[:, at] = 20 + torch.randn(T, generator=gen, device="cuda")
+    w = torch.randn(V, D, generator=gen, device="cuda") * (0.01 / math.sqrt(D))
+    w[0] = torch.randn(D, generator=gen, device="cuda") * 0.02
+    w[0, at] = 37 / 20
+    h, w, y = h.to(BF), w.to(BF), torch.ones(T, dtype=torch.int64, device="cuda")
+    loss, tl = torch.empty(1, device="cuda"), torch.empty(T, device="cuda")
+    ws = torch.empty(ss.ss_linear_ce_workspace(T, D, V, False), dtype=torch.uint8, device="cuda")
+    ss.ss_linear_cross_entropy(h, w, y, loss, ws, token_loss_out=tl)
+    logits = h.double() @ w.double().t()
+    want = torch.logsumexp(logits, 1) - logits[:, 1]
+    return float(((tl.double() - want) / logits[:, 0]).mean())
+
+
+# What the accumulator drops, and what is made good of it.  An add drops what lies below the running sum's 24 bits, half
+# a unit of the last place on average: 2^-25 to 2^-24 of the sum, for each 16 products behind the dominant one.  1.55e-8
+# (just above 2^-26) of each 16 products is added back, up to 16384 of them.  2^-22: the fp32 roundings beside it.
+
+@gpu
+def test_dropped_bits_over_the_positions(ss):
+    """A channel at any place: half of the adds come behind it on average, which leaves 2^-26 to 2^-25 less 1.55e-8."""
+    D = 4096
+    mean = sum(dominant_channel(ss, D, at) for at in range(D // 32, D, D // 16)) / 16
+    assert abs(mean) <= D / 16 * 2.0 ** -26 + 2.0 ** -22
+
+
+@gpu
+@pytest.mark.parametrize("D", [4096, 16384, 65536])
+def test_dropped_bits_first_and_last(ss, D):
+    """A channel at the start, behind which every add drops something, and at the end, where what is added back is the
+    whole error."""
+    back = 1.55e-8 * min(D, 16384) / 16
+    assert abs(dominant_channel(ss, D, 3)) <= D / 16 * 2.0 ** -24 + 2.0 ** -22
+    assert abs(dominant_channel(ss, D, D - 5)) <= back + 2.0 ** -22
+
+
 @gpu
 def test_same_bits_twice_and_on_another_stream(ss):
     c = Case(700, 3001, 136, mask="random")
