@@ -217,6 +217,64 @@ def test_captured(ss, name):
         assert torch.equal(o, (t.float() * norm[1]).to(t.dtype))
 
 
+# Forms that only larger or longer lists take: more than 8192 partials, with a fold launch of their own; more than 256
+# tensors with at most 1024 partials, which the second pass folds itself.
+LONG_LISTS = {
+    "fold_launch": ([70_000_001, 9_999, 600_001], [BF, F32, F32], [5, 1, 3]),
+    "self_folding": ([(i * 37) % 300 + 1 for i in range(400)], [BF if i % 3 else F32 for i in range(400)],
+                     [i % (8 if i % 3 else 4) for i in range(400)]),
+}
+
+
+@gpu
+@pytest.mark.parametrize("name", LONG_LISTS)
+def test_grad_norm_of_long_lists(ss, name, monkeypatch):
+    monkeypatch.setitem(LISTS, name, LONG_LISTS[name])
+    test_grad_norm(ss, name)
+
+
+@gpu
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("clips", [True, False])
+@pytest.mark.parametrize("name", LONG_LISTS)
+def test_clip_long_lists(ss, name, clips, in_place, monkeypatch):
+    monkeypatch.setitem(LISTS, name, LONG_LISTS[name])
+    test_clip_grads(ss, name, clips, in_place)
+
+
+# Above about 17 GB a partial is a sum of 64 values a thread: 72 * 2^-24 of it at most, half of that in the norm, and 2^-24.
+HUGE_RTOL = 2.3e-6
+
+
+def repeated(n, dtype):
+    """n elements of a random block of 2^26 again and again, and the sum of their squares."""
+    gen = torch.Generator("cuda").manual_seed(7)
+    block = (torch.randn(1 << 26, generator=gen, device="cuda") * 1e-2).to(dtype)
+    out = torch.empty(n, dtype=dtype, device="cuda")
+    for a in range(0, n, 1 << 26):
+        out[a:a + (1 << 26)] = block[:min(1 << 26, n - a)]
+    sq = lambda x: float(x.double().square().sum())
+    return out, block, n // (1 << 26) * sq(block) + sq(block[:n % (1 << 26)])
+
+
+@gpu
+def test_clip_more_than_the_partials_hold(ss):
+    """So much that a CTA takes more than one round of tiles: the norm, and clipping in place."""
+    n = 8_700_000_003
+    buf, block, sq = repeated(n, BF)
+    ts = [buf[:5_000_000_001], buf[5_000_000_001:]]  # the second starts 2 bytes past a boundary
+    norm, ws = torch.empty(2, device="cuda"), workspace(ss)
+    ss.ss_grad_norm(ts, norm, ws)
+    want = math.sqrt(sq)
+    assert abs(float(norm[0]) - want) <= HUGE_RTOL * want and float(norm[1]) == 1.0
+    ss.ss_clip_grads(ts, 0.25 * want, norm, ws)
+    c = float(norm[1])
+    assert abs(float(norm[0]) - want) <= HUGE_RTOL * want and abs(c - 0.25) <= HUGE_RTOL
+    scaled = (block.float() * c).to(BF)
+    for a in range(0, n, 1 << 26):
+        assert torch.equal(buf[a:a + (1 << 26)], scaled[:min(1 << 26, n - a)]), a
+
+
 # ---------------------------------------------------------------------------
 # the sharded step
 # ---------------------------------------------------------------------------
@@ -363,6 +421,75 @@ def test_clipped_step(ss, kind, by_group):
         check_adamw_state(s.master.cpu().numpy(), s.m.cpu().numpy(), s.v.cpu().numpy(), th, m, v, prev[0], prev[1],
                           grad)
         assert torch.equal(s.shards, s.master.to(s.ps.dtype))
+
+
+# Groups of more than 608 CTAs' work in either type (1.25 M bf16 elements), which take the factor from a launch of its
+# own, with ranges that start and end inside a 16-byte vector.
+def large_plan(dtype):
+    return W.ParamSet([f"p{i}" for i in range(5)], [(1301, 1003), (7,), (1399, 1001), (5,), (3,)], [2, 2, 1], 3,
+                      W.PER_PARAM_DIM0, dtype, seed=9, uniform=True)
+
+
+@pytest.fixture(params=[BF, F32], ids=["bf16", "fp32"])
+def large(request, monkeypatch):
+    monkeypatch.setitem(globals(), "plan_of", lambda ss, kind: large_plan(request.param))
+
+
+@gpu
+@pytest.mark.parametrize("by_group", [False, True])
+def test_large_reduce_scatter_norm(ss, large, by_group):
+    test_reduce_scatter_norm(ss, "large", by_group)
+
+
+@gpu
+@pytest.mark.parametrize("with_master", [True, False])
+def test_large_unclipped_is_the_plain_step(ss, large, with_master):
+    test_unclipped_is_the_plain_step(ss, "large", with_master)
+
+
+@gpu
+@pytest.mark.parametrize("by_group", [False, True])
+def test_large_clipped_step(ss, large, by_group):
+    test_clipped_step(ss, "large", by_group)
+
+
+@gpu
+@pytest.mark.parametrize("with_master", [True, False])
+def test_large_groups_are_the_whole_plan(ss, large, with_master):
+    """Clipped by the same sums, the groups one by one and the plan at once give the same bits, with and without master,
+    on one stream with nothing between the calls."""
+    a, b = Sharded(ss, "large", with_master), Sharded(ss, "large", with_master)
+    G = len(a.ps.groups)
+    sq = torch.empty(G, dtype=torch.float64, device="cuda")
+    ws = workspace(ss)
+    red = torch.empty(a.total, device="cuda")
+    for step in (1, 2):
+        hp = ss.adamw_params(step=step)
+        for g in range(G):
+            ss.fsdp_reduce_scatter_norm(a.plan, a.grads, red, sq[g:], ws, group=g)
+        for g in range(G):
+            ss.fsdp_clip_adamw(a.plan, red, sq, 0.1, a.master, a.m, a.v, a.shards, hp, a.norm, group=g)
+        ss.fsdp_clip_adamw(b.plan, red, sq, 0.1, b.master, b.m, b.v, b.shards, hp, b.norm)
+    assert torch.equal(a.norm, b.norm) and float(a.norm[1]) < 1.0
+    for x, y in zip(a.state(), b.state()):
+        assert torch.equal(x, y)
+
+
+@gpu
+def test_reduce_scatter_norm_past_32_bits(ss):
+    """More than 2^31 elements, and more CTAs than partials: the mean of two equal ranks is either, bit for bit."""
+    n = (1 << 31) + 8_000_003
+    plan = ss.fsdp_plan_create(W.FLAT_ORIG_FALSE, 2, 2, [n], [1])
+    total = plan.info().total_numel
+    grad, block, sq = repeated(total, BF)
+    red = torch.empty(total, device="cuda")
+    out = torch.empty(1, dtype=torch.float64, device="cuda")
+    ss.fsdp_reduce_scatter_norm(plan, [grad, grad], red, out, workspace(ss))
+    assert abs(float(out[0]) - sq) <= 2 * HUGE_RTOL * sq
+    wide = block.float()
+    for a in range(0, total, 1 << 26):
+        assert torch.equal(red[a:a + (1 << 26)], wide[:min(1 << 26, total - a)]), a
+    plan.destroy()
 
 
 @gpu
