@@ -869,10 +869,11 @@ auto pick_square(int N) {
     }
 }
 
-// CTAs up to which clip_adamw_kernel works its factor out itself, a launch less and
-// some hundred clocks more a CTA: the clipped step of 700 K elements takes 13.9 us so
-// and 16.4 with norm_kernel; at 1.7 M both take 17.0, at 60 M norm_kernel saves 1 %.
-constexpr int64_t kSelfGrid = 4 * 152;
+// CTAs an SM up to which clip_adamw_kernel works its factor out itself, a launch less
+// and some hundred clocks more a CTA: the clipped step of 700 K elements (2.3 CTAs an SM)
+// takes 13.9 us so and 16.4 with norm_kernel; at 1.7 M both take 17.0, at 60 M
+// norm_kernel saves 1 %.
+constexpr int kSelfCtas = 4;
 
 template <bool SELF>
 auto pick_adamw(int eb, bool master) {
@@ -961,7 +962,7 @@ int fsdp_clip_adamw(const ss_plan* plan, const float* reduced_grad, const double
     const Split s = split_range(lo, hi > lo ? hi : lo, 16 / plan->eb);
     const int64_t grid = s.nvec > 0 ? (s.nvec + kThreads - 1) / kThreads : 1;
     unsigned char* shards = static_cast<unsigned char*>(param_shards);
-    if (grid <= kSelfGrid)
+    if (grid <= (int64_t)ss::num_sms() * kSelfCtas)
         return ss::launch(pick_adamw<true>(plan->eb, master), grid, kThreads, 0, 0, true, st, reduced_grad, sq_sums,
                           num_sums, max_norm, norm_out, s, master, exp_avg, exp_avg_sq, shards, c);
     if (int rc = ss::launch(norm_kernel, 1, 32, 0, 0, true, st, sq_sums, num_sums, max_norm, norm_out)) return rc;
