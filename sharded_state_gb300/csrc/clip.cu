@@ -819,8 +819,9 @@ int list_mid(int num_tensors, const int64_t* numels, const int* elem_bytes, cons
     const int64_t most = (int64_t)ss::num_sms() * kMidCtas;
     if (int rc = fill_table(tab, most * kMidRounds, num_tensors, numels, elem_bytes, grads, out)) return rc;
     const int64_t tiles = tab.first[tab.count];
-    return ss::launch_cooperative(list_mid_kernel, tiles < most ? tiles : most, kThreads, st, tab, max_norm,
-                                  scale ? 1 : 0, partials, norm_out);
+    const int rc = ss::launch_cooperative(list_mid_kernel, tiles < most ? tiles : most, kThreads, st, tab, max_norm,
+                                          scale ? 1 : 0, partials, norm_out);
+    return rc == ss::kNotResident ? kNotSmall : rc;
 }
 
 // Partials up to which the second pass folds them itself, in every CTA.

@@ -47,8 +47,10 @@ int launch(void (*kernel)(P...), int64_t grid, int threads, int smem, int cluste
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
 
-// Launch of `grid` CTAs that may wait for one another (all resident at once, or
-// the launch fails).
+// Launch of `grid` CTAs that may wait for one another: all resident at once, or
+// kNotResident and nothing launched (where the stream has a part of the SMs only).
+constexpr int kNotResident = 1;
+
 template <class... P, class... A>
 int launch_cooperative(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t st, A&&... args) {
     cudaLaunchConfig_t cfg = {};
@@ -61,6 +63,10 @@ int launch_cooperative(void (*kernel)(P...), int64_t grid, int threads, cudaStre
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    if (e == cudaErrorCooperativeLaunchTooLarge) {
+        cudaGetLastError();
+        return kNotResident;
+    }
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
 
