@@ -43,7 +43,7 @@ constexpr int kTileBlocks = kThreads * kVecs;    // 16 KiB: a tile is one of the
 constexpr int kTab = 512;                        // tensors per launch
 constexpr int kTabSmall = 16;                    // of the one-cluster form (a short parameter block)
 constexpr double kEps = 1e-6;                    // added to the norm in the factor's denominator
-constexpr double kNormOnly = -1.0;               // max_norm of a call that scales nothing: its factor is 1
+constexpr double kNormOnly = -INFINITY;          // max_norm of a call that scales nothing: its factor is 1
 constexpr int kFoldSpan = 8192;                  // partials summed by one CTA of the first fold
 
 // The workspace: fp32 partials, then the doubles of a first fold.
@@ -190,15 +190,17 @@ __device__ __forceinline__ void write_norm(double sq, double max_norm, float* no
     float norm, c;
     if (sq > 1e-30 && sq < 1e38) {
         norm = __fsqrt_rn((float)sq);
-        c = __fdiv_rn((float)max_norm, norm + (float)kEps);
+        c = __fdiv_rn(fabsf((float)max_norm), norm + (float)kEps);
     } else {
         const double n = sqrt(sq);
         norm = (float)n;
-        c = (float)(max_norm / (n + kEps));
+        if (isinf(max_norm))
+            c = max_norm > 0.0 && isnan(norm) ? norm : 1.0f;
+        else
+            c = (float)(max_norm / (n + kEps));
     }
-    const bool unclipped = max_norm < 0.0 || c >= 1.0f || (isinf(max_norm) && !isnan(norm));
     norm_out[0] = norm;
-    norm_out[1] = unclipped ? 1.0f : c;
+    norm_out[1] = c >= 1.0f ? 1.0f : c;
 }
 
 // Last fold, one CTA: the sum of n partials, as it is (sq_out) or as norm and
