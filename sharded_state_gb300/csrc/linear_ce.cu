@@ -171,8 +171,8 @@ __device__ __forceinline__ void add_logits(const uint32_t (&r)[32], float log2e,
 }
 
 // A wait has run out: every loss from here on is NaN.  The flag first, then the loss,
-// as sum_losses may be writing it at this moment: whichever of the two fences comes
-// first, the last store is a NaN.
+// as the launch may be summing it at this moment: whichever of the two fences (the other
+// is behind that store) comes first, the last store is a NaN.
 __device__ __forceinline__ void give_up(Header* header, float* loss) {
     *static_cast<volatile int*>(&header->failed) = 1;
     __threadfence();
@@ -181,19 +181,14 @@ __device__ __forceinline__ void give_up(Header* header, float* loss) {
 
 // The loss, by one warp: the partials' sum in a fixed order, over the tokens that
 // count for a mean, 0 when there are none.
-__device__ __forceinline__ void sum_losses(const Header* header, const double* partials, int n, int live, int mean,
-                                           float* loss) {
+__device__ __forceinline__ void sum_losses(const double* partials, int n, int live, int mean, float* loss) {
     const int lane = threadIdx.x & 31;
     double s = 0.0;
 #pragma unroll 8
     for (int i = lane; i < n; i += 32) s += __ldcg(partials + i);
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, k);
-    if (lane == 0) {
-        *static_cast<volatile float*>(loss) = (float)(mean && live > 0 ? s / live : s);
-        __threadfence();
-        if (*static_cast<const volatile int*>(&header->failed)) *static_cast<volatile float*>(loss) = NAN;
-    }
+    if (lane == 0) *static_cast<volatile float*>(loss) = (float)(mean && live > 0 ? s / live : s);
 }
 
 // This lane's row, columns 32 h .. of 64, as bf16 words in its warp's shared memory.
@@ -423,7 +418,9 @@ ce_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmAr
             if (t.w < 0) break;
         }
     } else if (warp == 3 && rank == 1 && first == 0 && g.partials) {
-        sum_losses(g.header, g.partials, g.n_partials, live, g.mean, g.loss);
+        sum_losses(g.partials, g.n_partials, live, g.mean, g.loss);
+        __threadfence();
+        if (lane == 0 && *static_cast<volatile int*>(&g.header->failed)) *static_cast<volatile float*>(g.loss) = NAN;
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const uint32_t acc_empty0 = tc::map_to_rank(acc_empty, 0);
@@ -1001,7 +998,7 @@ constexpr int kLossSlices = 32;
 // gradient to follow, the last CTA to finish sums the partials (sum_losses); else
 // the next launch does, off the gradients' path, and h is given: the gathered hidden
 // states are zeroed from the last row to the next whole k block.  Where the statistics
-// gave up, every token's loss is NaN, and so are the gradients made of it.
+// gave up, every token's loss is NaN, and so are the loss and the gradients made of it.
 __global__ void __launch_bounds__(kLossThreads)
 ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, int rows,
                const float* __restrict__ target_logit, const int* __restrict__ row_map,
@@ -1082,7 +1079,7 @@ ce_loss_kernel(Header* header, const float2* __restrict__ stats, int n_tiles, in
             last = __shfl_sync(0xFFFFFFFFu, last, 0);
         }
         __syncwarp();
-        if (last) sum_losses(header, partials, gridDim.x, live, mean, loss_out);
+        if (last) sum_losses(partials, gridDim.x, live, mean, loss_out);
     }
 }
 
