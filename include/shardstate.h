@@ -37,8 +37,9 @@
  *     arrays of device pointers; they are read during the call and may be
  *     reused as soon as it returns.
  *   - The arithmetic never traps: no device-side assert, no trap, and no
- *     kernel waits on another.  Waits inside a kernel (for copies, products and
- *     the other CTAs of a cluster) are bounded or end with the CTAs themselves.
+ *     kernel waits on another.  Waits inside a kernel (for copies, products, the
+ *     other CTAs of a cluster, and in ss_clip_grads and ss_grad_norm the grid of a
+ *     cooperative launch) are bounded or end with the CTAs themselves.
  *
  * Element types: elem_bytes 2 = bf16 (gradients, parameters, shards),
  * elem_bytes 4 = fp32.  Optimizer state is always fp32.

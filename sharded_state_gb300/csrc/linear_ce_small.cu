@@ -259,8 +259,9 @@ static_assert(kMaxSmem <= 222 * 1024, "the largest sizes fit an SM");
 
 namespace ss {
 
-// Device time of a training call, here and by the launches of linear_ce.cu (tokens
-// x vocabulary x hidden size): 50 x 128 x 64 13.9 and 24.9 us, 64 x 256 x 64 17.1 and
+// Time of a training call, here and by the launches of linear_ce.cu, as measured side by
+// side when the rule was chosen (tokens x vocabulary x hidden size): 50 x 128 x 64 13.9 (12.7
+// by now) and 24.9 us, 64 x 256 x 64 17.1 and
 // 25.2, 8 x 512 x 256 22.3 and 27.4, 64 x 64 x 256 28.0 and 27.8; with twice the work
 // those are ahead (64 x 300 x 128 30.9 and 27.2), and without gradients everywhere.
 bool linear_ce_fits_small(int64_t T, int64_t D, int64_t V) {
