@@ -495,6 +495,189 @@ int ss_linear_ce_workspace(int64_t num_tokens, int64_t hidden_size, int64_t voca
 int ss_linear_cross_entropy(const ss_linear_ce* args, ss_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
+/* the residual stream between two layers                                  */
+/* ---------------------------------------------------------------------- */
+
+/*
+ * Dropout.  Of element (r, c) of a [rows, cols] matrix the 16 bits
+ *   u = bits 16 (c % 8) .. 16 (c % 8) + 15 of the 128 bits (lowest first) of
+ *       Philox4x32-10 with key {seed} and counter {c / 8, r, offset}
+ * decide: out = x / (1 - d) where u >= 65536 d, else 0 (whatever x holds), with
+ * d = p rounded to a multiple of 2^-16.  No mask is stored: the backward pass is
+ * the same call on the gradient.
+ *   elem_bytes  2 (bf16) or 4 (fp32): of x and out, row-major with a row stride
+ *               in elements (>= cols) and any element alignment.
+ *   p           in [0, 1), and not so near 1 that d is 1.
+ *   rng         device, {seed, offset}, 64 bits each: read when the call runs, so
+ *               that a captured call draws a new mask once they are changed.
+ *   out         may be x (with its stride); it overlaps no input otherwise.
+ * Errors: SS_EINVAL, SS_EALIGN, SS_EOVERFLOW (2^31 rows, 2^35 columns or strides
+ * beyond 64-bit offsets), SS_ECUDA.
+ */
+int ss_dropout(int64_t rows, int64_t cols, int elem_bytes, const void* x, int64_t x_stride, void* out,
+               int64_t out_stride, double p, const int64_t* rng, ss_stream_t stream);
+
+/*
+ * What happens to the residual stream between two layers:
+ *   h    = dropout(x) + residual, rounded to the type
+ *   rstd = 1 / sqrt(mean over the row of h^2 + eps)
+ *   out  = h * rstd * weight
+ * without the dropout where its probability is 0 and without the residual where
+ * it is NULL; the dropout is ss_dropout's of a [rows, cols] matrix.  Sums and
+ * statistics are fp32 (a square passes it from |h| = 1.8e19 on), out is rounded
+ * once.  A row that holds a NaN is NaN; beside an infinity, which is NaN itself,
+ * the row is 0.  The same inputs give the same bits.
+ *
+ * All matrices are of the type elem_bytes says (2: bf16, 4: fp32), row-major with
+ * a row stride in elements and any element alignment.  sum_out may be x or the
+ * residual, out may be x (each with its stride); outputs overlap no input and no
+ * other output otherwise.
+ */
+typedef struct {
+    int64_t rows; /* >= 0 */
+    int64_t cols; /* 1..32768 */
+    int elem_bytes;
+    const void* x;
+    int64_t x_stride;
+    const void* residual; /* nullable */
+    int64_t residual_stride;
+    const void* weight; /* [cols] */
+    double eps;         /* >= 0, finite in fp32 */
+    double dropout;     /* probability, as ss_dropout's */
+    const int64_t* rng; /* device {seed, offset}; NULL without dropout */
+    void* sum_out;      /* nullable: h */
+    int64_t sum_stride;
+    void* out; /* nullable */
+    int64_t out_stride;
+    float* rstd_out; /* nullable: device [rows] */
+    void* mx_data;   /* nullable: the rows of out as SS_MXFP8, rounded from fp32 */
+    void* mx_scales;
+} ss_norm;
+
+/* At least one output.  Errors: SS_EINVAL, SS_EALIGN, SS_EOVERFLOW, SS_ECUDA. */
+int ss_rms_norm(const ss_norm* args, ss_stream_t stream);
+
+/*
+ * Its gradients, of the h and rstd that it left:
+ *   n = h * rstd, g = d_out * weight
+ *   d_h      = rstd * (g - n * mean over the row of g n) + d_sum: the gradient of
+ *              the sum, and so the residual's
+ *   d_x      = dropout(d_h), with the mask of the forward pass
+ *   d_weight = sum over the rows of d_out * n
+ * d_sum (nullable) is the gradient that reaches h from elsewhere.  Sums are fp32,
+ * in an order that depends on the sizes and the device alone.  d_h may be d_out
+ * or d_sum (with its stride); outputs overlap no input and no other output
+ * otherwise.
+ */
+typedef struct {
+    int64_t rows;
+    int64_t cols; /* 1..32768 */
+    int elem_bytes;
+    const void* d_out;
+    int64_t d_out_stride;
+    const void* h;
+    int64_t h_stride;
+    const void* weight;
+    const float* rstd;
+    const void* d_sum; /* nullable */
+    int64_t d_sum_stride;
+    double dropout;
+    const int64_t* rng;
+    void* d_h; /* nullable */
+    int64_t d_h_stride;
+    void* d_x; /* nullable */
+    int64_t d_x_stride;
+    void* d_weight;  /* nullable: [cols] */
+    void* workspace; /* with d_weight: 16-byte aligned, no contents expected or kept */
+    size_t workspace_bytes;
+} ss_norm_grad;
+
+/* Bytes of workspace ss_rms_norm_backward takes on the current device. */
+int ss_rms_norm_workspace(int64_t rows, int64_t cols, size_t* bytes_out);
+
+/* At least one output.  Errors: as ss_rms_norm. */
+int ss_rms_norm_backward(const ss_norm_grad* args, ss_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* matrices in few bits                                                    */
+/* ---------------------------------------------------------------------- */
+
+/*
+ * Microscaled floats (OCP Microscaling Formats, v1.0): 32 consecutive elements of
+ * a row share a power of two; the elements are e2m1 (SS_MXFP4) or e4m3 (SS_MXFP8).
+ * The scale of a block is 2^(floor(log2 max|x|) - e), e = 2 or 8 (2^-127 at the
+ * least), elements beyond the format's largest (6 or 448) saturate.  A block that
+ * holds an infinity or a NaN is NaN throughout.
+ *
+ * A quantised [rows, cols] matrix is two buffers, 16-byte aligned, of the sizes
+ * that ss_mx_bytes tells:
+ *   data    row r at r * W * (64 or 128) bytes, W = ceil(cols / 128): its elements,
+ *           then zeros to a multiple of 128; of two e2m1 elements in a byte the
+ *           first is the low half.
+ *   scales  [ceil(rows / 128)][W] tiles of 512 bytes: the scale of row r, block b
+ *           (exponent + 127; 255: NaN) at byte 16 (r % 32) + 4 (r % 128 / 32) +
+ *           b % 4 of tile [r / 128][b / 4]; 0 for blocks behind the last column.
+ *           Those of rows behind the last are not written and do not matter.
+ */
+enum { SS_MXFP4 = 0, SS_MXFP8 = 1 };
+
+int ss_mx_bytes(int64_t rows, int64_t cols, int format, size_t* data_bytes, size_t* scale_bytes);
+
+/*
+ * Quantises a matrix, its transpose, or both from one read.  Elements go to the
+ * nearest (ties to even), or, with rng, to one of the two neighbours: up, away from
+ * zero, where the part cut off and u / 65536 make 1, u being the 16 bits that
+ * ss_dropout takes for the element's place in x (the same for the transpose).  With
+ * bf16 inputs the expected value is then the input up to 2^-16 of a step.
+ */
+typedef struct {
+    int64_t rows;
+    int64_t cols;
+    int elem_bytes; /* of x: 2 (bf16) or 4 (fp32) */
+    const void* x;  /* [rows, cols], any element alignment */
+    int64_t stride;
+    int format;
+    void* data; /* nullable with scales */
+    void* scales;
+    void* t_data; /* nullable with t_scales: the transpose's */
+    void* t_scales;
+    const int64_t* rng; /* nullable: device {seed, offset} */
+} ss_mx_quant;
+
+/* Errors: SS_EINVAL, SS_EALIGN, SS_EOVERFLOW, SS_ECUDA. */
+int ss_mx_quantize(const ss_mx_quant* args, ss_stream_t stream);
+
+/* The values that a quantised matrix stands for, rounded to bf16 (elem_bytes 2) or
+ * as they are (4).  Errors: as ss_mx_quantize. */
+int ss_mx_dequantize(int64_t rows, int64_t cols, int format, const void* data, const void* scales, void* out,
+                     int64_t out_stride, int elem_bytes, ss_stream_t stream);
+
+/*
+ * out[m, n] = sum over k of A[m, k] B[n, k] of two quantised matrices of one
+ * format, [M, K] and [N, K]: a linear layer of a [N, K] weight, and, with transposes
+ * from ss_mx_quantize, both its gradients.  Products and sums are the tensor cores'
+ * (fp32 accumulators), out is rounded once to bf16 (elem_bytes 2) or fp32 (4).  The
+ * same inputs give the same bits.  Should a wait inside the kernel run out (two
+ * seconds; none does but by a fault of the device), what it did not reach is NaN.
+ */
+typedef struct {
+    int64_t M;
+    int64_t N;
+    int64_t K; /* >= 1 */
+    int format;
+    const void* a_data;
+    const void* a_scales;
+    const void* b_data;
+    const void* b_scales;
+    void* out; /* [M, N], any element alignment */
+    int64_t out_stride;
+    int elem_bytes; /* of out */
+} ss_mx_product;
+
+/* Errors: SS_EINVAL, SS_EALIGN, SS_EOVERFLOW (sizes above 2^30), SS_ECUDA. */
+int ss_mx_matmul(const ss_mx_product* args, ss_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
 /* gradient norm and clipping                                              */
 /* ---------------------------------------------------------------------- */
 

@@ -37,6 +37,8 @@ SS_LOSS_MEAN = 0
 SS_LOSS_SUM = 1
 SS_CE_GRADIENT = 1
 SS_CE_STAGE_WEIGHT = 2
+SS_MXFP4 = 0
+SS_MXFP8 = 1
 SS_MAX_WORLD = 64
 SS_MAX_REPLICAS = 64
 
@@ -48,7 +50,9 @@ EXPORTED = ("fsdp_plan_create", "fsdp_plan_layout", "fsdp_plan_info", "fsdp_plan
             "ss_launch_count", "ddp_bucket_pack_average_noalloc", "fsdp_sharded_step",
             "fsdp_reduce_scatter_accumulate", "fsdp_plan_validate", "ss_grad_norm", "ss_clip_grads",
             "fsdp_reduce_scatter_norm", "fsdp_clip_adamw", "ss_linear_ce_workspace",
-            "ss_linear_cross_entropy", "ss_linear_ce_expire_wait")
+            "ss_linear_cross_entropy", "ss_linear_ce_expire_wait", "ss_dropout", "ss_rms_norm",
+            "ss_rms_norm_workspace", "ss_rms_norm_backward", "ss_mx_bytes", "ss_mx_quantize", "ss_mx_dequantize",
+            "ss_mx_matmul")
 
 
 class ShardStateError(RuntimeError):
@@ -102,6 +106,39 @@ class _LinearCE(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class _Norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("elem_bytes", ctypes.c_int),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("residual", ctypes.c_void_p),
+                ("residual_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("eps", ctypes.c_double),
+                ("dropout", ctypes.c_double), ("rng", ctypes.c_void_p), ("sum_out", ctypes.c_void_p),
+                ("sum_stride", ctypes.c_int64), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("rstd_out", ctypes.c_void_p), ("mx_data", ctypes.c_void_p), ("mx_scales", ctypes.c_void_p)]
+
+
+class _NormGrad(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("elem_bytes", ctypes.c_int),
+                ("d_out", ctypes.c_void_p), ("d_out_stride", ctypes.c_int64), ("h", ctypes.c_void_p),
+                ("h_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("d_sum", ctypes.c_void_p), ("d_sum_stride", ctypes.c_int64), ("dropout", ctypes.c_double),
+                ("rng", ctypes.c_void_p), ("d_h", ctypes.c_void_p), ("d_h_stride", ctypes.c_int64),
+                ("d_x", ctypes.c_void_p), ("d_x_stride", ctypes.c_int64), ("d_weight", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class _MxQuant(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("elem_bytes", ctypes.c_int),
+                ("x", ctypes.c_void_p), ("stride", ctypes.c_int64), ("format", ctypes.c_int),
+                ("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("t_data", ctypes.c_void_p),
+                ("t_scales", ctypes.c_void_p), ("rng", ctypes.c_void_p)]
+
+
+class _MxProduct(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("format", ctypes.c_int),
+                ("a_data", ctypes.c_void_p), ("a_scales", ctypes.c_void_p), ("b_data", ctypes.c_void_p),
+                ("b_scales", ctypes.c_void_p), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("elem_bytes", ctypes.c_int)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python sharded_state_gb300/build.py` "
@@ -140,6 +177,14 @@ def _load() -> ctypes.CDLL:
         "ss_linear_ce_workspace": ([i64, i64, i64, ctypes.c_uint, ctypes.POINTER(ctypes.c_size_t)], i32),
         "ss_linear_cross_entropy": ([ctypes.POINTER(_LinearCE), vp], i32),
         "ss_linear_ce_expire_wait": ([i32], i32),
+        "ss_dropout": ([i64, i64, i32, vp, i64, vp, i64, ctypes.c_double, vp, vp], i32),
+        "ss_rms_norm": ([ctypes.POINTER(_Norm), vp], i32),
+        "ss_rms_norm_workspace": ([i64, i64, ctypes.POINTER(ctypes.c_size_t)], i32),
+        "ss_rms_norm_backward": ([ctypes.POINTER(_NormGrad), vp], i32),
+        "ss_mx_bytes": ([i64, i64, i32, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)], i32),
+        "ss_mx_quantize": ([ctypes.POINTER(_MxQuant), vp], i32),
+        "ss_mx_dequantize": ([i64, i64, i32, vp, vp, vp, i64, i32, vp], i32),
+        "ss_mx_matmul": ([ctypes.POINTER(_MxProduct), vp], i32),
         "ss_strerror": ([i32], ctypes.c_char_p),
         "ss_last_cuda_error": ([], i32),
         "ss_version": ([], ctypes.c_char_p),
@@ -658,3 +703,193 @@ def ss_linear_cross_entropy(hidden, weight, targets, loss_out, workspace, token_
                      SS_LOSS_MEAN if reduction == "mean" else SS_LOSS_SUM, grad_scale, loss, token_loss, dh, ld_dh, dw,
                      ld_dw, ws, nbytes)
     _check(fn, _lib.ss_linear_cross_entropy(ctypes.byref(args), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# the residual stream between two layers
+# ---------------------------------------------------------------------------
+
+def _device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def _row_dtype(fn: str, t, what: str):
+    """The type of the bf16 or fp32 matrix that gives a call its sizes."""
+    if t.dim() != 2 or t.dtype not in (_dtype("bfloat16"), _dtype("float32")):
+        raise ShardStateError(fn, SS_EINVAL, f"{what}: a bf16 or fp32 matrix is wanted")
+    return t.dtype
+
+
+def _rows(fn: str, t, what: str, rows: int, cols: int, dtype, device: int):
+    """Address and row stride of a matrix of that type on the current device (NULL, 0 for None)."""
+    if t is None:
+        return None, 0
+    if t.get_device() != device or t.dtype != dtype or t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1):
+        raise ShardStateError(fn, SS_EINVAL, f"{what}: {dtype} [{rows}, {cols}] on the current GPU with unit column "
+                                             "stride is wanted")
+    stride = t.stride(0)
+    return t.data_ptr(), stride if rows > 1 or stride > cols else cols
+
+
+def _flat(fn: str, t, what: str, dtype, numel: int, device: int) -> Optional[int]:
+    """Address of a contiguous tensor of at least numel elements on the current device (NULL for None)."""
+    if t is None:
+        return None
+    if t.get_device() != device or t.dtype != dtype or t.numel() < numel or not t.is_contiguous():
+        raise ShardStateError(fn, SS_EINVAL, f"{what}: contiguous {dtype} on the current GPU, at least {numel} elements")
+    return t.data_ptr()
+
+
+def ss_dropout(x, out, p: float, rng, stream=None) -> None:
+    """out = dropout(x) with probability p (in steps of 2^-16), for bf16 or fp32
+    matrices (rows may be strided; out may be x): the mask follows from rng (2 int64 on
+    the device: seed, offset) and from each element's place, and the same call on a
+    gradient is the backward pass."""
+    fn = "ss_dropout"
+    dtype, dev = _row_dtype(fn, x, "x"), _device()
+    rows, cols = x.shape
+    ax, ldx = _rows(fn, x, "x", rows, cols, dtype, dev)
+    ao, ldo = _rows(fn, out, "out", rows, cols, dtype, dev)
+    status = _lib.ss_dropout(rows, cols, x.element_size(), ax, ldx, ao, ldo, p,
+                             _flat(fn, rng, "rng", _dtype("int64"), 2, dev), _stream(stream))
+    if status != SS_OK:
+        _check(fn, status)
+
+
+def ss_rms_norm(x, weight, eps: float, out=None, residual=None, sum_out=None, rstd_out=None, mx_data=None,
+                mx_scales=None, dropout: float = 0.0, rng=None, stream=None) -> None:
+    """h = dropout(x) + residual (into sum_out), out = h * rstd * weight with
+    rstd = 1 / sqrt(mean(h^2) + eps) of each row (into rstd_out [rows], fp32); x,
+    residual, sum_out and out are bf16 or fp32 matrices of one type (rows may be
+    strided; sum_out may be x or residual, out may be x), weight [cols] too.  mx_data
+    and mx_scales get out as SS_MXFP8 (buffers of ss_mx_bytes).  At least one output is
+    wanted; residual and dropout are optional."""
+    fn = "ss_rms_norm"
+    dtype, dev = _row_dtype(fn, x, "x"), _device()
+    rows, cols = x.shape
+    ax, ldx = _rows(fn, x, "x", rows, cols, dtype, dev)
+    ar, ldr = _rows(fn, residual, "residual", rows, cols, dtype, dev)
+    ah, ldh = _rows(fn, sum_out, "sum_out", rows, cols, dtype, dev)
+    ao, ldo = _rows(fn, out, "out", rows, cols, dtype, dev)
+    if weight is None or weight.numel() != cols:
+        raise ShardStateError(fn, SS_EINVAL, f"weight: {cols} elements are wanted")
+    md, ms = _mx_buffers(fn, mx_data, mx_scales, "mx", rows, cols, SS_MXFP8, dev)
+    args = _Norm(rows, cols, x.element_size(), ax, ldx, ar, ldr, _flat(fn, weight, "weight", dtype, cols, dev), eps,
+                 dropout, _flat(fn, rng, "rng", _dtype("int64"), 2, dev), ah, ldh, ao, ldo,
+                 _flat(fn, rstd_out, "rstd_out", _dtype("float32"), rows, dev), md, ms)
+    status = _lib.ss_rms_norm(ctypes.byref(args), _stream(stream))
+    if status != SS_OK:
+        _check(fn, status)
+
+
+def ss_rms_norm_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace ss_rms_norm_backward takes on the current device."""
+    out = ctypes.c_size_t()
+    _check("ss_rms_norm_workspace", _lib.ss_rms_norm_workspace(rows, cols, ctypes.byref(out)))
+    return out.value
+
+
+def ss_rms_norm_backward(d_out, h, weight, rstd, d_h, workspace, d_sum=None, d_x=None, d_weight=None,
+                         dropout: float = 0.0, rng=None, stream=None) -> None:
+    """Gradients of ss_rms_norm from what it left (h, its sum_out, and rstd): d_h is the
+    gradient of the sum, d_sum included (the part that reaches h from elsewhere); d_x that
+    of x behind the forward pass's dropout; d_weight [cols] that of the weight.  d_h (which
+    may be d_out or d_sum), d_x and d_weight are optional; the workspace
+    (ss_rms_norm_workspace bytes) is for d_weight."""
+    fn = "ss_rms_norm_backward"
+    dtype, dev = _row_dtype(fn, h, "h"), _device()
+    rows, cols = h.shape
+    ay, ldy = _rows(fn, d_out, "d_out", rows, cols, dtype, dev)
+    ah, ldh = _rows(fn, h, "h", rows, cols, dtype, dev)
+    as_, lds = _rows(fn, d_sum, "d_sum", rows, cols, dtype, dev)
+    ag, ldg = _rows(fn, d_h, "d_h", rows, cols, dtype, dev)
+    ax, ldx = _rows(fn, d_x, "d_x", rows, cols, dtype, dev)
+    for name, t in (("weight", weight), ("d_weight", d_weight)):
+        if t is not None and t.numel() != cols:
+            raise ShardStateError(fn, SS_EINVAL, f"{name}: {cols} elements are wanted")
+    ws, nbytes = (None, 0) if workspace is None else _workspace(fn, workspace)
+    args = _NormGrad(rows, cols, h.element_size(), ay, ldy, ah, ldh, _flat(fn, weight, "weight", dtype, cols, dev),
+                     _flat(fn, rstd, "rstd", _dtype("float32"), rows, dev), as_, lds, dropout,
+                     _flat(fn, rng, "rng", _dtype("int64"), 2, dev), ag, ldg, ax, ldx,
+                     _flat(fn, d_weight, "d_weight", dtype, cols, dev), ws, nbytes)
+    status = _lib.ss_rms_norm_backward(ctypes.byref(args), _stream(stream))
+    if status != SS_OK:
+        _check(fn, status)
+
+
+# ---------------------------------------------------------------------------
+# matrices in few bits
+# ---------------------------------------------------------------------------
+
+def ss_mx_bytes(rows: int, cols: int, format: int):
+    """(bytes of data, bytes of scales) of a [rows, cols] matrix in SS_MXFP4 or SS_MXFP8."""
+    data, scales = ctypes.c_size_t(), ctypes.c_size_t()
+    _check("ss_mx_bytes", _lib.ss_mx_bytes(rows, cols, format, ctypes.byref(data), ctypes.byref(scales)))
+    return data.value, scales.value
+
+
+def _mx_buffers(fn: str, data, scales, what: str, rows: int, cols: int, format: int, device: int):
+    """Addresses of a quantised matrix's buffers, uint8 and large enough (NULL, NULL for None, None)."""
+    if data is None and scales is None:
+        return None, None
+    if data is None or scales is None:
+        raise ShardStateError(fn, SS_EINVAL, f"{what}: data and scales are wanted together")
+    wide = -(-cols // 128)
+    byte = _dtype("uint8")
+    return (_flat(fn, data, what + " data", byte, rows * wide * (64 if format == SS_MXFP4 else 128), device),
+            _flat(fn, scales, what + " scales", byte, -(-rows // 128) * wide * 512, device))
+
+
+def _mx_format(fn: str, format: int) -> None:
+    if format not in (SS_MXFP4, SS_MXFP8):
+        raise ShardStateError(fn, SS_EINVAL, "format: SS_MXFP4 or SS_MXFP8")
+
+
+def ss_mx_quantize(x, format: int, data=None, scales=None, t_data=None, t_scales=None, rng=None, stream=None) -> None:
+    """Quantise a bf16 or fp32 matrix x [R, C] (rows may be strided) to SS_MXFP4 or
+    SS_MXFP8: along its rows into data and scales, along its columns (x.T, [C, R]) into
+    t_data and t_scales, either or both from one read; uint8 buffers of ss_mx_bytes.  To
+    the nearest, or stochastically with rng (2 int64 on the device: seed, offset)."""
+    fn = "ss_mx_quantize"
+    dtype, dev = _row_dtype(fn, x, "x"), _device()
+    _mx_format(fn, format)
+    rows, cols = x.shape
+    ax, ldx = _rows(fn, x, "x", rows, cols, dtype, dev)
+    d, s = _mx_buffers(fn, data, scales, "quantised", rows, cols, format, dev)
+    td, ts = _mx_buffers(fn, t_data, t_scales, "transposed", cols, rows, format, dev)
+    args = _MxQuant(rows, cols, x.element_size(), ax, ldx, format, d, s, td, ts,
+                    _flat(fn, rng, "rng", _dtype("int64"), 2, dev))
+    status = _lib.ss_mx_quantize(ctypes.byref(args), _stream(stream))
+    if status != SS_OK:
+        _check(fn, status)
+
+
+def ss_mx_dequantize(data, scales, format: int, out, stream=None) -> None:
+    """The values of a quantised matrix into out [R, C], bf16 or fp32 (rows may be strided)."""
+    fn = "ss_mx_dequantize"
+    dtype, dev = _row_dtype(fn, out, "out"), _device()
+    _mx_format(fn, format)
+    rows, cols = out.shape
+    ao, ldo = _rows(fn, out, "out", rows, cols, dtype, dev)
+    d, s = _mx_buffers(fn, data, scales, "quantised", rows, cols, format, dev)
+    status = _lib.ss_mx_dequantize(rows, cols, format, d, s, ao, ldo, out.element_size(), _stream(stream))
+    if status != SS_OK:
+        _check(fn, status)
+
+
+def ss_mx_matmul(a_data, a_scales, b_data, b_scales, K: int, format: int, out, stream=None) -> None:
+    """out [M, N] (bf16 or fp32, rows may be strided) = A B^T of two quantised matrices
+    of one format, A [M, K] and B [N, K]: a linear layer whose weight is B, and with the
+    transposes of ss_mx_quantize both of its gradients."""
+    fn = "ss_mx_matmul"
+    dtype, dev = _row_dtype(fn, out, "out"), _device()
+    _mx_format(fn, format)
+    M, N = out.shape
+    ao, ldo = _rows(fn, out, "out", M, N, dtype, dev)
+    ad, as_ = _mx_buffers(fn, a_data, a_scales, "A", M, K, format, dev)
+    bd, bs = _mx_buffers(fn, b_data, b_scales, "B", N, K, format, dev)
+    args = _MxProduct(M, N, K, format, ad, as_, bd, bs, ao, ldo, out.element_size())
+    status = _lib.ss_mx_matmul(ctypes.byref(args), _stream(stream))
+    if status != SS_OK:
+        _check(fn, status)

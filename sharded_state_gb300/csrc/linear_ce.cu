@@ -43,6 +43,7 @@
 #include "launch.cuh"
 #include "segmap.cuh"
 #include "tcgen05.cuh"
+#include "tma_host.h"
 
 namespace {
 
@@ -1191,27 +1192,10 @@ Layout plan_layout(int64_t T, int64_t D, int64_t V, bool grad, bool stage, int p
     return l;
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder() {
-    static const EncodeTiled fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
 // A [rows][cols] bf16 matrix of row stride ld, in boxes of 64 columns and
 // box_rows rows, out-of-range elements read as zero.
 int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
-    const EncodeTiled fn = encoder();
+    const ss::EncodeTiled fn = ss::tensor_map_encoder();
     if (!fn) return ss::cuda_fail(cudaErrorNotSupported);
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
@@ -1228,31 +1212,18 @@ int launch(K kernel, int64_t grid, int threads, int smem, cudaStream_t st, A&&..
     return ss::launch(kernel, grid, threads, smem, 0, true, st, args...);
 }
 
-// Raises a kernel's limit of dynamic shared memory, once for each device.
-int allow_smem(std::atomic<uint64_t>& ready, const void* kernel, int bytes) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return ss::cuda_fail(e);
-    const uint64_t bit = 1ull << (dev & 63);
-    if (ready.load(std::memory_order_acquire) & bit) return SS_OK;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return ss::cuda_fail(e);
-    if (dev < 64) ready.fetch_or(bit, std::memory_order_release);
-    return SS_OK;
-}
-
 template <int TOKENS>
 int launch_few(const GatherArgs& a, const uint16_t* w, int64_t ldw, int64_t slices, int64_t rows,
                float2* stats, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
     const auto kernel = ce_few_kernel<TOKENS, few_rows(TOKENS)>;
-    if (int rc = allow_smem(ready, reinterpret_cast<const void*>(kernel), kFewSmem)) return rc;
+    if (int rc = ss::allow_smem(ready, reinterpret_cast<const void*>(kernel), kFewSmem)) return rc;
     return launch(kernel, slices + 1, kThreads, TOKENS * a.Dp * 2, st, a, w, ldw, (int)rows, stats);
 }
 
 int launch_gemm(const Maps& maps, GemmArgs& g, int64_t tiles, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
-    if (int rc = allow_smem(ready, reinterpret_cast<const void*>(ce_gemm_kernel), kSmemBytes)) return rc;
+    if (int rc = ss::allow_smem(ready, reinterpret_cast<const void*>(ce_gemm_kernel), kSmemBytes)) return rc;
     const int64_t pairs = ss::num_sms() / 2;
     const int rc = launch(ce_gemm_kernel, 2 * (tiles < pairs ? tiles : pairs), kGemmThreads, kSmemBytes, st, maps, g);
     ++g.next;

@@ -1,0 +1,531 @@
+// mx_matmul.cu -- products of microscaled matrices on the tensor cores:
+//
+//   out[m, n] = sum_k A[m, k] B[n, k],  A[m, k] = 2^sa[m, k / 32] a[m, k], B alike
+//
+// Elements and scales go to the tensor cores as they are stored (mx.cuh): TMA brings
+// 128 bytes of k of each row and the tiles of scales that belong to them to shared
+// memory, the scales go on to tensor memory, the accumulators are fp32.
+//
+// Two kernels.  Where there are tiles enough for every pair of SMs, a pair takes tiles
+// of 256 x 256; else one CTA takes 128 rows of one operand and up to 128 of the other,
+// and a cluster of up to 8 shares k, so that few tokens read a weight with every SM.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <utility>
+
+#include "device_utils.cuh"
+#include "internal.h"
+#include "launch.cuh"
+#include "mx.cuh"
+#include "tcgen05.cuh"
+#include "tma_host.h"
+
+namespace {
+
+namespace tc = ss::tc;
+using ss::launch_after;
+using ss::wait_before;
+
+constexpr int kRowBytes = 128;               // of k a stage
+constexpr int kHalf = 128;                   // rows of an operand that a CTA holds
+constexpr int kOperand = kHalf * kRowBytes;  // bytes
+
+// Tiles of scales (128 elements of k) a stage, and their bytes for 128 rows.
+__host__ __device__ constexpr int scale_tiles(int format) { return format == SS_MXFP4 ? 2 : 1; }
+__host__ __device__ constexpr int scale_bytes(int format) { return scale_tiles(format) * ss::kMxTileBytes; }
+
+// data: rows of bytes; scales: words, a row of them for each 128 rows.
+struct Maps {
+    CUtensorMap a, b, a_scales, b_scales;
+};
+
+// After a wait that ran out: copies in flight land before the CTA goes (its other
+// roles' since; its own are two seconds old).
+__device__ __forceinline__ void let_copies_land() {
+    const uint64_t t0 = tc::global_ns();
+    while (tc::global_ns() - t0 < 1000000ull) __nanosleep(20000);
+}
+
+// The products of one stage: per tile of scales its copies to tensor memory (A's 4
+// columns, then B's, 4 for each 128 rows), then an instruction for each 32 bytes of k.
+template <int FORMAT, bool PAIR>
+__device__ __forceinline__ void stage_products(uint32_t d, uint32_t scales, uint32_t a, uint32_t b, uint32_t sa,
+                                               uint32_t sb, uint32_t idesc, bool accumulate) {
+    constexpr bool FOUR = FORMAT == SS_MXFP4;
+    constexpr int T = scale_tiles(FORMAT), per = 4 / T;  // instructions for a tile of scales
+    const uint64_t da = tc::operand_desc(a, 16, 1024), db = tc::operand_desc(b, 16, 1024);
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        tc::copy_scales<PAIR>(scales, tc::scale_desc(sa + t * ss::kMxTileBytes));
+#pragma unroll
+        for (int r = 0; r < (PAIR ? 2 : 1); ++r)
+            tc::copy_scales<PAIR>(scales + 4 + 4 * r, tc::scale_desc(sb + (r * T + t) * ss::kMxTileBytes));
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+            const uint64_t step = (uint64_t)((t * per + i) * 32 >> 4);
+            tc::mma_scaled<PAIR, FOUR>(d, da + step, db + step, idesc + tc::scale_id(FOUR ? 2 * i : i), scales,
+                                       scales + 4, accumulate || t > 0 || i > 0);
+        }
+    }
+}
+
+__device__ __forceinline__ void store_one(void* out, int64_t at, float v, int elem_bytes) {
+    if (elem_bytes == 2)
+        static_cast<uint16_t*>(out)[at] = ss::f32_to_bf16(v);
+    else
+        static_cast<float*>(out)[at] = v;
+}
+
+// ---------------------------------------------------------------------------
+// 256 x 256 tiles, a pair of CTAs
+// ---------------------------------------------------------------------------
+
+constexpr int kTile = 256;
+constexpr int kStages = 5;
+constexpr int kEpilogueWarps = 8;  // two for each 32 rows, half of the columns each
+constexpr int kColumns = kTile / 2;
+constexpr int kPairThreads = 32 * (4 + kEpilogueWarps);
+
+__host__ __device__ constexpr int pair_stage(int format) {
+    return 2 * kOperand + (3 * scale_bytes(format) + 1023) / 1024 * 1024;
+}
+constexpr int kTurn = 32 * 128;  // bytes of an epilogue warp: 32 rows of 128
+__host__ __device__ constexpr int pair_smem(int format) {
+    return kStages * pair_stage(format) + kEpilogueWarps * kTurn + 1024;
+}
+
+struct PairArgs {
+    int64_t M, N, out_stride;
+    int m_tiles, n_tiles, k_blocks;
+    void* out;
+    int elem_bytes;
+    int vector;  // rows of out on 16 bytes
+};
+
+template <int FORMAT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairArgs g) {
+    extern __shared__ unsigned char raw[];
+    __shared__ uint64_t bars[2 * kStages + 2];
+    __shared__ uint32_t tmem_base;
+    constexpr int kStage = pair_stage(FORMAT), kScales = scale_bytes(FORMAT);
+
+    launch_after();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_ctarank();
+    const uint32_t smem = (tc::smem_addr(raw) + 1023u) & ~1023u;
+    const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
+    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 8;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(full + 8 * i, 1);
+            tc::mbar_init(empty + 8 * i, 1);
+        }
+        tc::mbar_init(acc_full, 1);
+        tc::mbar_init(acc_empty, 2 * kEpilogueWarps);
+        tc::mbar_init_fence();
+        tc::prefetch_map(&maps.a);
+        tc::prefetch_map(&maps.b);
+        tc::prefetch_map(&maps.a_scales);
+        tc::prefetch_map(&maps.b_scales);
+    }
+    if (warp == 2) tc::tmem_alloc(tc::smem_addr(&tmem_base), 512);
+    tc::fence_before();
+    tc::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = tmem_base;
+    wait_before();
+
+    const int first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int64_t tiles = (int64_t)g.m_tiles * g.n_tiles;
+    bool ok = true;
+
+    if (warp == 0 && lane == 0) {
+        int it = 0;
+        for (int64_t id = first; id < tiles && ok; id += pairs) {
+            const int m = (int)(id % g.m_tiles), n = (int)(id / g.m_tiles);
+            for (int k = 0; k < g.k_blocks; ++k, ++it) {
+                const int st = it % kStages;
+                const uint32_t a = smem + st * kStage, b = a + kOperand, sa = b + kOperand, sb = sa + kScales;
+                ok = tc::mbar_wait(empty + 8 * st, ((it / kStages) & 1) ^ 1);
+                if (!ok) break;
+                const uint32_t bar = tc::map_to_rank(full + 8 * st, 0);
+                if (rank == 0) tc::mbar_expect_tx(full + 8 * st, 2 * (2 * kOperand + 3 * kScales));
+                tc::tma_load_2d(a, &maps.a, k * kRowBytes, m * kTile + (int)rank * kHalf, bar);
+                tc::tma_load_2d(b, &maps.b, k * kRowBytes, n * kTile + (int)rank * kHalf, bar);
+                // each CTA's own rows of A; all rows of B, which both multiply with
+                tc::tma_load_2d(sa, &maps.a_scales, k * (kScales / 4), m * 2 + (int)rank, bar);
+                tc::tma_load_2d(sb, &maps.b_scales, k * (kScales / 4), n * 2, bar);
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        const uint32_t idesc = tc::scaled_desc(FORMAT == SS_MXFP4, kTile, kTile);
+        int it = 0, j = 0;
+        for (int64_t id = first; id < tiles; id += pairs, ++j) {
+            ok = tc::mbar_wait(acc_empty, (j & 1) ^ 1);
+            if (!ok) break;
+            tc::fence_after();
+            for (int k = 0; k < g.k_blocks; ++k, ++it) {
+                const int st = it % kStages;
+                ok = tc::mbar_wait(full + 8 * st, (it / kStages) & 1);
+                if (!ok) break;
+                tc::fence_after();
+                const uint32_t a = smem + st * kStage, b = a + kOperand, sa = b + kOperand, sb = sa + kScales;
+                stage_products<FORMAT, true>(tmem, tmem + kTile, a, b, sa, sb, idesc, k > 0);
+                tc::commit_pair(empty + 8 * st);
+            }
+            if (!ok) break;
+            tc::commit_pair(acc_full);
+        }
+    } else if (warp >= 4) {
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t acc_empty0 = tc::map_to_rank(acc_empty, 0);
+        uint32_t* words = reinterpret_cast<uint32_t*>(raw + (smem - tc::smem_addr(raw)) + kStages * kStage +
+                                                      (warp - 4) * kTurn);
+        const int per = g.elem_bytes == 2 ? 2 : 1;  // columns a word
+        int j = 0;
+        for (int64_t id = first; id < tiles; id += pairs, ++j) {
+            const int m = (int)(id % g.m_tiles), n = (int)(id / g.m_tiles);
+            const int64_t row0 = (int64_t)m * kTile + rank * kHalf + quad * 32;
+            const int64_t col0 = (int64_t)n * kTile + half * kColumns;
+            const uint32_t d = tmem + half * kColumns + ((uint32_t)quad << 21);
+            ok = ok && tc::mbar_wait(acc_full, j & 1);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            tc::fence_after();
+            // 128 bytes of every row at a time, through shared memory (16-byte groups of row i at group
+            // ^ (i & 7), free of bank conflicts both ways)
+#pragma unroll 1
+            for (int c = 0; c < kColumns && col0 + c < g.N; c += 32 * per) {
+#pragma unroll 1
+                for (int h = 0; h < per; ++h) {
+                    uint32_t r[32];
+                    __syncwarp();
+                    tc::tmem_ld32(d + c + 32 * h, r);
+                    tc::tmem_wait(r);
+                    if (!ok) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) r[i] = 0x7FFFFFFFu;
+                    }
+                    if (per == 2) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = ss::pack_bf16x2(__uint_as_float(r[8 * i + 2 * e]),
+                                                       __uint_as_float(r[8 * i + 2 * e + 1]));
+                            *reinterpret_cast<uint4*>(words + lane * 32 + 4 * ((4 * h + i) ^ (lane & 7))) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4*>(words + lane * 32 + 4 * (i ^ (lane & 7))) =
+                                make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                    }
+                }
+                __syncwarp();
+                const int k = lane & 7;
+                const int left = (int)min(g.N - (col0 + c), (int64_t)(32 * per));  // columns of this piece
+                if (g.vector) {
+                    const int mine = min(left - 4 * per * k, 4 * per);  // columns of this lane's 16 bytes
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int q = 4 * i + (lane >> 3);
+                        if (row0 + q >= g.M || mine <= 0) continue;
+                        unsigned char* o = static_cast<unsigned char*>(g.out) +
+                                           ((row0 + q) * g.out_stride + col0 + c + 4 * per * k) * g.elem_bytes;
+                        const uint4 v = *reinterpret_cast<const uint4*>(words + q * 32 + 4 * (k ^ (q & 7)));
+                        if (mine == 4 * per) {
+                            *reinterpret_cast<uint4*>(o) = v;
+                        } else {
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                if (e >= mine) continue;
+                                if (per == 2)
+                                    reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                                else if (e < 4)
+                                    reinterpret_cast<uint32_t*>(o)[e] = w[e];
+                            }
+                        }
+                    }
+                } else {
+                    for (int q = 0; q < 32 && row0 + q < g.M; ++q) {
+                        const int64_t at = (row0 + q) * g.out_stride + col0 + c;
+                        const uint32_t w = words[q * 32 + 4 * ((lane >> 2) ^ (q & 7)) + (lane & 3)];
+                        if (per == 2) {
+                            uint16_t* o = static_cast<uint16_t*>(g.out) + at;
+                            if (2 * lane < left) o[2 * lane] = (uint16_t)w;
+                            if (2 * lane + 1 < left) o[2 * lane + 1] = (uint16_t)(w >> 16);
+                        } else if (lane < left) {
+                            static_cast<uint32_t*>(g.out)[at + lane] = w;
+                        }
+                    }
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(acc_empty0);
+        }
+    }
+    if (!ok) let_copies_land();
+    __syncwarp();
+    tc::fence_before();
+    tc::cluster_sync();
+    tc::fence_after();
+    if (warp == 2) tc::tmem_free(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// 128 rows of one operand, few of the other, k over a cluster
+// ---------------------------------------------------------------------------
+
+constexpr int kFewStages = 4;
+constexpr int kFewThreads = 32 * 6;
+constexpr int kPartPitch = kHalf + 1;  // floats of a column of partial sums: free of bank conflicts both ways
+
+__host__ __device__ constexpr int few_stage(int format, int few) {
+    return kOperand + few * kRowBytes + 2 * scale_bytes(format);
+}
+__host__ __device__ constexpr int few_smem(int format, int few) { return kFewStages * few_stage(format, few) + 1024; }
+// Columns of tensor memory: the accumulator's and the scales' 8.
+__host__ __device__ constexpr uint32_t few_tmem(int few) { return few <= 16 ? 32 : 2 * few; }
+
+// a: the operand of 128 rows a CTA; b: the other one.
+struct FewArgs {
+    int64_t rows, few;           // of the two operands
+    int64_t row_step, few_step;  // elements of out between two rows of a, of b
+    int row_tiles, k_blocks, splits;
+    void* out;
+    int elem_bytes;
+};
+
+template <int FORMAT, int FEW>
+__global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_constant__ Maps maps,
+                                                            const __grid_constant__ FewArgs g) {
+    extern __shared__ unsigned char raw[];
+    __shared__ uint64_t bars[2 * kFewStages + 1];
+    __shared__ uint32_t tmem_base;
+    constexpr int kStage = few_stage(FORMAT, FEW), kScales = scale_bytes(FORMAT);
+    static_assert(kStage % 1024 == 0 && FEW * kPartPitch * 4 <= kFewStages * kStage, "shared memory");
+
+    launch_after();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t smem = (tc::smem_addr(raw) + 1023u) & ~1023u;
+    const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kFewStages, done = empty + 8 * kFewStages;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kFewStages; ++i) {
+            tc::mbar_init(full + 8 * i, 1);
+            tc::mbar_init(empty + 8 * i, 1);
+        }
+        tc::mbar_init(done, 1);
+        tc::mbar_init_fence();
+        tc::prefetch_map(&maps.a);
+        tc::prefetch_map(&maps.b);
+        tc::prefetch_map(&maps.a_scales);
+        tc::prefetch_map(&maps.b_scales);
+    }
+    if (warp == 1) tc::tmem_alloc_one(tc::smem_addr(&tmem_base), few_tmem(FEW));
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = tmem_base;
+    wait_before();
+
+    const int split = g.splits > 1 ? (int)tc::cluster_ctarank() : 0;
+    const int tile = blockIdx.x / g.splits, rt = tile % g.row_tiles, ft = tile / g.row_tiles;
+    const int per = (g.k_blocks + g.splits - 1) / g.splits;
+    const int kb = min(split * per, g.k_blocks), ke = min(kb + per, g.k_blocks);
+    bool ok = true;
+
+    if (warp == 0 && lane == 0) {
+        for (int k = kb; k < ke; ++k) {
+            const int it = k - kb, st = it % kFewStages;
+            const uint32_t a = smem + st * kStage, b = a + kOperand, sa = b + FEW * kRowBytes, sb = sa + kScales;
+            ok = tc::mbar_wait(empty + 8 * st, ((it / kFewStages) & 1) ^ 1);
+            if (!ok) break;
+            tc::mbar_expect_tx(full + 8 * st, kOperand + FEW * kRowBytes + 2 * kScales);
+            tc::tma_load_2d_one(a, &maps.a, k * kRowBytes, rt * kHalf, full + 8 * st);
+            tc::tma_load_2d_one(sa, &maps.a_scales, k * (kScales / 4), rt, full + 8 * st);
+            tc::tma_load_2d_one(b, &maps.b, k * kRowBytes, ft * FEW, full + 8 * st);
+            tc::tma_load_2d_one(sb, &maps.b_scales, k * (kScales / 4), ft, full + 8 * st);
+        }
+    } else if (warp == 1 && lane == 0) {
+        const uint32_t idesc = tc::scaled_desc(FORMAT == SS_MXFP4, kHalf, FEW);
+        for (int k = kb; k < ke; ++k) {
+            const int it = k - kb, st = it % kFewStages;
+            ok = tc::mbar_wait(full + 8 * st, (it / kFewStages) & 1);
+            if (!ok) break;
+            tc::fence_after();
+            const uint32_t a = smem + st * kStage, b = a + kOperand, sa = b + FEW * kRowBytes, sb = sa + kScales;
+            stage_products<FORMAT, false>(tmem, tmem + FEW, a, b, sa, sb, idesc, k > kb);
+            tc::commit_one(empty + 8 * st);
+        }
+        if (ok) tc::commit_one(done);
+    } else if (warp >= 2) {
+        const int quad = warp & 3, row = quad * 32 + lane;
+        ok = tc::mbar_wait(done, 0);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc::fence_after();
+        // every stage has been read: its shared memory takes the sums
+        float* part = reinterpret_cast<float*>(raw + (smem - tc::smem_addr(raw)));
+        const bool none = kb == ke;  // no k: the accumulator holds something else
+#pragma unroll 1
+        for (int c = 0; c < FEW; c += 32) {
+            uint32_t r[32];
+            __syncwarp();
+            tc::tmem_ld32(tmem + c + ((uint32_t)quad << 21), r);
+            tc::tmem_wait(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (c + i < FEW) part[(c + i) * kPartPitch + row] = !ok ? NAN : none ? 0.f : __uint_as_float(r[i]);
+        }
+    }
+    if (!ok) let_copies_land();
+    __syncwarp();
+    tc::fence_before();
+    if (g.splits > 1)
+        tc::cluster_sync();
+    else
+        __syncthreads();
+    tc::fence_after();
+    if (warp == 1) tc::tmem_free_one(tmem, few_tmem(FEW));
+
+    // this CTA's share of the columns, the splits added in their order
+    const int share = FEW / g.splits, c0 = split * share;
+    for (int i = threadIdx.x; i < share * kHalf; i += kFewThreads) {
+        // neighbouring threads along out's contiguous direction
+        const int c = c0 + (g.row_step == 1 ? i / kHalf : i % share), row = g.row_step == 1 ? i % kHalf : i / share;
+        const int64_t r = (int64_t)rt * kHalf + row, f = (int64_t)ft * FEW + c;
+        if (r >= g.rows || f >= g.few) continue;
+        const uint32_t at = smem + (uint32_t)(c * kPartPitch + row) * 4;
+        float s = 0.f;
+        if (g.splits > 1) {
+            for (int q = 0; q < g.splits; ++q) {
+                float v;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tc::map_to_rank(at, q)) : "memory");
+                s += v;
+            }
+        } else {
+            asm volatile("ld.shared::cta.f32 %0, [%1];" : "=f"(s) : "r"(at) : "memory");
+        }
+        store_one(g.out, r * g.row_step + f * g.few_step, s, g.elem_bytes);
+    }
+    if (g.splits > 1) tc::cluster_sync();
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kMaxSize = (int64_t)1 << 30;
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Data of a quantised matrix in boxes of 128 bytes and box_rows rows, zeros outside.
+int data_map(CUtensorMap* map, const void* data, int64_t rows, int64_t K, int format, int box_rows) {
+    const ss::EncodeTiled fn = ss::tensor_map_encoder();
+    if (!fn) return ss::cuda_fail(cudaErrorNotSupported);
+    const cuuint64_t pitch = (cuuint64_t)div_up(K, ss::kMxTile) * (format == SS_MXFP4 ? 64 : 128);
+    const cuuint64_t dims[2] = {pitch, (cuuint64_t)rows}, strides[1] = {pitch};
+    const cuuint32_t box[2] = {kRowBytes, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(data), dims, strides, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SS_OK : ss::cuda_fail(cudaErrorInvalidValue);
+}
+
+// Its scales, as words, in boxes of a stage's tiles and `tiles` rows of tiles; zeros,
+// which are the lowest scale, outside.
+int scale_map(CUtensorMap* map, const void* scales, int64_t rows, int64_t K, int format, int tiles) {
+    const ss::EncodeTiled fn = ss::tensor_map_encoder();
+    if (!fn) return ss::cuda_fail(cudaErrorNotSupported);
+    const cuuint64_t pitch = (cuuint64_t)div_up(K, ss::kMxTile) * ss::kMxTileBytes;
+    const cuuint64_t dims[2] = {pitch / 4, (cuuint64_t)div_up(rows, ss::kMxTile)}, strides[1] = {pitch};
+    const cuuint32_t box[2] = {(cuuint32_t)scale_bytes(format) / 4, (cuuint32_t)tiles}, step[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void*>(scales), dims, strides, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SS_OK : ss::cuda_fail(cudaErrorInvalidValue);
+}
+
+struct Operand {
+    const void *data, *scales;
+    int64_t rows;
+};
+
+int make_maps(Maps* maps, const Operand& a, const Operand& b, int64_t K, int format, int b_rows, int b_tiles) {
+    if (int rc = data_map(&maps->a, a.data, a.rows, K, format, kHalf)) return rc;
+    if (int rc = data_map(&maps->b, b.data, b.rows, K, format, b_rows)) return rc;
+    if (int rc = scale_map(&maps->a_scales, a.scales, a.rows, K, format, 1)) return rc;
+    return scale_map(&maps->b_scales, b.scales, b.rows, K, format, b_tiles);
+}
+
+template <int FORMAT>
+int launch_pair(const ss_mx_product* p, int64_t k_blocks, cudaStream_t st) {
+    static std::atomic<uint64_t> ready{0};
+    const auto kernel = mx_pair_kernel<FORMAT>;
+    constexpr int smem = pair_smem(FORMAT);
+    if (int rc = ss::allow_smem(ready, reinterpret_cast<const void*>(kernel), smem)) return rc;
+    Maps maps;
+    if (int rc = make_maps(&maps, {p->a_data, p->a_scales, p->M}, {p->b_data, p->b_scales, p->N}, p->K, FORMAT, kHalf, 2))
+        return rc;
+    const int64_t m_tiles = div_up(p->M, kTile), n_tiles = div_up(p->N, kTile), pairs = ss::num_sms() / 2;
+    const PairArgs g = {p->M, p->N, p->out_stride, (int)m_tiles, (int)n_tiles, (int)k_blocks, p->out, p->elem_bytes,
+                        ss::aligned(p->out, 16) && p->out_stride * p->elem_bytes % 16 == 0};
+    return ss::launch(kernel, 2 * std::min(m_tiles * n_tiles, pairs), kPairThreads, smem, 0, true, st, maps, g);
+}
+
+template <int FORMAT, int FEW>
+int launch_few(const ss_mx_product* p, int64_t k_blocks, bool swap, cudaStream_t st) {
+    static std::atomic<uint64_t> ready{0};
+    const auto kernel = mx_few_kernel<FORMAT, FEW>;
+    constexpr int smem = few_smem(FORMAT, FEW);
+    if (int rc = ss::allow_smem(ready, reinterpret_cast<const void*>(kernel), smem)) return rc;
+    Operand a = {p->b_data, p->b_scales, p->N}, b = {p->a_data, p->a_scales, p->M};
+    if (swap) std::swap(a, b);
+    Maps maps;
+    if (int rc = make_maps(&maps, a, b, p->K, FORMAT, FEW, 1)) return rc;
+    const int64_t row_tiles = div_up(a.rows, kHalf), few_tiles = div_up(b.rows, FEW), tiles = row_tiles * few_tiles;
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= 2 * ss::num_sms() && k_blocks >= 4 * splits) splits *= 2;
+    const FewArgs g = {a.rows, b.rows, swap ? p->out_stride : 1, swap ? 1 : p->out_stride, (int)row_tiles, (int)k_blocks,
+                       splits, p->out, p->elem_bytes};
+    if (tiles * splits > INT32_MAX) return SS_EOVERFLOW;
+    return ss::launch(kernel, tiles * splits, kFewThreads, smem, splits > 1 ? splits : 0, true, st, maps, g);
+}
+
+template <int FORMAT>
+int launch_product(const ss_mx_product* p, cudaStream_t st) {
+    const int64_t k_blocks = div_up(div_up(p->K, ss::kMxTile), scale_tiles(FORMAT));
+    const int64_t big = div_up(p->M, kTile) * div_up(p->N, kTile);
+    if (2 * big >= ss::num_sms() / 2) return launch_pair<FORMAT>(p, k_blocks, st);
+    const bool swap = p->N < p->M && p->N <= 64;  // the few are B's rows
+    const int64_t few = swap ? p->N : p->M;
+    if (few <= 16) return launch_few<FORMAT, 16>(p, k_blocks, swap, st);
+    if (few <= 32) return launch_few<FORMAT, 32>(p, k_blocks, swap, st);
+    if (few <= 64) return launch_few<FORMAT, 64>(p, k_blocks, swap, st);
+    return launch_few<FORMAT, 128>(p, k_blocks, swap, st);
+}
+
+}  // namespace
+
+extern "C" int ss_mx_matmul(const ss_mx_product* p, ss_stream_t stream) {
+    if (!p || p->M < 0 || p->N < 0 || p->K < 1 || (p->format != SS_MXFP4 && p->format != SS_MXFP8) ||
+        (p->elem_bytes != 2 && p->elem_bytes != 4))
+        return SS_EINVAL;
+    if (p->M > kMaxSize || p->N > kMaxSize || p->K > kMaxSize) return SS_EOVERFLOW;
+    if (p->M == 0 || p->N == 0) return SS_OK;
+    if (!p->a_data || !p->a_scales || !p->b_data || !p->b_scales || !p->out || p->out_stride < p->N) return SS_EINVAL;
+    if (p->out_stride > INT64_MAX / 8 / p->M) return SS_EOVERFLOW;
+    if (!ss::aligned(p->a_data, 16) || !ss::aligned(p->a_scales, 16) || !ss::aligned(p->b_data, 16) ||
+        !ss::aligned(p->b_scales, 16) || !ss::aligned(p->out, (uintptr_t)p->elem_bytes))
+        return SS_EALIGN;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return p->format == SS_MXFP4 ? launch_product<SS_MXFP4>(p, st) : launch_product<SS_MXFP8>(p, st);
+}

@@ -1,0 +1,514 @@
+// norm.cu -- dropout, and the residual stream's step between two layers: dropout of
+// the branch, the residual's addition and the root-mean-square norm, with the
+// backward pass.
+//
+//   h  = round(dropout(x) + residual)      the stream, in its type
+//   r  = 1 / sqrt(mean_c h_c^2 + eps)      one per row, fp32
+//   y  = h r w                             rounded to the type, or to MXFP8
+//
+//   n  = h r,  g = dy w
+//   dh = r (g - n mean_c(g n)) + d_sum     d_sum: what arrives at h from elsewhere
+//   dx = dropout(dh)                       the same mask, made again
+//   dw = sum over the rows of dy n
+//
+// The statistics are taken of h as it is stored, so that the backward pass, which
+// reads the stored h, is the gradient of what the forward pass computed.
+//
+// All of it moves each element once, and the memory is what bounds it: a row stays in
+// its threads' registers (8 elements a load, up to 8 loads a thread) between the sum
+// over it and the outputs.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+#include "launch.cuh"
+#include "mx.cuh"
+#include "philox.cuh"
+#include "vec8.cuh"
+
+namespace {
+
+using ss::launch_after;
+using ss::Vec8;
+using ss::wait_before;
+
+// ---------------------------------------------------------------------------
+// dropout
+// ---------------------------------------------------------------------------
+
+constexpr int kDropThreads = 256;
+
+struct DropArgs {
+    int64_t rows, cols, groups;  // groups: of 8 columns in a row
+    const void* x;
+    int64_t x_stride;
+    void* out;
+    int64_t out_stride;
+    const int64_t* rng;
+    uint32_t drop;
+    float scale;
+    int64_t step_rows, step_groups;  // the grid's threads, as rows and groups
+};
+
+template <class T, bool ALIGNED>
+__global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_constant__ DropArgs a) {
+    launch_after();
+    const int64_t first = (int64_t)blockIdx.x * kDropThreads + threadIdx.x;
+    int64_t row = first / a.groups, group = first - row * a.groups;
+    wait_before();
+    const ss::Philox philox(a.rng);
+    const T* x = static_cast<const T*>(a.x);
+    T* out = static_cast<T*>(a.out);
+    while (row < a.rows) {
+        const int64_t col = 8 * group;
+        const int n = (int)min(a.cols - col, (int64_t)8);
+        Vec8<T> v;
+        v.template load<ALIGNED>(x + row * a.x_stride + col, n);
+        float f[8];
+        v.get(f);
+        ss::drop8(f, philox((uint32_t)row, (uint32_t)group), a.drop, a.scale);
+        v.set(f);
+        v.template store<ALIGNED>(out + row * a.out_stride + col, n);
+        row += a.step_rows;
+        group += a.step_groups;
+        if (group >= a.groups) group -= a.groups, ++row;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the norm
+// ---------------------------------------------------------------------------
+
+struct NormArgs {
+    int64_t rows;
+    int cols, team;  // team: threads of a row
+    const void *x, *residual, *weight;
+    int64_t x_stride, residual_stride;
+    float eps, inv_cols;
+    const int64_t* rng;
+    uint32_t drop;
+    float scale;
+    void *sum_out, *out;
+    int64_t sum_stride, out_stride;
+    float* rstd_out;
+    unsigned char *mx_data, *mx_scales;
+    int mx_tiles;  // tiles of 128 columns
+};
+
+struct NormGradArgs {
+    int64_t rows;
+    int cols, team;
+    const void *d_out, *h, *weight, *d_sum;
+    int64_t d_out_stride, h_stride, d_sum_stride;
+    const float* rstd;
+    float inv_cols;
+    const int64_t* rng;
+    uint32_t drop;
+    float scale;
+    void *d_h, *d_x;
+    int64_t d_h_stride, d_x_stride;
+    float* part;  // [gridDim.x][cols]: each CTA's share of d_weight (NULL: not asked for)
+};
+
+// Sum over a row's team, the same in all of its threads: over the warp in registers,
+// then over the warps in a fixed order through `lane_sums` (one float a warp; another
+// one at every other call).
+__device__ __forceinline__ float team_sum(float s, int team, float* lane_sums) {
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, k);
+    if (team == 32) return s;
+    const int warp = threadIdx.x >> 5, warps = team >> 5, first = warp / warps * warps;
+    if ((threadIdx.x & 31) == 0) lane_sums[warp] = s;
+    __syncthreads();
+    float t = 0.f;
+    for (int i = 0; i < warps; ++i) t += lane_sums[first + i];
+    return t;
+}
+
+// 8 normed values as MXFP8: their block is this lane's and its 3 neighbours'.
+__device__ __forceinline__ void store_mx8(const NormArgs& a, int64_t row, int col, const float (&y)[8]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, ss::abs_bits(y[i]));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    if (row >= a.rows || col >= a.mx_tiles * ss::kMxTile) return;
+    const uint32_t byte = ss::mx_scale<SS_MXFP8>(top);
+    const float inverse = ss::mx_inverse(byte);
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = byte == 255u ? 0.f : y[i] * inverse;
+    *reinterpret_cast<uint2*>(a.mx_data + (row * a.mx_tiles * ss::kMxTile + col)) = ss::Mx<SS_MXFP8>::encode(f);
+    if ((threadIdx.x & 3) == 0) a.mx_scales[ss::mx_scale_at(row, col >> 5, a.mx_tiles)] = (unsigned char)byte;
+}
+
+// VECS loads of 8 elements a thread, `team` threads a row, blockDim / team rows a CTA.
+template <class T, int VECS, bool ALIGNED>
+__global__ void __launch_bounds__(VECS > 2 ? 512 : 256) norm_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float lane_sums[16];
+    launch_after();
+    const int mine = threadIdx.x % a.team;
+    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / a.team) + threadIdx.x / a.team;
+    const bool live = row < a.rows;
+    const T* weight = static_cast<const T*>(a.weight);
+    wait_before();
+    Vec8<T> x[VECS], r[VECS];
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+        const int col = 8 * (mine + i * a.team), n = live ? a.cols - col : 0;
+        x[i].clear();
+        r[i].clear();
+        if (n > 0) x[i].template load<ALIGNED>(static_cast<const T*>(a.x) + row * a.x_stride + col, n);
+        if (n > 0 && a.residual)
+            r[i].template load<ALIGNED>(static_cast<const T*>(a.residual) + row * a.residual_stride + col, n);
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+        const int col = 8 * (mine + i * a.team), n = live ? a.cols - col : 0;
+        if (a.drop || a.residual) {
+            float f[8], q[8];
+            x[i].get(f);
+            r[i].get(q);
+            if (a.drop) ss::drop8(f, ss::Philox(a.rng)((uint32_t)row, (uint32_t)(col >> 3)), a.drop, a.scale);
+            if (a.residual) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] = __fadd_rn(f[k], q[k]);
+            }
+            x[i].set(f);
+        }
+        if (n > 0 && a.sum_out) x[i].template store<ALIGNED>(static_cast<T*>(a.sum_out) + row * a.sum_stride + col, n);
+        float f[8];
+        x[i].get(f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < n) s = fmaf(f[k], f[k], s);
+    }
+    s = team_sum(s, a.team, lane_sums);
+    const float rstd = 1.f / sqrtf(fmaf(s, a.inv_cols, a.eps));
+    if (live && mine == 0 && a.rstd_out) a.rstd_out[row] = rstd;
+    if (!a.out && !a.mx_data) return;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+        const int col = 8 * (mine + i * a.team), n = live ? a.cols - col : 0;
+        Vec8<T> w;
+        w.clear();
+        if (n > 0) w.template load<ALIGNED>(weight + col, n);
+        float f[8], q[8];
+        x[i].get(f);
+        w.get(q);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = k < n ? f[k] * rstd * q[k] : 0.f;
+        if (n > 0 && a.out) {
+            w.set(f);
+            w.template store<ALIGNED>(static_cast<T*>(a.out) + row * a.out_stride + col, n);
+        }
+        if (a.mx_data) store_mx8(a, row, col, f);
+    }
+}
+
+template <class T, int VECS, bool ALIGNED>
+__global__ void __launch_bounds__(VECS > 2 ? 512 : 256) norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
+    extern __shared__ float joined[];  // [rows at a time][cols], where that is more than one
+    __shared__ float lane_sums[2][16];
+    launch_after();
+    const int mine = threadIdx.x % a.team, teams = blockDim.x / a.team, team = threadIdx.x / a.team;
+    const T* weight = static_cast<const T*>(a.weight);
+    wait_before();
+    float dw[VECS][8];
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dw[i][k] = 0.f;
+    int parity = 0;
+    for (int64_t first = (int64_t)blockIdx.x * teams; first < a.rows; first += (int64_t)gridDim.x * teams, parity ^= 1) {
+        const int64_t row = first + team;
+        const bool live = row < a.rows;
+        Vec8<T> dy[VECS], h[VECS], ds[VECS];
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+            const int col = 8 * (mine + i * a.team), n = live ? a.cols - col : 0;
+            dy[i].clear();
+            h[i].clear();
+            ds[i].clear();
+            if (n > 0) {
+                dy[i].template load<ALIGNED>(static_cast<const T*>(a.d_out) + row * a.d_out_stride + col, n);
+                h[i].template load<ALIGNED>(static_cast<const T*>(a.h) + row * a.h_stride + col, n);
+                if (a.d_sum) ds[i].template load<ALIGNED>(static_cast<const T*>(a.d_sum) + row * a.d_sum_stride + col, n);
+            }
+        }
+        const float rstd = live ? a.rstd[row] : 0.f;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+            const int col = 8 * (mine + i * a.team), n = live ? a.cols - col : 0;
+            Vec8<T> w;
+            w.clear();
+            if (n > 0) w.template load<ALIGNED>(weight + col, n);
+            float f[8], q[8], g[8];
+            dy[i].get(f);
+            h[i].get(q);
+            w.get(g);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < n) {
+                    const float t = f[k] * (q[k] * rstd);
+                    s = fmaf(t, g[k], s);
+                    dw[i][k] += t;
+                }
+        }
+        s = team_sum(s, a.team, lane_sums[parity]) * a.inv_cols;
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+            const int col = 8 * (mine + i * a.team), n = live ? a.cols - col : 0;
+            if (n <= 0) continue;
+            Vec8<T> w;
+            w.template load<ALIGNED>(weight + col, n);
+            float f[8], q[8], g[8], d[8];
+            dy[i].get(f);
+            h[i].get(q);
+            w.get(g);
+            ds[i].get(d);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = fmaf(rstd, fmaf(-q[k] * rstd, s, f[k] * g[k]), d[k]);
+            if (a.d_h) {
+                w.set(f);
+                w.template store<ALIGNED>(static_cast<T*>(a.d_h) + row * a.d_h_stride + col, n);
+            }
+            if (a.d_x) {
+                if (a.drop) ss::drop8(f, ss::Philox(a.rng)((uint32_t)row, (uint32_t)(col >> 3)), a.drop, a.scale);
+                w.set(f);
+                w.template store<ALIGNED>(static_cast<T*>(a.d_x) + row * a.d_x_stride + col, n);
+            }
+        }
+    }
+    if (!a.part) return;
+    float* part = a.part + (int64_t)blockIdx.x * a.cols;
+    float* to = teams > 1 ? joined + team * a.cols : part;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+        const int col = 8 * (mine + i * a.team);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (col + k < a.cols) to[col + k] = dw[i][k];
+    }
+    if (teams == 1) return;
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+        float s = 0.f;
+        for (int t = 0; t < teams; ++t) s += joined[t * a.cols + c];
+        part[c] = s;
+    }
+}
+
+// d_weight: the CTAs' shares summed in a fixed order, 32 columns a CTA.
+constexpr int kJoinRows = 16;
+
+template <class T>
+__global__ void __launch_bounds__(32 * kJoinRows) norm_join_kernel(const float* part, int parts, int cols, T* out) {
+    __shared__ float sums[kJoinRows][33];
+    launch_after();
+    wait_before();
+    const int lane = threadIdx.x & 31, line = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    float s = 0.f;
+    if (col < cols) {
+#pragma unroll 8
+        for (int p = line; p < parts; p += kJoinRows) s += part[(int64_t)p * cols + col];
+    }
+    sums[line][lane] = s;
+    __syncthreads();
+    if (line > 0 || col >= cols) return;
+#pragma unroll
+    for (int i = 1; i < kJoinRows; ++i) s += sums[i][lane];
+    if (sizeof(T) == 2)
+        reinterpret_cast<uint16_t*>(out)[col] = ss::f32_to_bf16(s);
+    else
+        reinterpret_cast<float*>(out)[col] = s;
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kMaxRows = INT32_MAX;
+constexpr int64_t kMaxCols = 32768;  // 512 threads hold a row in registers
+
+// Threads of a row and of a CTA, and loads of 8 elements a thread: few loads a thread
+// as long as 256 threads suffice, so that many rows are in flight.
+struct Shape {
+    int vecs, team, threads;
+};
+
+Shape choose_shape(int64_t vectors) {
+    if (vectors <= 512) {
+        int team = 32;
+        while (team < 256 && team * 2 < vectors) team *= 2;
+        return {vectors <= team ? 1 : 2, team, 256};
+    }
+    const int vecs = vectors <= 2048 ? 4 : 8;
+    const int team = (int)((vectors + vecs - 1) / vecs + 31) / 32 * 32;
+    return {vecs, team, team};
+}
+
+// CTAs that take the rows of a backward pass in turn.
+int64_t grad_grid(int64_t rows, const Shape& s) {
+    const int64_t teams = s.threads / s.team, need = (rows + teams - 1) / teams;
+    return std::min(need, (int64_t)ss::num_sms() * 2);
+}
+
+template <class F>
+int with_shape(int elem_bytes, int vecs, bool aligned, F&& f) {
+    auto pick = [&](auto t, auto v) { return aligned ? f(t, v, std::true_type()) : f(t, v, std::false_type()); };
+    auto vec = [&](auto t) {
+        switch (vecs) {
+            case 1: return pick(t, std::integral_constant<int, 1>());
+            case 2: return pick(t, std::integral_constant<int, 2>());
+            case 4: return pick(t, std::integral_constant<int, 4>());
+            default: return pick(t, std::integral_constant<int, 8>());
+        }
+    };
+    return elem_bytes == 2 ? vec(uint16_t()) : vec(float());
+}
+
+// A matrix that may be absent: its row stride, its addresses.
+struct Matrix {
+    const void* p;
+    int64_t stride;
+};
+
+int check_matrices(int64_t rows, int64_t cols, int elem_bytes, std::initializer_list<Matrix> list) {
+    for (const Matrix& m : list) {
+        if (!m.p) continue;
+        if (m.stride < cols) return SS_EINVAL;
+        if (rows > 0 && m.stride > INT64_MAX / 8 / rows) return SS_EOVERFLOW;
+    }
+    for (const Matrix& m : list)
+        if (!ss::aligned(m.p, (uintptr_t)elem_bytes)) return SS_EALIGN;
+    return SS_OK;
+}
+
+// Rows of all of them on 16 bytes.
+bool rows_on_16(int elem_bytes, std::initializer_list<Matrix> list) {
+    for (const Matrix& m : list)
+        if (m.p && (!ss::aligned(m.p, 16) || m.stride * elem_bytes % 16 != 0)) return false;
+    return true;
+}
+
+// A probability in steps of 2^-16 and the factor of what is kept; SS_EINVAL where
+// nothing would be.
+int choose_drop(double p, const int64_t* rng, uint32_t* drop, float* scale) {
+    if (!(p >= 0.0 && p < 1.0)) return SS_EINVAL;
+    *drop = (uint32_t)std::nearbyint(p * 65536.0);
+    if (*drop >= 65536u) return SS_EINVAL;
+    if (*drop > 0 && !rng) return SS_EINVAL;
+    *scale = (float)(65536.0 / (65536.0 - *drop));
+    return ss::aligned(rng, 8) ? SS_OK : SS_EALIGN;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ss_dropout(int64_t rows, int64_t cols, int elem_bytes, const void* x, int64_t x_stride, void* out,
+               int64_t out_stride, double p, const int64_t* rng, ss_stream_t stream) {
+    if (rows < 0 || cols < 0 || (elem_bytes != 2 && elem_bytes != 4)) return SS_EINVAL;
+    DropArgs a = {};
+    if (int rc = choose_drop(p, rng, &a.drop, &a.scale)) return rc;
+    if (!rng) return SS_EINVAL;
+    if (rows == 0 || cols == 0) return SS_OK;
+    if (!x || !out) return SS_EINVAL;
+    if (rows > kMaxRows || cols > INT64_MAX / 16 / rows || cols > (int64_t)8 * UINT32_MAX) return SS_EOVERFLOW;
+    if (int rc = check_matrices(rows, cols, elem_bytes, {{x, x_stride}, {out, out_stride}})) return rc;
+    a.rows = rows, a.cols = cols, a.groups = (cols + 7) / 8;
+    a.x = x, a.x_stride = x_stride, a.out = out, a.out_stride = out_stride, a.rng = rng;
+    const int64_t total = a.rows * a.groups;
+    const int64_t grid = std::min((total + kDropThreads - 1) / kDropThreads, (int64_t)ss::num_sms() * 8);
+    a.step_rows = grid * kDropThreads / a.groups;
+    a.step_groups = grid * kDropThreads % a.groups;
+    const bool al = rows_on_16(elem_bytes, {{x, x_stride}, {out, out_stride}});
+    const auto kernel = elem_bytes == 2 ? (al ? dropout_kernel<uint16_t, true> : dropout_kernel<uint16_t, false>)
+                                        : (al ? dropout_kernel<float, true> : dropout_kernel<float, false>);
+    return ss::launch(kernel, grid, kDropThreads, 0, 0, true, reinterpret_cast<cudaStream_t>(stream), a);
+}
+
+int ss_rms_norm(const ss_norm* n, ss_stream_t stream) {
+    if (!n || n->rows < 0 || n->cols < 1 || (n->elem_bytes != 2 && n->elem_bytes != 4)) return SS_EINVAL;
+    if (!(n->eps >= 0.0) || !std::isfinite((float)n->eps)) return SS_EINVAL;
+    NormArgs a = {};
+    if (int rc = choose_drop(n->dropout, n->rng, &a.drop, &a.scale)) return rc;
+    if (n->rows > kMaxRows || n->cols > kMaxCols) return SS_EOVERFLOW;
+    if (n->rows == 0) return SS_OK;
+    if (!n->sum_out && !n->out && !n->rstd_out && !n->mx_data) return SS_EINVAL;
+    if (!n->x || !n->weight || !n->mx_data != !n->mx_scales) return SS_EINVAL;
+    const Matrix x = {n->x, n->x_stride}, res = {n->residual, n->residual_stride}, w = {n->weight, n->cols};
+    const Matrix sum = {n->sum_out, n->sum_stride}, out = {n->out, n->out_stride};
+    if (int rc = check_matrices(n->rows, n->cols, n->elem_bytes, {x, res, w, sum, out})) return rc;
+    if (!ss::aligned(n->rstd_out, 4) || !ss::aligned(n->mx_data, 16) || !ss::aligned(n->mx_scales, 16)) return SS_EALIGN;
+    a.rows = n->rows, a.cols = (int)n->cols;
+    a.x = n->x, a.x_stride = n->x_stride, a.residual = n->residual, a.residual_stride = n->residual_stride;
+    a.weight = n->weight, a.eps = (float)n->eps, a.inv_cols = 1.f / (float)n->cols, a.rng = n->rng;
+    a.sum_out = n->sum_out, a.sum_stride = n->sum_stride, a.out = n->out, a.out_stride = n->out_stride;
+    a.rstd_out = n->rstd_out;
+    a.mx_data = static_cast<unsigned char*>(n->mx_data), a.mx_scales = static_cast<unsigned char*>(n->mx_scales);
+    a.mx_tiles = (int)((n->cols + ss::kMxTile - 1) / ss::kMxTile);
+    const Shape s = choose_shape(n->mx_data ? (int64_t)a.mx_tiles * (ss::kMxTile / 8) : (n->cols + 7) / 8);
+    a.team = s.team;
+    const int64_t teams = s.threads / s.team, grid = (n->rows + teams - 1) / teams;
+    // the weight is one row: its own stride does not matter
+    const bool al = rows_on_16(n->elem_bytes, {x, res, sum, out}) && ss::aligned(n->weight, 16);
+    return with_shape(n->elem_bytes, s.vecs, al, [&](auto t, auto v, auto aligned) {
+        return ss::launch(norm_kernel<decltype(t), decltype(v)::value, decltype(aligned)::value>, grid, s.threads, 0, 0,
+                          true, reinterpret_cast<cudaStream_t>(stream), a);
+    });
+}
+
+int ss_rms_norm_workspace(int64_t rows, int64_t cols, size_t* bytes_out) {
+    if (rows < 0 || cols < 1 || !bytes_out) return SS_EINVAL;
+    if (rows > kMaxRows || cols > kMaxCols) return SS_EOVERFLOW;
+    *bytes_out = (size_t)(std::max<int64_t>(grad_grid(rows, choose_shape((cols + 7) / 8)), 1) * cols * 4);
+    return SS_OK;
+}
+
+int ss_rms_norm_backward(const ss_norm_grad* n, ss_stream_t stream) {
+    if (!n || n->rows < 0 || n->cols < 1 || (n->elem_bytes != 2 && n->elem_bytes != 4)) return SS_EINVAL;
+    if (n->rows > 0 && !n->d_h && !n->d_x && !n->d_weight) return SS_EINVAL;
+    NormGradArgs a = {};
+    if (int rc = choose_drop(n->dropout, n->rng, &a.drop, &a.scale)) return rc;
+    if (n->rows > kMaxRows || n->cols > kMaxCols) return SS_EOVERFLOW;
+    if (!n->weight || (n->rows > 0 && (!n->d_out || !n->h || !n->rstd))) return SS_EINVAL;
+    const Matrix dy = {n->d_out, n->d_out_stride}, h = {n->h, n->h_stride}, ds = {n->d_sum, n->d_sum_stride};
+    const Matrix w = {n->weight, n->cols}, dh = {n->d_h, n->d_h_stride}, dx = {n->d_x, n->d_x_stride};
+    if (int rc = check_matrices(n->rows, n->cols, n->elem_bytes, {dy, h, ds, w, dh, dx, {n->d_weight, n->cols}}))
+        return rc;
+    if (!ss::aligned(n->rstd, 4) || !ss::aligned(n->workspace, 16)) return SS_EALIGN;
+    const Shape s = choose_shape((n->cols + 7) / 8);
+    const int64_t grid = std::max<int64_t>(grad_grid(n->rows, s), 1);
+    if (n->d_weight && (!n->workspace || n->workspace_bytes < (size_t)(grid * n->cols * 4))) return SS_EINVAL;
+    if (n->rows == 0 && !n->d_weight) return SS_OK;
+    a.rows = n->rows, a.cols = (int)n->cols, a.team = s.team;
+    a.d_out = n->d_out, a.d_out_stride = n->d_out_stride, a.h = n->h, a.h_stride = n->h_stride;
+    a.weight = n->weight, a.d_sum = n->d_sum, a.d_sum_stride = n->d_sum_stride, a.rstd = n->rstd;
+    a.inv_cols = 1.f / (float)n->cols, a.rng = n->rng;
+    a.d_h = n->d_h, a.d_h_stride = n->d_h_stride, a.d_x = n->d_x, a.d_x_stride = n->d_x_stride;
+    a.part = n->d_weight ? static_cast<float*>(n->workspace) : nullptr;
+    const bool al = rows_on_16(n->elem_bytes, {dy, h, ds, dh, dx}) && ss::aligned(n->weight, 16);
+    const int teams = s.threads / s.team;
+    const int smem = teams > 1 ? teams * a.cols * 4 : 0;  // at most 8 x 512 floats, or 4 x 1024, ...
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (int rc = with_shape(n->elem_bytes, s.vecs, al, [&](auto t, auto v, auto aligned) {
+            return ss::launch(norm_grad_kernel<decltype(t), decltype(v)::value, decltype(aligned)::value>, grid,
+                              s.threads, smem, 0, true, st, a);
+        }))
+        return rc;
+    if (!n->d_weight) return SS_OK;
+    const int64_t blocks = (n->cols + 31) / 32;
+    if (n->elem_bytes == 2)
+        return ss::launch(norm_join_kernel<uint16_t>, blocks, 32 * kJoinRows, 0, 0, true, st, a.part, (int)grid, a.cols,
+                          static_cast<uint16_t*>(n->d_weight));
+    return ss::launch(norm_join_kernel<float>, blocks, 32 * kJoinRows, 0, 0, true, st, a.part, (int)grid, a.cols,
+                      static_cast<float*>(n->d_weight));
+}
+
+}  // extern "C"

@@ -1,6 +1,6 @@
 // tcgen05.cuh -- sm_103a primitives the matrix kernels use: mbarriers with
 // bounded waits, tiled TMA loads, tensor memory, and the fifth-generation
-// tensor-core product issued for a pair of CTAs (cta_group::2).
+// tensor-core products issued for a pair of CTAs (cta_group::2) or for one.
 #pragma once
 
 #include <cuda.h>
@@ -128,6 +128,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// The same for a CTA on its own barrier.
+__device__ __forceinline__ void tma_load_2d_one(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // tensor memory and the tensor-core product
 // ---------------------------------------------------------------------------
@@ -179,6 +188,70 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
         "h"((uint16_t)3)
         : "memory");
+}
+
+// The forms of one CTA (cta_group::1); a kernel uses these or the pair's.
+__device__ __forceinline__ void tmem_alloc_one(uint32_t smem_dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_free_one(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+
+__device__ __forceinline__ void commit_one(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// products of microscaled operands
+// ---------------------------------------------------------------------------
+
+// Shared-memory descriptor of a tile of scales: 128 rows' 4 bytes in 32 lines of 16,
+// not swizzled, 8 lines 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+
+// Instruction descriptor: both operands e2m1 (FOUR) or e4m3, K-major, scales powers
+// of two (ue8m0), fp32 accumulator, M x N.  Bits 4-5 and 29-30 say which of the
+// scales' 4 bytes an instruction starts with: scale_id() of it is added.
+__host__ __device__ constexpr uint32_t scaled_desc(bool four, int m, int n) {
+    return (four ? (1u << 7) | (1u << 10) : 0u) | (1u << 23) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t scale_id(int id) { return ((uint32_t)id << 4) | ((uint32_t)id << 29); }
+
+// A tile of scales from shared memory to 4 columns of tensor memory, the same in all
+// four groups of 32 lanes; in line with the products that the same thread issues.
+// PAIR: in both CTAs of the pair, each from its own shared memory.
+template <bool PAIR>
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+    if (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+// D (+)= (A sa) (B sb)^T over 32 bytes of every row: 64 e2m1 or 32 e4m3 elements.
+template <bool PAIR, bool FOUR>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                           bool accumulate) {
+#define SS_MMA_SCALED(GROUP, KIND)                                                                                    \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                    \
+                 "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),    \
+                 "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)accumulate)                              \
+                 : "memory")
+    if (PAIR && FOUR)
+        SS_MMA_SCALED("2", "mxf4.block_scale.scale_vec::2X");
+    else if (PAIR)
+        SS_MMA_SCALED("2", "mxf8f6f4.block_scale.scale_vec::1X");
+    else if (FOUR)
+        SS_MMA_SCALED("1", "mxf4.block_scale.scale_vec::2X");
+    else
+        SS_MMA_SCALED("1", "mxf8f6f4.block_scale.scale_vec::1X");
+#undef SS_MMA_SCALED
 }
 
 // 32 columns of this warp's 32 lanes, lane i of the warp getting row i: asked for
