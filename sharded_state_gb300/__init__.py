@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -106,37 +107,13 @@ class _LinearCE(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
-class _Norm(ctypes.Structure):
-    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("elem_bytes", ctypes.c_int),
-                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("residual", ctypes.c_void_p),
-                ("residual_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("eps", ctypes.c_double),
-                ("dropout", ctypes.c_double), ("rng", ctypes.c_void_p), ("sum_out", ctypes.c_void_p),
-                ("sum_stride", ctypes.c_int64), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
-                ("rstd_out", ctypes.c_void_p), ("mx_data", ctypes.c_void_p), ("mx_scales", ctypes.c_void_p)]
-
-
-class _NormGrad(ctypes.Structure):
-    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("elem_bytes", ctypes.c_int),
-                ("d_out", ctypes.c_void_p), ("d_out_stride", ctypes.c_int64), ("h", ctypes.c_void_p),
-                ("h_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
-                ("d_sum", ctypes.c_void_p), ("d_sum_stride", ctypes.c_int64), ("dropout", ctypes.c_double),
-                ("rng", ctypes.c_void_p), ("d_h", ctypes.c_void_p), ("d_h_stride", ctypes.c_int64),
-                ("d_x", ctypes.c_void_p), ("d_x_stride", ctypes.c_int64), ("d_weight", ctypes.c_void_p),
-                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
-
-
-class _MxQuant(ctypes.Structure):
-    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("elem_bytes", ctypes.c_int),
-                ("x", ctypes.c_void_p), ("stride", ctypes.c_int64), ("format", ctypes.c_int),
-                ("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("t_data", ctypes.c_void_p),
-                ("t_scales", ctypes.c_void_p), ("rng", ctypes.c_void_p)]
-
-
-class _MxProduct(ctypes.Structure):
-    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("format", ctypes.c_int),
-                ("a_data", ctypes.c_void_p), ("a_scales", ctypes.c_void_p), ("b_data", ctypes.c_void_p),
-                ("b_scales", ctypes.c_void_p), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
-                ("elem_bytes", ctypes.c_int)]
+# The argument blocks of the calls that a small model makes many times a step are packed
+# (a quarter of a ctypes structure's time): ss_norm, ss_norm_grad, ss_mx_quant and
+# ss_mx_product as the C ABI lays them out, NULL as 0.
+_NORM = struct.Struct("@qqiPqPqPddPPqPqPPP")
+_NORM_GRAD = struct.Struct("@qqiPqPqPPPqdPPqPqPPN")
+_MX_QUANT = struct.Struct("@qqiPqiPPPPP")
+_MX_PRODUCT = struct.Struct("@qqqiPPPPPqi0q")
 
 
 def _load() -> ctypes.CDLL:
@@ -178,13 +155,13 @@ def _load() -> ctypes.CDLL:
         "ss_linear_cross_entropy": ([ctypes.POINTER(_LinearCE), vp], i32),
         "ss_linear_ce_expire_wait": ([i32], i32),
         "ss_dropout": ([i64, i64, i32, vp, i64, vp, i64, ctypes.c_double, vp, vp], i32),
-        "ss_rms_norm": ([ctypes.POINTER(_Norm), vp], i32),
+        "ss_rms_norm": ([ctypes.c_char_p, vp], i32),
         "ss_rms_norm_workspace": ([i64, i64, ctypes.POINTER(ctypes.c_size_t)], i32),
-        "ss_rms_norm_backward": ([ctypes.POINTER(_NormGrad), vp], i32),
+        "ss_rms_norm_backward": ([ctypes.c_char_p, vp], i32),
         "ss_mx_bytes": ([i64, i64, i32, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)], i32),
-        "ss_mx_quantize": ([ctypes.POINTER(_MxQuant), vp], i32),
+        "ss_mx_quantize": ([ctypes.c_char_p, vp], i32),
         "ss_mx_dequantize": ([i64, i64, i32, vp, vp, vp, i64, i32, vp], i32),
-        "ss_mx_matmul": ([ctypes.POINTER(_MxProduct), vp], i32),
+        "ss_mx_matmul": ([ctypes.c_char_p, vp], i32),
         "ss_strerror": ([i32], ctypes.c_char_p),
         "ss_last_cuda_error": ([], i32),
         "ss_version": ([], ctypes.c_char_p),
@@ -710,8 +687,16 @@ def ss_linear_cross_entropy(hidden, weight, targets, loss_out, workspace, token_
 # ---------------------------------------------------------------------------
 
 def _device() -> int:
-    import torch
-    return torch.cuda.current_device()
+    """The current device, by torch's own accessor where it has one (see _current_stream)."""
+    global _get_device
+    if _get_device is None:
+        import torch
+        torch.cuda.current_device()  # initialises CUDA
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _get_device()
+
+
+_get_device = None
 
 
 def _row_dtype(fn: str, t, what: str):
@@ -722,21 +707,21 @@ def _row_dtype(fn: str, t, what: str):
 
 
 def _rows(fn: str, t, what: str, rows: int, cols: int, dtype, device: int):
-    """Address and row stride of a matrix of that type on the current device (NULL, 0 for None)."""
+    """Address and row stride of a matrix of that type on the current device (0, 0 for None)."""
     if t is None:
-        return None, 0
-    if t.get_device() != device or t.dtype != dtype or t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1):
+        return 0, 0
+    if t.get_device() != device or t.dtype is not dtype or t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1):
         raise ShardStateError(fn, SS_EINVAL, f"{what}: {dtype} [{rows}, {cols}] on the current GPU with unit column "
                                              "stride is wanted")
     stride = t.stride(0)
     return t.data_ptr(), stride if rows > 1 or stride > cols else cols
 
 
-def _flat(fn: str, t, what: str, dtype, numel: int, device: int) -> Optional[int]:
-    """Address of a contiguous tensor of at least numel elements on the current device (NULL for None)."""
+def _flat(fn: str, t, what: str, dtype, numel: int, device: int) -> int:
+    """Address of a contiguous tensor of at least numel elements on the current device (0 for None)."""
     if t is None:
-        return None
-    if t.get_device() != device or t.dtype != dtype or t.numel() < numel or not t.is_contiguous():
+        return 0
+    if t.get_device() != device or t.dtype is not dtype or t.numel() < numel or not t.is_contiguous():
         raise ShardStateError(fn, SS_EINVAL, f"{what}: contiguous {dtype} on the current GPU, at least {numel} elements")
     return t.data_ptr()
 
@@ -775,10 +760,10 @@ def ss_rms_norm(x, weight, eps: float, out=None, residual=None, sum_out=None, rs
     if weight is None or weight.numel() != cols:
         raise ShardStateError(fn, SS_EINVAL, f"weight: {cols} elements are wanted")
     md, ms = _mx_buffers(fn, mx_data, mx_scales, "mx", rows, cols, SS_MXFP8, dev)
-    args = _Norm(rows, cols, x.element_size(), ax, ldx, ar, ldr, _flat(fn, weight, "weight", dtype, cols, dev), eps,
+    args = _NORM.pack(rows, cols, x.element_size(), ax, ldx, ar, ldr, _flat(fn, weight, "weight", dtype, cols, dev), eps,
                  dropout, _flat(fn, rng, "rng", _dtype("int64"), 2, dev), ah, ldh, ao, ldo,
                  _flat(fn, rstd_out, "rstd_out", _dtype("float32"), rows, dev), md, ms)
-    status = _lib.ss_rms_norm(ctypes.byref(args), _stream(stream))
+    status = _lib.ss_rms_norm(args, _stream(stream))
     if status != SS_OK:
         _check(fn, status)
 
@@ -808,12 +793,12 @@ def ss_rms_norm_backward(d_out, h, weight, rstd, d_h, workspace, d_sum=None, d_x
     for name, t in (("weight", weight), ("d_weight", d_weight)):
         if t is not None and t.numel() != cols:
             raise ShardStateError(fn, SS_EINVAL, f"{name}: {cols} elements are wanted")
-    ws, nbytes = (None, 0) if workspace is None else _workspace(fn, workspace)
-    args = _NormGrad(rows, cols, h.element_size(), ay, ldy, ah, ldh, _flat(fn, weight, "weight", dtype, cols, dev),
+    ws, nbytes = (0, 0) if workspace is None else _workspace(fn, workspace)
+    args = _NORM_GRAD.pack(rows, cols, h.element_size(), ay, ldy, ah, ldh, _flat(fn, weight, "weight", dtype, cols, dev),
                      _flat(fn, rstd, "rstd", _dtype("float32"), rows, dev), as_, lds, dropout,
                      _flat(fn, rng, "rng", _dtype("int64"), 2, dev), ag, ldg, ax, ldx,
                      _flat(fn, d_weight, "d_weight", dtype, cols, dev), ws, nbytes)
-    status = _lib.ss_rms_norm_backward(ctypes.byref(args), _stream(stream))
+    status = _lib.ss_rms_norm_backward(args, _stream(stream))
     if status != SS_OK:
         _check(fn, status)
 
@@ -830,9 +815,9 @@ def ss_mx_bytes(rows: int, cols: int, format: int):
 
 
 def _mx_buffers(fn: str, data, scales, what: str, rows: int, cols: int, format: int, device: int):
-    """Addresses of a quantised matrix's buffers, uint8 and large enough (NULL, NULL for None, None)."""
+    """Addresses of a quantised matrix's buffers, uint8 and large enough (0, 0 for None, None)."""
     if data is None and scales is None:
-        return None, None
+        return 0, 0
     if data is None or scales is None:
         raise ShardStateError(fn, SS_EINVAL, f"{what}: data and scales are wanted together")
     wide = -(-cols // 128)
@@ -858,9 +843,9 @@ def ss_mx_quantize(x, format: int, data=None, scales=None, t_data=None, t_scales
     ax, ldx = _rows(fn, x, "x", rows, cols, dtype, dev)
     d, s = _mx_buffers(fn, data, scales, "quantised", rows, cols, format, dev)
     td, ts = _mx_buffers(fn, t_data, t_scales, "transposed", cols, rows, format, dev)
-    args = _MxQuant(rows, cols, x.element_size(), ax, ldx, format, d, s, td, ts,
+    args = _MX_QUANT.pack(rows, cols, x.element_size(), ax, ldx, format, d, s, td, ts,
                     _flat(fn, rng, "rng", _dtype("int64"), 2, dev))
-    status = _lib.ss_mx_quantize(ctypes.byref(args), _stream(stream))
+    status = _lib.ss_mx_quantize(args, _stream(stream))
     if status != SS_OK:
         _check(fn, status)
 
@@ -889,7 +874,7 @@ def ss_mx_matmul(a_data, a_scales, b_data, b_scales, K: int, format: int, out, s
     ao, ldo = _rows(fn, out, "out", M, N, dtype, dev)
     ad, as_ = _mx_buffers(fn, a_data, a_scales, "A", M, K, format, dev)
     bd, bs = _mx_buffers(fn, b_data, b_scales, "B", N, K, format, dev)
-    args = _MxProduct(M, N, K, format, ad, as_, bd, bs, ao, ldo, out.element_size())
-    status = _lib.ss_mx_matmul(ctypes.byref(args), _stream(stream))
+    args = _MX_PRODUCT.pack(M, N, K, format, ad, as_, bd, bs, ao, ldo, out.element_size())
+    status = _lib.ss_mx_matmul(args, _stream(stream))
     if status != SS_OK:
         _check(fn, status)

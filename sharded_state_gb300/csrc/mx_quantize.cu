@@ -23,6 +23,7 @@ namespace {
 using ss::kMxTile;
 using ss::launch_after;
 using ss::Mx;
+using ss::Run;
 using ss::Vec8;
 using ss::wait_before;
 
@@ -63,15 +64,14 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
     const int64_t tr = blockIdx.x / a.col_tiles, tc = blockIdx.x - tr * a.col_tiles;
     const int line = threadIdx.x >> 4, c8 = threadIdx.x & 15;
     const int64_t row0 = tr * kMxTile, col0 = tc * kMxTile;
-    const int n = (int)max((int64_t)0, min(a.cols - col0 - 8 * c8, (int64_t)8));
     wait_before();
     const T* x = static_cast<const T*>(a.x) + row0 * a.stride + col0 + 8 * c8;
     Vec8<T> v[kRounds];
 #pragma unroll
     for (int i = 0; i < kRounds; ++i) {
         const int r = 16 * i + line;
-        v[i].clear();
-        if (row0 + r < a.rows && n > 0) v[i].template load<ALIGNED>(x + r * a.stride, n);
+        v[i].template load<ALIGNED>(x + r * a.stride,
+                                    Run(row0 + r < a.rows ? a.cols - col0 - 8 * c8 : 0, c8 == 0, c8 == 15));
     }
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
         uint4 bits = make_uint4(0, 0, 0, 0);
         if (RANDOM) bits = ss::Philox(a.rng)((uint32_t)row, (uint32_t)(tc * 16 + c8));
         if (TRANSPOSE) {
-            v[i].template store<true>(tile + r * kMxTile + 8 * c8, 8);
+            v[i].template store<true>(tile + r * kMxTile + 8 * c8, Run(8, true, true));
             if (RANDOM) *reinterpret_cast<uint4*>(random + r * kMxTile + 8 * c8) = bits;
         }
         if (!a.data) continue;
@@ -174,22 +174,22 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_const
     const int64_t tr = blockIdx.x / a.col_tiles, tc = blockIdx.x - tr * a.col_tiles;
     const int line = threadIdx.x >> 4, c8 = threadIdx.x & 15;
     const int64_t col = tc * kMxTile + 8 * c8;
-    const int n = (int)min(a.cols - col, (int64_t)8);
     wait_before();
-    if (n <= 0) return;
     Word w[kRounds];
     unsigned char byte[kRounds];
 #pragma unroll
     for (int i = 0; i < kRounds; ++i) {
         const int64_t row = tr * kMxTile + 16 * i + line;
-        if (row >= a.rows) break;
+        w[i] = Word();
+        byte[i] = 0;
+        if (row >= a.rows || col >= a.cols) continue;
         w[i] = *reinterpret_cast<const Word*>(a.data + (row * a.col_tiles + tc) * M::kTileRow + c8 * (int)sizeof(Word));
         byte[i] = a.scales[ss::mx_scale_at(row, col >> 5, a.col_tiles)];
     }
 #pragma unroll
     for (int i = 0; i < kRounds; ++i) {
         const int64_t row = tr * kMxTile + 16 * i + line;
-        if (row >= a.rows) break;
+        if (row - (line & 1) >= a.rows) break;  // both rows of the warp are behind the last
         float f[8];
         M::decode(w[i], f);
         const float scale = ss::mx_value(byte[i]);
@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_const
         for (int k = 0; k < 8; ++k) f[k] *= scale;
         Vec8<T> v;
         v.set(f);
-        v.template store<ALIGNED>(static_cast<T*>(a.out) + row * a.stride + col, n);
+        v.template store<ALIGNED>(static_cast<T*>(a.out) + row * a.stride + col,
+                                  Run(row < a.rows ? a.cols - col : 0, c8 == 0, c8 == 15));
     }
 }
 

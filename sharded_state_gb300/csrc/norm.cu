@@ -31,6 +31,7 @@
 namespace {
 
 using ss::launch_after;
+using ss::Run;
 using ss::Vec8;
 using ss::wait_before;
 
@@ -39,6 +40,7 @@ using ss::wait_before;
 // ---------------------------------------------------------------------------
 
 constexpr int kDropThreads = 256;
+constexpr int kDropVecs = 2;
 
 struct DropArgs {
     int64_t rows, cols, groups;  // groups: of 8 columns in a row
@@ -52,28 +54,39 @@ struct DropArgs {
     int64_t step_rows, step_groups;  // the grid's threads, as rows and groups
 };
 
+// Threads take groups of 8 in the order of the matrix, kDropVecs of them at a time so
+// that as many loads are on their way.
 template <class T, bool ALIGNED>
 __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_constant__ DropArgs a) {
     launch_after();
     const int64_t first = (int64_t)blockIdx.x * kDropThreads + threadIdx.x;
+    const int lane = threadIdx.x & 31;
     int64_t row = first / a.groups, group = first - row * a.groups;
     wait_before();
     const ss::Philox philox(a.rng);
     const T* x = static_cast<const T*>(a.x);
     T* out = static_cast<T*>(a.out);
-    while (row < a.rows) {
-        const int64_t col = 8 * group;
-        const int n = (int)min(a.cols - col, (int64_t)8);
-        Vec8<T> v;
-        v.template load<ALIGNED>(x + row * a.x_stride + col, n);
-        float f[8];
-        v.get(f);
-        ss::drop8(f, philox((uint32_t)row, (uint32_t)group), a.drop, a.scale);
-        v.set(f);
-        v.template store<ALIGNED>(out + row * a.out_stride + col, n);
-        row += a.step_rows;
-        group += a.step_groups;
-        if (group >= a.groups) group -= a.groups, ++row;
+    while (__any_sync(0xFFFFFFFFu, row < a.rows)) {
+        Vec8<T> v[kDropVecs];
+        int64_t rows[kDropVecs], groups[kDropVecs];
+#pragma unroll
+        for (int i = 0; i < kDropVecs; ++i) {
+            rows[i] = row, groups[i] = group;
+            const Run run(row < a.rows ? a.cols - 8 * group : 0, lane == 0 || group == 0, lane == 31);
+            v[i].template load<ALIGNED>(x + row * a.x_stride + 8 * group, run);
+            row += a.step_rows;
+            group += a.step_groups;
+            if (group >= a.groups) group -= a.groups, ++row;
+        }
+#pragma unroll
+        for (int i = 0; i < kDropVecs; ++i) {
+            const Run run(rows[i] < a.rows ? a.cols - 8 * groups[i] : 0, lane == 0 || groups[i] == 0, lane == 31);
+            float f[8];
+            v[i].get(f);
+            ss::drop8(f, philox((uint32_t)rows[i], (uint32_t)groups[i]), a.drop, a.scale);
+            v[i].set(f);
+            v[i].template store<ALIGNED>(out + rows[i] * a.out_stride + 8 * groups[i], run);
+        }
     }
 }
 
@@ -149,42 +162,39 @@ template <class T, int VECS, bool ALIGNED>
 __global__ void __launch_bounds__(VECS > 2 ? 512 : 256) norm_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float lane_sums[16];
     launch_after();
-    const int mine = threadIdx.x % a.team;
+    const int mine = threadIdx.x % a.team, lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / a.team) + threadIdx.x / a.team;
     const bool live = row < a.rows;
-    const T* weight = static_cast<const T*>(a.weight);
+    auto run = [&](int col) { return Run(live ? a.cols - col : 0, lane == 0, lane == 31); };
     wait_before();
     Vec8<T> x[VECS], r[VECS];
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
-        const int col = 8 * (mine + i * a.team), n = live ? a.cols - col : 0;
-        x[i].clear();
-        r[i].clear();
-        if (n > 0) x[i].template load<ALIGNED>(static_cast<const T*>(a.x) + row * a.x_stride + col, n);
-        if (n > 0 && a.residual)
-            r[i].template load<ALIGNED>(static_cast<const T*>(a.residual) + row * a.residual_stride + col, n);
+        const int col = 8 * (mine + i * a.team);
+        x[i].template load<ALIGNED>(static_cast<const T*>(a.x) + row * a.x_stride + col, run(col));
+        if (a.residual)
+            r[i].template load<ALIGNED>(static_cast<const T*>(a.residual) + row * a.residual_stride + col, run(col));
     }
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
-        const int col = 8 * (mine + i * a.team), n = live ? a.cols - col : 0;
+        const int col = 8 * (mine + i * a.team);
+        float f[8];
         if (a.drop || a.residual) {
-            float f[8], q[8];
             x[i].get(f);
-            r[i].get(q);
             if (a.drop) ss::drop8(f, ss::Philox(a.rng)((uint32_t)row, (uint32_t)(col >> 3)), a.drop, a.scale);
             if (a.residual) {
+                float q[8];
+                r[i].get(q);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) f[k] = __fadd_rn(f[k], q[k]);
             }
             x[i].set(f);
         }
-        if (n > 0 && a.sum_out) x[i].template store<ALIGNED>(static_cast<T*>(a.sum_out) + row * a.sum_stride + col, n);
-        float f[8];
-        x[i].get(f);
+        if (a.sum_out) x[i].template store<ALIGNED>(static_cast<T*>(a.sum_out) + row * a.sum_stride + col, run(col));
+        x[i].get(f);  // zeros behind the row's end
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < n) s = fmaf(f[k], f[k], s);
+        for (int k = 0; k < 8; ++k) s = fmaf(f[k], f[k], s);
     }
     s = team_sum(s, a.team, lane_sums);
     const float rstd = 1.f / sqrtf(fmaf(s, a.inv_cols, a.eps));
@@ -192,97 +202,114 @@ __global__ void __launch_bounds__(VECS > 2 ? 512 : 256) norm_kernel(const __grid
     if (!a.out && !a.mx_data) return;
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
-        const int col = 8 * (mine + i * a.team), n = live ? a.cols - col : 0;
+        const int col = 8 * (mine + i * a.team);
         Vec8<T> w;
-        w.clear();
-        if (n > 0) w.template load<ALIGNED>(weight + col, n);
+        w.template load<ALIGNED>(static_cast<const T*>(a.weight) + col, run(col));
         float f[8], q[8];
         x[i].get(f);
         w.get(q);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = k < n ? f[k] * rstd * q[k] : 0.f;
-        if (n > 0 && a.out) {
+        for (int k = 0; k < 8; ++k) f[k] = f[k] * rstd * q[k];
+        if (a.out) {
             w.set(f);
-            w.template store<ALIGNED>(static_cast<T*>(a.out) + row * a.out_stride + col, n);
+            w.template store<ALIGNED>(static_cast<T*>(a.out) + row * a.out_stride + col, run(col));
         }
-        if (a.mx_data) store_mx8(a, row, col, f);
+        if (a.mx_data) {
+            const int n = run(col).n;  // an infinite rstd would make the zeros behind the end NaN
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = k < n ? f[k] : 0.f;
+            store_mx8(a, row, col, f);
+        }
     }
 }
 
+// The rows of a backward pass in turn, each CTA its own; the next row's elements are
+// on their way while one is worked on (VECS <= 2: more do not fit the registers).
 template <class T, int VECS, bool ALIGNED>
-__global__ void __launch_bounds__(VECS > 2 ? 512 : 256) norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
+__global__ void __launch_bounds__(VECS > 2 ? 512 : 256, VECS > 2 ? 1 : 2)
+norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
     extern __shared__ float joined[];  // [rows at a time][cols], where that is more than one
     __shared__ float lane_sums[2][16];
+    constexpr bool kAhead = VECS <= 2;
     launch_after();
     const int mine = threadIdx.x % a.team, teams = blockDim.x / a.team, team = threadIdx.x / a.team;
-    const T* weight = static_cast<const T*>(a.weight);
+    const int lane = threadIdx.x & 31;
     wait_before();
     float dw[VECS][8];
 #pragma unroll
     for (int i = 0; i < VECS; ++i)
 #pragma unroll
         for (int k = 0; k < 8; ++k) dw[i][k] = 0.f;
-    int parity = 0;
-    for (int64_t first = (int64_t)blockIdx.x * teams; first < a.rows; first += (int64_t)gridDim.x * teams, parity ^= 1) {
-        const int64_t row = first + team;
-        const bool live = row < a.rows;
+    auto run = [&](int64_t row, int col) { return Run(row < a.rows ? a.cols - col : 0, lane == 0, lane == 31); };
+    struct Row {
         Vec8<T> dy[VECS], h[VECS], ds[VECS];
+        float rstd;
+    };
+    auto load = [&](Row& x, int64_t row) {
 #pragma unroll
         for (int i = 0; i < VECS; ++i) {
-            const int col = 8 * (mine + i * a.team), n = live ? a.cols - col : 0;
-            dy[i].clear();
-            h[i].clear();
-            ds[i].clear();
-            if (n > 0) {
-                dy[i].template load<ALIGNED>(static_cast<const T*>(a.d_out) + row * a.d_out_stride + col, n);
-                h[i].template load<ALIGNED>(static_cast<const T*>(a.h) + row * a.h_stride + col, n);
-                if (a.d_sum) ds[i].template load<ALIGNED>(static_cast<const T*>(a.d_sum) + row * a.d_sum_stride + col, n);
-            }
+            const int col = 8 * (mine + i * a.team);
+            x.dy[i].template load<ALIGNED>(static_cast<const T*>(a.d_out) + row * a.d_out_stride + col, run(row, col));
+            x.h[i].template load<ALIGNED>(static_cast<const T*>(a.h) + row * a.h_stride + col, run(row, col));
+            if (a.d_sum)
+                x.ds[i].template load<ALIGNED>(static_cast<const T*>(a.d_sum) + row * a.d_sum_stride + col, run(row, col));
+            else
+                x.ds[i].clear();
         }
-        const float rstd = live ? a.rstd[row] : 0.f;
+        x.rstd = row < a.rows ? a.rstd[row] : 0.f;
+    };
+    int parity = 0;
+    const int64_t step = (int64_t)gridDim.x * teams;
+    Row x, ahead;
+    if (kAhead) load(x, (int64_t)blockIdx.x * teams + team);
+    for (int64_t first = (int64_t)blockIdx.x * teams; first < a.rows; first += step, parity ^= 1) {
+        const int64_t row = first + team;
+        if (kAhead)
+            load(ahead, row + step);
+        else
+            load(x, row);
+        const float rstd = x.rstd;
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < VECS; ++i) {
-            const int col = 8 * (mine + i * a.team), n = live ? a.cols - col : 0;
+            const int col = 8 * (mine + i * a.team);
             Vec8<T> w;
-            w.clear();
-            if (n > 0) w.template load<ALIGNED>(weight + col, n);
+            w.template load<ALIGNED>(static_cast<const T*>(a.weight) + col, Run(a.cols - col, lane == 0, lane == 31));
             float f[8], q[8], g[8];
-            dy[i].get(f);
-            h[i].get(q);
+            x.dy[i].get(f);
+            x.h[i].get(q);
             w.get(g);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < n) {
-                    const float t = f[k] * (q[k] * rstd);
-                    s = fmaf(t, g[k], s);
-                    dw[i][k] += t;
-                }
+            for (int k = 0; k < 8; ++k) {  // zeros behind the row's end
+                const float t = f[k] * (q[k] * rstd);
+                s = fmaf(t, g[k], s);
+                dw[i][k] += t;
+            }
         }
         s = team_sum(s, a.team, lane_sums[parity]) * a.inv_cols;
 #pragma unroll
         for (int i = 0; i < VECS; ++i) {
-            const int col = 8 * (mine + i * a.team), n = live ? a.cols - col : 0;
-            if (n <= 0) continue;
+            const int col = 8 * (mine + i * a.team);
             Vec8<T> w;
-            w.template load<ALIGNED>(weight + col, n);
+            w.template load<ALIGNED>(static_cast<const T*>(a.weight) + col, Run(a.cols - col, lane == 0, lane == 31));
             float f[8], q[8], g[8], d[8];
-            dy[i].get(f);
-            h[i].get(q);
+            x.dy[i].get(f);
+            x.h[i].get(q);
             w.get(g);
-            ds[i].get(d);
+            x.ds[i].get(d);
 #pragma unroll
             for (int k = 0; k < 8; ++k) f[k] = fmaf(rstd, fmaf(-q[k] * rstd, s, f[k] * g[k]), d[k]);
             if (a.d_h) {
                 w.set(f);
-                w.template store<ALIGNED>(static_cast<T*>(a.d_h) + row * a.d_h_stride + col, n);
+                w.template store<ALIGNED>(static_cast<T*>(a.d_h) + row * a.d_h_stride + col, run(row, col));
             }
             if (a.d_x) {
                 if (a.drop) ss::drop8(f, ss::Philox(a.rng)((uint32_t)row, (uint32_t)(col >> 3)), a.drop, a.scale);
                 w.set(f);
-                w.template store<ALIGNED>(static_cast<T*>(a.d_x) + row * a.d_x_stride + col, n);
+                w.template store<ALIGNED>(static_cast<T*>(a.d_x) + row * a.d_x_stride + col, run(row, col));
             }
         }
+        if (kAhead) x = ahead;
     }
     if (!a.part) return;
     float* part = a.part + (int64_t)blockIdx.x * a.cols;

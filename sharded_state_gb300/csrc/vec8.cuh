@@ -1,10 +1,17 @@
-// vec8.cuh -- 8 consecutive elements of a matrix row, bf16 or fp32, at any element
-// alignment, as a thread of the row kernels holds them.
+// vec8.cuh -- 8 consecutive elements of a matrix row, bf16 or fp32, as a thread of the
+// row kernels holds them, loaded and stored in 16-byte blocks at any element alignment.
+//
+// Where rows do not start on 16 bytes, a group's bytes lie in two (bf16) or three
+// (fp32) aligned blocks.  Neighbouring lanes hold neighbouring groups of a row, so each
+// block is loaded once, by the lane that needs its last bytes, and realigned with the
+// next lane's; stores are put together the same way.  (Element by element instead: 1021
+// rows of 1001 bf16, forward and backward 58 us where this takes less than half.)
 #pragma once
 
 #include <cstdint>
 
 #include "device_utils.cuh"
+#include "segmap.cuh"
 
 namespace ss {
 
@@ -18,27 +25,63 @@ __device__ __forceinline__ uint4 ld_row_u4(const void* p) {
     return r;
 }
 
+__device__ __forceinline__ uint4 from_next_lane(uint4 v) {
+    return make_uint4(__shfl_down_sync(0xFFFFFFFFu, v.x, 1), __shfl_down_sync(0xFFFFFFFFu, v.y, 1),
+                      __shfl_down_sync(0xFFFFFFFFu, v.z, 1), __shfl_down_sync(0xFFFFFFFFu, v.w, 1));
+}
+
+// Words [lo, hi) of the 16-byte value v to blk.
+__device__ __forceinline__ void st_words(unsigned char* blk, uint4 v, int lo, int hi) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(blk);
+    if (lo <= 0 && hi > 0) w[0] = v.x;
+    if (lo <= 1 && hi > 1) w[1] = v.y;
+    if (lo <= 2 && hi > 2) w[2] = v.z;
+    if (lo <= 3 && hi > 3) w[3] = v.w;
+}
+
+// A lane's place in its row: n elements of its own (0: none), `after` in the next lane
+// (0 where that is not the group behind this one), and whether the lane before holds
+// the group before.
+struct Run {
+    int n, after;
+    bool prev;
+
+    // left: elements of the row from this group on (any sign); first, last: of the
+    // lanes that hold neighbouring groups.
+    __device__ __forceinline__ Run(int64_t left, bool first, bool last)
+        : n((int)max((int64_t)0, min(left, (int64_t)8))),
+          after(last ? 0 : (int)max((int64_t)0, min(left - 8, (int64_t)8))),
+          prev(!first && left > 0) {}
+};
+
 template <class T>
 struct Vec8;
 
+// Loads and stores with ALIGNED want p on 16 bytes; without, the whole warp makes them.
 template <>
 struct Vec8<uint16_t> {  // bf16
     uint4 r;
 
     __device__ __forceinline__ void clear() { r = make_uint4(0, 0, 0, 0); }
 
-    // Elements [0, n) of the 8 at p, the others 0.  ALIGNED: p is on 16 bytes.
+    // The lane's n elements at p, zeros behind them.
     template <bool ALIGNED>
-    __device__ __forceinline__ void load(const uint16_t* p, int n) {
-        if (ALIGNED && n >= 8) {
-            r = ld_row_u4(p);
-            return;
+    __device__ __forceinline__ void load(const uint16_t* p, const Run& run) {
+        const int sh = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+        const unsigned char* blk = reinterpret_cast<const unsigned char*>(p) - sh;
+        r = make_uint4(0, 0, 0, 0);
+        if (run.n > 0) r = ld_row_u4(blk);
+        if (!ALIGNED) {
+            uint4 next = from_next_lane(r);
+            if (run.after == 0 && sh + 2 * run.n > 16) next = ld_row_u4(blk + 16);
+            r = realign16(r, next, sh);
         }
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) w[i >> 1] |= (uint32_t)*reinterpret_cast<const volatile uint16_t*>(p + i) << (16 * (i & 1));
-        r = make_uint4(w[0], w[1], w[2], w[3]);
+        if (run.n < 8) {
+            r.x = run.n > 1 ? r.x : run.n > 0 ? r.x & 0xFFFFu : 0u;
+            r.y = run.n > 3 ? r.y : run.n > 2 ? r.y & 0xFFFFu : 0u;
+            r.z = run.n > 5 ? r.z : run.n > 4 ? r.z & 0xFFFFu : 0u;
+            r.w = run.n > 6 ? r.w & 0xFFFFu : 0u;
+        }
     }
 
     __device__ __forceinline__ void get(float (&f)[8]) const {
@@ -53,15 +96,25 @@ struct Vec8<uint16_t> {  // bf16
     }
 
     template <bool ALIGNED>
-    __device__ __forceinline__ void store(uint16_t* p, int n) const {
-        if (ALIGNED && n >= 8) {
-            *reinterpret_cast<uint4*>(p) = r;
+    __device__ __forceinline__ void store(uint16_t* p, const Run& run) const {
+        unsigned char* c = reinterpret_cast<unsigned char*>(p);
+        const int sh = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+        uint4 next = make_uint4(0, 0, 0, 0);
+        if (!ALIGNED) next = from_next_lane(r);
+        if (run.n == 0) return;
+        if (sh == 0) {
+            if (run.n == 8)
+                *reinterpret_cast<uint4*>(p) = r;
+            else
+                st_bytes(c, r, 0, 2 * run.n);
             return;
         }
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+        const int head = 16 - sh;  // bytes that go into the block before
+        if (run.n == 8 && 2 * run.after >= head)
+            *reinterpret_cast<uint4*>(c + head) = realign16(r, next, head);
+        else
+            st_bytes(c + head, realign16(r, r, head), 0, 2 * run.n - head);
+        if (!run.prev || 2 * run.n < head) st_bytes(c - sh, realign16(r, r, head), sh, min(16, sh + 2 * run.n));
     }
 };
 
@@ -72,17 +125,24 @@ struct Vec8<float> {
     __device__ __forceinline__ void clear() { r[0] = r[1] = make_uint4(0, 0, 0, 0); }
 
     template <bool ALIGNED>
-    __device__ __forceinline__ void load(const float* p, int n) {
-        if (ALIGNED && n >= 8) {
-            r[0] = ld_row_u4(p);
-            r[1] = ld_row_u4(p + 4);
-            return;
+    __device__ __forceinline__ void load(const float* p, const Run& run) {
+        const int sh = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+        const unsigned char* blk = reinterpret_cast<const unsigned char*>(p) - sh;
+        clear();
+        if (run.n > 0) r[0] = ld_row_u4(blk);
+        if (sh + 4 * run.n > 16) r[1] = ld_row_u4(blk + 16);
+        if (!ALIGNED) {
+            uint4 next = from_next_lane(r[0]);
+            if (run.after == 0 && sh + 4 * run.n > 32) next = ld_row_u4(blk + 32);
+            r[0] = realign16(r[0], r[1], sh);
+            r[1] = realign16(r[1], next, sh);
         }
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = i < n ? *reinterpret_cast<const volatile uint32_t*>(p + i) : 0u;
-        r[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        r[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        if (run.n < 8) {
+            r[0].x = run.n > 0 ? r[0].x : 0u, r[0].y = run.n > 1 ? r[0].y : 0u;
+            r[0].z = run.n > 2 ? r[0].z : 0u, r[0].w = run.n > 3 ? r[0].w : 0u;
+            r[1].x = run.n > 4 ? r[1].x : 0u, r[1].y = run.n > 5 ? r[1].y : 0u;
+            r[1].z = run.n > 6 ? r[1].z : 0u, r[1].w = 0u;
+        }
     }
 
     __device__ __forceinline__ void get(float (&f)[8]) const {
@@ -101,16 +161,33 @@ struct Vec8<float> {
     }
 
     template <bool ALIGNED>
-    __device__ __forceinline__ void store(float* p, int n) const {
-        if (ALIGNED && n >= 8) {
-            *reinterpret_cast<uint4*>(p) = r[0];
-            *reinterpret_cast<uint4*>(p + 4) = r[1];
+    __device__ __forceinline__ void store(float* p, const Run& run) const {
+        unsigned char* c = reinterpret_cast<unsigned char*>(p);
+        const int sh = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+        uint4 next = make_uint4(0, 0, 0, 0);
+        if (!ALIGNED) next = from_next_lane(r[0]);
+        if (run.n == 0) return;
+        if (sh == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (run.n >= 4 * i + 4)
+                    *reinterpret_cast<uint4*>(c + 16 * i) = r[i];
+                else
+                    st_words(c + 16 * i, r[i], 0, run.n - 4 * i);
+            }
             return;
         }
-        const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = __uint_as_float(w[i]);
+        const int head = 16 - sh, words = head >> 2;  // that go into the block before
+        const uint4 first = realign16(r[0], r[1], head), second = realign16(r[1], next, head);
+        if (run.n >= words + 4)
+            *reinterpret_cast<uint4*>(c + head) = first;
+        else
+            st_words(c + head, first, 0, run.n - words);
+        if (run.n == 8 && run.after >= words)
+            *reinterpret_cast<uint4*>(c + head + 16) = second;
+        else
+            st_words(c + head + 16, second, 0, run.n - words - 4);
+        if (!run.prev || run.n < words) st_words(c - sh, realign16(r[0], r[0], head), sh >> 2, min(4, (sh >> 2) + run.n));
     }
 };
 

@@ -5,14 +5,13 @@ products in the tensor cores' fp32 accumulator, 64 (MXFP4) or 32 (MXFP8) an inst
 its error is at most (K / 32 + 10) * 2^-22 * sum_k |a_k b_k| (2^-22: an add that keeps 24 bits and may truncate, twice
 over for the products' own alignment), and half a step of the result's type.
 """
-import ctypes
 import math
 
 import pytest
 import torch
 
 from tests import stream_reference as ref
-from tests.test_norm import matrix, outside_kept, randn, rng_of
+from tests.test_norm import block, matrix, outside_kept, randn, rng_of
 
 gpu = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -63,10 +62,8 @@ def test_refusals_of_the_c_calls(ss):
     lib, n, a = ss.lib(), ss.ss_launch_count(), 4096
 
     def quant(**kw):
-        s = ss._MxQuant(4, 8, 2, a, 8, 0, a, a, a, a, a)
-        for k, v in kw.items():
-            setattr(s, k, v)
-        return lib.ss_mx_quantize(ctypes.byref(s), None)
+        s = dict(rows=4, cols=8, elem_bytes=2, x=a, stride=8, format=0, data=a, scales=a, t_data=a, t_scales=a, rng=a)
+        return lib.ss_mx_quantize(block(ss._MX_QUANT, s, kw), None)
     assert quant(rows=-1) == quant(cols=-1) == quant(elem_bytes=1) == quant(format=2) == quant(x=None) == ss.SS_EINVAL
     assert quant(data=None) == quant(scales=None) == quant(t_data=None) == quant(t_scales=None) == ss.SS_EINVAL
     none = dict(data=None, scales=None, t_data=None, t_scales=None)
@@ -86,10 +83,8 @@ def test_refusals_of_the_c_calls(ss):
     assert back(rows=0) == ss.SS_OK
 
     def product(**kw):
-        s = ss._MxProduct(4, 8, 32, 0, a, a, a, a, a, 8, 2)
-        for k, v in kw.items():
-            setattr(s, k, v)
-        return lib.ss_mx_matmul(ctypes.byref(s), None)
+        s = dict(M=4, N=8, K=32, format=0, a_data=a, a_scales=a, b_data=a, b_scales=a, out=a, out_stride=8, elem_bytes=2)
+        return lib.ss_mx_matmul(block(ss._MX_PRODUCT, s, kw), None)
     assert product(M=-1) == product(N=-1) == product(K=0) == product(format=5) == product(elem_bytes=8) == ss.SS_EINVAL
     for field in ("a_data", "a_scales", "b_data", "b_scales", "out"):
         assert product(**{field: None}) == ss.SS_EINVAL and product(**{field: a + 1}) == ss.SS_EALIGN, field

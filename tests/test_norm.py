@@ -49,6 +49,12 @@ def outside_kept(buf, view, fill):
     return bool((buf[mask] == fill).all())
 
 
+def block(layout, fields, changed):
+    """An argument block of the C ABI, some of its fields changed."""
+    assert set(changed) <= set(fields)
+    return layout.pack(*(0 if v is None else v for v in {**fields, **changed}.values()))
+
+
 def rng_of(seed=12345, offset=77):
     return torch.tensor([seed, offset], dtype=torch.int64, device="cuda")
 
@@ -85,10 +91,9 @@ def test_refusals_of_the_c_calls(ss):
     assert drop(rows=0, x=None, out=None) == drop(cols=0, ldx=0, ldo=0) == ss.SS_OK
 
     def norm(**kw):
-        s = ss._Norm(4, 8, 2, a, 8, a, 8, a, 1e-5, 0.0, None, a, 8, a, 8, a, a, a)
-        for k, v in kw.items():
-            setattr(s, k, v)
-        return lib.ss_rms_norm(ctypes.byref(s), None)
+        s = dict(rows=4, cols=8, elem_bytes=2, x=a, x_stride=8, residual=a, residual_stride=8, weight=a, eps=1e-5,
+                 dropout=0.0, rng=None, sum_out=a, sum_stride=8, out=a, out_stride=8, rstd_out=a, mx_data=a, mx_scales=a)
+        return lib.ss_rms_norm(block(ss._NORM, s, kw), None)
     none = dict(sum_out=None, out=None, rstd_out=None, mx_data=None, mx_scales=None)
     assert norm(rows=-1) == norm(cols=0) == norm(elem_bytes=8) == norm(x=None) == norm(weight=None) == ss.SS_EINVAL
     assert norm(eps=-1.0) == norm(eps=math.inf) == norm(eps=math.nan) == norm(eps=1e300) == norm(**none) == ss.SS_EINVAL
@@ -100,10 +105,10 @@ def test_refusals_of_the_c_calls(ss):
     assert norm(rows=0, **none) == ss.SS_OK and lib.ss_rms_norm(None, None) == ss.SS_EINVAL
 
     def grad(**kw):
-        s = ss._NormGrad(4, 8, 2, a, 8, a, 8, a, a, a, 8, 0.0, None, a, 8, a, 8, a, a, 1 << 20)
-        for k, v in kw.items():
-            setattr(s, k, v)
-        return lib.ss_rms_norm_backward(ctypes.byref(s), None)
+        s = dict(rows=4, cols=8, elem_bytes=2, d_out=a, d_out_stride=8, h=a, h_stride=8, weight=a, rstd=a, d_sum=a,
+                 d_sum_stride=8, dropout=0.0, rng=None, d_h=a, d_h_stride=8, d_x=a, d_x_stride=8, d_weight=a, workspace=a,
+                 workspace_bytes=1 << 20)
+        return lib.ss_rms_norm_backward(block(ss._NORM_GRAD, s, kw), None)
     assert grad(rows=-1) == grad(cols=0) == grad(elem_bytes=1) == grad(d_out=None) == grad(h=None) == ss.SS_EINVAL
     assert grad(weight=None) == grad(rstd=None) == grad(workspace=None) == grad(workspace_bytes=31) == ss.SS_EINVAL
     assert grad(d_h=None, d_x=None, d_weight=None) == grad(dropout=0.5) == grad(d_sum_stride=7) == ss.SS_EINVAL
