@@ -699,22 +699,26 @@ def _device() -> int:
 _get_device = None
 
 
+
 def _row_dtype(fn: str, t, what: str):
-    """The type of the bf16 or fp32 matrix that gives a call its sizes."""
-    if t.dim() != 2 or t.dtype not in (_dtype("bfloat16"), _dtype("float32")):
+    """The type and shape of the bf16 or fp32 matrix that gives a call its sizes."""
+    dtype, shape = t.dtype, t.shape
+    if len(shape) != 2 or (dtype is not _dtype("bfloat16") and dtype is not _dtype("float32")):
         raise ShardStateError(fn, SS_EINVAL, f"{what}: a bf16 or fp32 matrix is wanted")
-    return t.dtype
+    return dtype, shape
 
 
-def _rows(fn: str, t, what: str, rows: int, cols: int, dtype, device: int):
+def _rows(fn: str, t, what: str, shape, dtype, device: int):
     """Address and row stride of a matrix of that type on the current device (0, 0 for None)."""
     if t is None:
         return 0, 0
-    if t.get_device() != device or t.dtype is not dtype or t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1):
-        raise ShardStateError(fn, SS_EINVAL, f"{what}: {dtype} [{rows}, {cols}] on the current GPU with unit column "
-                                             "stride is wanted")
-    stride = t.stride(0)
-    return t.data_ptr(), stride if rows > 1 or stride > cols else cols
+    if t.get_device() == device and t.dtype is dtype and t.shape == shape:
+        stride, unit = t.stride()
+        rows, cols = shape
+        if unit == 1 or cols <= 1:
+            return t.data_ptr(), stride if rows > 1 or stride > cols else cols
+    raise ShardStateError(fn, SS_EINVAL, f"{what}: {dtype} {list(shape)} on the current GPU with unit column stride "
+                                         "is wanted")
 
 
 def _flat(fn: str, t, what: str, dtype, numel: int, device: int) -> int:
@@ -732,11 +736,11 @@ def ss_dropout(x, out, p: float, rng, stream=None) -> None:
     the device: seed, offset) and from each element's place, and the same call on a
     gradient is the backward pass."""
     fn = "ss_dropout"
-    dtype, dev = _row_dtype(fn, x, "x"), _device()
-    rows, cols = x.shape
-    ax, ldx = _rows(fn, x, "x", rows, cols, dtype, dev)
-    ao, ldo = _rows(fn, out, "out", rows, cols, dtype, dev)
-    status = _lib.ss_dropout(rows, cols, x.element_size(), ax, ldx, ao, ldo, p,
+    (dtype, shape), dev = _row_dtype(fn, x, "x"), _device()
+    rows, cols = shape
+    ax, ldx = _rows(fn, x, "x", shape, dtype, dev)
+    ao, ldo = _rows(fn, out, "out", shape, dtype, dev)
+    status = _lib.ss_dropout(rows, cols, dtype.itemsize, ax, ldx, ao, ldo, p,
                              _flat(fn, rng, "rng", _dtype("int64"), 2, dev), _stream(stream))
     if status != SS_OK:
         _check(fn, status)
@@ -751,16 +755,16 @@ def ss_rms_norm(x, weight, eps: float, out=None, residual=None, sum_out=None, rs
     and mx_scales get out as SS_MXFP8 (buffers of ss_mx_bytes).  At least one output is
     wanted; residual and dropout are optional."""
     fn = "ss_rms_norm"
-    dtype, dev = _row_dtype(fn, x, "x"), _device()
-    rows, cols = x.shape
-    ax, ldx = _rows(fn, x, "x", rows, cols, dtype, dev)
-    ar, ldr = _rows(fn, residual, "residual", rows, cols, dtype, dev)
-    ah, ldh = _rows(fn, sum_out, "sum_out", rows, cols, dtype, dev)
-    ao, ldo = _rows(fn, out, "out", rows, cols, dtype, dev)
+    (dtype, shape), dev = _row_dtype(fn, x, "x"), _device()
+    rows, cols = shape
+    ax, ldx = _rows(fn, x, "x", shape, dtype, dev)
+    ar, ldr = _rows(fn, residual, "residual", shape, dtype, dev)
+    ah, ldh = _rows(fn, sum_out, "sum_out", shape, dtype, dev)
+    ao, ldo = _rows(fn, out, "out", shape, dtype, dev)
     if weight is None or weight.numel() != cols:
         raise ShardStateError(fn, SS_EINVAL, f"weight: {cols} elements are wanted")
     md, ms = _mx_buffers(fn, mx_data, mx_scales, "mx", rows, cols, SS_MXFP8, dev)
-    args = _NORM.pack(rows, cols, x.element_size(), ax, ldx, ar, ldr, _flat(fn, weight, "weight", dtype, cols, dev), eps,
+    args = _NORM.pack(rows, cols, dtype.itemsize, ax, ldx, ar, ldr, _flat(fn, weight, "weight", dtype, cols, dev), eps,
                  dropout, _flat(fn, rng, "rng", _dtype("int64"), 2, dev), ah, ldh, ao, ldo,
                  _flat(fn, rstd_out, "rstd_out", _dtype("float32"), rows, dev), md, ms)
     status = _lib.ss_rms_norm(args, _stream(stream))
@@ -783,18 +787,18 @@ def ss_rms_norm_backward(d_out, h, weight, rstd, d_h, workspace, d_sum=None, d_x
     may be d_out or d_sum), d_x and d_weight are optional; the workspace
     (ss_rms_norm_workspace bytes) is for d_weight."""
     fn = "ss_rms_norm_backward"
-    dtype, dev = _row_dtype(fn, h, "h"), _device()
-    rows, cols = h.shape
-    ay, ldy = _rows(fn, d_out, "d_out", rows, cols, dtype, dev)
-    ah, ldh = _rows(fn, h, "h", rows, cols, dtype, dev)
-    as_, lds = _rows(fn, d_sum, "d_sum", rows, cols, dtype, dev)
-    ag, ldg = _rows(fn, d_h, "d_h", rows, cols, dtype, dev)
-    ax, ldx = _rows(fn, d_x, "d_x", rows, cols, dtype, dev)
+    (dtype, shape), dev = _row_dtype(fn, h, "h"), _device()
+    rows, cols = shape
+    ay, ldy = _rows(fn, d_out, "d_out", shape, dtype, dev)
+    ah, ldh = _rows(fn, h, "h", shape, dtype, dev)
+    as_, lds = _rows(fn, d_sum, "d_sum", shape, dtype, dev)
+    ag, ldg = _rows(fn, d_h, "d_h", shape, dtype, dev)
+    ax, ldx = _rows(fn, d_x, "d_x", shape, dtype, dev)
     for name, t in (("weight", weight), ("d_weight", d_weight)):
         if t is not None and t.numel() != cols:
             raise ShardStateError(fn, SS_EINVAL, f"{name}: {cols} elements are wanted")
     ws, nbytes = (0, 0) if workspace is None else _workspace(fn, workspace)
-    args = _NORM_GRAD.pack(rows, cols, h.element_size(), ay, ldy, ah, ldh, _flat(fn, weight, "weight", dtype, cols, dev),
+    args = _NORM_GRAD.pack(rows, cols, dtype.itemsize, ay, ldy, ah, ldh, _flat(fn, weight, "weight", dtype, cols, dev),
                      _flat(fn, rstd, "rstd", _dtype("float32"), rows, dev), as_, lds, dropout,
                      _flat(fn, rng, "rng", _dtype("int64"), 2, dev), ag, ldg, ax, ldx,
                      _flat(fn, d_weight, "d_weight", dtype, cols, dev), ws, nbytes)
@@ -837,13 +841,13 @@ def ss_mx_quantize(x, format: int, data=None, scales=None, t_data=None, t_scales
     t_data and t_scales, either or both from one read; uint8 buffers of ss_mx_bytes.  To
     the nearest, or stochastically with rng (2 int64 on the device: seed, offset)."""
     fn = "ss_mx_quantize"
-    dtype, dev = _row_dtype(fn, x, "x"), _device()
+    (dtype, shape), dev = _row_dtype(fn, x, "x"), _device()
     _mx_format(fn, format)
-    rows, cols = x.shape
-    ax, ldx = _rows(fn, x, "x", rows, cols, dtype, dev)
+    rows, cols = shape
+    ax, ldx = _rows(fn, x, "x", shape, dtype, dev)
     d, s = _mx_buffers(fn, data, scales, "quantised", rows, cols, format, dev)
     td, ts = _mx_buffers(fn, t_data, t_scales, "transposed", cols, rows, format, dev)
-    args = _MX_QUANT.pack(rows, cols, x.element_size(), ax, ldx, format, d, s, td, ts,
+    args = _MX_QUANT.pack(rows, cols, dtype.itemsize, ax, ldx, format, d, s, td, ts,
                     _flat(fn, rng, "rng", _dtype("int64"), 2, dev))
     status = _lib.ss_mx_quantize(args, _stream(stream))
     if status != SS_OK:
@@ -853,12 +857,12 @@ def ss_mx_quantize(x, format: int, data=None, scales=None, t_data=None, t_scales
 def ss_mx_dequantize(data, scales, format: int, out, stream=None) -> None:
     """The values of a quantised matrix into out [R, C], bf16 or fp32 (rows may be strided)."""
     fn = "ss_mx_dequantize"
-    dtype, dev = _row_dtype(fn, out, "out"), _device()
+    (dtype, shape), dev = _row_dtype(fn, out, "out"), _device()
     _mx_format(fn, format)
-    rows, cols = out.shape
-    ao, ldo = _rows(fn, out, "out", rows, cols, dtype, dev)
+    rows, cols = shape
+    ao, ldo = _rows(fn, out, "out", shape, dtype, dev)
     d, s = _mx_buffers(fn, data, scales, "quantised", rows, cols, format, dev)
-    status = _lib.ss_mx_dequantize(rows, cols, format, d, s, ao, ldo, out.element_size(), _stream(stream))
+    status = _lib.ss_mx_dequantize(rows, cols, format, d, s, ao, ldo, dtype.itemsize, _stream(stream))
     if status != SS_OK:
         _check(fn, status)
 
@@ -868,13 +872,13 @@ def ss_mx_matmul(a_data, a_scales, b_data, b_scales, K: int, format: int, out, s
     of one format, A [M, K] and B [N, K]: a linear layer whose weight is B, and with the
     transposes of ss_mx_quantize both of its gradients."""
     fn = "ss_mx_matmul"
-    dtype, dev = _row_dtype(fn, out, "out"), _device()
+    (dtype, shape), dev = _row_dtype(fn, out, "out"), _device()
     _mx_format(fn, format)
-    M, N = out.shape
-    ao, ldo = _rows(fn, out, "out", M, N, dtype, dev)
+    M, N = shape
+    ao, ldo = _rows(fn, out, "out", shape, dtype, dev)
     ad, as_ = _mx_buffers(fn, a_data, a_scales, "A", M, K, format, dev)
     bd, bs = _mx_buffers(fn, b_data, b_scales, "B", N, K, format, dev)
-    args = _MX_PRODUCT.pack(M, N, K, format, ad, as_, bd, bs, ao, ldo, out.element_size())
+    args = _MX_PRODUCT.pack(M, N, K, format, ad, as_, bd, bs, ao, ldo, dtype.itemsize)
     status = _lib.ss_mx_matmul(args, _stream(stream))
     if status != SS_OK:
         _check(fn, status)

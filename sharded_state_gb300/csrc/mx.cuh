@@ -16,6 +16,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cstring>
 
 #include "shardstate.h"
 
@@ -33,7 +34,8 @@ struct Mx<SS_MXFP4> {
     static constexpr int kTop = 2;        // exponent of the largest element
     static constexpr int kLowest = 0;     // lowest exponent of a normal element
     static constexpr int kFraction = 1;   // bits
-    static constexpr float kMost = 6.f;
+    static constexpr int kBits = 4;
+    static constexpr uint32_t kMostCode = 7;
     static constexpr int kTileRow = 64;   // bytes of 128 elements
     using Word = uint32_t;                // 8 elements
 
@@ -74,7 +76,8 @@ struct Mx<SS_MXFP8> {
     static constexpr int kTop = 8;
     static constexpr int kLowest = -6;
     static constexpr int kFraction = 3;
-    static constexpr float kMost = 448.f;
+    static constexpr int kBits = 8;
+    static constexpr uint32_t kMostCode = 0x7E;
     static constexpr int kTileRow = 128;
     using Word = uint2;
 
@@ -131,16 +134,47 @@ __device__ __forceinline__ int64_t mx_scale_at(int64_t r, int64_t b, int64_t til
     return ((r >> 7) * tiles + (b >> 2)) * kMxTileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
 }
 
-// An element in units of its scale rounded down or up to an element of the format:
-// up where what is cut off and u (in [0, 1), a multiple of 2^-16) make one step.
+// The code (sign, magnitude) of an element v in units of its scale, rounded down or up
+// in magnitude: up where what is cut off and the 16 bits u / 2^16 make one step.  In
+// the format's normal range the codes are the leading bits of the fp32 magnitude, and
+// adding the random bits right behind them carries into them just then; below it the
+// lowest normal number is added first, which puts every element on the same steps
+// (towards zero, so that nothing is rounded but by the cut).
 template <int FORMAT>
-__device__ __forceinline__ float mx_round_random(float v, float u) {
-    constexpr uint32_t kLow = (uint32_t)(127 + Mx<FORMAT>::kLowest) << 23;
-    const uint32_t e = max(abs_bits(v) & 0x7F800000u, kLow);
-    const float inverse = __uint_as_float(((254u + Mx<FORMAT>::kFraction) << 23) - e);
-    const float step = __uint_as_float(e - ((uint32_t)Mx<FORMAT>::kFraction << 23));
-    const float size = floorf(fmaf(fabsf(v), inverse, u)) * step;
-    return copysignf(fminf(size, Mx<FORMAT>::kMost), v);
+__device__ __forceinline__ uint32_t mx_code_random(float v, uint32_t u) {
+    using M = Mx<FORMAT>;
+    constexpr int kCut = 23 - M::kFraction;
+    constexpr uint32_t kBase = (uint32_t)(127 + M::kLowest) << M::kFraction;
+    const float size = fabsf(v), least = __uint_as_float((uint32_t)(127 + M::kLowest) << 23);
+    const bool small = size < least;
+    const float t = small ? __fadd_rz(size, least) : size;
+    const uint32_t code = ((__float_as_uint(t) + (u << (kCut - 16))) >> kCut) - (small ? kBase : kBase - (1u << M::kFraction));
+    return min(code, M::kMostCode) | (__float_as_uint(v) >> 31) << (M::kBits - 1);
+}
+
+// 8 elements times `inverse`, their random bits two in a word.
+template <int FORMAT>
+__device__ __forceinline__ typename Mx<FORMAT>::Word mx_encode_random(const float (&f)[8], float inverse, uint4 bits) {
+    constexpr int kBits = Mx<FORMAT>::kBits;
+    const uint32_t b[4] = {bits.x, bits.y, bits.z, bits.w};
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t u = i & 1 ? b[i >> 1] >> 16 : b[i >> 1] & 0xFFFFu;
+        w[i * kBits / 32] |= mx_code_random<FORMAT>(f[i] * inverse, u) << (i * kBits % 32);
+    }
+    typename Mx<FORMAT>::Word out;
+    memcpy(&out, w, sizeof(out));
+    return out;
+}
+
+// 8 elements times `inverse`, to the nearest.
+template <int FORMAT>
+__device__ __forceinline__ typename Mx<FORMAT>::Word mx_encode(const float (&f)[8], float inverse) {
+    float g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = f[i] * inverse;
+    return Mx<FORMAT>::encode(g);
 }
 
 }  // namespace ss

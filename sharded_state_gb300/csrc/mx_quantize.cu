@@ -39,27 +39,89 @@ struct QuantArgs {
     const int64_t* rng;
 };
 
-// Element as the format's, in units of the scale: exact where RANDOM, else left to
-// the conversion's rounding.
-template <int FORMAT, bool RANDOM>
-__device__ __forceinline__ float element(float x, uint32_t byte, float inverse, uint32_t bits) {
-    if (byte == 255u) return 0.f;
-    const float v = x * inverse;
-    return RANDOM ? ss::mx_round_random<FORMAT>(v, (float)bits * 0x1p-16f) : v;
-}
-
 template <class T, bool RANDOM>
 constexpr int tile_bytes() {
     return kMxTile * kMxTile * (int)(sizeof(T) + (RANDOM ? 2 : 0));
 }
 
+// Bits of the largest magnitude of 8 elements.
+__device__ __forceinline__ uint32_t largest(const Vec8<uint16_t>& v) {
+    const uint32_t m = __vmaxu2(__vmaxu2(v.r.x & 0x7FFF7FFFu, v.r.y & 0x7FFF7FFFu),
+                                __vmaxu2(v.r.z & 0x7FFF7FFFu, v.r.w & 0x7FFF7FFFu));
+    return max(m << 16, m & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t largest(const Vec8<float>& v) {
+    float f[8];
+    v.get(f);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, ss::abs_bits(f[i]));
+    return m;
+}
+
+template <int FORMAT, bool RANDOM>
+__device__ __forceinline__ typename Mx<FORMAT>::Word encode(const float (&f)[8], uint32_t byte, uint4 bits) {
+    if (byte == 255u) return typename Mx<FORMAT>::Word();
+    return RANDOM ? ss::mx_encode_random<FORMAT>(f, ss::mx_inverse(byte), bits)
+                  : ss::mx_encode<FORMAT>(f, ss::mx_inverse(byte));
+}
+
+// Rows of a tile in shared memory, in words, those of every 32 rows turned by 8 words
+// more: threads that read 8 neighbouring columns of 4 blocks of rows at once meet all
+// banks.
+template <int WORDS>
+__device__ __forceinline__ int turned(int row, int word) {
+    return row * WORDS + ((word + 8 * (row >> 5)) & (WORDS - 1));
+}
+
+// Two columns of 32 rows out of the tile, as two's 16-bit halves or as floats.
+template <class T>
+struct Columns;
+
+template <>
+struct Columns<uint16_t> {
+    uint32_t w[32];
+    __device__ __forceinline__ void load(const uint32_t* tile, int block, int pair) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) w[k] = tile[turned<kMxTile / 2>(32 * block + k, pair)];
+    }
+    __device__ __forceinline__ void largest(uint32_t (&top)[2]) const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) m = __vmaxu2(m, w[k] & 0x7FFF7FFFu);
+        top[0] = m << 16, top[1] = m & 0xFFFF0000u;
+    }
+    __device__ __forceinline__ float get(int j, int k) const { return j ? ss::bf16_hi(w[k]) : ss::bf16_lo(w[k]); }
+};
+
+template <>
+struct Columns<float> {
+    float w[32][2];
+    __device__ __forceinline__ void load(const uint32_t* tile, int block, int pair) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            const float2 v = *reinterpret_cast<const float2*>(tile + turned<kMxTile>(32 * block + k, 2 * pair));
+            w[k][0] = v.x, w[k][1] = v.y;
+        }
+    }
+    __device__ __forceinline__ void largest(uint32_t (&top)[2]) const {
+        top[0] = top[1] = 0;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            top[0] = max(top[0], ss::abs_bits(w[k][0]));
+            top[1] = max(top[1], ss::abs_bits(w[k][1]));
+        }
+    }
+    __device__ __forceinline__ float get(int j, int k) const { return w[k][j]; }
+};
+
 template <class T, int FORMAT, bool TRANSPOSE, bool RANDOM, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constant__ QuantArgs a) {
     using M = Mx<FORMAT>;
     using Word = typename M::Word;
-    extern __shared__ __align__(16) unsigned char raw[];
-    T* tile = reinterpret_cast<T*>(raw);                                        // [128][128]
-    uint16_t* random = reinterpret_cast<uint16_t*>(raw + kMxTile * kMxTile * sizeof(T));  // [128][128]
+    constexpr int kWords = kMxTile * (int)sizeof(T) / 4;  // of a row of the tile
+    extern __shared__ __align__(16) uint32_t tile[];      // [128][kWords], then the random bits, [128][64]
+    uint32_t* random = tile + kMxTile * kWords;
     launch_after();
     const int64_t tr = blockIdx.x / a.col_tiles, tc = blockIdx.x - tr * a.col_tiles;
     const int line = threadIdx.x >> 4, c8 = threadIdx.x & 15;
@@ -73,7 +135,6 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
         v[i].template load<ALIGNED>(x + r * a.stride,
                                     Run(row0 + r < a.rows ? a.cols - col0 - 8 * c8 : 0, c8 == 0, c8 == 15));
     }
-    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < kRounds; ++i) {
         const int r = 16 * i + line;
@@ -82,80 +143,67 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
         uint4 bits = make_uint4(0, 0, 0, 0);
         if (RANDOM) bits = ss::Philox(a.rng)((uint32_t)row, (uint32_t)(tc * 16 + c8));
         if (TRANSPOSE) {
-            v[i].template store<true>(tile + r * kMxTile + 8 * c8, Run(8, true, true));
-            if (RANDOM) *reinterpret_cast<uint4*>(random + r * kMxTile + 8 * c8) = bits;
+            if constexpr (sizeof(T) == 2) {
+                *reinterpret_cast<uint4*>(tile + turned<kWords>(r, 4 * c8)) = v[i].r;
+            } else {
+                *reinterpret_cast<uint4*>(tile + turned<kWords>(r, 8 * c8)) = v[i].r[0];
+                *reinterpret_cast<uint4*>(tile + turned<kWords>(r, 8 * c8 + 4)) = v[i].r[1];
+            }
+            if (RANDOM) *reinterpret_cast<uint4*>(random + turned<kMxTile / 2>(r, 4 * c8)) = bits;
         }
         if (!a.data) continue;
-        float f[8];
-        v[i].get(f);
-        uint32_t top = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = max(top, ss::abs_bits(f[k]));
+        uint32_t top = largest(v[i]);
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
         const uint32_t byte = ss::mx_scale<FORMAT>(top);
-        const float inverse = ss::mx_inverse(byte);
-        const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = element<FORMAT, RANDOM>(f[k], byte, inverse, w[k >> 1] >> (16 * (k & 1)) & 0xFFFFu);
         // the row's 4 scales of the tile in its first lane
         uint32_t four = byte << (8 * (c8 >> 2));
         four |= __shfl_xor_sync(0xFFFFFFFFu, four, 4);
         four |= __shfl_xor_sync(0xFFFFFFFFu, four, 8);
         if (row < a.rows) {
+            float f[8];
+            v[i].get(f);
             unsigned char* out = a.data + (row * a.col_tiles + tc) * M::kTileRow + c8 * (int)sizeof(Word);
-            *reinterpret_cast<Word*>(out) = M::encode(f);
-            if ((lane & 15) == 0)
-                *reinterpret_cast<uint32_t*>(a.scales + ss::mx_scale_at(row, 4 * tc, a.col_tiles)) = four;
+            *reinterpret_cast<Word*>(out) = encode<FORMAT, RANDOM>(f, byte, bits);
+            if (c8 == 0) *reinterpret_cast<uint32_t*>(a.scales + ss::mx_scale_at(row, 4 * tc, a.col_tiles)) = four;
         }
     }
     if (!TRANSPOSE) return;
     __syncthreads();
-    const int pair = threadIdx.x & 63, block = threadIdx.x >> 6;
-    float f[2][kMxTile / 4];
-    uint32_t top[2] = {0, 0};
-#pragma unroll
-    for (int k = 0; k < 32; ++k) {
-        const T* at = tile + (32 * block + k) * kMxTile + 2 * pair;
-        if (sizeof(T) == 2) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(at);
-            f[0][k] = ss::bf16_lo(w), f[1][k] = ss::bf16_hi(w);
-        } else {
-            const float2 w = *reinterpret_cast<const float2*>(at);
-            f[0][k] = w.x, f[1][k] = w.y;
-        }
-        top[0] = max(top[0], ss::abs_bits(f[0][k]));
-        top[1] = max(top[1], ss::abs_bits(f[1][k]));
-    }
-    uint32_t byte[2];
-    float inverse[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) byte[j] = ss::mx_scale<FORMAT>(top[j]), inverse[j] = ss::mx_inverse(byte[j]);
-#pragma unroll
-    for (int k = 0; k < 32; ++k) {
-        uint32_t u = 0;
-        if (RANDOM) u = *reinterpret_cast<const uint32_t*>(random + (32 * block + k) * kMxTile + 2 * pair);
-        f[0][k] = element<FORMAT, RANDOM>(f[0][k], byte[0], inverse[0], u & 0xFFFFu);
-        f[1][k] = element<FORMAT, RANDOM>(f[1][k], byte[1], inverse[1], u >> 16);
-    }
+    // 4 neighbouring threads write a row of the transpose: 64 or 128 bytes, and its 4 scales
+    const int pair = threadIdx.x >> 2, block = threadIdx.x & 3;
+    Columns<T> c;
+    c.load(tile, block, pair);
+    uint32_t top[2];
+    c.largest(top);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
+        const uint32_t byte = ss::mx_scale<FORMAT>(top[j]);
+        uint32_t four = byte << (8 * block);
+        four |= __shfl_xor_sync(0xFFFFFFFFu, four, 1);
+        four |= __shfl_xor_sync(0xFFFFFFFFu, four, 2);
         const int64_t row = col0 + 2 * pair + j;  // of the transpose
-        if (row >= a.cols) break;
-        unsigned char* out = a.t_data + (row * a.row_tiles + tr) * M::kTileRow + block * (M::kTileRow / 4);
-        __align__(16) uint32_t words[M::kTileRow / 16];
+        if (row >= a.cols) continue;
+        __align__(16) Word words[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float g[8];
+            float f[8];
+            uint32_t b[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) g[k] = f[j][8 * i + k];
-            *reinterpret_cast<Word*>(words + i * (int)sizeof(Word) / 4) = M::encode(g);
+            for (int k = 0; k < 8; ++k) f[k] = c.get(j, 8 * i + k);
+            if (RANDOM) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    b[k] = __byte_perm(random[turned<kMxTile / 2>(32 * block + 8 * i + 2 * k, pair)],
+                                       random[turned<kMxTile / 2>(32 * block + 8 * i + 2 * k + 1, pair)], j ? 0x7632 : 0x5410);
+            }
+            words[i] = encode<FORMAT, RANDOM>(f, byte, make_uint4(b[0], b[1], b[2], b[3]));
         }
+        unsigned char* out = a.t_data + (row * a.row_tiles + tr) * M::kTileRow + block * (M::kTileRow / 4);
 #pragma unroll
-        for (int i = 0; i < M::kTileRow / 64; ++i)
-            *reinterpret_cast<uint4*>(out + 16 * i) =
-                make_uint4(words[4 * i], words[4 * i + 1], words[4 * i + 2], words[4 * i + 3]);
-        a.t_scales[ss::mx_scale_at(row, 4 * tr + block, a.row_tiles)] = (unsigned char)byte[j];
+        for (int i = 0; i < (int)sizeof(words) / 16; ++i)
+            reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(words)[i];
+        if (block == 0) *reinterpret_cast<uint32_t*>(a.t_scales + ss::mx_scale_at(row, 4 * tr, a.row_tiles)) = four;
     }
 }
 

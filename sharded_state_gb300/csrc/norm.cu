@@ -26,9 +26,12 @@
 #include "launch.cuh"
 #include "mx.cuh"
 #include "philox.cuh"
+#include "tcgen05.cuh"
 #include "vec8.cuh"
 
 namespace {
+
+namespace tc = ss::tc;
 
 using ss::launch_after;
 using ss::Run;
@@ -51,6 +54,7 @@ struct DropArgs {
     const int64_t* rng;
     uint32_t drop;
     float scale;
+    int last;                        // columns of a row's last group
     int64_t step_rows, step_groups;  // the grid's threads, as rows and groups
 };
 
@@ -122,7 +126,8 @@ struct NormGradArgs {
     float scale;
     void *d_h, *d_x;
     int64_t d_h_stride, d_x_stride;
-    float* part;  // [gridDim.x][cols]: each CTA's share of d_weight (NULL: not asked for)
+    float* part;     // [gridDim.x][cols]: each CTA's share of d_weight, to be joined by another kernel
+    void* d_weight;  // or: the grid is one cluster that joins them itself
 };
 
 // Sum over a row's team, the same in all of its threads: over the warp in registers,
@@ -139,6 +144,9 @@ __device__ __forceinline__ float team_sum(float s, int team, float* lane_sums) {
     for (int i = 0; i < warps; ++i) t += lane_sums[first + i];
     return t;
 }
+
+__device__ __forceinline__ void store_weight(uint16_t* p, float v) { *p = ss::f32_to_bf16(v); }
+__device__ __forceinline__ void store_weight(float* p, float v) { *p = v; }
 
 // 8 normed values as MXFP8: their block is this lane's and its 3 neighbours'.
 __device__ __forceinline__ void store_mx8(const NormArgs& a, int64_t row, int col, const float (&y)[8]) {
@@ -311,9 +319,9 @@ norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
         }
         if (kAhead) x = ahead;
     }
-    if (!a.part) return;
+    if (!a.part && !a.d_weight) return;
     float* part = a.part + (int64_t)blockIdx.x * a.cols;
-    float* to = teams > 1 ? joined + team * a.cols : part;
+    float* to = teams > 1 || a.d_weight ? joined + team * a.cols : part;
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
         const int col = 8 * (mine + i * a.team);
@@ -321,13 +329,30 @@ norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
         for (int k = 0; k < 8; ++k)
             if (col + k < a.cols) to[col + k] = dw[i][k];
     }
-    if (teams == 1) return;
+    if (to == part) return;
     __syncthreads();
+    float* joint = a.d_weight ? joined : part;
     for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
         float s = 0.f;
         for (int t = 0; t < teams; ++t) s += joined[t * a.cols + c];
-        part[c] = s;
+        joint[c] = s;
     }
+    if (!a.d_weight) return;
+    tc::cluster_sync();
+    const int ctas = gridDim.x, share = (a.cols + ctas - 1) / ctas, c0 = blockIdx.x * share;
+    for (int c = c0 + threadIdx.x; c < min(c0 + share, a.cols); c += blockDim.x) {
+        float s = 0.f;
+        for (int q = 0; q < ctas; ++q) {
+            float v;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                         : "=f"(v)
+                         : "r"(tc::map_to_rank(tc::smem_addr(joined + c), q))
+                         : "memory");
+            s += v;
+        }
+        store_weight(static_cast<T*>(a.d_weight) + c, s);
+    }
+    tc::cluster_sync();
 }
 
 // d_weight: the CTAs' shares summed in a fixed order, 32 columns a CTA.
@@ -349,10 +374,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) norm_join_kernel(const float* 
     if (line > 0 || col >= cols) return;
 #pragma unroll
     for (int i = 1; i < kJoinRows; ++i) s += sums[i][lane];
-    if (sizeof(T) == 2)
-        reinterpret_cast<uint16_t*>(out)[col] = ss::f32_to_bf16(s);
-    else
-        reinterpret_cast<float*>(out)[col] = s;
+    store_weight(out + col, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -511,7 +533,7 @@ int ss_rms_norm_backward(const ss_norm_grad* n, ss_stream_t stream) {
         return rc;
     if (!ss::aligned(n->rstd, 4) || !ss::aligned(n->workspace, 16)) return SS_EALIGN;
     const Shape s = choose_shape((n->cols + 7) / 8);
-    const int64_t grid = std::max<int64_t>(grad_grid(n->rows, s), 1);
+    int64_t grid = std::max<int64_t>(grad_grid(n->rows, s), 1);
     if (n->d_weight && (!n->workspace || n->workspace_bytes < (size_t)(grid * n->cols * 4))) return SS_EINVAL;
     if (n->rows == 0 && !n->d_weight) return SS_OK;
     a.rows = n->rows, a.cols = (int)n->cols, a.team = s.team;
@@ -519,16 +541,27 @@ int ss_rms_norm_backward(const ss_norm_grad* n, ss_stream_t stream) {
     a.weight = n->weight, a.d_sum = n->d_sum, a.d_sum_stride = n->d_sum_stride, a.rstd = n->rstd;
     a.inv_cols = 1.f / (float)n->cols, a.rng = n->rng;
     a.d_h = n->d_h, a.d_h_stride = n->d_h_stride, a.d_x = n->d_x, a.d_x_stride = n->d_x_stride;
-    a.part = n->d_weight ? static_cast<float*>(n->workspace) : nullptr;
     const bool al = rows_on_16(n->elem_bytes, {dy, h, ds, dh, dx}) && ss::aligned(n->weight, 16);
     const int teams = s.threads / s.team;
-    const int smem = teams > 1 ? teams * a.cols * 4 : 0;  // at most 8 x 512 floats, or 4 x 1024, ...
+    // Few rows (up to 4 in turn for each team of 8 CTAs) are one cluster's, which joins d_weight in
+    // its shared memory: one launch for two (50 x 64: 3.4 us where this takes 2.7).
+    const bool cluster = n->d_weight && s.vecs <= 2 && n->rows <= 32 * teams;
+    if (cluster) {
+        grid = std::min<int64_t>((n->rows + teams - 1) / teams, 8);
+        grid = std::max<int64_t>(grid, 1);
+        a.d_weight = n->d_weight;
+    } else if (n->d_weight) {
+        a.part = static_cast<float*>(n->workspace);
+    }
+    // with several teams at most 8 x 512 floats, or 4 x 1024, ...; 4096 in a cluster
+    const int smem = teams > 1 || cluster ? teams * a.cols * 4 : 0;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (int rc = with_shape(n->elem_bytes, s.vecs, al, [&](auto t, auto v, auto aligned) {
             return ss::launch(norm_grad_kernel<decltype(t), decltype(v)::value, decltype(aligned)::value>, grid,
-                              s.threads, smem, 0, true, st, a);
+                              s.threads, smem, cluster ? (int)grid : 0, true, st, a);
         }))
         return rc;
+    if (cluster) return SS_OK;
     if (!n->d_weight) return SS_OK;
     const int64_t blocks = (n->cols + 31) / 32;
     if (n->elem_bytes == 2)
