@@ -511,8 +511,8 @@ int ss_linear_cross_entropy(const ss_linear_ce* args, ss_stream_t stream);
  *   rng         device, {seed, offset}, 64 bits each: read when the call runs, so
  *               that a captured call draws a new mask once they are changed.
  *   out         may be x (with its stride); it overlaps no input otherwise.
- * Errors: SS_EINVAL, SS_EALIGN, SS_EOVERFLOW (2^31 rows, 2^35 columns or strides
- * beyond 64-bit offsets), SS_ECUDA.
+ * Errors: SS_EINVAL, SS_EALIGN, SS_EOVERFLOW (2^31 rows, above 2^33 columns,
+ * strides beyond 64-bit offsets), SS_ECUDA.
  */
 int ss_dropout(int64_t rows, int64_t cols, int elem_bytes, const void* x, int64_t x_stride, void* out,
                int64_t out_stride, double p, const int64_t* rng, ss_stream_t stream);

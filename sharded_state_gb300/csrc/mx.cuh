@@ -16,7 +16,6 @@
 #pragma once
 
 #include <cstdint>
-#include <cstring>
 
 #include "shardstate.h"
 
@@ -134,37 +133,43 @@ __device__ __forceinline__ int64_t mx_scale_at(int64_t r, int64_t b, int64_t til
     return ((r >> 7) * tiles + (b >> 2)) * kMxTileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
 }
 
-// The code (sign, magnitude) of an element v in units of its scale, rounded down or up
-// in magnitude: up where what is cut off and the 16 bits u / 2^16 make one step.  In
-// the format's normal range the codes are the leading bits of the fp32 magnitude, and
-// adding the random bits right behind them carries into them just then; below it the
-// lowest normal number is added first, which puts every element on the same steps
-// (towards zero, so that nothing is rounded but by the cut).
+// 8 elements times `inverse`, rounded down or up in magnitude: up where what is cut off
+// and the element's 16 random bits / 2^16 (u[i]) make one step.  In the format's normal
+// range the codes are the leading bits of the fp32 magnitude, and the random bits,
+// added right behind them, carry into them just then; below it the lowest normal number
+// is added first, which puts every element on the same steps, and half of the sum has
+// the leading bits that continue the codes (towards zero, so that nothing is rounded
+// but by the cut).  10 instructions an element.
 template <int FORMAT>
-__device__ __forceinline__ uint32_t mx_code_random(float v, uint32_t u) {
+__device__ __forceinline__ typename Mx<FORMAT>::Word mx_encode_random(const float (&f)[8], float inverse,
+                                                                      const uint32_t (&u)[8]) {
     using M = Mx<FORMAT>;
-    constexpr int kCut = 23 - M::kFraction;
-    constexpr uint32_t kBase = (uint32_t)(127 + M::kLowest) << M::kFraction;
-    const float size = fabsf(v), least = __uint_as_float((uint32_t)(127 + M::kLowest) << 23);
-    const bool small = size < least;
-    const float t = small ? __fadd_rz(size, least) : size;
-    const uint32_t code = ((__float_as_uint(t) + (u << (kCut - 16))) >> kCut) - (small ? kBase : kBase - (1u << M::kFraction));
-    return min(code, M::kMostCode) | (__float_as_uint(v) >> 31) << (M::kBits - 1);
-}
-
-// 8 elements times `inverse`, their random bits two in a word.
-template <int FORMAT>
-__device__ __forceinline__ typename Mx<FORMAT>::Word mx_encode_random(const float (&f)[8], float inverse, uint4 bits) {
-    constexpr int kBits = Mx<FORMAT>::kBits;
-    const uint32_t b[4] = {bits.x, bits.y, bits.z, bits.w};
-    uint32_t w[2] = {0, 0};
+    constexpr int kCut = 23 - M::kFraction, kPer = 32 / M::kBits;  // elements a word
+    constexpr uint32_t kFirst = ((uint32_t)(127 + M::kLowest - 1) << M::kFraction);  // leading bits of code 0
+    const float least = __uint_as_float((uint32_t)(127 + M::kLowest) << 23);
+    uint32_t w[8 / kPer], sign[8];
+#pragma unroll
+    for (int i = 0; i < 8 / kPer; ++i) w[i] = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t u = i & 1 ? b[i >> 1] >> 16 : b[i >> 1] & 0xFFFFu;
-        w[i * kBits / 32] |= mx_code_random<FORMAT>(f[i] * inverse, u) << (i * kBits % 32);
+        const float v = fabsf(f[i]) * inverse;
+        float t = v;
+        if (v < least) t = __fmaf_rz(v, 0.5f, 0.5f * least);
+        const uint32_t code = min(((u[i] << (kCut - 16)) + __float_as_uint(t)) >> kCut, kFirst + M::kMostCode) - kFirst;
+        w[i / kPer] += code << (M::kBits * (i % kPer));
+        sign[i] = __float_as_uint(f[i]);
     }
-    typename Mx<FORMAT>::Word out;
-    memcpy(&out, w, sizeof(out));
+    // the signs' bytes, four at a time
+    auto top = [&](int i, int step) {
+        return __byte_perm(__byte_perm(sign[i], sign[i + step], 0x0073), __byte_perm(sign[i + 2 * step], sign[i + 3 * step], 0x0073),
+                           0x5410) & 0x80808080u;
+    };
+    typename M::Word out;
+    if constexpr (M::kBits == 4) {
+        out = w[0] | top(0, 2) >> 4 | top(1, 2);
+    } else {
+        out = make_uint2(w[0] | top(0, 1), w[1] | top(4, 1));
+    }
     return out;
 }
 

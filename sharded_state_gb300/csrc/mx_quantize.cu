@@ -60,9 +60,9 @@ __device__ __forceinline__ uint32_t largest(const Vec8<float>& v) {
 }
 
 template <int FORMAT, bool RANDOM>
-__device__ __forceinline__ typename Mx<FORMAT>::Word encode(const float (&f)[8], uint32_t byte, uint4 bits) {
+__device__ __forceinline__ typename Mx<FORMAT>::Word encode(const float (&f)[8], uint32_t byte, const uint32_t (&u)[8]) {
     if (byte == 255u) return typename Mx<FORMAT>::Word();
-    return RANDOM ? ss::mx_encode_random<FORMAT>(f, ss::mx_inverse(byte), bits)
+    return RANDOM ? ss::mx_encode_random<FORMAT>(f, ss::mx_inverse(byte), u)
                   : ss::mx_encode<FORMAT>(f, ss::mx_inverse(byte));
 }
 
@@ -127,21 +127,24 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
     const int line = threadIdx.x >> 4, c8 = threadIdx.x & 15;
     const int64_t row0 = tr * kMxTile, col0 = tc * kMxTile;
     wait_before();
-    const T* x = static_cast<const T*>(a.x) + row0 * a.stride + col0 + 8 * c8;
+    const T* x = static_cast<const T*>(a.x) + (row0 + line) * a.stride + col0 + 8 * c8;
+    const int rows = (int)min(a.rows - row0, (int64_t)kMxTile), left = (int)min(a.cols - col0 - 8 * c8, (int64_t)16);
     Vec8<T> v[kRounds];
 #pragma unroll
     for (int i = 0; i < kRounds; ++i) {
-        const int r = 16 * i + line;
-        v[i].template load<ALIGNED>(x + r * a.stride,
-                                    Run(row0 + r < a.rows ? a.cols - col0 - 8 * c8 : 0, c8 == 0, c8 == 15));
+        v[i].template load<ALIGNED>(x, Run(16 * i + line < rows ? left : 0, c8 == 0, c8 == 15));
+        x += 16 * a.stride;
     }
+    const int64_t pitch = a.col_tiles * M::kTileRow;
+    unsigned char* out = a.data + (row0 + line) * pitch + tc * M::kTileRow + c8 * (int)sizeof(Word);
+    unsigned char* scales = a.scales + blockIdx.x * (int64_t)ss::kMxTileBytes + 16 * line;
+    const ss::Philox philox = RANDOM ? ss::Philox(a.rng) : ss::Philox();
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
+    for (int i = 0; i < kRounds; ++i, out += 16 * pitch) {
         const int r = 16 * i + line;
-        const int64_t row = row0 + r;
-        if (!TRANSPOSE && row - (line & 1) >= a.rows) break;  // both rows of the warp are behind the last
+        if (!TRANSPOSE && 16 * i + (line & ~1) >= rows) break;  // both rows of the warp are behind the last
         uint4 bits = make_uint4(0, 0, 0, 0);
-        if (RANDOM) bits = ss::Philox(a.rng)((uint32_t)row, (uint32_t)(tc * 16 + c8));
+        if (RANDOM) bits = philox((uint32_t)row0 + r, (uint32_t)tc * 16 + c8);
         if (TRANSPOSE) {
             if constexpr (sizeof(T) == 2) {
                 *reinterpret_cast<uint4*>(tile + turned<kWords>(r, 4 * c8)) = v[i].r;
@@ -160,12 +163,13 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
         uint32_t four = byte << (8 * (c8 >> 2));
         four |= __shfl_xor_sync(0xFFFFFFFFu, four, 4);
         four |= __shfl_xor_sync(0xFFFFFFFFu, four, 8);
-        if (row < a.rows) {
+        if (r < rows) {
             float f[8];
             v[i].get(f);
-            unsigned char* out = a.data + (row * a.col_tiles + tc) * M::kTileRow + c8 * (int)sizeof(Word);
-            *reinterpret_cast<Word*>(out) = encode<FORMAT, RANDOM>(f, byte, bits);
-            if (c8 == 0) *reinterpret_cast<uint32_t*>(a.scales + ss::mx_scale_at(row, 4 * tc, a.col_tiles)) = four;
+            const uint32_t u[8] = {bits.x & 0xFFFFu, bits.x >> 16, bits.y & 0xFFFFu, bits.y >> 16,
+                                   bits.z & 0xFFFFu, bits.z >> 16, bits.w & 0xFFFFu, bits.w >> 16};
+            *reinterpret_cast<Word*>(out) = encode<FORMAT, RANDOM>(f, byte, u);
+            if (c8 == 0) *reinterpret_cast<uint32_t*>(scales + 256 * (i & 1) + 4 * (i >> 1)) = four;
         }
     }
     if (!TRANSPOSE) return;
@@ -188,16 +192,16 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float f[8];
-            uint32_t b[4] = {0, 0, 0, 0};
+            uint32_t u[8] = {};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = c.get(j, 8 * i + k);
-            if (RANDOM) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    b[k] = __byte_perm(random[turned<kMxTile / 2>(32 * block + 8 * i + 2 * k, pair)],
-                                       random[turned<kMxTile / 2>(32 * block + 8 * i + 2 * k + 1, pair)], j ? 0x7632 : 0x5410);
+            for (int k = 0; k < 8; ++k) {
+                f[k] = c.get(j, 8 * i + k);
+                if (RANDOM) {
+                    const uint32_t w = random[turned<kMxTile / 2>(32 * block + 8 * i + k, pair)];
+                    u[k] = j ? w >> 16 : w & 0xFFFFu;
+                }
             }
-            words[i] = encode<FORMAT, RANDOM>(f, byte, make_uint4(b[0], b[1], b[2], b[3]));
+            words[i] = encode<FORMAT, RANDOM>(f, byte, u);
         }
         unsigned char* out = a.t_data + (row * a.row_tiles + tr) * M::kTileRow + block * (M::kTileRow / 4);
 #pragma unroll
@@ -221,23 +225,26 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_const
     launch_after();
     const int64_t tr = blockIdx.x / a.col_tiles, tc = blockIdx.x - tr * a.col_tiles;
     const int line = threadIdx.x >> 4, c8 = threadIdx.x & 15;
-    const int64_t col = tc * kMxTile + 8 * c8;
+    const int64_t row0 = tr * kMxTile, col = tc * kMxTile + 8 * c8;
+    const int rows = (int)min(a.rows - row0, (int64_t)kMxTile), left = (int)min(a.cols - col, (int64_t)16);
+    const int64_t pitch = a.col_tiles * M::kTileRow;
+    const unsigned char* data = a.data + (row0 + line) * pitch + tc * M::kTileRow + c8 * (int)sizeof(Word);
+    const unsigned char* scales = a.scales + blockIdx.x * (int64_t)ss::kMxTileBytes + 16 * line + (c8 >> 2);
     wait_before();
     Word w[kRounds];
     unsigned char byte[kRounds];
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        const int64_t row = tr * kMxTile + 16 * i + line;
+    for (int i = 0; i < kRounds; ++i, data += 16 * pitch) {
         w[i] = Word();
         byte[i] = 0;
-        if (row >= a.rows || col >= a.cols) continue;
-        w[i] = *reinterpret_cast<const Word*>(a.data + (row * a.col_tiles + tc) * M::kTileRow + c8 * (int)sizeof(Word));
-        byte[i] = a.scales[ss::mx_scale_at(row, col >> 5, a.col_tiles)];
+        if (16 * i + line >= rows || left <= 0) continue;
+        w[i] = *reinterpret_cast<const Word*>(data);
+        byte[i] = scales[256 * (i & 1) + 4 * (i >> 1)];
     }
+    T* out = static_cast<T*>(a.out) + (row0 + line) * a.stride + col;
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        const int64_t row = tr * kMxTile + 16 * i + line;
-        if (row - (line & 1) >= a.rows) break;  // both rows of the warp are behind the last
+    for (int i = 0; i < kRounds; ++i, out += 16 * a.stride) {
+        if (16 * i + (line & ~1) >= rows) break;  // both rows of the warp are behind the last
         float f[8];
         M::decode(w[i], f);
         const float scale = ss::mx_value(byte[i]);
@@ -245,8 +252,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_const
         for (int k = 0; k < 8; ++k) f[k] *= scale;
         Vec8<T> v;
         v.set(f);
-        v.template store<ALIGNED>(static_cast<T*>(a.out) + row * a.stride + col,
-                                  Run(row < a.rows ? a.cols - col : 0, c8 == 0, c8 == 15));
+        v.template store<ALIGNED>(out, Run(16 * i + line < rows ? left : 0, c8 == 0, c8 == 15));
     }
 }
 

@@ -43,10 +43,10 @@ using ss::wait_before;
 // ---------------------------------------------------------------------------
 
 constexpr int kDropThreads = 256;
-constexpr int kDropVecs = 2;
 
 struct DropArgs {
-    int64_t rows, cols, groups;  // groups: of 8 columns in a row
+    int64_t rows;
+    int groups, last;  // groups of 8 columns in a row, columns of the last one
     const void* x;
     int64_t x_stride;
     void* out;
@@ -54,43 +54,41 @@ struct DropArgs {
     const int64_t* rng;
     uint32_t drop;
     float scale;
-    int last;                        // columns of a row's last group
-    int64_t step_rows, step_groups;  // the grid's threads, as rows and groups
+    int64_t step_rows;  // the grid's threads, as rows and groups
+    int step_groups;
+    int64_t x_step, out_step;  // and as elements
 };
 
-// Threads take groups of 8 in the order of the matrix, kDropVecs of them at a time so
-// that as many loads are on their way.
+// Threads take groups of 8 in the order of the matrix, as far apart as the grid has
+// threads; places in it are carried on by adding (a row's index times its stride for
+// each group cost as much as the mask: 181 instructions a group for 100).
 template <class T, bool ALIGNED>
 __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_constant__ DropArgs a) {
     launch_after();
     const int64_t first = (int64_t)blockIdx.x * kDropThreads + threadIdx.x;
     const int lane = threadIdx.x & 31;
-    int64_t row = first / a.groups, group = first - row * a.groups;
+    int64_t row = first / a.groups;
+    int group = (int)(first - row * a.groups);
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride + 8 * (int64_t)group;
+    T* out = static_cast<T*>(a.out) + row * a.out_stride + 8 * (int64_t)group;
+    const int64_t x_turn = a.x_stride - 8 * (int64_t)a.groups, out_turn = a.out_stride - 8 * (int64_t)a.groups;
     wait_before();
     const ss::Philox philox(a.rng);
-    const T* x = static_cast<const T*>(a.x);
-    T* out = static_cast<T*>(a.out);
-    while (__any_sync(0xFFFFFFFFu, row < a.rows)) {
-        Vec8<T> v[kDropVecs];
-        int64_t rows[kDropVecs], groups[kDropVecs];
-#pragma unroll
-        for (int i = 0; i < kDropVecs; ++i) {
-            rows[i] = row, groups[i] = group;
-            const Run run(row < a.rows ? a.cols - 8 * group : 0, lane == 0 || group == 0, lane == 31);
-            v[i].template load<ALIGNED>(x + row * a.x_stride + 8 * group, run);
-            row += a.step_rows;
-            group += a.step_groups;
-            if (group >= a.groups) group -= a.groups, ++row;
-        }
-#pragma unroll
-        for (int i = 0; i < kDropVecs; ++i) {
-            const Run run(rows[i] < a.rows ? a.cols - 8 * groups[i] : 0, lane == 0 || groups[i] == 0, lane == 31);
-            float f[8];
-            v[i].get(f);
-            ss::drop8(f, philox((uint32_t)rows[i], (uint32_t)groups[i]), a.drop, a.scale);
-            v[i].set(f);
-            v[i].template store<ALIGNED>(out + rows[i] * a.out_stride + 8 * groups[i], run);
-        }
+    while (ALIGNED ? row < a.rows : __any_sync(0xFFFFFFFFu, row < a.rows)) {
+        const int after = group + 2 < a.groups ? 8 : group + 1 < a.groups ? a.last : 0;  // columns of the next group
+        const Run run(row >= a.rows ? 0 : after ? 8 + after : a.last, lane == 0 || group == 0, lane == 31);
+        Vec8<T> v;
+        v.template load<ALIGNED>(x, run);
+        float f[8];
+        v.get(f);
+        ss::drop8(f, philox((uint32_t)row, (uint32_t)group), a.drop, a.scale);
+        v.set(f);
+        v.template store<ALIGNED>(out, run);
+        row += a.step_rows;
+        group += a.step_groups;
+        x += a.x_step;
+        out += a.out_step;
+        if (group >= a.groups) group -= a.groups, ++row, x += x_turn, out += out_turn;
     }
 }
 
@@ -383,6 +381,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) norm_join_kernel(const float* 
 
 constexpr int64_t kMaxRows = INT32_MAX;
 constexpr int64_t kMaxCols = 32768;  // 512 threads hold a row in registers
+constexpr int64_t kMaxFlat = (int64_t)1 << 33;  // columns of dropout: groups count in 32 bits
 
 // Threads of a row and of a CTA, and loads of 8 elements a thread: few loads a thread
 // as long as 256 threads suffice, so that many rows are in flight.
@@ -468,14 +467,16 @@ int ss_dropout(int64_t rows, int64_t cols, int elem_bytes, const void* x, int64_
     if (!rng) return SS_EINVAL;
     if (rows == 0 || cols == 0) return SS_OK;
     if (!x || !out) return SS_EINVAL;
-    if (rows > kMaxRows || cols > INT64_MAX / 16 / rows || cols > (int64_t)8 * UINT32_MAX) return SS_EOVERFLOW;
+    if (rows > kMaxRows || cols > kMaxFlat) return SS_EOVERFLOW;
     if (int rc = check_matrices(rows, cols, elem_bytes, {{x, x_stride}, {out, out_stride}})) return rc;
-    a.rows = rows, a.cols = cols, a.groups = (cols + 7) / 8;
+    a.rows = rows, a.groups = (int)((cols + 7) / 8), a.last = (int)(cols - 8 * (int64_t)(a.groups - 1));
     a.x = x, a.x_stride = x_stride, a.out = out, a.out_stride = out_stride, a.rng = rng;
     const int64_t total = a.rows * a.groups;
     const int64_t grid = std::min((total + kDropThreads - 1) / kDropThreads, (int64_t)ss::num_sms() * 8);
     a.step_rows = grid * kDropThreads / a.groups;
-    a.step_groups = grid * kDropThreads % a.groups;
+    a.step_groups = (int)(grid * kDropThreads % a.groups);
+    a.x_step = a.step_rows * x_stride + 8 * (int64_t)a.step_groups;
+    a.out_step = a.step_rows * out_stride + 8 * (int64_t)a.step_groups;
     const bool al = rows_on_16(elem_bytes, {{x, x_stride}, {out, out_stride}});
     const auto kernel = elem_bytes == 2 ? (al ? dropout_kernel<uint16_t, true> : dropout_kernel<uint16_t, false>)
                                         : (al ? dropout_kernel<float, true> : dropout_kernel<float, false>);

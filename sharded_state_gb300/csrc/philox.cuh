@@ -17,6 +17,8 @@ namespace ss {
 struct Philox {
     uint32_t key0, key1, off0, off1;
 
+    Philox() = default;
+
     // rng: {seed, offset} on the device.
     __device__ __forceinline__ explicit Philox(const int64_t* rng) {
         const uint64_t seed = (uint64_t)rng[0], offset = (uint64_t)rng[1];

@@ -48,10 +48,8 @@ struct Run {
 
     // left: elements of the row from this group on (any sign); first, last: of the
     // lanes that hold neighbouring groups.
-    __device__ __forceinline__ Run(int64_t left, bool first, bool last)
-        : n((int)max((int64_t)0, min(left, (int64_t)8))),
-          after(last ? 0 : (int)max((int64_t)0, min(left - 8, (int64_t)8))),
-          prev(!first && left > 0) {}
+    __device__ __forceinline__ Run(int left, bool first, bool last)
+        : n(max(0, min(left, 8))), after(last ? 0 : max(0, min(left - 8, 8))), prev(!first && left > 0) {}
 };
 
 template <class T>
