@@ -50,26 +50,34 @@ __device__ __forceinline__ void let_copies_land() {
     while (tc::global_ns() - t0 < 1000000ull) __nanosleep(20000);
 }
 
-// The products of one stage: per tile of scales its copies to tensor memory (A's 4
-// columns, then B's, 4 for each 128 rows), then an instruction for each 32 bytes of k.
+// Columns of tensor memory for one tile of scales: A's 4, then B's, 4 for each 128 rows.
+template <bool PAIR>
+__host__ __device__ constexpr int scale_columns() { return PAIR ? 12 : 8; }
+
+// The products of one stage: its scales' copies to tensor memory, then an instruction
+// for each 32 bytes of k.  Two sets of columns take turns from one tile of scales to the
+// next, so that a copy need not wait for the products that read the ones before.
 template <int FORMAT, bool PAIR>
-__device__ __forceinline__ void stage_products(uint32_t d, uint32_t scales, uint32_t a, uint32_t b, uint32_t sa,
+__device__ __forceinline__ void stage_products(uint32_t d, uint32_t scales, int it, uint32_t a, uint32_t b, uint32_t sa,
                                                uint32_t sb, uint32_t idesc, bool accumulate) {
     constexpr bool FOUR = FORMAT == SS_MXFP4;
     constexpr int T = scale_tiles(FORMAT), per = 4 / T;  // instructions for a tile of scales
     const uint64_t da = tc::operand_desc(a, 16, 1024), db = tc::operand_desc(b, 16, 1024);
+    const uint32_t first = scales + (T == 1 && (it & 1) ? scale_columns<PAIR>() : 0);
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-        tc::copy_scales<PAIR>(scales, tc::scale_desc(sa + t * ss::kMxTileBytes));
+        const uint32_t at = first + t * scale_columns<PAIR>();
+        tc::copy_scales<PAIR>(at, tc::scale_desc(sa + t * ss::kMxTileBytes));
 #pragma unroll
         for (int r = 0; r < (PAIR ? 2 : 1); ++r)
-            tc::copy_scales<PAIR>(scales + 4 + 4 * r, tc::scale_desc(sb + (r * T + t) * ss::kMxTileBytes));
+            tc::copy_scales<PAIR>(at + 4 + 4 * r, tc::scale_desc(sb + (r * T + t) * ss::kMxTileBytes));
+    }
 #pragma unroll
-        for (int i = 0; i < per; ++i) {
-            const uint64_t step = (uint64_t)((t * per + i) * 32 >> 4);
-            tc::mma_scaled<PAIR, FOUR>(d, da + step, db + step, idesc + tc::scale_id(FOUR ? 2 * i : i), scales,
-                                       scales + 4, accumulate || t > 0 || i > 0);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t step = (uint64_t)(i * 32 >> 4);
+        const uint32_t at = first + i / per * scale_columns<PAIR>();
+        tc::mma_scaled<PAIR, FOUR>(d, da + step, db + step, idesc + tc::scale_id(FOUR ? 2 * (i % per) : i), at, at + 4,
+                                   accumulate || i > 0);
     }
 }
 
@@ -81,7 +89,7 @@ __device__ __forceinline__ void store_one(void* out, int64_t at, float v, int el
 }
 
 // ---------------------------------------------------------------------------
-// 256 x 256 tiles, a pair of CTAs
+// 256 x 256 tiles, a pair of CTAs each
 // ---------------------------------------------------------------------------
 
 constexpr int kTile = 256;
@@ -89,6 +97,10 @@ constexpr int kStages = 5;
 constexpr int kEpilogueWarps = 8;  // two for each 32 rows, half of the columns each
 constexpr int kColumns = kTile / 2;
 constexpr int kPairThreads = 32 * (4 + kEpilogueWarps);
+// Two accumulators of 256 columns leave no room in tensor memory for the scales, so the
+// second one begins inside the first.  The columns that they share are read first.
+constexpr int kShared = 32;
+constexpr int kScaleColumns = 2 * kTile - kShared;
 
 __host__ __device__ constexpr int pair_stage(int format) {
     return 2 * kOperand + (3 * scale_bytes(format) + 1023) / 1024 * 1024;
@@ -106,27 +118,96 @@ struct PairArgs {
     int vector;  // rows of out on 16 bytes
 };
 
+// 32 columns of this lane's row as bf16 words (or fp32 ones) in its warp's shared memory:
+// 16-byte groups of row i at group ^ (i & 7), free of bank conflicts both ways.
+__device__ __forceinline__ void turn_half(uint32_t* words, int lane, int h, const uint32_t (&r)[32]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = ss::pack_bf16x2(__uint_as_float(r[8 * i + 2 * e]), __uint_as_float(r[8 * i + 2 * e + 1]));
+        *reinterpret_cast<uint4*>(words + lane * 32 + 4 * ((4 * h + i) ^ (lane & 7))) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+__device__ __forceinline__ void turn_full(uint32_t* words, int lane, const uint32_t (&r)[32]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(words + lane * 32 + 4 * (i ^ (lane & 7))) =
+            make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+}
+
+// The warp's 32 rows of 128 bytes from its shared memory to out, from (row0, col0) on.
+__device__ __forceinline__ void write_turned(const PairArgs& g, const uint32_t* words, int lane, int64_t row0, int64_t col0) {
+    const int per = g.elem_bytes == 2 ? 2 : 1;  // columns a word
+    const int k = lane & 7, left = (int)min(g.N - col0, (int64_t)(32 * per));
+    if (g.vector) {
+        const int mine = min(left - 4 * per * k, 4 * per);  // columns of this lane's 16 bytes
+        if (mine <= 0) return;
+        unsigned char* o = static_cast<unsigned char*>(g.out) +
+                           ((row0 + (lane >> 3)) * g.out_stride + col0 + 4 * per * k) * g.elem_bytes;
+        const int64_t step = 4 * g.out_stride * g.elem_bytes;
+#pragma unroll
+        for (int i = 0; i < 8; ++i, o += step) {
+            const int q = 4 * i + (lane >> 3);
+            if (row0 + q >= g.M) return;
+            const uint4 v = *reinterpret_cast<const uint4*>(words + q * 32 + 4 * (k ^ (q & 7)));
+            if (mine == 4 * per) {
+                *reinterpret_cast<uint4*>(o) = v;
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (e >= mine) continue;
+                    if (per == 2)
+                        reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                    else if (e < 4)
+                        reinterpret_cast<uint32_t*>(o)[e] = w[e];
+                }
+            }
+        }
+    } else {
+        for (int q = 0; q < 32 && row0 + q < g.M; ++q) {
+            const int64_t at = (row0 + q) * g.out_stride + col0;
+            const uint32_t w = words[q * 32 + 4 * ((lane >> 2) ^ (q & 7)) + (lane & 3)];
+            if (per == 2) {
+                uint16_t* o = static_cast<uint16_t*>(g.out) + at;
+                if (2 * lane < left) o[2 * lane] = (uint16_t)w;
+                if (2 * lane + 1 < left) o[2 * lane + 1] = (uint16_t)(w >> 16);
+            } else if (lane < left) {
+                static_cast<uint32_t*>(g.out)[at + lane] = w;
+            }
+        }
+    }
+}
+
+// Persistent pairs, each a tile of 256 x 256 at a time, its first CTA the upper 128 rows.
+// Warp 0 loads, warp 1 of the first CTA issues the products, warps 4.. read finished
+// accumulators while the next tile's products go to the other one.
 template <int FORMAT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairArgs g) {
     extern __shared__ unsigned char raw[];
-    __shared__ uint64_t bars[2 * kStages + 2];
+    __shared__ uint64_t bars[2 * kStages + 5];
     __shared__ uint32_t tmem_base;
     constexpr int kStage = pair_stage(FORMAT), kScales = scale_bytes(FORMAT);
 
     launch_after();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_ctarank();
     const uint32_t smem = (tc::smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
-    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 8;
+    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, shared_read = acc_empty + 16;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             tc::mbar_init(full + 8 * i, 1);
             tc::mbar_init(empty + 8 * i, 1);
         }
-        tc::mbar_init(acc_full, 1);
-        tc::mbar_init(acc_empty, 2 * kEpilogueWarps);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(acc_full + 8 * i, 1);
+            tc::mbar_init(acc_empty + 8 * i, 2 * kEpilogueWarps);
+        }
+        tc::mbar_init(shared_read, kEpilogueWarps);
         tc::mbar_init_fence();
         tc::prefetch_map(&maps.a);
         tc::prefetch_map(&maps.b);
@@ -144,133 +225,100 @@ mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairAr
     const int64_t tiles = (int64_t)g.m_tiles * g.n_tiles;
     bool ok = true;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
+        const uint32_t full0 = tc::map_to_rank(full, 0);
         int it = 0;
         for (int64_t id = first; id < tiles && ok; id += pairs) {
             const int m = (int)(id % g.m_tiles), n = (int)(id / g.m_tiles);
+            const int a_row = m * kTile + (int)rank * kHalf, b_row = n * kTile + (int)rank * kHalf;
             for (int k = 0; k < g.k_blocks; ++k, ++it) {
                 const int st = it % kStages;
                 const uint32_t a = smem + st * kStage, b = a + kOperand, sa = b + kOperand, sb = sa + kScales;
-                ok = tc::mbar_wait(empty + 8 * st, ((it / kStages) & 1) ^ 1);
+                ok = tc::mbar_wait_warp(empty + 8 * st, ((it / kStages) & 1) ^ 1);
                 if (!ok) break;
-                const uint32_t bar = tc::map_to_rank(full + 8 * st, 0);
+                if (!tc::elect_one()) continue;
+                const uint32_t bar = full0 + 8 * st;
                 if (rank == 0) tc::mbar_expect_tx(full + 8 * st, 2 * (2 * kOperand + 3 * kScales));
-                tc::tma_load_2d(a, &maps.a, k * kRowBytes, m * kTile + (int)rank * kHalf, bar);
-                tc::tma_load_2d(b, &maps.b, k * kRowBytes, n * kTile + (int)rank * kHalf, bar);
-                // each CTA's own rows of A; all rows of B, which both multiply with
+                tc::tma_load_2d(a, &maps.a, k * kRowBytes, a_row, bar);
                 tc::tma_load_2d(sa, &maps.a_scales, k * (kScales / 4), m * 2 + (int)rank, bar);
-                tc::tma_load_2d(sb, &maps.b_scales, k * (kScales / 4), n * 2, bar);
+                tc::tma_load_2d(b, &maps.b, k * kRowBytes, b_row, bar);
+                // the scales of all of B's rows, which both CTAs multiply with: half from either
+                tc::tma_load_2d_multicast(sb + rank * kScales, &maps.b_scales, k * (kScales / 4), n * 2 + (int)rank, bar, 3);
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
         const uint32_t idesc = tc::scaled_desc(FORMAT == SS_MXFP4, kTile, kTile);
         int it = 0, j = 0;
         for (int64_t id = first; id < tiles; id += pairs, ++j) {
-            ok = tc::mbar_wait(acc_empty, (j & 1) ^ 1);
+            ok = tc::mbar_wait_warp(acc_empty + 8 * (j & 1), ((j >> 1) & 1) ^ 1) &&
+                 (j == 0 || tc::mbar_wait_warp(shared_read, (j - 1) & 1));
             if (!ok) break;
             tc::fence_after();
+            const uint32_t d = tmem + (j & 1) * (kTile - kShared);
             for (int k = 0; k < g.k_blocks; ++k, ++it) {
                 const int st = it % kStages;
-                ok = tc::mbar_wait(full + 8 * st, (it / kStages) & 1);
+                const uint32_t a = smem + st * kStage, b = a + kOperand, sa = b + kOperand, sb = sa + kScales;
+                ok = tc::mbar_wait_warp(full + 8 * st, (it / kStages) & 1);
                 if (!ok) break;
                 tc::fence_after();
-                const uint32_t a = smem + st * kStage, b = a + kOperand, sa = b + kOperand, sb = sa + kScales;
-                stage_products<FORMAT, true>(tmem, tmem + kTile, a, b, sa, sb, idesc, k > 0);
-                tc::commit_pair(empty + 8 * st);
+                if (tc::elect_one()) {
+                    stage_products<FORMAT, true>(d, tmem + kScaleColumns, it, a, b, sa, sb, idesc, k > 0);
+                    tc::commit_pair(empty + 8 * st);
+                    if (k + 1 == g.k_blocks) tc::commit_pair(acc_full + 8 * (j & 1));
+                }
+                __syncwarp();
             }
             if (!ok) break;
-            tc::commit_pair(acc_full);
         }
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t acc_empty0 = tc::map_to_rank(acc_empty, 0);
+        const uint32_t acc_empty0 = tc::map_to_rank(acc_empty, 0), shared_read0 = tc::map_to_rank(shared_read, 0);
         uint32_t* words = reinterpret_cast<uint32_t*>(raw + (smem - tc::smem_addr(raw)) + kStages * kStage +
                                                       (warp - 4) * kTurn);
-        const int per = g.elem_bytes == 2 ? 2 : 1;  // columns a word
+        const int wide = g.elem_bytes == 2 ? 64 : 32, pieces = kColumns / wide;  // columns a piece
         int j = 0;
         for (int64_t id = first; id < tiles; id += pairs, ++j) {
             const int m = (int)(id % g.m_tiles), n = (int)(id / g.m_tiles);
             const int64_t row0 = (int64_t)m * kTile + rank * kHalf + quad * 32;
             const int64_t col0 = (int64_t)n * kTile + half * kColumns;
-            const uint32_t d = tmem + half * kColumns + ((uint32_t)quad << 21);
-            ok = ok && tc::mbar_wait(acc_full, j & 1);
+            const uint32_t d = tmem + (j & 1) * (kTile - kShared) + half * kColumns + ((uint32_t)quad << 21);
+            // the shared columns are the first accumulator's last and the second one's first
+            const bool shares = half != (j & 1);
+            const int start = shares && half ? pieces - 1 : 0;
+            ok = ok && tc::mbar_wait(acc_full + 8 * (j & 1), (j >> 1) & 1);
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc::fence_after();
-            // 128 bytes of every row at a time, through shared memory (16-byte groups of row i at group
-            // ^ (i & 7), free of bank conflicts both ways)
 #pragma unroll 1
-            for (int c = 0; c < kColumns && col0 + c < g.N; c += 32 * per) {
-#pragma unroll 1
-                for (int h = 0; h < per; ++h) {
-                    uint32_t r[32];
+            for (int i = 0; i < pieces; ++i) {
+                const int c = (start + i) % pieces * wide;
+                uint32_t r[2][32];
+                __syncwarp();
+                tc::tmem_ld32(d + c, r[0]);
+                if (wide == 64) tc::tmem_ld32(d + c + 32, r[1]);
+                tc::tmem_wait(r[0]);
+                if (wide == 64) tc::tmem_wait(r[1]);
+                if (i == 0 && shares) {
+                    tc::fence_before();
                     __syncwarp();
-                    tc::tmem_ld32(d + c + 32 * h, r);
-                    tc::tmem_wait(r);
-                    if (!ok) {
+                    if (lane == 0) tc::mbar_arrive_cluster(shared_read0);
+                }
+                if (!ok) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] = 0x7FFFFFFFu;
-                    }
-                    if (per == 2) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = ss::pack_bf16x2(__uint_as_float(r[8 * i + 2 * e]),
-                                                       __uint_as_float(r[8 * i + 2 * e + 1]));
-                            *reinterpret_cast<uint4*>(words + lane * 32 + 4 * ((4 * h + i) ^ (lane & 7))) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<uint4*>(words + lane * 32 + 4 * (i ^ (lane & 7))) =
-                                make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-                    }
+                    for (int e = 0; e < 32; ++e) r[0][e] = r[1][e] = 0x7FFFFFFFu;
+                }
+                if (row0 >= g.M || col0 + c >= g.N) continue;
+                if (wide == 64) {
+                    turn_half(words, lane, 0, r[0]);
+                    turn_half(words, lane, 1, r[1]);
+                } else {
+                    turn_full(words, lane, r[0]);
                 }
                 __syncwarp();
-                const int k = lane & 7;
-                const int left = (int)min(g.N - (col0 + c), (int64_t)(32 * per));  // columns of this piece
-                if (g.vector) {
-                    const int mine = min(left - 4 * per * k, 4 * per);  // columns of this lane's 16 bytes
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int q = 4 * i + (lane >> 3);
-                        if (row0 + q >= g.M || mine <= 0) continue;
-                        unsigned char* o = static_cast<unsigned char*>(g.out) +
-                                           ((row0 + q) * g.out_stride + col0 + c + 4 * per * k) * g.elem_bytes;
-                        const uint4 v = *reinterpret_cast<const uint4*>(words + q * 32 + 4 * (k ^ (q & 7)));
-                        if (mine == 4 * per) {
-                            *reinterpret_cast<uint4*>(o) = v;
-                        } else {
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                if (e >= mine) continue;
-                                if (per == 2)
-                                    reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-                                else if (e < 4)
-                                    reinterpret_cast<uint32_t*>(o)[e] = w[e];
-                            }
-                        }
-                    }
-                } else {
-                    for (int q = 0; q < 32 && row0 + q < g.M; ++q) {
-                        const int64_t at = (row0 + q) * g.out_stride + col0 + c;
-                        const uint32_t w = words[q * 32 + 4 * ((lane >> 2) ^ (q & 7)) + (lane & 3)];
-                        if (per == 2) {
-                            uint16_t* o = static_cast<uint16_t*>(g.out) + at;
-                            if (2 * lane < left) o[2 * lane] = (uint16_t)w;
-                            if (2 * lane + 1 < left) o[2 * lane + 1] = (uint16_t)(w >> 16);
-                        } else if (lane < left) {
-                            static_cast<uint32_t*>(g.out)[at + lane] = w;
-                        }
-                    }
-                }
+                write_turned(g, words, lane, row0, col0 + c);
             }
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(acc_empty0);
+            if (lane == 0) tc::mbar_arrive_cluster(acc_empty0 + 8 * (j & 1));
         }
     }
     if (!ok) let_copies_land();
@@ -293,7 +341,7 @@ __host__ __device__ constexpr int few_stage(int format, int few) {
     return kOperand + few * kRowBytes + 2 * scale_bytes(format);
 }
 __host__ __device__ constexpr int few_smem(int format, int few) { return kFewStages * few_stage(format, few) + 1024; }
-// Columns of tensor memory: the accumulator's and the scales' 8.
+// Columns of tensor memory: the accumulator's and the scales' 16.
 __host__ __device__ constexpr uint32_t few_tmem(int few) { return few <= 16 ? 32 : 2 * few; }
 
 // a: the operand of 128 rows a CTA; b: the other one.
@@ -315,7 +363,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
     static_assert(kStage % 1024 == 0 && FEW * kPartPitch * 4 <= kFewStages * kStage, "shared memory");
 
     launch_after();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t smem = (tc::smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kFewStages, done = empty + 8 * kFewStages;
     if (threadIdx.x == 0) {
@@ -343,30 +391,35 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
     const int kb = min(split * per, g.k_blocks), ke = min(kb + per, g.k_blocks);
     bool ok = true;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         for (int k = kb; k < ke; ++k) {
             const int it = k - kb, st = it % kFewStages;
             const uint32_t a = smem + st * kStage, b = a + kOperand, sa = b + FEW * kRowBytes, sb = sa + kScales;
-            ok = tc::mbar_wait(empty + 8 * st, ((it / kFewStages) & 1) ^ 1);
+            ok = tc::mbar_wait_warp(empty + 8 * st, ((it / kFewStages) & 1) ^ 1);
             if (!ok) break;
+            if (!tc::elect_one()) continue;
             tc::mbar_expect_tx(full + 8 * st, kOperand + FEW * kRowBytes + 2 * kScales);
             tc::tma_load_2d_one(a, &maps.a, k * kRowBytes, rt * kHalf, full + 8 * st);
             tc::tma_load_2d_one(sa, &maps.a_scales, k * (kScales / 4), rt, full + 8 * st);
             tc::tma_load_2d_one(b, &maps.b, k * kRowBytes, ft * FEW, full + 8 * st);
             tc::tma_load_2d_one(sb, &maps.b_scales, k * (kScales / 4), ft, full + 8 * st);
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         const uint32_t idesc = tc::scaled_desc(FORMAT == SS_MXFP4, kHalf, FEW);
         for (int k = kb; k < ke; ++k) {
             const int it = k - kb, st = it % kFewStages;
-            ok = tc::mbar_wait(full + 8 * st, (it / kFewStages) & 1);
+            const uint32_t a = smem + st * kStage, b = a + kOperand, sa = b + FEW * kRowBytes, sb = sa + kScales;
+            ok = tc::mbar_wait_warp(full + 8 * st, (it / kFewStages) & 1);
             if (!ok) break;
             tc::fence_after();
-            const uint32_t a = smem + st * kStage, b = a + kOperand, sa = b + FEW * kRowBytes, sb = sa + kScales;
-            stage_products<FORMAT, false>(tmem, tmem + FEW, a, b, sa, sb, idesc, k > kb);
-            tc::commit_one(empty + 8 * st);
+            if (tc::elect_one()) {
+                stage_products<FORMAT, false>(tmem, tmem + FEW, it, a, b, sa, sb, idesc, k > kb);
+                tc::commit_one(empty + 8 * st);
+                if (k + 1 == ke) tc::commit_one(done);
+            }
+            __syncwarp();
         }
-        if (ok) tc::commit_one(done);
+        if (kb == ke && tc::elect_one()) tc::commit_one(done);
     } else if (warp >= 2) {
         const int quad = warp & 3, row = quad * 32 + lane;
         ok = tc::mbar_wait(done, 0);
@@ -440,14 +493,14 @@ int data_map(CUtensorMap* map, const void* data, int64_t rows, int64_t K, int fo
     return r == CUDA_SUCCESS ? SS_OK : ss::cuda_fail(cudaErrorInvalidValue);
 }
 
-// Its scales, as words, in boxes of a stage's tiles and `tiles` rows of tiles; zeros,
-// which are the lowest scale, outside.
-int scale_map(CUtensorMap* map, const void* scales, int64_t rows, int64_t K, int format, int tiles) {
+// Its scales, as words, in boxes of a stage's tiles for 128 rows; zeros, which are the
+// lowest scale, outside.
+int scale_map(CUtensorMap* map, const void* scales, int64_t rows, int64_t K, int format) {
     const ss::EncodeTiled fn = ss::tensor_map_encoder();
     if (!fn) return ss::cuda_fail(cudaErrorNotSupported);
     const cuuint64_t pitch = (cuuint64_t)div_up(K, ss::kMxTile) * ss::kMxTileBytes;
     const cuuint64_t dims[2] = {pitch / 4, (cuuint64_t)div_up(rows, ss::kMxTile)}, strides[1] = {pitch};
-    const cuuint32_t box[2] = {(cuuint32_t)scale_bytes(format) / 4, (cuuint32_t)tiles}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)scale_bytes(format) / 4, 1}, step[2] = {1, 1};
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void*>(scales), dims, strides, box, step,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -459,11 +512,11 @@ struct Operand {
     int64_t rows;
 };
 
-int make_maps(Maps* maps, const Operand& a, const Operand& b, int64_t K, int format, int b_rows, int b_tiles) {
+int make_maps(Maps* maps, const Operand& a, const Operand& b, int64_t K, int format, int b_rows) {
     if (int rc = data_map(&maps->a, a.data, a.rows, K, format, kHalf)) return rc;
     if (int rc = data_map(&maps->b, b.data, b.rows, K, format, b_rows)) return rc;
-    if (int rc = scale_map(&maps->a_scales, a.scales, a.rows, K, format, 1)) return rc;
-    return scale_map(&maps->b_scales, b.scales, b.rows, K, format, b_tiles);
+    if (int rc = scale_map(&maps->a_scales, a.scales, a.rows, K, format)) return rc;
+    return scale_map(&maps->b_scales, b.scales, b.rows, K, format);
 }
 
 template <int FORMAT>
@@ -473,7 +526,7 @@ int launch_pair(const ss_mx_product* p, int64_t k_blocks, cudaStream_t st) {
     constexpr int smem = pair_smem(FORMAT);
     if (int rc = ss::allow_smem(ready, reinterpret_cast<const void*>(kernel), smem)) return rc;
     Maps maps;
-    if (int rc = make_maps(&maps, {p->a_data, p->a_scales, p->M}, {p->b_data, p->b_scales, p->N}, p->K, FORMAT, kHalf, 2))
+    if (int rc = make_maps(&maps, {p->a_data, p->a_scales, p->M}, {p->b_data, p->b_scales, p->N}, p->K, FORMAT, kHalf))
         return rc;
     const int64_t m_tiles = div_up(p->M, kTile), n_tiles = div_up(p->N, kTile), pairs = ss::num_sms() / 2;
     const PairArgs g = {p->M, p->N, p->out_stride, (int)m_tiles, (int)n_tiles, (int)k_blocks, p->out, p->elem_bytes,
@@ -490,7 +543,7 @@ int launch_few(const ss_mx_product* p, int64_t k_blocks, bool swap, cudaStream_t
     Operand a = {p->b_data, p->b_scales, p->N}, b = {p->a_data, p->a_scales, p->M};
     if (swap) std::swap(a, b);
     Maps maps;
-    if (int rc = make_maps(&maps, a, b, p->K, FORMAT, FEW, 1)) return rc;
+    if (int rc = make_maps(&maps, a, b, p->K, FORMAT, FEW)) return rc;
     const int64_t row_tiles = div_up(a.rows, kHalf), few_tiles = div_up(b.rows, FEW), tiles = row_tiles * few_tiles;
     int splits = 1;
     while (splits < 8 && tiles * splits * 2 <= 2 * ss::num_sms() && k_blocks >= 4 * splits) splits *= 2;
