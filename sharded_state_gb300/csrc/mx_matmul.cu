@@ -297,11 +297,10 @@ mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairAr
                 if (wide == 64) tc::tmem_ld32(d + c + 32, r[1]);
                 tc::tmem_wait(r[0]);
                 if (wide == 64) tc::tmem_wait(r[1]);
-                if (i == 0 && shares) {
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cluster(shared_read0);
-                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0 && i == 0 && shares) tc::mbar_arrive_read(shared_read0);
+                if (lane == 0 && i + 1 == pieces) tc::mbar_arrive_read(acc_empty0 + 8 * (j & 1));
                 if (!ok) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) r[0][e] = r[1][e] = 0x7FFFFFFFu;
@@ -316,9 +315,6 @@ mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairAr
                 __syncwarp();
                 write_turned(g, words, lane, row0, col0 + c);
             }
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(acc_empty0 + 8 * (j & 1));
         }
     }
     if (!ok) let_copies_land();
