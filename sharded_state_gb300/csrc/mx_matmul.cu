@@ -81,11 +81,28 @@ __device__ __forceinline__ void stage_products(uint32_t d, uint32_t scales, int 
     }
 }
 
-__device__ __forceinline__ void store_one(void* out, int64_t at, float v, int elem_bytes) {
-    if (elem_bytes == 2)
-        static_cast<uint16_t*>(out)[at] = ss::f32_to_bf16(v);
-    else
-        static_cast<float*>(out)[at] = v;
+// The first n of four neighbouring elements of out.
+__device__ __forceinline__ void store_four(void* out, int64_t at, float4 v, int n, int elem_bytes) {
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    if (elem_bytes == 2) {
+        uint16_t* o = static_cast<uint16_t*>(out) + at;
+        if (n >= 4 && (reinterpret_cast<uintptr_t>(o) & 7u) == 0) {
+            *reinterpret_cast<uint2*>(o) = make_uint2(ss::pack_bf16x2(f[0], f[1]), ss::pack_bf16x2(f[2], f[3]));
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) o[i] = ss::f32_to_bf16(f[i]);
+    } else {
+        float* o = static_cast<float*>(out) + at;
+        if (n >= 4 && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+            *reinterpret_cast<float4*>(o) = v;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) o[i] = f[i];
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -331,7 +348,6 @@ mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairAr
 
 constexpr int kFewStages = 4;
 constexpr int kFewThreads = 32 * 6;
-constexpr int kPartPitch = kHalf + 1;  // floats of a column of partial sums: free of bank conflicts both ways
 
 __host__ __device__ constexpr int few_stage(int format, int few) {
     return kOperand + few * kRowBytes + 2 * scale_bytes(format);
@@ -356,7 +372,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
     __shared__ uint64_t bars[2 * kFewStages + 1];
     __shared__ uint32_t tmem_base;
     constexpr int kStage = few_stage(FORMAT, FEW), kScales = scale_bytes(FORMAT);
-    static_assert(kStage % 1024 == 0 && FEW * kPartPitch * 4 <= kFewStages * kStage, "shared memory");
+    static_assert(kStage % 1024 == 0 && FEW * kHalf * 4 <= kFewStages * kStage, "shared memory");
 
     launch_after();
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -432,7 +448,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
             tc::tmem_wait(r);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                if (c + i < FEW) part[(c + i) * kPartPitch + row] = !ok ? NAN : none ? 0.f : __uint_as_float(r[i]);
+                if (c + i < FEW) part[(c + i) * kHalf + row] = !ok ? NAN : none ? 0.f : __uint_as_float(r[i]);
         }
     }
     if (!ok) let_copies_land();
@@ -445,25 +461,54 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
     tc::fence_after();
     if (warp == 1) tc::tmem_free_one(tmem, few_tmem(FEW));
 
-    // this CTA's share of the columns, the splits added in their order
-    const int share = FEW / g.splits, c0 = split * share;
-    for (int i = threadIdx.x; i < share * kHalf; i += kFewThreads) {
-        // neighbouring threads along out's contiguous direction
-        const int c = c0 + (g.row_step == 1 ? i / kHalf : i % share), row = g.row_step == 1 ? i % kHalf : i / share;
-        const int64_t r = (int64_t)rt * kHalf + row, f = (int64_t)ft * FEW + c;
-        if (r >= g.rows || f >= g.few) continue;
-        const uint32_t at = smem + (uint32_t)(c * kPartPitch + row) * 4;
-        float s = 0.f;
-        if (g.splits > 1) {
+    // this CTA's share of the columns, the splits added in their order; four columns at a time, so
+    // that as many loads from the other CTAs are on their way
+    const int share = (FEW + g.splits - 1) / g.splits, c0 = split * share;
+    const int64_t few0 = (int64_t)ft * FEW;
+    const int columns = (int)min(min((int64_t)c0 + share, (int64_t)FEW), g.few - few0) - c0;  // that exist
+    if (g.row_step == 1) {
+        const int64_t r = (int64_t)rt * kHalf + 4 * lane;
+        const int have = (int)min(g.rows - r, (int64_t)4);
+        for (int c = 4 * warp; c < columns && have > 0; c += 4 * (kFewThreads / 32)) {
+            float4 s[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
             for (int q = 0; q < g.splits; ++q) {
-                float v;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tc::map_to_rank(at, q)) : "memory");
-                s += v;
+                const uint32_t at = tc::map_to_rank(smem + (uint32_t)((c0 + c) * kHalf + 4 * lane) * 4, q);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (c + u >= columns) continue;
+                    float4 v;
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                                 : "r"(at + u * kHalf * 4)
+                                 : "memory");
+                    s[u].x += v.x, s[u].y += v.y, s[u].z += v.z, s[u].w += v.w;
+                }
             }
-        } else {
-            asm volatile("ld.shared::cta.f32 %0, [%1];" : "=f"(s) : "r"(at) : "memory");
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (c + u < columns) store_four(g.out, r + (few0 + c0 + c + u) * g.few_step, s[u], have, g.elem_bytes);
         }
-        store_one(g.out, r * g.row_step + f * g.few_step, s, g.elem_bytes);
+    } else {  // out is contiguous along the few: a row a lane, four of them a thread
+        const int row = threadIdx.x & (kHalf - 1);
+        const int64_t r = (int64_t)rt * kHalf + row;
+        for (int c = 4 * (threadIdx.x / kHalf); c < columns && r < g.rows && threadIdx.x < kHalf; c += 4) {
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+            for (int q = 0; q < g.splits; ++q) {
+                const uint32_t at = tc::map_to_rank(smem + (uint32_t)((c0 + c) * kHalf + row) * 4, q);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    float v;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at + u * kHalf * 4) : "memory");
+                    s[u] += v;
+                }
+            }
+            store_four(g.out, r * g.row_step + few0 + c0 + c, make_float4(s[0], s[1], s[2], s[3]), min(columns - c, 4),
+                       g.elem_bytes);
+        }
     }
     if (g.splits > 1) tc::cluster_sync();
 }
@@ -530,6 +575,20 @@ int launch_pair(const ss_mx_product* p, int64_t k_blocks, cudaStream_t st) {
     return ss::launch(kernel, 2 * std::min(m_tiles * n_tiles, pairs), kPairThreads, smem, 0, true, st, maps, g);
 }
 
+// CTAs that share k, for which the fullest SM has the fewest k blocks to go through (as
+// far as the SMs hold the CTAs at once); of equals the fewest.
+int choose_splits(int64_t tiles, int64_t k_blocks, int smem) {
+    const int64_t sms = ss::num_sms(), held = sms * (smem <= 112 * 1024 ? 2 : 1);
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int s = 1; s <= 8 && s <= k_blocks; ++s) {
+        if (s > 1 && tiles * s > held) break;
+        const int64_t blocks = div_up(tiles * s, sms) * div_up(k_blocks, s) + 1;  // 1: what a CTA costs beside
+        if (blocks < least) best = s, least = blocks;
+    }
+    return best;
+}
+
 template <int FORMAT, int FEW>
 int launch_few(const ss_mx_product* p, int64_t k_blocks, bool swap, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
@@ -541,8 +600,7 @@ int launch_few(const ss_mx_product* p, int64_t k_blocks, bool swap, cudaStream_t
     Maps maps;
     if (int rc = make_maps(&maps, a, b, p->K, FORMAT, FEW)) return rc;
     const int64_t row_tiles = div_up(a.rows, kHalf), few_tiles = div_up(b.rows, FEW), tiles = row_tiles * few_tiles;
-    int splits = 1;
-    while (splits < 8 && tiles * splits * 2 <= 2 * ss::num_sms() && k_blocks >= 4 * splits) splits *= 2;
+    const int splits = choose_splits(tiles, k_blocks, smem);
     const FewArgs g = {a.rows, b.rows, swap ? p->out_stride : 1, swap ? 1 : p->out_stride, (int)row_tiles, (int)k_blocks,
                        splits, p->out, p->elem_bytes};
     if (tiles * splits > INT32_MAX) return SS_EOVERFLOW;
