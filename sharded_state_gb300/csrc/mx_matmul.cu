@@ -347,7 +347,7 @@ mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairAr
 // ---------------------------------------------------------------------------
 
 constexpr int kFewStages = 4;
-constexpr int kFewThreads = 32 * 6;
+constexpr int kFewThreads = 32 * 8;  // loader, issuer, four that read the accumulator; all join the shares
 
 __host__ __device__ constexpr int few_stage(int format, int few) {
     return kOperand + few * kRowBytes + 2 * scale_bytes(format);
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
             __syncwarp();
         }
         if (kb == ke && tc::elect_one()) tc::commit_one(done);
-    } else if (warp >= 2) {
+    } else if (warp >= 2 && warp < 6) {
         const int quad = warp & 3, row = quad * 32 + lane;
         ok = tc::mbar_wait(done, 0);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -461,56 +461,55 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
     tc::fence_after();
     if (warp == 1) tc::tmem_free_one(tmem, few_tmem(FEW));
 
-    // this CTA's share of the columns, the splits added in their order; four columns at a time, so
-    // that as many loads from the other CTAs are on their way
+    // this CTA's share of the columns, the splits added in their order; eight columns a warp at a
+    // time, so that as many loads from the other CTAs are on their way
     const int share = (FEW + g.splits - 1) / g.splits, c0 = split * share;
     const int64_t few0 = (int64_t)ft * FEW;
     const int columns = (int)min(min((int64_t)c0 + share, (int64_t)FEW), g.few - few0) - c0;  // that exist
     if (g.row_step == 1) {
         const int64_t r = (int64_t)rt * kHalf + 4 * lane;
         const int have = (int)min(g.rows - r, (int64_t)4);
-        for (int c = 4 * warp; c < columns && have > 0; c += 4 * (kFewThreads / 32)) {
-            float4 s[4];
+        for (int c = 8 * warp; c < columns && have > 0; c += 8 * (kFewThreads / 32)) {
+            float4 s[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) s[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+            for (int u = 0; u < 8; ++u) s[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int q = 0; q < g.splits; ++q) {
                 const uint32_t at = tc::map_to_rank(smem + (uint32_t)((c0 + c) * kHalf + 4 * lane) * 4, q);
+                float4 v[8];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (c + u >= columns) continue;
-                    float4 v;
-                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                                 : "r"(at + u * kHalf * 4)
-                                 : "memory");
-                    s[u].x += v.x, s[u].y += v.y, s[u].z += v.z, s[u].w += v.w;
-                }
+                for (int u = 0; u < 8; ++u)
+                    if (c + u < columns)
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(v[u].x), "=f"(v[u].y), "=f"(v[u].z), "=f"(v[u].w)
+                                     : "r"(at + u * kHalf * 4));
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (c + u < columns) s[u].x += v[u].x, s[u].y += v[u].y, s[u].z += v[u].z, s[u].w += v[u].w;
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 8; ++u)
                 if (c + u < columns) store_four(g.out, r + (few0 + c0 + c + u) * g.few_step, s[u], have, g.elem_bytes);
         }
-    } else {  // out is contiguous along the few: a row a lane, four of them a thread
+    } else {  // out is contiguous along the few: a row a lane, four columns at a time
         const int row = threadIdx.x & (kHalf - 1);
         const int64_t r = (int64_t)rt * kHalf + row;
-        for (int c = 4 * (threadIdx.x / kHalf); c < columns && r < g.rows && threadIdx.x < kHalf; c += 4) {
+        for (int c = 4 * (threadIdx.x / kHalf); c < columns && r < g.rows; c += 4 * (kFewThreads / kHalf)) {
             float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
             for (int q = 0; q < g.splits; ++q) {
                 const uint32_t at = tc::map_to_rank(smem + (uint32_t)((c0 + c) * kHalf + row) * 4, q);
+                float v[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    float v;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at + u * kHalf * 4) : "memory");
-                    s[u] += v;
-                }
+                for (int u = 0; u < 4; ++u)
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[u]) : "r"(at + u * kHalf * 4));
+#pragma unroll
+                for (int u = 0; u < 4; ++u) s[u] += v[u];
             }
             store_four(g.out, r * g.row_step + few0 + c0 + c, make_float4(s[0], s[1], s[2], s[3]), min(columns - c, 4),
                        g.elem_bytes);
         }
     }
-    if (g.splits > 1) tc::cluster_sync();
+    __syncwarp();
+    if (g.splits > 1) tc::cluster_sync_read();
 }
 
 // ---------------------------------------------------------------------------
@@ -611,7 +610,7 @@ template <int FORMAT>
 int launch_product(const ss_mx_product* p, cudaStream_t st) {
     const int64_t k_blocks = div_up(div_up(p->K, ss::kMxTile), scale_tiles(FORMAT));
     const int64_t big = div_up(p->M, kTile) * div_up(p->N, kTile);
-    if (2 * big >= ss::num_sms() / 2) return launch_pair<FORMAT>(p, k_blocks, st);
+    if (2 * big >= ss::num_sms() / 2 && p->M > kHalf && p->N > kHalf) return launch_pair<FORMAT>(p, k_blocks, st);
     const bool swap = p->N < p->M && p->N <= 64;  // the few are B's rows
     const int64_t few = swap ? p->N : p->M;
     if (few <= 16) return launch_few<FORMAT, 16>(p, k_blocks, swap, st);

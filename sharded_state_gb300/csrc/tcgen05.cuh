@@ -32,6 +32,12 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The same where nothing is handed over: every thread of the cluster has read what it
+// reads of the others' shared memory.  It does not wait for stores on their way.
+__device__ __forceinline__ void cluster_sync_read() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // One lane of a whole warp, the same each time.  Work for one thread that is issued
 // under it, in a loop that the warp runs together, has its operands in uniform
 // registers; in a branch of one lane each of them is moved there first (a scaled product
