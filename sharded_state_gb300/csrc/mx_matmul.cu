@@ -105,6 +105,22 @@ __device__ __forceinline__ void store_four(void* out, int64_t at, float4 v, int 
     }
 }
 
+__device__ __forceinline__ void store_one(void* out, int64_t at, float v, int elem_bytes) {
+    if (elem_bytes == 2)
+        static_cast<uint16_t*>(out)[at] = ss::f32_to_bf16(v);
+    else
+        static_cast<float*>(out)[at] = v;
+}
+
+// s[u] of registers.
+__device__ __forceinline__ float4 pick(const float4 (&s)[8], int u) {
+    float4 v = s[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+        if (u == i) v = s[i];
+    return v;
+}
+
 // ---------------------------------------------------------------------------
 // 256 x 256 tiles, a pair of CTAs each
 // ---------------------------------------------------------------------------
@@ -363,6 +379,7 @@ struct FewArgs {
     int row_tiles, k_blocks, splits;
     void* out;
     int elem_bytes;
+    int vector;  // out's four neighbouring elements lie on their size
 };
 
 template <int FORMAT, int FEW>
@@ -372,7 +389,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
     __shared__ uint64_t bars[2 * kFewStages + 1];
     __shared__ uint32_t tmem_base;
     constexpr int kStage = few_stage(FORMAT, FEW), kScales = scale_bytes(FORMAT);
-    static_assert(kStage % 1024 == 0 && FEW * kHalf * 4 <= kFewStages * kStage, "shared memory");
+    static_assert(kStage % 1024 == 0 && (FEW + kFewThreads / 32) * kHalf * 4 <= kFewStages * kStage, "shared memory");
 
     launch_after();
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -397,6 +414,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
     const uint32_t tmem = tmem_base;
     wait_before();
 
+    float* part_all = reinterpret_cast<float*>(raw + (smem - tc::smem_addr(raw)));
     const int split = g.splits > 1 ? (int)tc::cluster_ctarank() : 0;
     const int tile = blockIdx.x / g.splits, rt = tile % g.row_tiles, ft = tile / g.row_tiles;
     const int per = (g.k_blocks + g.splits - 1) / g.splits;
@@ -438,7 +456,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc::fence_after();
         // every stage has been read: its shared memory takes the sums
-        float* part = reinterpret_cast<float*>(raw + (smem - tc::smem_addr(raw)));
+        float* part = part_all;
         const bool none = kb == ke;  // no k: the accumulator holds something else
 #pragma unroll 1
         for (int c = 0; c < FEW; c += 32) {
@@ -469,7 +487,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
     if (g.row_step == 1) {
         const int64_t r = (int64_t)rt * kHalf + 4 * lane;
         const int have = (int)min(g.rows - r, (int64_t)4);
-        for (int c = 8 * warp; c < columns && have > 0; c += 8 * (kFewThreads / 32)) {
+        for (int c = 8 * warp; c < columns; c += 8 * (kFewThreads / 32)) {
             float4 s[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) s[u] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -486,9 +504,22 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
                 for (int u = 0; u < 8; ++u)
                     if (c + u < columns) s[u].x += v[u].x, s[u].y += v[u].y, s[u].z += v[u].z, s[u].w += v[u].w;
             }
+            if (g.vector) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (c + u < columns) store_four(g.out, r + (few0 + c0 + c + u) * g.few_step, s[u], have, g.elem_bytes);
+                for (int u = 0; u < 8; ++u)
+                    if (c + u < columns) store_four(g.out, r + (few0 + c0 + c + u) * g.few_step, s[u], have, g.elem_bytes);
+            } else {  // lanes along the row, through the shared memory behind the sums
+                float* mine = part_all + FEW * kHalf + warp * kHalf;
+                for (int u = 0; u < 8 && c + u < columns; ++u) {
+                    __syncwarp();
+                    *reinterpret_cast<float4*>(mine + 4 * lane) = pick(s, u);
+                    __syncwarp();
+                    const int64_t at = (int64_t)rt * kHalf + (few0 + c0 + c + u) * g.few_step;
+#pragma unroll
+                    for (int k = lane; k < kHalf; k += 32)
+                        if ((int64_t)rt * kHalf + k < g.rows) store_one(g.out, at + k, mine[k], g.elem_bytes);
+                }
+            }
         }
     } else {  // out is contiguous along the few: a row a lane, four columns at a time
         const int row = threadIdx.x & (kHalf - 1);
@@ -601,7 +632,8 @@ int launch_few(const ss_mx_product* p, int64_t k_blocks, bool swap, cudaStream_t
     const int64_t row_tiles = div_up(a.rows, kHalf), few_tiles = div_up(b.rows, FEW), tiles = row_tiles * few_tiles;
     const int splits = choose_splits(tiles, k_blocks, smem);
     const FewArgs g = {a.rows, b.rows, swap ? p->out_stride : 1, swap ? 1 : p->out_stride, (int)row_tiles, (int)k_blocks,
-                       splits, p->out, p->elem_bytes};
+                       splits, p->out, p->elem_bytes,
+                       ss::aligned(p->out, 4 * p->elem_bytes) && p->out_stride % 4 == 0};
     if (tiles * splits > INT32_MAX) return SS_EOVERFLOW;
     return ss::launch(kernel, tiles * splits, kFewThreads, smem, splits > 1 ? splits : 0, true, st, maps, g);
 }

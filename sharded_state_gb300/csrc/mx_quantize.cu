@@ -130,11 +130,10 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
     const T* x = static_cast<const T*>(a.x) + (row0 + line) * a.stride + col0 + 8 * c8;
     const int rows = (int)min(a.rows - row0, (int64_t)kMxTile), left = (int)min(a.cols - col0 - 8 * c8, (int64_t)16);
     Vec8<T> v[kRounds];
+    uint4 tail[kRounds] = {};
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        v[i].template load<ALIGNED>(x, Run(16 * i + line < rows ? left : 0, c8 == 0, c8 == 15));
-        x += 16 * a.stride;
-    }
+    for (int i = 0; i < kRounds; ++i)
+        v[i].template fetch<ALIGNED>(x + 16 * i * a.stride, Run(16 * i + line < rows ? left : 0, c8 == 0, c8 == 15), tail[i]);
     const int64_t pitch = a.col_tiles * M::kTileRow;
     unsigned char* out = a.data + (row0 + line) * pitch + tc * M::kTileRow + c8 * (int)sizeof(Word);
     unsigned char* scales = a.scales + blockIdx.x * (int64_t)ss::kMxTileBytes + 16 * line;
@@ -143,6 +142,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
     for (int i = 0; i < kRounds; ++i, out += 16 * pitch) {
         const int r = 16 * i + line;
         if (!TRANSPOSE && 16 * i + (line & ~1) >= rows) break;  // both rows of the warp are behind the last
+        v[i].template settle<ALIGNED>(x + 16 * i * a.stride, Run(r < rows ? left : 0, c8 == 0, c8 == 15), tail[i]);
         uint4 bits = make_uint4(0, 0, 0, 0);
         if (RANDOM) bits = philox((uint32_t)row0 + r, (uint32_t)tc * 16 + c8);
         if (TRANSPOSE) {

@@ -166,6 +166,7 @@ __device__ __forceinline__ void store_mx8(const NormArgs& a, int64_t row, int co
 // VECS loads of 8 elements a thread, `team` threads a row, blockDim / team rows a CTA.
 template <class T, int VECS, bool ALIGNED>
 __global__ void __launch_bounds__(VECS > 2 ? 512 : 256) norm_kernel(const __grid_constant__ NormArgs a) {
+    constexpr bool kWeightAhead = VECS <= 4;  // asked for with the row
     __shared__ float lane_sums[16];
     launch_after();
     const int mine = threadIdx.x % a.team, lane = threadIdx.x & 31;
@@ -173,24 +174,36 @@ __global__ void __launch_bounds__(VECS > 2 ? 512 : 256) norm_kernel(const __grid
     const bool live = row < a.rows;
     auto run = [&](int col) { return Run(live ? a.cols - col : 0, lane == 0, lane == 31); };
     wait_before();
-    Vec8<T> x[VECS], r[VECS];
+    Vec8<T> x[VECS], r[VECS], w[VECS];
+    uint4 x_tail[VECS] = {}, r_tail[VECS] = {}, w_tail[VECS] = {};
+    const T* x_row = static_cast<const T*>(a.x) + row * a.x_stride;
+    const T* r_row = static_cast<const T*>(a.residual) + row * a.residual_stride;
+    const T* weight = static_cast<const T*>(a.weight);
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
         const int col = 8 * (mine + i * a.team);
-        x[i].template load<ALIGNED>(static_cast<const T*>(a.x) + row * a.x_stride + col, run(col));
-        if (a.residual)
-            r[i].template load<ALIGNED>(static_cast<const T*>(a.residual) + row * a.residual_stride + col, run(col));
+        x[i].template fetch<ALIGNED>(x_row + col, run(col), x_tail[i]);
+        if (a.residual) r[i].template fetch<ALIGNED>(r_row + col, run(col), r_tail[i]);
+    }
+    if (kWeightAhead) {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+            const int col = 8 * (mine + i * a.team);
+            w[i].template fetch<ALIGNED>(weight + col, run(col), w_tail[i]);
+        }
     }
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
         const int col = 8 * (mine + i * a.team);
         float f[8];
+        x[i].template settle<ALIGNED>(x_row + col, run(col), x_tail[i]);
         if (a.drop || a.residual) {
             x[i].get(f);
             if (a.drop) ss::drop8(f, ss::Philox(a.rng)((uint32_t)row, (uint32_t)(col >> 3)), a.drop, a.scale);
             if (a.residual) {
                 float q[8];
+                r[i].template settle<ALIGNED>(r_row + col, run(col), r_tail[i]);
                 r[i].get(q);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) f[k] = __fadd_rn(f[k], q[k]);
@@ -209,16 +222,16 @@ __global__ void __launch_bounds__(VECS > 2 ? 512 : 256) norm_kernel(const __grid
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
         const int col = 8 * (mine + i * a.team);
-        Vec8<T> w;
-        w.template load<ALIGNED>(static_cast<const T*>(a.weight) + col, run(col));
+        if (!kWeightAhead) w[i].template fetch<ALIGNED>(weight + col, run(col), w_tail[i]);
+        w[i].template settle<ALIGNED>(weight + col, run(col), w_tail[i]);
         float f[8], q[8];
         x[i].get(f);
-        w.get(q);
+        w[i].get(q);
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[k] = f[k] * rstd * q[k];
         if (a.out) {
-            w.set(f);
-            w.template store<ALIGNED>(static_cast<T*>(a.out) + row * a.out_stride + col, run(col));
+            w[i].set(f);
+            w[i].template store<ALIGNED>(static_cast<T*>(a.out) + row * a.out_stride + col, run(col));
         }
         if (a.mx_data) {
             const int n = run(col).n;  // an infinite rstd would make the zeros behind the end NaN
@@ -230,13 +243,16 @@ __global__ void __launch_bounds__(VECS > 2 ? 512 : 256) norm_kernel(const __grid
 }
 
 // The rows of a backward pass in turn, each CTA its own; the next row's elements are
-// on their way while one is worked on (VECS <= 2: more do not fit the registers).
+// on their way while one is worked on, where the registers hold both.
+template <class T, int VECS, bool ALIGNED>
+__host__ __device__ constexpr bool loads_ahead() { return VECS * sizeof(T) <= (ALIGNED ? 4 : 2) || VECS == 1; }
+
 template <class T, int VECS, bool ALIGNED>
 __global__ void __launch_bounds__(VECS > 2 ? 512 : 256, VECS > 2 ? 1 : 2)
 norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
     extern __shared__ float joined[];  // [rows at a time][cols], where that is more than one
     __shared__ float lane_sums[2][16];
-    constexpr bool kAhead = VECS <= 2;
+    constexpr bool kAhead = loads_ahead<T, VECS, ALIGNED>();
     launch_after();
     const int mine = threadIdx.x % a.team, teams = blockDim.x / a.team, team = threadIdx.x / a.team;
     const int lane = threadIdx.x & 31;
@@ -249,42 +265,70 @@ norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
     auto run = [&](int64_t row, int col) { return Run(row < a.rows ? a.cols - col : 0, lane == 0, lane == 31); };
     struct Row {
         Vec8<T> dy[VECS], h[VECS], ds[VECS];
+        uint4 dy_tail[VECS], h_tail[VECS], ds_tail[VECS];
         float rstd;
     };
-    auto load = [&](Row& x, int64_t row) {
+    auto fetch = [&](Row& x, int64_t row) {
+        const T* dy = static_cast<const T*>(a.d_out) + row * a.d_out_stride;
+        const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
+        const T* ds = static_cast<const T*>(a.d_sum) + row * a.d_sum_stride;
 #pragma unroll
         for (int i = 0; i < VECS; ++i) {
             const int col = 8 * (mine + i * a.team);
-            x.dy[i].template load<ALIGNED>(static_cast<const T*>(a.d_out) + row * a.d_out_stride + col, run(row, col));
-            x.h[i].template load<ALIGNED>(static_cast<const T*>(a.h) + row * a.h_stride + col, run(row, col));
-            if (a.d_sum)
-                x.ds[i].template load<ALIGNED>(static_cast<const T*>(a.d_sum) + row * a.d_sum_stride + col, run(row, col));
-            else
-                x.ds[i].clear();
+            x.dy_tail[i] = x.h_tail[i] = x.ds_tail[i] = make_uint4(0, 0, 0, 0);
+            x.dy[i].template fetch<ALIGNED>(dy + col, run(row, col), x.dy_tail[i]);
+            x.h[i].template fetch<ALIGNED>(h + col, run(row, col), x.h_tail[i]);
+            x.ds[i].clear();
+            if (a.d_sum) x.ds[i].template fetch<ALIGNED>(ds + col, run(row, col), x.ds_tail[i]);
         }
         x.rstd = row < a.rows ? a.rstd[row] : 0.f;
+    };
+    auto settle = [&](Row& x, int64_t row) {
+        const T* dy = static_cast<const T*>(a.d_out) + row * a.d_out_stride;
+        const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
+        const T* ds = static_cast<const T*>(a.d_sum) + row * a.d_sum_stride;
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+            const int col = 8 * (mine + i * a.team);
+            x.dy[i].template settle<ALIGNED>(dy + col, run(row, col), x.dy_tail[i]);
+            x.h[i].template settle<ALIGNED>(h + col, run(row, col), x.h_tail[i]);
+            if (a.d_sum) x.ds[i].template settle<ALIGNED>(ds + col, run(row, col), x.ds_tail[i]);
+        }
     };
     int parity = 0;
     const int64_t step = (int64_t)gridDim.x * teams;
     Row x, ahead;
-    if (kAhead) load(x, (int64_t)blockIdx.x * teams + team);
+    Vec8<T> w[kAhead ? VECS : 1];
+    if (kAhead) {
+        fetch(x, (int64_t)blockIdx.x * teams + team);
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+            const int col = 8 * (mine + i * a.team);
+            w[i].template load<ALIGNED>(static_cast<const T*>(a.weight) + col, Run(a.cols - col, lane == 0, lane == 31));
+        }
+    }
+    auto weight = [&](int i, float (&g)[8]) {
+        if (!kAhead) {
+            const int col = 8 * (mine + i * a.team);
+            w[0].template load<ALIGNED>(static_cast<const T*>(a.weight) + col, Run(a.cols - col, lane == 0, lane == 31));
+        }
+        w[kAhead ? i : 0].get(g);
+    };
     for (int64_t first = (int64_t)blockIdx.x * teams; first < a.rows; first += step, parity ^= 1) {
         const int64_t row = first + team;
         if (kAhead)
-            load(ahead, row + step);
+            fetch(ahead, row + step);
         else
-            load(x, row);
+            fetch(x, row);
+        settle(x, row);
         const float rstd = x.rstd;
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < VECS; ++i) {
-            const int col = 8 * (mine + i * a.team);
-            Vec8<T> w;
-            w.template load<ALIGNED>(static_cast<const T*>(a.weight) + col, Run(a.cols - col, lane == 0, lane == 31));
             float f[8], q[8], g[8];
+            weight(i, g);
             x.dy[i].get(f);
             x.h[i].get(q);
-            w.get(g);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {  // zeros behind the row's end
                 const float t = f[k] * (q[k] * rstd);
@@ -296,23 +340,22 @@ norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
 #pragma unroll
         for (int i = 0; i < VECS; ++i) {
             const int col = 8 * (mine + i * a.team);
-            Vec8<T> w;
-            w.template load<ALIGNED>(static_cast<const T*>(a.weight) + col, Run(a.cols - col, lane == 0, lane == 31));
             float f[8], q[8], g[8], d[8];
+            weight(i, g);
             x.dy[i].get(f);
             x.h[i].get(q);
-            w.get(g);
             x.ds[i].get(d);
 #pragma unroll
             for (int k = 0; k < 8; ++k) f[k] = fmaf(rstd, fmaf(-q[k] * rstd, s, f[k] * g[k]), d[k]);
+            Vec8<T> v;
             if (a.d_h) {
-                w.set(f);
-                w.template store<ALIGNED>(static_cast<T*>(a.d_h) + row * a.d_h_stride + col, run(row, col));
+                v.set(f);
+                v.template store<ALIGNED>(static_cast<T*>(a.d_h) + row * a.d_h_stride + col, run(row, col));
             }
             if (a.d_x) {
                 if (a.drop) ss::drop8(f, ss::Philox(a.rng)((uint32_t)row, (uint32_t)(col >> 3)), a.drop, a.scale);
-                w.set(f);
-                w.template store<ALIGNED>(static_cast<T*>(a.d_x) + row * a.d_x_stride + col, run(row, col));
+                v.set(f);
+                v.template store<ALIGNED>(static_cast<T*>(a.d_x) + row * a.d_x_stride + col, run(row, col));
             }
         }
         if (kAhead) x = ahead;
@@ -389,15 +432,21 @@ struct Shape {
     int vecs, team, threads;
 };
 
-Shape choose_shape(int64_t vectors) {
+Shape choose_shape(int64_t vectors, int most = 2) {
     if (vectors <= 512) {
         int team = 32;
-        while (team < 256 && team * 2 < vectors) team *= 2;
+        while (team < 256 && team * most < vectors) team *= 2;
         return {vectors <= team ? 1 : 2, team, 256};
     }
     const int vecs = vectors <= 2048 ? 4 : 8;
     const int team = (int)((vectors + vecs - 1) / vecs + 31) / 32 * 32;
     return {vecs, team, team};
+}
+
+// The backward pass's: one load a thread where fp32 or unaligned rows would leave no
+// registers for the next row's.
+Shape choose_grad_shape(int64_t cols, int elem_bytes, bool aligned) {
+    return choose_shape((cols + 7) / 8, elem_bytes == 2 && aligned ? 2 : 1);
 }
 
 // CTAs that take the rows of a backward pass in turn.
@@ -517,7 +566,7 @@ int ss_rms_norm(const ss_norm* n, ss_stream_t stream) {
 int ss_rms_norm_workspace(int64_t rows, int64_t cols, size_t* bytes_out) {
     if (rows < 0 || cols < 1 || !bytes_out) return SS_EINVAL;
     if (rows > kMaxRows || cols > kMaxCols) return SS_EOVERFLOW;
-    *bytes_out = (size_t)(std::max<int64_t>(grad_grid(rows, choose_shape((cols + 7) / 8)), 1) * cols * 4);
+    *bytes_out = (size_t)(std::max<int64_t>(grad_grid(rows, choose_grad_shape(cols, 4, false)), 1) * cols * 4);
     return SS_OK;
 }
 
@@ -533,16 +582,18 @@ int ss_rms_norm_backward(const ss_norm_grad* n, ss_stream_t stream) {
     if (int rc = check_matrices(n->rows, n->cols, n->elem_bytes, {dy, h, ds, w, dh, dx, {n->d_weight, n->cols}}))
         return rc;
     if (!ss::aligned(n->rstd, 4) || !ss::aligned(n->workspace, 16)) return SS_EALIGN;
-    const Shape s = choose_shape((n->cols + 7) / 8);
+    size_t wanted = 0;
+    if (int rc = ss_rms_norm_workspace(n->rows, n->cols, &wanted)) return rc;
+    if (n->d_weight && (!n->workspace || n->workspace_bytes < wanted)) return SS_EINVAL;
+    const bool al = rows_on_16(n->elem_bytes, {dy, h, ds, dh, dx}) && ss::aligned(n->weight, 16);
+    const Shape s = choose_grad_shape(n->cols, n->elem_bytes, al);
     int64_t grid = std::max<int64_t>(grad_grid(n->rows, s), 1);
-    if (n->d_weight && (!n->workspace || n->workspace_bytes < (size_t)(grid * n->cols * 4))) return SS_EINVAL;
     if (n->rows == 0 && !n->d_weight) return SS_OK;
     a.rows = n->rows, a.cols = (int)n->cols, a.team = s.team;
     a.d_out = n->d_out, a.d_out_stride = n->d_out_stride, a.h = n->h, a.h_stride = n->h_stride;
     a.weight = n->weight, a.d_sum = n->d_sum, a.d_sum_stride = n->d_sum_stride, a.rstd = n->rstd;
     a.inv_cols = 1.f / (float)n->cols, a.rng = n->rng;
     a.d_h = n->d_h, a.d_h_stride = n->d_h_stride, a.d_x = n->d_x, a.d_x_stride = n->d_x_stride;
-    const bool al = rows_on_16(n->elem_bytes, {dy, h, ds, dh, dx}) && ss::aligned(n->weight, 16);
     const int teams = s.threads / s.team;
     // Few rows (up to 4 in turn for each team of 8 CTAs) are one cluster's, which joins d_weight in
     // its shared memory: one launch for two (50 x 64: 3.4 us where this takes 2.7).
@@ -554,7 +605,7 @@ int ss_rms_norm_backward(const ss_norm_grad* n, ss_stream_t stream) {
     } else if (n->d_weight) {
         a.part = static_cast<float*>(n->workspace);
     }
-    // with several teams at most 8 x 512 floats, or 4 x 1024, ...; 4096 in a cluster
+    // with several teams at most 8 x 512 floats, 4 x 1024 or 2 x 2048; 4096 in a cluster
     const int smem = teams > 1 || cluster ? teams * a.cols * 4 : 0;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (int rc = with_shape(n->elem_bytes, s.vecs, al, [&](auto t, auto v, auto aligned) {

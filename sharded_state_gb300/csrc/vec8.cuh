@@ -56,23 +56,29 @@ template <class T>
 struct Vec8;
 
 // Loads and stores with ALIGNED want p on 16 bytes; without, the whole warp makes them.
+// A load is in two steps, so that many can be on their way: fetch() asks for the blocks
+// (`tail` for one that no other lane loads), settle() of the same p and run makes of them
+// the lane's n elements, zeros behind them.
 template <>
 struct Vec8<uint16_t> {  // bf16
     uint4 r;
 
     __device__ __forceinline__ void clear() { r = make_uint4(0, 0, 0, 0); }
 
-    // The lane's n elements at p, zeros behind them.
     template <bool ALIGNED>
-    __device__ __forceinline__ void load(const uint16_t* p, const Run& run) {
+    __device__ __forceinline__ void fetch(const uint16_t* p, const Run& run, uint4& tail) {
         const int sh = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15u);
         const unsigned char* blk = reinterpret_cast<const unsigned char*>(p) - sh;
         r = make_uint4(0, 0, 0, 0);
         if (run.n > 0) r = ld_row_u4(blk);
+        if (!ALIGNED && run.after == 0 && sh + 2 * run.n > 16) tail = ld_row_u4(blk + 16);
+    }
+
+    template <bool ALIGNED>
+    __device__ __forceinline__ void settle(const uint16_t* p, const Run& run, const uint4& tail) {
         if (!ALIGNED) {
-            uint4 next = from_next_lane(r);
-            if (run.after == 0 && sh + 2 * run.n > 16) next = ld_row_u4(blk + 16);
-            r = realign16(r, next, sh);
+            const uint4 next = from_next_lane(r);
+            r = realign16(r, run.after == 0 ? tail : next, (int)(reinterpret_cast<uintptr_t>(p) & 15u));
         }
         if (run.n < 8) {
             r.x = run.n > 1 ? r.x : run.n > 0 ? r.x & 0xFFFFu : 0u;
@@ -80,6 +86,13 @@ struct Vec8<uint16_t> {  // bf16
             r.z = run.n > 5 ? r.z : run.n > 4 ? r.z & 0xFFFFu : 0u;
             r.w = run.n > 6 ? r.w & 0xFFFFu : 0u;
         }
+    }
+
+    template <bool ALIGNED>
+    __device__ __forceinline__ void load(const uint16_t* p, const Run& run) {
+        uint4 tail = make_uint4(0, 0, 0, 0);
+        fetch<ALIGNED>(p, run, tail);
+        settle<ALIGNED>(p, run, tail);
     }
 
     __device__ __forceinline__ void get(float (&f)[8]) const {
@@ -123,17 +136,22 @@ struct Vec8<float> {
     __device__ __forceinline__ void clear() { r[0] = r[1] = make_uint4(0, 0, 0, 0); }
 
     template <bool ALIGNED>
-    __device__ __forceinline__ void load(const float* p, const Run& run) {
+    __device__ __forceinline__ void fetch(const float* p, const Run& run, uint4& tail) {
         const int sh = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15u);
         const unsigned char* blk = reinterpret_cast<const unsigned char*>(p) - sh;
         clear();
         if (run.n > 0) r[0] = ld_row_u4(blk);
         if (sh + 4 * run.n > 16) r[1] = ld_row_u4(blk + 16);
+        if (!ALIGNED && run.after == 0 && sh + 4 * run.n > 32) tail = ld_row_u4(blk + 32);
+    }
+
+    template <bool ALIGNED>
+    __device__ __forceinline__ void settle(const float* p, const Run& run, const uint4& tail) {
         if (!ALIGNED) {
-            uint4 next = from_next_lane(r[0]);
-            if (run.after == 0 && sh + 4 * run.n > 32) next = ld_row_u4(blk + 32);
+            const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+            const uint4 next = from_next_lane(r[0]);
             r[0] = realign16(r[0], r[1], sh);
-            r[1] = realign16(r[1], next, sh);
+            r[1] = realign16(r[1], run.after == 0 ? tail : next, sh);
         }
         if (run.n < 8) {
             r[0].x = run.n > 0 ? r[0].x : 0u, r[0].y = run.n > 1 ? r[0].y : 0u;
@@ -141,6 +159,13 @@ struct Vec8<float> {
             r[1].x = run.n > 4 ? r[1].x : 0u, r[1].y = run.n > 5 ? r[1].y : 0u;
             r[1].z = run.n > 6 ? r[1].z : 0u, r[1].w = 0u;
         }
+    }
+
+    template <bool ALIGNED>
+    __device__ __forceinline__ void load(const float* p, const Run& run) {
+        uint4 tail = make_uint4(0, 0, 0, 0);
+        fetch<ALIGNED>(p, run, tail);
+        settle<ALIGNED>(p, run, tail);
     }
 
     __device__ __forceinline__ void get(float (&f)[8]) const {
