@@ -112,15 +112,6 @@ __device__ __forceinline__ void store_one(void* out, int64_t at, float v, int el
         static_cast<float*>(out)[at] = v;
 }
 
-// s[u] of registers.
-__device__ __forceinline__ float4 pick(const float4 (&s)[8], int u) {
-    float4 v = s[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i)
-        if (u == i) v = s[i];
-    return v;
-}
-
 // ---------------------------------------------------------------------------
 // 256 x 256 tiles, a pair of CTAs each
 // ---------------------------------------------------------------------------
@@ -389,7 +380,7 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
     __shared__ uint64_t bars[2 * kFewStages + 1];
     __shared__ uint32_t tmem_base;
     constexpr int kStage = few_stage(FORMAT, FEW), kScales = scale_bytes(FORMAT);
-    static_assert(kStage % 1024 == 0 && (FEW + kFewThreads / 32) * kHalf * 4 <= kFewStages * kStage, "shared memory");
+    static_assert(kStage % 1024 == 0 && (FEW + 8 * kFewThreads / 32) * kHalf * 4 <= kFewStages * kStage, "shared memory");
 
     launch_after();
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -509,15 +500,18 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
                 for (int u = 0; u < 8; ++u)
                     if (c + u < columns) store_four(g.out, r + (few0 + c0 + c + u) * g.few_step, s[u], have, g.elem_bytes);
             } else {  // lanes along the row, through the shared memory behind the sums
-                float* mine = part_all + FEW * kHalf + warp * kHalf;
-                for (int u = 0; u < 8 && c + u < columns; ++u) {
-                    __syncwarp();
-                    *reinterpret_cast<float4*>(mine + 4 * lane) = pick(s, u);
-                    __syncwarp();
+                float* mine = part_all + FEW * kHalf + warp * 8 * kHalf;
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < 8; ++u) *reinterpret_cast<float4*>(mine + u * kHalf + 4 * lane) = s[u];
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
                     const int64_t at = (int64_t)rt * kHalf + (few0 + c0 + c + u) * g.few_step;
 #pragma unroll
                     for (int k = lane; k < kHalf; k += 32)
-                        if ((int64_t)rt * kHalf + k < g.rows) store_one(g.out, at + k, mine[k], g.elem_bytes);
+                        if (c + u < columns && (int64_t)rt * kHalf + k < g.rows)
+                            store_one(g.out, at + k, mine[u * kHalf + k], g.elem_bytes);
                 }
             }
         }

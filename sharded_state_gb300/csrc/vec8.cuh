@@ -39,6 +39,22 @@ __device__ __forceinline__ void st_words(unsigned char* blk, uint4 v, int lo, in
     if (lo <= 3 && hi > 3) w[3] = v.w;
 }
 
+// The first `bytes` (even, up to 14) of an aligned 16-byte block, or its last ones.
+__device__ __forceinline__ void st_head(unsigned char* blk, uint4 v, int bytes) {
+    if (bytes & 8) *reinterpret_cast<uint2*>(blk) = make_uint2(v.x, v.y);
+    const uint32_t w = bytes & 8 ? v.z : v.x, x = bytes & 8 ? v.w : v.y;
+    blk += bytes & 8;
+    if (bytes & 4) *reinterpret_cast<uint32_t*>(blk) = w;
+    if (bytes & 2) *reinterpret_cast<uint16_t*>(blk + (bytes & 4)) = (uint16_t)(bytes & 4 ? x : w);
+}
+__device__ __forceinline__ void st_tail(unsigned char* blk, uint4 v, int bytes) {
+    if (bytes & 8) *reinterpret_cast<uint2*>(blk + 8) = make_uint2(v.z, v.w);
+    const uint32_t w = bytes & 8 ? v.y : v.w, x = bytes & 8 ? v.x : v.z;
+    blk += bytes & 8 ? 8 : 16;
+    if (bytes & 4) *reinterpret_cast<uint32_t*>(blk - 4) = w;
+    if (bytes & 2) *reinterpret_cast<uint16_t*>(blk - (bytes & 4) - 2) = (uint16_t)((bytes & 4 ? x : w) >> 16);
+}
+
 // A lane's place in its row: n elements of its own (0: none), `after` in the next lane
 // (0 where that is not the group behind this one), and whether the lane before holds
 // the group before.
@@ -117,15 +133,19 @@ struct Vec8<uint16_t> {  // bf16
             if (run.n == 8)
                 *reinterpret_cast<uint4*>(p) = r;
             else
-                st_bytes(c, r, 0, 2 * run.n);
+                st_head(c, r, 2 * run.n);
             return;
         }
         const int head = 16 - sh;  // bytes that go into the block before
         if (run.n == 8 && 2 * run.after >= head)
             *reinterpret_cast<uint4*>(c + head) = realign16(r, next, head);
-        else
-            st_bytes(c + head, realign16(r, r, head), 0, 2 * run.n - head);
-        if (!run.prev || 2 * run.n < head) st_bytes(c - sh, realign16(r, r, head), sh, min(16, sh + 2 * run.n));
+        else if (2 * run.n > head)
+            st_head(c + head, realign16(r, r, head), 2 * run.n - head);
+        if (run.prev && 2 * run.n >= head) return;  // the lane before has written them
+        if (2 * run.n >= head)
+            st_tail(c - sh, realign16(r, r, head), head);
+        else  // both ends inside one block
+            st_bytes(c - sh, realign16(r, r, head), sh, sh + 2 * run.n);
     }
 };
 
