@@ -34,7 +34,6 @@ struct Mx<SS_MXFP4> {
     static constexpr int kLowest = 0;     // lowest exponent of a normal element
     static constexpr int kFraction = 1;   // bits
     static constexpr int kBits = 4;
-    static constexpr uint32_t kMostCode = 7;
     static constexpr int kTileRow = 64;   // bytes of 128 elements
     using Word = uint32_t;                // 8 elements
 
@@ -76,7 +75,6 @@ struct Mx<SS_MXFP8> {
     static constexpr int kLowest = -6;
     static constexpr int kFraction = 3;
     static constexpr int kBits = 8;
-    static constexpr uint32_t kMostCode = 0x7E;
     static constexpr int kTileRow = 128;
     using Word = uint2;
 
@@ -133,30 +131,38 @@ __device__ __forceinline__ int64_t mx_scale_at(int64_t r, int64_t b, int64_t til
     return ((r >> 7) * tiles + (b >> 2)) * kMxTileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
 }
 
+// The lower or upper 16 random bits of a word as mx_encode_random takes them: where they
+// belong behind a code that stands in the top bits, and what the codes begin with in fp32
+// taken off (for both formats 12 or 192 of 16 or 256, so 4 or 64 to be added).
+template <int FORMAT>
+__device__ __forceinline__ uint32_t mx_random(uint32_t word, bool upper) {
+    constexpr int kAt = 16 - Mx<FORMAT>::kBits;
+    return ((upper ? word >> (16 - kAt) : word << kAt) & (0xFFFFu << kAt)) | 0x40000000u;
+}
+
 // 8 elements times `inverse`, rounded down or up in magnitude: up where what is cut off
-// and the element's 16 random bits / 2^16 (u[i]) make one step.  In the format's normal
-// range the codes are the leading bits of the fp32 magnitude, and the random bits,
-// added right behind them, carry into them just then; below it the lowest normal number
-// is added first, which puts every element on the same steps, and half of the sum has
-// the leading bits that continue the codes (towards zero, so that nothing is rounded
-// but by the cut).  10 instructions an element.
+// and the element's 16 random bits / 2^16 make one step.  In the format's normal range
+// the codes are the leading bits of the fp32 magnitude, and the random bits, added right
+// behind them, carry into them just then; below it the lowest normal number is added
+// first, which puts every element on the same steps, and half of the sum has the leading
+// bits that continue the codes (towards zero, so that nothing is rounded but by the cut).
+// The codes are shifted out of the top of each sum into the result, the last one first;
+// one past the largest is put right for all of them at once.  9 instructions an element.
 template <int FORMAT>
 __device__ __forceinline__ typename Mx<FORMAT>::Word mx_encode_random(const float (&f)[8], float inverse,
-                                                                      const uint32_t (&u)[8]) {
+                                                                      const uint32_t (&random)[8]) {
     using M = Mx<FORMAT>;
     constexpr int kCut = 23 - M::kFraction, kPer = 32 / M::kBits;  // elements a word
-    constexpr uint32_t kFirst = ((uint32_t)(127 + M::kLowest - 1) << M::kFraction);  // leading bits of code 0
+    static_assert(((127 + M::kLowest - 1) << M::kFraction) % (1 << M::kBits) == (M::kBits == 4 ? 12 : 192), "mx_random");
     const float least = __uint_as_float((uint32_t)(127 + M::kLowest) << 23);
     uint32_t w[8 / kPer], sign[8];
 #pragma unroll
-    for (int i = 0; i < 8 / kPer; ++i) w[i] = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 7; i >= 0; --i) {
         const float v = fabsf(f[i]) * inverse;
         float t = v;
         if (v < least) t = __fmaf_rz(v, 0.5f, 0.5f * least);
-        const uint32_t code = min(((u[i] << (kCut - 16)) + __float_as_uint(t)) >> kCut, kFirst + M::kMostCode) - kFirst;
-        w[i / kPer] += code << (M::kBits * (i % kPer));
+        const uint32_t sum = __float_as_uint(t) * (1u << (32 - M::kBits - kCut)) + random[i];
+        w[i / kPer] = i % kPer == kPer - 1 ? sum >> (32 - M::kBits) : __funnelshift_l(sum, w[i / kPer], M::kBits);
         sign[i] = __float_as_uint(f[i]);
     }
     // the signs' bytes, four at a time
@@ -166,8 +172,13 @@ __device__ __forceinline__ typename Mx<FORMAT>::Word mx_encode_random(const floa
     };
     typename M::Word out;
     if constexpr (M::kBits == 4) {
-        out = w[0] | top(0, 2) >> 4 | top(1, 2);
+        out = (w[0] - (w[0] >> 3 & 0x11111111u)) | top(0, 2) >> 4 | top(1, 2);  // 8 -> 7
     } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // 0x7F, 0x80 -> 0x7E
+            const uint32_t over = (((w[i] + 0x01010101u) | w[i]) & 0x80808080u) >> 7;
+            w[i] = (w[i] & ~(over * 0xFFu)) | over * 0x7Eu;
+        }
         out = make_uint2(w[0] | top(0, 1), w[1] | top(4, 1));
     }
     return out;

@@ -28,7 +28,8 @@ using ss::Vec8;
 using ss::wait_before;
 
 constexpr int kThreads = 256;
-constexpr int kRounds = kMxTile * kMxTile / 8 / kThreads;  // loads of 8 elements a thread
+constexpr int kRounds = kMxTile * kMxTile / 8 / kThreads;  // loads of 8 elements a thread for a whole tile
+constexpr int kFewRounds = 2;  // without the transpose, where whole tiles would leave SMs idle
 
 struct QuantArgs {
     int64_t rows, cols;
@@ -115,7 +116,8 @@ struct Columns<float> {
     __device__ __forceinline__ float get(int j, int k) const { return w[k][j]; }
 };
 
-template <class T, int FORMAT, bool TRANSPOSE, bool RANDOM, bool ALIGNED>
+// ROUNDS x 16 rows of 128 columns: whole tiles for the transpose.
+template <class T, int FORMAT, int ROUNDS, bool TRANSPOSE, bool RANDOM, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constant__ QuantArgs a) {
     using M = Mx<FORMAT>;
     using Word = typename M::Word;
@@ -123,23 +125,23 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
     extern __shared__ __align__(16) uint32_t tile[];      // [128][kWords], then the random bits, [128][64]
     uint32_t* random = tile + kMxTile * kWords;
     launch_after();
-    const int64_t tr = blockIdx.x / a.col_tiles, tc = blockIdx.x - tr * a.col_tiles;
+    const int64_t part = blockIdx.x / a.col_tiles, tc = blockIdx.x - part * a.col_tiles;
+    const int64_t row0 = part * (16 * ROUNDS), col0 = tc * kMxTile, tr = row0 / kMxTile;
     const int line = threadIdx.x >> 4, c8 = threadIdx.x & 15;
-    const int64_t row0 = tr * kMxTile, col0 = tc * kMxTile;
     wait_before();
     const T* x = static_cast<const T*>(a.x) + (row0 + line) * a.stride + col0 + 8 * c8;
-    const int rows = (int)min(a.rows - row0, (int64_t)kMxTile), left = (int)min(a.cols - col0 - 8 * c8, (int64_t)16);
-    Vec8<T> v[kRounds];
-    uint4 tail[kRounds] = {};
+    const int rows = (int)min(a.rows - row0, (int64_t)(16 * ROUNDS)), left = (int)min(a.cols - col0 - 8 * c8, (int64_t)16);
+    Vec8<T> v[ROUNDS];
+    uint4 tail[ROUNDS] = {};
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i)
+    for (int i = 0; i < ROUNDS; ++i)
         v[i].template fetch<ALIGNED>(x + 16 * i * a.stride, Run(16 * i + line < rows ? left : 0, c8 == 0, c8 == 15), tail[i]);
     const int64_t pitch = a.col_tiles * M::kTileRow;
     unsigned char* out = a.data + (row0 + line) * pitch + tc * M::kTileRow + c8 * (int)sizeof(Word);
-    unsigned char* scales = a.scales + blockIdx.x * (int64_t)ss::kMxTileBytes + 16 * line;
+    unsigned char* scales = a.scales + ss::mx_scale_at(row0, 4 * tc, a.col_tiles) + 16 * line;
     const ss::Philox philox = RANDOM ? ss::Philox(a.rng) : ss::Philox();
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i, out += 16 * pitch) {
+    for (int i = 0; i < ROUNDS; ++i, out += 16 * pitch) {
         const int r = 16 * i + line;
         if (!TRANSPOSE && 16 * i + (line & ~1) >= rows) break;  // both rows of the warp are behind the last
         v[i].template settle<ALIGNED>(x + 16 * i * a.stride, Run(r < rows ? left : 0, c8 == 0, c8 == 15), tail[i]);
@@ -166,8 +168,10 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
         if (r < rows) {
             float f[8];
             v[i].get(f);
-            const uint32_t u[8] = {bits.x & 0xFFFFu, bits.x >> 16, bits.y & 0xFFFFu, bits.y >> 16,
-                                   bits.z & 0xFFFFu, bits.z >> 16, bits.w & 0xFFFFu, bits.w >> 16};
+            const uint32_t words[4] = {bits.x, bits.y, bits.z, bits.w};
+            uint32_t u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = ss::mx_random<FORMAT>(words[k >> 1], k & 1);
             *reinterpret_cast<Word*>(out) = encode<FORMAT, RANDOM>(f, byte, u);
             if (c8 == 0) *reinterpret_cast<uint32_t*>(scales + 256 * (i & 1) + 4 * (i >> 1)) = four;
         }
@@ -196,10 +200,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 f[k] = c.get(j, 8 * i + k);
-                if (RANDOM) {
-                    const uint32_t w = random[turned<kMxTile / 2>(32 * block + 8 * i + k, pair)];
-                    u[k] = j ? w >> 16 : w & 0xFFFFu;
-                }
+                if (RANDOM) u[k] = ss::mx_random<FORMAT>(random[turned<kMxTile / 2>(32 * block + 8 * i + k, pair)], j);
             }
             words[i] = encode<FORMAT, RANDOM>(f, byte, u);
         }
@@ -218,23 +219,23 @@ struct DequantArgs {
     int64_t stride;
 };
 
-template <class T, int FORMAT, bool ALIGNED>
+template <class T, int FORMAT, int ROUNDS, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_constant__ DequantArgs a) {
     using M = Mx<FORMAT>;
     using Word = typename M::Word;
     launch_after();
-    const int64_t tr = blockIdx.x / a.col_tiles, tc = blockIdx.x - tr * a.col_tiles;
+    const int64_t part = blockIdx.x / a.col_tiles, tc = blockIdx.x - part * a.col_tiles;
     const int line = threadIdx.x >> 4, c8 = threadIdx.x & 15;
-    const int64_t row0 = tr * kMxTile, col = tc * kMxTile + 8 * c8;
-    const int rows = (int)min(a.rows - row0, (int64_t)kMxTile), left = (int)min(a.cols - col, (int64_t)16);
+    const int64_t row0 = part * (16 * ROUNDS), col = tc * kMxTile + 8 * c8;
+    const int rows = (int)min(a.rows - row0, (int64_t)(16 * ROUNDS)), left = (int)min(a.cols - col, (int64_t)16);
     const int64_t pitch = a.col_tiles * M::kTileRow;
     const unsigned char* data = a.data + (row0 + line) * pitch + tc * M::kTileRow + c8 * (int)sizeof(Word);
-    const unsigned char* scales = a.scales + blockIdx.x * (int64_t)ss::kMxTileBytes + 16 * line + (c8 >> 2);
+    const unsigned char* scales = a.scales + ss::mx_scale_at(row0, 4 * tc + (c8 >> 2), a.col_tiles) + 16 * line;
     wait_before();
-    Word w[kRounds];
-    unsigned char byte[kRounds];
+    Word w[ROUNDS];
+    unsigned char byte[ROUNDS];
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i, data += 16 * pitch) {
+    for (int i = 0; i < ROUNDS; ++i, data += 16 * pitch) {
         w[i] = Word();
         byte[i] = 0;
         if (16 * i + line >= rows || left <= 0) continue;
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_const
     }
     T* out = static_cast<T*>(a.out) + (row0 + line) * a.stride + col;
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i, out += 16 * a.stride) {
+    for (int i = 0; i < ROUNDS; ++i, out += 16 * a.stride) {
         if (16 * i + (line & ~1) >= rows) break;  // both rows of the warp are behind the last
         float f[8];
         M::decode(w[i], f);
@@ -269,17 +270,28 @@ int with_flags(bool first, bool second, F&& f) {
     return first ? with_second(std::true_type()) : with_second(std::false_type());
 }
 
+// Parts of a matrix by rows where one CTA takes `rounds` x 16 of them.
+int64_t parts(int64_t rows, int rounds) { return (rows + 16 * rounds - 1) / (16 * rounds); }
+
+// Whole tiles as soon as there are 8 for each SM; below, a quarter of one (fp32 2043 x 1001
+// in 8 bits 5.2 us as 128 tiles, 32000 x 2048 29 us as 4000).
+bool few_tiles(int64_t row_tiles, int64_t col_tiles) { return row_tiles * col_tiles < 8 * (int64_t)ss::num_sms(); }
+
 template <class T, int FORMAT>
 int launch_quantize(const QuantArgs& a, bool transpose, bool random, bool aligned, cudaStream_t st) {
-    const int64_t grid = a.row_tiles * a.col_tiles;
+    if (!transpose && few_tiles(a.row_tiles, a.col_tiles))
+        return with_flags(random, aligned, [&](auto r, auto al) {
+            return ss::launch(quantize_kernel<T, FORMAT, kFewRounds, false, decltype(r)::value, decltype(al)::value>,
+                              parts(a.rows, kFewRounds) * a.col_tiles, kThreads, 0, 0, true, st, a);
+        });
     return with_flags(transpose, random, [&](auto t, auto r) {
         constexpr bool TR = decltype(t)::value, RA = decltype(r)::value;
         static std::atomic<uint64_t> ready[2]{};
         const int smem = TR ? tile_bytes<T, RA>() : 0;
-        const auto kernel = aligned ? quantize_kernel<T, FORMAT, TR, RA, true> : quantize_kernel<T, FORMAT, TR, RA, false>;
+        const auto kernel = aligned ? quantize_kernel<T, FORMAT, kRounds, TR, RA, true> : quantize_kernel<T, FORMAT, kRounds, TR, RA, false>;
         if (smem > 48 * 1024)
             if (int rc = ss::allow_smem(ready[aligned], reinterpret_cast<const void*>(kernel), smem)) return rc;
-        return ss::launch(kernel, grid, kThreads, smem, 0, true, st, a);
+        return ss::launch(kernel, a.row_tiles * a.col_tiles, kThreads, smem, 0, true, st, a);
     });
 }
 
@@ -302,7 +314,7 @@ int ss_mx_quantize(const ss_mx_quant* q, ss_stream_t stream) {
     if (q->rows == 0 || q->cols == 0) return SS_OK;
     if (!q->data != !q->scales || !q->t_data != !q->t_scales || (!q->data && !q->t_data)) return SS_EINVAL;
     if (!q->x || q->stride < q->cols) return SS_EINVAL;
-    if (q->stride > INT64_MAX / 8 / q->rows || tiles(q->rows) * tiles(q->cols) > INT32_MAX) return SS_EOVERFLOW;
+    if (q->stride > INT64_MAX / 8 / q->rows || 4 * tiles(q->rows) * tiles(q->cols) > INT32_MAX) return SS_EOVERFLOW;
     if (!ss::aligned(q->x, (uintptr_t)q->elem_bytes) || !ss::aligned(q->data, 16) || !ss::aligned(q->scales, 16) ||
         !ss::aligned(q->t_data, 16) || !ss::aligned(q->t_scales, 16) || !ss::aligned(q->rng, 8))
         return SS_EALIGN;
@@ -325,7 +337,7 @@ int ss_mx_dequantize(int64_t rows, int64_t cols, int format, const void* data, c
     if (rows > kMaxSize || cols > kMaxSize) return SS_EOVERFLOW;
     if (rows == 0 || cols == 0) return SS_OK;
     if (!data || !scales || !out || out_stride < cols) return SS_EINVAL;
-    if (out_stride > INT64_MAX / 8 / rows || tiles(rows) * tiles(cols) > INT32_MAX) return SS_EOVERFLOW;
+    if (out_stride > INT64_MAX / 8 / rows || 4 * tiles(rows) * tiles(cols) > INT32_MAX) return SS_EOVERFLOW;
     if (!ss::aligned(out, (uintptr_t)elem_bytes) || !ss::aligned(data, 16) || !ss::aligned(scales, 16)) return SS_EALIGN;
     const DequantArgs a = {rows, cols, tiles(cols), static_cast<const unsigned char*>(data),
                            static_cast<const unsigned char*>(scales), out, out_stride};
@@ -333,8 +345,11 @@ int ss_mx_dequantize(int64_t rows, int64_t cols, int format, const void* data, c
     return with_flags(format == SS_MXFP4, elem_bytes == 4, [&](auto four, auto wide) {
         constexpr int F = decltype(four)::value ? SS_MXFP4 : SS_MXFP8;
         using T = std::conditional_t<decltype(wide)::value, float, uint16_t>;
-        return ss::launch(aligned ? dequantize_kernel<T, F, true> : dequantize_kernel<T, F, false>,
-                          tiles(rows) * a.col_tiles, kThreads, 0, 0, true, reinterpret_cast<cudaStream_t>(stream), a);
+        const bool few = few_tiles(tiles(rows), a.col_tiles);
+        const auto kernel = few ? (aligned ? dequantize_kernel<T, F, kFewRounds, true> : dequantize_kernel<T, F, kFewRounds, false>)
+                                : (aligned ? dequantize_kernel<T, F, kRounds, true> : dequantize_kernel<T, F, kRounds, false>);
+        return ss::launch(kernel, parts(rows, few ? kFewRounds : kRounds) * a.col_tiles, kThreads, 0, 0, true,
+                          reinterpret_cast<cudaStream_t>(stream), a);
     });
 }
 

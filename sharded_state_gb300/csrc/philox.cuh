@@ -15,30 +15,32 @@
 namespace ss {
 
 struct Philox {
-    uint32_t key0, key1, off0, off1;
+    uint32_t key0[10], key1[10];  // of every round: a thread's calls share them
+    uint32_t off0, off1;
 
     Philox() = default;
 
     // rng: {seed, offset} on the device.
     __device__ __forceinline__ explicit Philox(const int64_t* rng) {
         const uint64_t seed = (uint64_t)rng[0], offset = (uint64_t)rng[1];
-        key0 = (uint32_t)seed, key1 = (uint32_t)(seed >> 32);
+#pragma unroll
+        for (int i = 0; i < 10; ++i) {
+            key0[i] = (uint32_t)seed + i * 0x9E3779B9u;
+            key1[i] = (uint32_t)(seed >> 32) + i * 0xBB67AE85u;
+        }
         off0 = (uint32_t)offset, off1 = (uint32_t)(offset >> 32);
     }
 
     // The 128 bits of columns 8 group .. 8 group + 7 of a row, lowest first.
     __device__ __forceinline__ uint4 operator()(uint32_t row, uint32_t group) const {
-        uint32_t a = group, b = row, c = off0, d = off1, k0 = key0, k1 = key1;
+        uint32_t a = group, b = row, c = off0, d = off1;
 #pragma unroll
         for (int i = 0; i < 10; ++i) {
             const uint64_t p = (uint64_t)0xD2511F53u * a, q = (uint64_t)0xCD9E8D57u * c;
-            const uint32_t ph = (uint32_t)(p >> 32), qh = (uint32_t)(q >> 32);
-            a = qh ^ b ^ k0;
-            c = ph ^ d ^ k1;
+            a = (uint32_t)(q >> 32) ^ b ^ key0[i];
+            c = (uint32_t)(p >> 32) ^ d ^ key1[i];
             b = (uint32_t)q;
             d = (uint32_t)p;
-            k0 += 0x9E3779B9u;
-            k1 += 0xBB67AE85u;
         }
         return make_uint4(a, b, c, d);
     }
