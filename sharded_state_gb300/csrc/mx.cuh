@@ -131,55 +131,54 @@ __device__ __forceinline__ int64_t mx_scale_at(int64_t r, int64_t b, int64_t til
     return ((r >> 7) * tiles + (b >> 2)) * kMxTileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
 }
 
-// The lower or upper 16 random bits of a word as mx_encode_random takes them: where they
-// belong behind a code that stands in the top bits, and what the codes begin with in fp32
-// taken off (for both formats 12 or 192 of 16 or 256, so 4 or 64 to be added).
+// The lower or upper 16 random bits of a word as mx_encode_random takes them: in the
+// middle bytes, behind a code in the top one, with what the codes begin with in fp32
+// taken off there (252 or 192 of 256, so 4 or 64 to be added).
 template <int FORMAT>
 __device__ __forceinline__ uint32_t mx_random(uint32_t word, bool upper) {
-    constexpr int kAt = 16 - Mx<FORMAT>::kBits;
-    return ((upper ? word >> (16 - kAt) : word << kAt) & (0xFFFFu << kAt)) | 0x40000000u;
+    return __byte_perm(word, Mx<FORMAT>::kBits == 4 ? 0x04000000u : 0x40000000u, upper ? 0x7324 : 0x7104);
 }
 
 // 8 elements times `inverse`, rounded down or up in magnitude: up where what is cut off
 // and the element's 16 random bits / 2^16 make one step.  In the format's normal range
 // the codes are the leading bits of the fp32 magnitude, and the random bits, added right
 // behind them, carry into them just then; below it the lowest normal number is added
-// first, which puts every element on the same steps, and half of the sum has the leading
-// bits that continue the codes (towards zero, so that nothing is rounded but by the cut).
-// The codes are shifted out of the top of each sum into the result, the last one first;
-// one past the largest is put right for all of them at once.  9 instructions an element.
+// first, which puts every element on the same steps, and half of the sum, which is more
+// than the element there and no more above, has the leading bits that continue the codes
+// (towards zero, so that nothing is rounded but by the cut).  The sums' top bytes are the
+// codes; one past the largest is put right for all of them at once.
 template <int FORMAT>
 __device__ __forceinline__ typename Mx<FORMAT>::Word mx_encode_random(const float (&f)[8], float inverse,
                                                                       const uint32_t (&random)[8]) {
     using M = Mx<FORMAT>;
-    constexpr int kCut = 23 - M::kFraction, kPer = 32 / M::kBits;  // elements a word
-    static_assert(((127 + M::kLowest - 1) << M::kFraction) % (1 << M::kBits) == (M::kBits == 4 ? 12 : 192), "mx_random");
+    constexpr int kCut = 23 - M::kFraction;
+    static_assert(((127 + M::kLowest - 1) << M::kFraction) % 256 == (M::kBits == 4 ? 252 : 192), "mx_random");
     const float least = __uint_as_float((uint32_t)(127 + M::kLowest) << 23);
-    uint32_t w[8 / kPer], sign[8];
+    uint32_t sum[8], sign[8];
 #pragma unroll
-    for (int i = 7; i >= 0; --i) {
+    for (int i = 0; i < 8; ++i) {
         const float v = fabsf(f[i]) * inverse;
-        float t = v;
-        if (v < least) t = __fmaf_rz(v, 0.5f, 0.5f * least);
-        const uint32_t sum = __float_as_uint(t) * (1u << (32 - M::kBits - kCut)) + random[i];
-        w[i / kPer] = i % kPer == kPer - 1 ? sum >> (32 - M::kBits) : __funnelshift_l(sum, w[i / kPer], M::kBits);
+        const float t = fmaxf(v, __fmaf_rz(v, 0.5f, 0.5f * least));
+        sum[i] = __float_as_uint(t) * (1u << (24 - kCut)) + random[i];
         sign[i] = __float_as_uint(f[i]);
     }
-    // the signs' bytes, four at a time
-    auto top = [&](int i, int step) {
-        return __byte_perm(__byte_perm(sign[i], sign[i + step], 0x0073), __byte_perm(sign[i + 2 * step], sign[i + 3 * step], 0x0073),
-                           0x5410) & 0x80808080u;
+    // top bytes, four at a time
+    auto top = [](const uint32_t (&x)[8], int i, int step) {
+        return __byte_perm(__byte_perm(x[i], x[i + step], 0x0073), __byte_perm(x[i + 2 * step], x[i + 3 * step], 0x0073),
+                           0x5410);
     };
     typename M::Word out;
     if constexpr (M::kBits == 4) {
-        out = (w[0] - (w[0] >> 3 & 0x11111111u)) | top(0, 2) >> 4 | top(1, 2);  // 8 -> 7
+        const uint32_t w = top(sum, 0, 2) + top(sum, 1, 2) * 16u;
+        out = (w - (w >> 3 & 0x11111111u)) | (top(sign, 0, 2) >> 4 & 0x08080808u) | (top(sign, 1, 2) & 0x80808080u);  // 8 -> 7
     } else {
+        uint32_t w[2] = {top(sum, 0, 1), top(sum, 4, 1)};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // 0x7F, 0x80 -> 0x7E
             const uint32_t over = (((w[i] + 0x01010101u) | w[i]) & 0x80808080u) >> 7;
             w[i] = (w[i] & ~(over * 0xFFu)) | over * 0x7Eu;
         }
-        out = make_uint2(w[0] | top(0, 1), w[1] | top(4, 1));
+        out = make_uint2(w[0] | (top(sign, 0, 1) & 0x80808080u), w[1] | (top(sign, 4, 1) & 0x80808080u));
     }
     return out;
 }

@@ -15,20 +15,19 @@
 namespace ss {
 
 struct Philox {
-    uint32_t key0[10], key1[10];  // of every round: a thread's calls share them
-    uint32_t off0, off1;
+    uint32_t key0, key1, off0, off1;
 
     Philox() = default;
 
-    // rng: {seed, offset} on the device.
+    // rng: {seed, offset} on the device.  The whole warp: what it reads is one value for
+    // all lanes, which a reduction over them puts in uniform registers, and the rounds'
+    // keys are formed there.
     __device__ __forceinline__ explicit Philox(const int64_t* rng) {
         const uint64_t seed = (uint64_t)rng[0], offset = (uint64_t)rng[1];
-#pragma unroll
-        for (int i = 0; i < 10; ++i) {
-            key0[i] = (uint32_t)seed + i * 0x9E3779B9u;
-            key1[i] = (uint32_t)(seed >> 32) + i * 0xBB67AE85u;
-        }
-        off0 = (uint32_t)offset, off1 = (uint32_t)(offset >> 32);
+        key0 = __reduce_or_sync(0xFFFFFFFFu, (uint32_t)seed);
+        key1 = __reduce_or_sync(0xFFFFFFFFu, (uint32_t)(seed >> 32));
+        off0 = __reduce_or_sync(0xFFFFFFFFu, (uint32_t)offset);
+        off1 = __reduce_or_sync(0xFFFFFFFFu, (uint32_t)(offset >> 32));
     }
 
     // The 128 bits of columns 8 group .. 8 group + 7 of a row, lowest first.
@@ -37,8 +36,8 @@ struct Philox {
 #pragma unroll
         for (int i = 0; i < 10; ++i) {
             const uint64_t p = (uint64_t)0xD2511F53u * a, q = (uint64_t)0xCD9E8D57u * c;
-            a = (uint32_t)(q >> 32) ^ b ^ key0[i];
-            c = (uint32_t)(p >> 32) ^ d ^ key1[i];
+            a = (uint32_t)(q >> 32) ^ b ^ (key0 + i * 0x9E3779B9u);
+            c = (uint32_t)(p >> 32) ^ d ^ (key1 + i * 0xBB67AE85u);
             b = (uint32_t)q;
             d = (uint32_t)p;
         }
