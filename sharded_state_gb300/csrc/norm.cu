@@ -54,12 +54,56 @@ struct DropArgs {
     const int64_t* rng;
     uint32_t drop;
     float scale;
-    int64_t step_rows;  // the grid's threads, as rows and groups
+    int64_t step_rows;  // the grid's threads (or warps), as rows and groups (or pieces)
     int step_groups;
     int64_t x_step, out_step;  // and as elements
 };
 
-// Threads take groups of 8 in the order of the matrix, as far apart as the grid has
+// A warp takes pieces of kDropPiece groups of a row, two a lane: a place in the matrix is
+// worked out once for both, and what the generator makes of the row alone once for all.
+constexpr int kDropPiece = 64;
+
+template <class T, bool ALIGNED>
+__global__ void __launch_bounds__(kDropThreads) dropout_rows_kernel(const __grid_constant__ DropArgs a) {
+    launch_after();
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
+    const int pieces = (a.groups + kDropPiece - 1) / kDropPiece;
+    const int64_t first = (int64_t)blockIdx.x * (kDropThreads / 32) + warp;
+    int64_t row = first / pieces;
+    int piece = (int)(first - row * pieces);
+    wait_before();
+    const ss::Philox philox(a.rng);
+    for (; row < a.rows; row += a.step_rows) {
+        const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+        T* out = static_cast<T*>(a.out) + row * a.out_stride;
+        const int g0 = piece * kDropPiece + lane;
+        Vec8<T> v[2];
+        uint4 tail[2] = {};
+        auto run = [&](int g) {  // of the columns from this group on, as far as two groups go
+            return Run(g + 2 < a.groups ? 16 : (a.groups - 1 - g) * 8 + a.last, lane == 0, lane == 31);
+        };
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int g = g0 + 32 * i;
+            v[i].template fetch<ALIGNED>(x + 8 * (int64_t)g, run(g), tail[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int g = g0 + 32 * i;
+            v[i].template settle<ALIGNED>(x + 8 * (int64_t)g, run(g), tail[i]);
+            float f[8];
+            v[i].get(f);
+            ss::drop8(f, philox((uint32_t)row, (uint32_t)g), a.drop, a.scale);
+            v[i].set(f);
+            v[i].template store<ALIGNED>(out + 8 * (int64_t)g, run(g));
+        }
+        piece += a.step_groups;
+        if (piece >= pieces) piece -= pieces, ++row;
+    }
+}
+
+// Narrow matrices, whose rows would leave lanes of such pieces idle: threads take groups of
+// 8 in the order of the matrix, as far apart as the grid has
 // threads; places in it are carried on by adding (a row's index times its stride for
 // each group cost as much as the mask: 181 instructions a group for 100).
 template <class T, bool ALIGNED>
@@ -192,6 +236,8 @@ __global__ void __launch_bounds__(VECS > 2 ? 512 : 256) norm_kernel(const __grid
             w[i].template fetch<ALIGNED>(weight + col, run(col), w_tail[i]);
         }
     }
+    ss::Philox philox;
+    if (a.drop) philox = ss::Philox(a.rng);
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
@@ -200,7 +246,7 @@ __global__ void __launch_bounds__(VECS > 2 ? 512 : 256) norm_kernel(const __grid
         x[i].template settle<ALIGNED>(x_row + col, run(col), x_tail[i]);
         if (a.drop || a.residual) {
             x[i].get(f);
-            if (a.drop) ss::drop8(f, ss::Philox(a.rng)((uint32_t)row, (uint32_t)(col >> 3)), a.drop, a.scale);
+            if (a.drop) ss::drop8(f, philox((uint32_t)row, (uint32_t)(col >> 3)), a.drop, a.scale);
             if (a.residual) {
                 float q[8];
                 r[i].template settle<ALIGNED>(r_row + col, run(col), r_tail[i]);
@@ -307,6 +353,8 @@ norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
             w[i].template load<ALIGNED>(static_cast<const T*>(a.weight) + col, Run(a.cols - col, lane == 0, lane == 31));
         }
     }
+    ss::Philox philox;
+    if (a.drop && a.d_x) philox = ss::Philox(a.rng);
     auto weight = [&](int i, float (&g)[8]) {
         if (!kAhead) {
             const int col = 8 * (mine + i * a.team);
@@ -353,7 +401,7 @@ norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
                 v.template store<ALIGNED>(static_cast<T*>(a.d_h) + row * a.d_h_stride + col, run(row, col));
             }
             if (a.d_x) {
-                if (a.drop) ss::drop8(f, ss::Philox(a.rng)((uint32_t)row, (uint32_t)(col >> 3)), a.drop, a.scale);
+                if (a.drop) ss::drop8(f, philox((uint32_t)row, (uint32_t)(col >> 3)), a.drop, a.scale);
                 v.set(f);
                 v.template store<ALIGNED>(static_cast<T*>(a.d_x) + row * a.d_x_stride + col, run(row, col));
             }
@@ -522,14 +570,25 @@ int ss_dropout(int64_t rows, int64_t cols, int elem_bytes, const void* x, int64_
     a.x = x, a.x_stride = x_stride, a.out = out, a.out_stride = out_stride, a.rng = rng;
     const int64_t total = a.rows * a.groups;
     const int64_t grid = std::min((total + kDropThreads - 1) / kDropThreads, (int64_t)ss::num_sms() * 8);
+    const bool al = rows_on_16(elem_bytes, {{x, x_stride}, {out, out_stride}});
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t pieces = (a.groups + kDropPiece - 1) / kDropPiece;
+    if (4 * (int64_t)a.groups >= 3 * kDropPiece * pieces) {  // three lanes of four have work
+        constexpr int64_t kWarps = kDropThreads / 32;
+        const int64_t ctas = std::min((a.rows * pieces + kWarps - 1) / kWarps, (int64_t)ss::num_sms() * 8);
+        a.step_rows = ctas * kWarps / pieces;
+        a.step_groups = (int)(ctas * kWarps % pieces);
+        const auto kernel = elem_bytes == 2 ? (al ? dropout_rows_kernel<uint16_t, true> : dropout_rows_kernel<uint16_t, false>)
+                                            : (al ? dropout_rows_kernel<float, true> : dropout_rows_kernel<float, false>);
+        return ss::launch(kernel, ctas, kDropThreads, 0, 0, true, st, a);
+    }
     a.step_rows = grid * kDropThreads / a.groups;
     a.step_groups = (int)(grid * kDropThreads % a.groups);
     a.x_step = a.step_rows * x_stride + 8 * (int64_t)a.step_groups;
     a.out_step = a.step_rows * out_stride + 8 * (int64_t)a.step_groups;
-    const bool al = rows_on_16(elem_bytes, {{x, x_stride}, {out, out_stride}});
     const auto kernel = elem_bytes == 2 ? (al ? dropout_kernel<uint16_t, true> : dropout_kernel<uint16_t, false>)
                                         : (al ? dropout_kernel<float, true> : dropout_kernel<float, false>);
-    return ss::launch(kernel, grid, kDropThreads, 0, 0, true, reinterpret_cast<cudaStream_t>(stream), a);
+    return ss::launch(kernel, grid, kDropThreads, 0, 0, true, st, a);
 }
 
 int ss_rms_norm(const ss_norm* n, ss_stream_t stream) {

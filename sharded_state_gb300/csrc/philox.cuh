@@ -19,15 +19,11 @@ struct Philox {
 
     Philox() = default;
 
-    // rng: {seed, offset} on the device.  The whole warp: what it reads is one value for
-    // all lanes, which a reduction over them puts in uniform registers, and the rounds'
-    // keys are formed there.
+    // rng: {seed, offset} on the device.
     __device__ __forceinline__ explicit Philox(const int64_t* rng) {
         const uint64_t seed = (uint64_t)rng[0], offset = (uint64_t)rng[1];
-        key0 = __reduce_or_sync(0xFFFFFFFFu, (uint32_t)seed);
-        key1 = __reduce_or_sync(0xFFFFFFFFu, (uint32_t)(seed >> 32));
-        off0 = __reduce_or_sync(0xFFFFFFFFu, (uint32_t)offset);
-        off1 = __reduce_or_sync(0xFFFFFFFFu, (uint32_t)(offset >> 32));
+        key0 = (uint32_t)seed, key1 = (uint32_t)(seed >> 32);
+        off0 = (uint32_t)offset, off1 = (uint32_t)(offset >> 32);
     }
 
     // The 128 bits of columns 8 group .. 8 group + 7 of a row, lowest first.
