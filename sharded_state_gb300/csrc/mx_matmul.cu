@@ -599,16 +599,22 @@ int launch_pair(const ss_mx_product* p, int64_t k_blocks, cudaStream_t st) {
     return ss::launch(kernel, 2 * std::min(m_tiles * n_tiles, pairs), kPairThreads, smem, 0, true, st, maps, g);
 }
 
-// CTAs that share k, for which the fullest SM has the fewest k blocks to go through (as
-// far as the SMs hold the CTAs at once); of equals the fewest.
-int choose_splits(int64_t tiles, int64_t k_blocks, int smem) {
-    const int64_t sms = ss::num_sms(), held = sms * (smem <= 112 * 1024 ? 2 : 1);
+// CTAs that share k: as many as make the time least, counted in k blocks of a CTA (0.19
+// us), of which a second CTA on an SM costs 0.7, and a share's join as much as a
+// forty-fifth of a block for each column.  All of them are held at once; clusters of 7
+// and 8 waste SMs of a GPC and are taken where that does not matter.  One token, 2048 x
+// 2048: 4.0 us alone, 3.6 with 4, 4.3 with 8; 11008 x 4096: 6.3 alone, 5.6 with 3, 8.7
+// with 4; 128 tokens, 2048 x 2048: 6.2 alone, 5.6 with 2, 7.1 with 4, 17 with 8.
+int choose_splits(int64_t tiles, int64_t k_blocks, int few, int smem) {
+    const int64_t sms = ss::num_sms(), each = smem <= 112 * 1024 ? 2 : 1;  // CTAs an SM holds
     int best = 1;
-    int64_t least = INT64_MAX;
+    double least = INFINITY;
     for (int s = 1; s <= 8 && s <= k_blocks; ++s) {
-        if (s > 1 && tiles * s > held) break;
-        const int64_t blocks = div_up(tiles * s, sms) * div_up(k_blocks, s) + 1;  // 1: what a CTA costs beside
-        if (blocks < least) best = s, least = blocks;
+        if (s > 1 && tiles * s * (s > 6 ? 2 : 1) > sms * each) continue;
+        const int64_t n = div_up(tiles * s, sms);
+        const double load = (double)(n / each) * (each == 2 ? 1.7 : 1.0) + (double)(n % each);
+        const double cost = load * (double)div_up(k_blocks, s) + (s - 1) * few / 45.0;
+        if (cost < least) best = s, least = cost;
     }
     return best;
 }
@@ -624,7 +630,7 @@ int launch_few(const ss_mx_product* p, int64_t k_blocks, bool swap, cudaStream_t
     Maps maps;
     if (int rc = make_maps(&maps, a, b, p->K, FORMAT, FEW)) return rc;
     const int64_t row_tiles = div_up(a.rows, kHalf), few_tiles = div_up(b.rows, FEW), tiles = row_tiles * few_tiles;
-    const int splits = choose_splits(tiles, k_blocks, smem);
+    const int splits = choose_splits(tiles, k_blocks, FEW, smem);
     const FewArgs g = {a.rows, b.rows, swap ? p->out_stride : 1, swap ? 1 : p->out_stride, (int)row_tiles, (int)k_blocks,
                        splits, p->out, p->elem_bytes,
                        ss::aligned(p->out, 4 * p->elem_bytes) && p->out_stride % 4 == 0};
