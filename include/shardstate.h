@@ -592,7 +592,8 @@ typedef struct {
     size_t workspace_bytes;
 } ss_norm_grad;
 
-/* Bytes of workspace ss_rms_norm_backward takes on the current device. */
+/* Bytes of workspace ss_rms_norm_backward takes on the current device.  Calls that
+ * may overlap on the GPU need one each. */
 int ss_rms_norm_workspace(int64_t rows, int64_t cols, size_t* bytes_out);
 
 /* At least one output.  Errors: as ss_rms_norm. */

@@ -221,6 +221,32 @@ def test_quantise_offsets_past_32_bits(ss):
 
 
 @gpu
+@pytest.mark.parametrize("format,dtype,extra", [(0, BF, 0), (1, BF, 5), (0, F32, 3), (1, F32, 4)])
+def test_a_large_matrix_is_its_parts(ss, format, dtype, extra):
+    """A matrix large enough for whole tiles a CTA gives the bits of its pieces of 384 rows, which are not."""
+    rows, cols = 10007, 2101
+    gen = torch.Generator("cuda").manual_seed(3)
+    x = randn(rows, cols, dtype, gen, extra=extra)
+    q = buffers(ss, rows, cols, format)
+    ss.ss_mx_quantize(x, format, *q)
+    out, buf = matrix(rows, cols, dtype, extra, 0, fill=5.0)
+    ss.ss_mx_dequantize(*q, format, out)
+    assert outside_kept(buf, out, 5.0)
+    data, scales = ss.ss_mx_bytes(rows, cols, format)
+    pitch, tile = data // rows, scales // (-(-rows // 128))
+    for r0 in range(0, rows, 384):
+        n = min(384, rows - r0)
+        p = buffers(ss, n, cols, format)
+        ss.ss_mx_quantize(x[r0:r0 + n], format, *p)
+        assert torch.equal(q[0][r0 * pitch:(r0 + n) * pitch], p[0][:n * pitch])
+        t0, tiles = r0 // 128 * tile, -(-n // 128) * tile
+        assert torch.equal(q[1][t0:t0 + tiles], p[1][:tiles])
+        back = torch.empty(n, cols, dtype=dtype, device="cuda")
+        ss.ss_mx_dequantize(*p, format, back)
+        assert torch.equal(back, out[r0:r0 + n])
+
+
+@gpu
 def test_empty_matrices(ss):
     x, none = torch.empty(0, 64, device="cuda"), torch.empty(0, dtype=torch.uint8, device="cuda")
     n = ss.ss_launch_count()
@@ -258,7 +284,8 @@ def check_product(out, a, b):
 
 SIZES = [(1, 1, 1), (1, 128, 32), (1, 11008, 4096), (16, 256, 128), (17, 33, 65), (3, 777, 1001), (33, 130, 257),
          (64, 500, 384), (65, 129, 129), (130, 129, 640), (200, 40, 1024), (1000, 7, 300), (256, 256, 2048),
-         (1021, 777, 1001), (5, 300, 20000)]
+         (1021, 777, 1001), (5, 300, 20000), (2003, 72, 2688), (72, 1501, 520), (300, 64, 1100), (128, 2048, 2048),
+         (40, 515, 5632), (1, 4099, 1100)]
 
 
 @gpu

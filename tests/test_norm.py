@@ -404,6 +404,26 @@ def test_the_same_bits_again(ss):
 
 
 @gpu
+def test_two_calls_at_once(ss):
+    """Calls on two streams, each with its own workspace, give what they give alone."""
+    a, b = Norm(ss, 900, 2048, BF, p=0.1, seed=1), Norm(ss, 1100, 1000, BF, p=0.2, seed=2)
+    want = [(n.backward(ss).dh.clone(), n.dw.clone()) for n in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    jobs = []
+    for n in (a, b):
+        ws = torch.empty(ss.ss_rms_norm_workspace(n.rows, n.cols), dtype=torch.uint8, device="cuda")
+        jobs.append((n, ws, torch.empty_like(n.dh), torch.empty_like(n.weight)))
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for stream, (n, ws, dh, dw) in zip(streams, jobs):
+            ss.ss_rms_norm_backward(n.dy, n.h, n.weight, n.rstd, dh, ws, d_sum=n.ds, d_weight=dw, dropout=n.p, rng=n.rng,
+                                    stream=stream)
+    torch.cuda.synchronize()
+    for (n, ws, dh, dw), (want_dh, want_dw) in zip(jobs, want):
+        assert torch.equal(dh, want_dh) and torch.equal(dw, want_dw[:n.cols])
+
+
+@gpu
 def test_refusals_of_the_binding(ss):
     x, w = torch.zeros(4, 64, device="cuda"), torch.ones(64, device="cuda")
     rng, out = rng_of(), torch.zeros(4, 64, device="cuda")
