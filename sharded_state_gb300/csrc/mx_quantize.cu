@@ -1,10 +1,10 @@
 // mx_quantize.cu -- matrices to microscaled floats and back (formats and layout:
 // mx.cuh).
 //
-// A CTA takes 128 x 128 elements, which are one tile of scales whichever way the
-// blocks run.  The blocks along the rows are formed on the way in, by 4 neighbouring
-// lanes; for the transpose the tile is kept in shared memory and each thread takes
-// two columns of 32 rows.  So one read of the matrix serves both, and the memory is
+// A CTA takes 64 rows of 128 columns, half a tile of scales whichever way the blocks
+// run.  The blocks along the rows are formed on the way in, by 4 neighbouring lanes; for
+// the transpose the elements are kept in shared memory and each thread takes two columns
+// of 32 rows.  So one read of the matrix serves both, and the memory is
 // what bounds it: 2 bytes read and 0.53 (MXFP4) or 1.03 (MXFP8) written for each
 // element and orientation.
 #include <cuda_runtime.h>
@@ -27,9 +27,11 @@ using ss::Run;
 using ss::Vec8;
 using ss::wait_before;
 
-constexpr int kThreads = 256;
-constexpr int kRounds = kMxTile * kMxTile / 8 / kThreads;  // loads of 8 elements a thread for a whole tile
-constexpr int kFewRounds = 2;  // without the transpose, where whole tiles would leave SMs idle
+constexpr int kThreads = 128;
+constexpr int kLines = kThreads / 16;  // rows loaded at a time: 16 lanes take 128 columns
+constexpr int kRounds = 8;             // loads of 8 elements a thread
+constexpr int kFewRounds = 2;          // without the transpose, where 64 rows a CTA would leave SMs idle
+constexpr int kRows = kLines * kRounds, kBlocks = kRows / 32;
 
 struct QuantArgs {
     int64_t rows, cols;
@@ -42,7 +44,7 @@ struct QuantArgs {
 
 template <class T, bool RANDOM>
 constexpr int tile_bytes() {
-    return kMxTile * kMxTile * (int)(sizeof(T) + (RANDOM ? 2 : 0));
+    return kRows * kMxTile * (int)(sizeof(T) + (RANDOM ? 2 : 0));
 }
 
 // Bits of the largest magnitude of 8 elements.
@@ -67,12 +69,12 @@ __device__ __forceinline__ typename Mx<FORMAT>::Word encode(const float (&f)[8],
                   : ss::mx_encode<FORMAT>(f, ss::mx_inverse(byte));
 }
 
-// Rows of a tile in shared memory, in words, those of every 32 rows turned by 8 words
-// more: threads that read 8 neighbouring columns of 4 blocks of rows at once meet all
-// banks.
+// Rows of a tile in shared memory, in words, those of every 32 rows turned by 16 words
+// more: threads that read 16 neighbouring pairs of columns of 2 blocks of rows at once
+// meet all banks.
 template <int WORDS>
 __device__ __forceinline__ int turned(int row, int word) {
-    return row * WORDS + ((word + 8 * (row >> 5)) & (WORDS - 1));
+    return row * WORDS + ((word + 16 * (row >> 5)) & (WORDS - 1));
 }
 
 // Two columns of 32 rows out of the tile, as two's 16-bit halves or as floats.
@@ -116,35 +118,35 @@ struct Columns<float> {
     __device__ __forceinline__ float get(int j, int k) const { return w[k][j]; }
 };
 
-// ROUNDS x 16 rows of 128 columns: whole tiles for the transpose.
+// ROUNDS x 8 rows of 128 columns: kRows for the transpose.
 template <class T, int FORMAT, int ROUNDS, bool TRANSPOSE, bool RANDOM, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && ALIGNED ? (RANDOM ? 5 : 6) : 4) quantize_kernel(const __grid_constant__ QuantArgs a) {
     using M = Mx<FORMAT>;
     using Word = typename M::Word;
     constexpr int kWords = kMxTile * (int)sizeof(T) / 4;  // of a row of the tile
-    extern __shared__ __align__(16) uint32_t tile[];      // [128][kWords], then the random bits, [128][64]
-    uint32_t* random = tile + kMxTile * kWords;
+    extern __shared__ __align__(16) uint32_t tile[];      // [kRows][kWords], then the random bits, [kRows][64]
+    uint32_t* random = tile + kRows * kWords;
     launch_after();
     const int64_t part = blockIdx.x / a.col_tiles, tc = blockIdx.x - part * a.col_tiles;
-    const int64_t row0 = part * (16 * ROUNDS), col0 = tc * kMxTile, tr = row0 / kMxTile;
+    const int64_t row0 = part * (kLines * ROUNDS), col0 = tc * kMxTile;
     const int line = threadIdx.x >> 4, c8 = threadIdx.x & 15;
     wait_before();
     const T* x = static_cast<const T*>(a.x) + (row0 + line) * a.stride + col0 + 8 * c8;
-    const int rows = (int)min(a.rows - row0, (int64_t)(16 * ROUNDS)), left = (int)min(a.cols - col0 - 8 * c8, (int64_t)16);
+    const int rows = (int)min(a.rows - row0, (int64_t)(kLines * ROUNDS)), left = (int)min(a.cols - col0 - 8 * c8, (int64_t)16);
     Vec8<T> v[ROUNDS];
     uint4 tail[ROUNDS] = {};
 #pragma unroll
     for (int i = 0; i < ROUNDS; ++i)
-        v[i].template fetch<ALIGNED>(x + 16 * i * a.stride, Run(16 * i + line < rows ? left : 0, c8 == 0, c8 == 15), tail[i]);
+        v[i].template fetch<ALIGNED>(x + kLines * i * a.stride, Run(kLines * i + line < rows ? left : 0, c8 == 0, c8 == 15), tail[i]);
     const int64_t pitch = a.col_tiles * M::kTileRow;
     unsigned char* out = a.data + (row0 + line) * pitch + tc * M::kTileRow + c8 * (int)sizeof(Word);
     unsigned char* scales = a.scales + ss::mx_scale_at(row0, 4 * tc, a.col_tiles) + 16 * line;
     const ss::Philox philox = RANDOM ? ss::Philox(a.rng) : ss::Philox();
 #pragma unroll
-    for (int i = 0; i < ROUNDS; ++i, out += 16 * pitch) {
-        const int r = 16 * i + line;
-        if (!TRANSPOSE && 16 * i + (line & ~1) >= rows) break;  // both rows of the warp are behind the last
-        v[i].template settle<ALIGNED>(x + 16 * i * a.stride, Run(r < rows ? left : 0, c8 == 0, c8 == 15), tail[i]);
+    for (int i = 0; i < ROUNDS; ++i, out += kLines * pitch) {
+        const int r = kLines * i + line;
+        if (!TRANSPOSE && kLines * i + (line & ~1) >= rows) break;  // both rows of the warp are behind the last
+        v[i].template settle<ALIGNED>(x + kLines * i * a.stride, Run(r < rows ? left : 0, c8 == 0, c8 == 15), tail[i]);
         uint4 bits = make_uint4(0, 0, 0, 0);
         if (RANDOM) bits = philox((uint32_t)row0 + r, (uint32_t)tc * 16 + c8);
         if (TRANSPOSE) {
@@ -173,42 +175,51 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
 #pragma unroll
             for (int k = 0; k < 8; ++k) u[k] = ss::mx_random<FORMAT>(words[k >> 1], k & 1);
             *reinterpret_cast<Word*>(out) = encode<FORMAT, RANDOM>(f, byte, u);
-            if (c8 == 0) *reinterpret_cast<uint32_t*>(scales + 256 * (i & 1) + 4 * (i >> 1)) = four;
+            if (c8 == 0) *reinterpret_cast<uint32_t*>(scales + 16 * kLines * (i & 3) + 4 * (i >> 2)) = four;
         }
     }
     if (!TRANSPOSE) return;
     __syncthreads();
-    // 4 neighbouring threads write a row of the transpose: 64 or 128 bytes, and its 4 scales
-    const int pair = threadIdx.x >> 2, block = threadIdx.x & 3;
+    // 2 neighbouring threads write a row's 64 elements of the transpose, and their 2 scales
+    const int pair = threadIdx.x / kBlocks, block = threadIdx.x % kBlocks;
+    const int64_t block0 = part * kBlocks;  // of 32 along the transpose's rows
     Columns<T> c;
     c.load(tile, block, pair);
-    uint32_t top[2];
-    c.largest(top);
+    uint32_t byte[2];
+    c.largest(byte);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint32_t byte = ss::mx_scale<FORMAT>(top[j]);
-        uint32_t four = byte << (8 * block);
-        four |= __shfl_xor_sync(0xFFFFFFFFu, four, 1);
-        four |= __shfl_xor_sync(0xFFFFFFFFu, four, 2);
-        const int64_t row = col0 + 2 * pair + j;  // of the transpose
-        if (row >= a.cols) continue;
-        __align__(16) Word words[4];
+    for (int j = 0; j < 2; ++j) byte[j] = ss::mx_scale<FORMAT>(byte[j]);
+    __align__(16) Word words[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[8] = {};
+        if (RANDOM) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = random[turned<kMxTile / 2>(32 * block + 8 * i + k, pair)];
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
             float f[8];
-            uint32_t u[8] = {};
+            uint32_t u[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 f[k] = c.get(j, 8 * i + k);
-                if (RANDOM) u[k] = ss::mx_random<FORMAT>(random[turned<kMxTile / 2>(32 * block + 8 * i + k, pair)], j);
+                u[k] = RANDOM ? ss::mx_random<FORMAT>(w[k], j) : 0;
             }
-            words[i] = encode<FORMAT, RANDOM>(f, byte, u);
+            words[j][i] = encode<FORMAT, RANDOM>(f, byte[j], u);
         }
-        unsigned char* out = a.t_data + (row * a.row_tiles + tr) * M::kTileRow + block * (M::kTileRow / 4);
+    }
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(words) / 16; ++i)
-            reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(words)[i];
-        if (block == 0) *reinterpret_cast<uint32_t*>(a.t_scales + ss::mx_scale_at(row, 4 * tr, a.row_tiles)) = four;
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t two = byte[j] << (8 * block) | __shfl_xor_sync(0xFFFFFFFFu, byte[j], 1) << (8 * (block ^ 1));
+        const int64_t row = col0 + 2 * pair + j;  // of the transpose
+        if (row >= a.cols) continue;
+        unsigned char* out = a.t_data + row * a.row_tiles * M::kTileRow + (block0 + block) * (M::kTileRow / 4);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(words[j]) / 16; ++i)
+            reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(words[j])[i];
+        if (block == 0)
+            *reinterpret_cast<uint16_t*>(a.t_scales + ss::mx_scale_at(row, block0, a.row_tiles)) = (uint16_t)two;
     }
 }
 
@@ -226,8 +237,8 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_const
     launch_after();
     const int64_t part = blockIdx.x / a.col_tiles, tc = blockIdx.x - part * a.col_tiles;
     const int line = threadIdx.x >> 4, c8 = threadIdx.x & 15;
-    const int64_t row0 = part * (16 * ROUNDS), col = tc * kMxTile + 8 * c8;
-    const int rows = (int)min(a.rows - row0, (int64_t)(16 * ROUNDS)), left = (int)min(a.cols - col, (int64_t)16);
+    const int64_t row0 = part * (kLines * ROUNDS), col = tc * kMxTile + 8 * c8;
+    const int rows = (int)min(a.rows - row0, (int64_t)(kLines * ROUNDS)), left = (int)min(a.cols - col, (int64_t)16);
     const int64_t pitch = a.col_tiles * M::kTileRow;
     const unsigned char* data = a.data + (row0 + line) * pitch + tc * M::kTileRow + c8 * (int)sizeof(Word);
     const unsigned char* scales = a.scales + ss::mx_scale_at(row0, 4 * tc + (c8 >> 2), a.col_tiles) + 16 * line;
@@ -235,17 +246,17 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_const
     Word w[ROUNDS];
     unsigned char byte[ROUNDS];
 #pragma unroll
-    for (int i = 0; i < ROUNDS; ++i, data += 16 * pitch) {
+    for (int i = 0; i < ROUNDS; ++i, data += kLines * pitch) {
         w[i] = Word();
         byte[i] = 0;
-        if (16 * i + line >= rows || left <= 0) continue;
+        if (kLines * i + line >= rows || left <= 0) continue;
         w[i] = *reinterpret_cast<const Word*>(data);
-        byte[i] = scales[256 * (i & 1) + 4 * (i >> 1)];
+        byte[i] = scales[16 * kLines * (i & 3) + 4 * (i >> 2)];
     }
     T* out = static_cast<T*>(a.out) + (row0 + line) * a.stride + col;
 #pragma unroll
-    for (int i = 0; i < ROUNDS; ++i, out += 16 * a.stride) {
-        if (16 * i + (line & ~1) >= rows) break;  // both rows of the warp are behind the last
+    for (int i = 0; i < ROUNDS; ++i, out += kLines * a.stride) {
+        if (kLines * i + (line & ~1) >= rows) break;  // both rows of the warp are behind the last
         float f[8];
         M::decode(w[i], f);
         const float scale = ss::mx_value(byte[i]);
@@ -253,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_const
         for (int k = 0; k < 8; ++k) f[k] *= scale;
         Vec8<T> v;
         v.set(f);
-        v.template store<ALIGNED>(out, Run(16 * i + line < rows ? left : 0, c8 == 0, c8 == 15));
+        v.template store<ALIGNED>(out, Run(kLines * i + line < rows ? left : 0, c8 == 0, c8 == 15));
     }
 }
 
@@ -270,8 +281,8 @@ int with_flags(bool first, bool second, F&& f) {
     return first ? with_second(std::true_type()) : with_second(std::false_type());
 }
 
-// Parts of a matrix by rows where one CTA takes `rounds` x 16 of them.
-int64_t parts(int64_t rows, int rounds) { return (rows + 16 * rounds - 1) / (16 * rounds); }
+// Parts of a matrix by rows where one CTA takes `rounds` loads a thread of them.
+int64_t parts(int64_t rows, int rounds) { return (rows + kLines * rounds - 1) / (kLines * rounds); }
 
 // Whole tiles as soon as there are 8 for each SM; below, a quarter of one (fp32 2043 x 1001
 // in 8 bits 5.2 us as 128 tiles, 32000 x 2048 29 us as 4000).
@@ -291,7 +302,9 @@ int launch_quantize(const QuantArgs& a, bool transpose, bool random, bool aligne
         const auto kernel = aligned ? quantize_kernel<T, FORMAT, kRounds, TR, RA, true> : quantize_kernel<T, FORMAT, kRounds, TR, RA, false>;
         if (smem > 48 * 1024)
             if (int rc = ss::allow_smem(ready[aligned], reinterpret_cast<const void*>(kernel), smem)) return rc;
-        return ss::launch(kernel, a.row_tiles * a.col_tiles, kThreads, smem, 0, true, st, a);
+        // the transpose's rows go on to a multiple of 128: parts of whole tiles
+        const int64_t by_rows = TR ? a.row_tiles * (kMxTile / kRows) : parts(a.rows, kRounds);
+        return ss::launch(kernel, by_rows * a.col_tiles, kThreads, smem, 0, true, st, a);
     });
 }
 
@@ -314,7 +327,7 @@ int ss_mx_quantize(const ss_mx_quant* q, ss_stream_t stream) {
     if (q->rows == 0 || q->cols == 0) return SS_OK;
     if (!q->data != !q->scales || !q->t_data != !q->t_scales || (!q->data && !q->t_data)) return SS_EINVAL;
     if (!q->x || q->stride < q->cols) return SS_EINVAL;
-    if (q->stride > INT64_MAX / 8 / q->rows || 4 * tiles(q->rows) * tiles(q->cols) > INT32_MAX) return SS_EOVERFLOW;
+    if (q->stride > INT64_MAX / 8 / q->rows || 8 * tiles(q->rows) * tiles(q->cols) > INT32_MAX) return SS_EOVERFLOW;
     if (!ss::aligned(q->x, (uintptr_t)q->elem_bytes) || !ss::aligned(q->data, 16) || !ss::aligned(q->scales, 16) ||
         !ss::aligned(q->t_data, 16) || !ss::aligned(q->t_scales, 16) || !ss::aligned(q->rng, 8))
         return SS_EALIGN;
@@ -337,7 +350,7 @@ int ss_mx_dequantize(int64_t rows, int64_t cols, int format, const void* data, c
     if (rows > kMaxSize || cols > kMaxSize) return SS_EOVERFLOW;
     if (rows == 0 || cols == 0) return SS_OK;
     if (!data || !scales || !out || out_stride < cols) return SS_EINVAL;
-    if (out_stride > INT64_MAX / 8 / rows || 4 * tiles(rows) * tiles(cols) > INT32_MAX) return SS_EOVERFLOW;
+    if (out_stride > INT64_MAX / 8 / rows || 8 * tiles(rows) * tiles(cols) > INT32_MAX) return SS_EOVERFLOW;
     if (!ss::aligned(out, (uintptr_t)elem_bytes) || !ss::aligned(data, 16) || !ss::aligned(scales, 16)) return SS_EALIGN;
     const DequantArgs a = {rows, cols, tiles(cols), static_cast<const unsigned char*>(data),
                            static_cast<const unsigned char*>(scales), out, out_stride};

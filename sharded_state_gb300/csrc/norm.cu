@@ -611,11 +611,11 @@ int ss_rms_norm(const ss_norm* n, ss_stream_t stream) {
     a.rstd_out = n->rstd_out;
     a.mx_data = static_cast<unsigned char*>(n->mx_data), a.mx_scales = static_cast<unsigned char*>(n->mx_scales);
     a.mx_tiles = (int)((n->cols + ss::kMxTile - 1) / ss::kMxTile);
-    const Shape s = choose_shape(n->mx_data ? (int64_t)a.mx_tiles * (ss::kMxTile / 8) : (n->cols + 7) / 8);
-    a.team = s.team;
-    const int64_t teams = s.threads / s.team, grid = (n->rows + teams - 1) / teams;
     // the weight is one row: its own stride does not matter
     const bool al = rows_on_16(n->elem_bytes, {x, res, sum, out}) && ss::aligned(n->weight, 16);
+    const Shape s = choose_shape(n->mx_data ? (int64_t)a.mx_tiles * (ss::kMxTile / 8) : (n->cols + 7) / 8, al ? 2 : 1);
+    a.team = s.team;
+    const int64_t teams = s.threads / s.team, grid = (n->rows + teams - 1) / teams;
     return with_shape(n->elem_bytes, s.vecs, al, [&](auto t, auto v, auto aligned) {
         return ss::launch(norm_kernel<decltype(t), decltype(v)::value, decltype(aligned)::value>, grid, s.threads, 0, 0,
                           true, reinterpret_cast<cudaStream_t>(stream), a);
