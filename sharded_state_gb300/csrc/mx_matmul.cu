@@ -208,6 +208,17 @@ __device__ __forceinline__ void write_turned(const PairArgs& g, const uint32_t* 
 // Persistent pairs, each a tile of 256 x 256 at a time, its first CTA the upper 128 rows.
 // Warp 0 loads, warp 1 of the first CTA issues the products, warps 4.. read finished
 // accumulators while the next tile's products go to the other one.
+//
+// Bound by the tensor cores: a stage's four instructions take the pair 512 clocks in
+// either format, for which each CTA reads 35 KB.  The stages of a tile follow one another
+// at that pace, 700 clocks pass between tiles, 2400 before the first stage of a launch and
+// 4800 behind the last one; pairs without a tile in the last round are what is lost beside
+// that.  8192 x 11008 x 4096 in 4 bits 105 us, 7.0 PFLOP/s, where the clock under that
+// load would allow 8.9; 8192 x 5632 x 2048 37 us, 5.1; 2048 x 5632 x 2048 in 8 bits 21 us,
+// 2.2 (2.3 rounds of tiles take 3).  What made it: the second accumulator (180 -> 165 us),
+// operands in uniform registers (-> 118), accumulators given back without a release (->
+// 105).  Handing B on to a second pair in clusters of 4 was 5 % slower: L2 is busy 28 % of
+// the time, and the device holds 36 such clusters, 144 SMs of 152.
 template <int FORMAT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairArgs g) {
@@ -363,6 +374,11 @@ __host__ __device__ constexpr int few_smem(int format, int few) { return kFewSta
 // Columns of tensor memory: the accumulator's and the scales' 16.
 __host__ __device__ constexpr uint32_t few_tmem(int few) { return few <= 16 ? 32 : 2 * few; }
 
+// Few rows are bound by the weight's read, and by the chain of a launch: 1800 clocks until
+// the first stage is there, 500 a stage from then on, 1500 for the sums to be in shared
+// memory and 1500 for the join.  One token through 11008 x 4096 in 4 bits (24 MB): 5.5 us
+// behind the launch that quantises it; 1021 x 777 x 1001: 5.6 us.
+//
 // a: the operand of 128 rows a CTA; b: the other one.
 struct FewArgs {
     int64_t rows, few;           // of the two operands
@@ -642,8 +658,13 @@ template <int FORMAT>
 int launch_product(const ss_mx_product* p, cudaStream_t st) {
     const int64_t k_blocks = div_up(div_up(p->K, ss::kMxTile), scale_tiles(FORMAT));
     const int64_t big = div_up(p->M, kTile) * div_up(p->N, kTile);
+    // half a round of tiles: 36 of them take the same either way (1536 x 1536 x 4096: 8.4 and 8.6 us),
+    // 16 are faster as the few (1021 x 777 x 4096: 7.0 and 10.1), 44 as pairs (512 x 5632 x 4096: 16 and 9.2)
     if (2 * big >= ss::num_sms() / 2 && p->M > kHalf && p->N > kHalf) return launch_pair<FORMAT>(p, k_blocks, st);
-    const bool swap = p->N < p->M && p->N <= 64;  // the few are B's rows
+    // the few are A's rows, or B's where those are no more than a tile (5003 x 72 x 2688: 7.4 us as A's,
+    // 6.8 as B's; 2000 x 100 x 4096 in 8 bits 9.0 and 6.6, in 4 bits 7.0 and 7.3); with more of them a row
+    // of out in one thread's hands costs more (1021 x 777 x 1024: 5.7 and 17)
+    const bool swap = p->N < p->M && p->N <= kHalf;
     const int64_t few = swap ? p->N : p->M;
     if (few <= 16) return launch_few<FORMAT, 16>(p, k_blocks, swap, st);
     if (few <= 32) return launch_few<FORMAT, 32>(p, k_blocks, swap, st);

@@ -4,9 +4,14 @@
 // A CTA takes 64 rows of 128 columns, half a tile of scales whichever way the blocks
 // run.  The blocks along the rows are formed on the way in, by 4 neighbouring lanes; for
 // the transpose the elements are kept in shared memory and each thread takes two columns
-// of 32 rows.  So one read of the matrix serves both, and the memory is
-// what bounds it: 2 bytes read and 0.53 (MXFP4) or 1.03 (MXFP8) written for each
-// element and orientation.
+// of 32 rows.  So one read of the matrix serves both: 2 bytes read and 0.53
+// (MXFP4) or 1.03 (MXFP8) written for each element and orientation.
+//
+// To the nearest along the rows the memory bounds it (32000 x 2048 bf16 to MXFP4: 28 us,
+// 6.0 TB/s; back 26 us, 6.4 TB/s), both ways the instructions begin to (18 an element;
+// 8192 x 2048 12.4 us, 4.1 TB/s), and at random they do: 41 an element both ways, the
+// integer pipe busy three quarters of the time (8192 x 5632 65 us, of which the generator
+// is 15, rounding at random rather than to the nearest 22).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -284,8 +289,8 @@ int with_flags(bool first, bool second, F&& f) {
 // Parts of a matrix by rows where one CTA takes `rounds` loads a thread of them.
 int64_t parts(int64_t rows, int rounds) { return (rows + kLines * rounds - 1) / (kLines * rounds); }
 
-// Whole tiles as soon as there are 8 for each SM; below, a quarter of one (fp32 2043 x 1001
-// in 8 bits 5.2 us as 128 tiles, 32000 x 2048 29 us as 4000).
+// 64 rows a CTA as soon as there are 8 tiles for each SM; below, 16 (fp32 2043 x 1001 to
+// 8 bits 5.2 us as tiles, 3.0 as quarters; 1 token of 4096 1.4 us either way).
 bool few_tiles(int64_t row_tiles, int64_t col_tiles) { return row_tiles * col_tiles < 8 * (int64_t)ss::num_sms(); }
 
 template <class T, int FORMAT>

@@ -14,9 +14,12 @@
 // The statistics are taken of h as it is stored, so that the backward pass, which
 // reads the stored h, is the gradient of what the forward pass computed.
 //
-// All of it moves each element once, and the memory is what bounds it: a row stays in
-// its threads' registers (8 elements a load, up to 8 loads a thread) between the sum
-// over it and the outputs.
+// Each element moves once, and the memory is what bounds it: a row stays in its threads'
+// registers (8 elements a load, up to 8 loads a thread) between the sum over it and the
+// outputs.  16384 x 4096 bf16, 537 MB either way: forward 81 us (6.6 TB/s, where a copy
+// makes 6.8), backward with d_weight 93 us (5.8 TB/s; 169 us without the next row on its
+// way).  Dropout is bound by the generator's instructions instead: 8192 x 11008 67 us,
+// 5.4 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -60,7 +63,8 @@ struct DropArgs {
 };
 
 // A warp takes pieces of kDropPiece groups of a row, two a lane: a place in the matrix is
-// worked out once for both, and what the generator makes of the row alone once for all.
+// worked out once for both, and both are on their way before the first is worked on (8192
+// x 11008: 72.5 -> 66.8 us).
 constexpr int kDropPiece = 64;
 
 template <class T, bool ALIGNED>
@@ -104,8 +108,8 @@ __global__ void __launch_bounds__(kDropThreads) dropout_rows_kernel(const __grid
 
 // Narrow matrices, whose rows would leave lanes of such pieces idle: threads take groups of
 // 8 in the order of the matrix, as far apart as the grid has
-// threads; places in it are carried on by adding (a row's index times its stride for
-// each group cost as much as the mask: 181 instructions a group for 100).
+// threads; places in it are carried on by adding (with a row's index times its stride for
+// each group it was 181 instructions a group for 145).
 template <class T, bool ALIGNED>
 __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_constant__ DropArgs a) {
     launch_after();
@@ -474,8 +478,8 @@ constexpr int64_t kMaxRows = INT32_MAX;
 constexpr int64_t kMaxCols = 32768;  // 512 threads hold a row in registers
 constexpr int64_t kMaxFlat = (int64_t)1 << 33;  // columns of dropout: groups count in 32 bits
 
-// Threads of a row and of a CTA, and loads of 8 elements a thread: few loads a thread
-// as long as 256 threads suffice, so that many rows are in flight.
+// Threads of a row and of a CTA, and loads of 8 elements a thread, `most` of them where 256
+// threads suffice.  Two: 2048 x 2048 forward 8.2 us where one takes 9.1 and four 9.7.
 struct Shape {
     int vecs, team, threads;
 };
@@ -492,7 +496,8 @@ Shape choose_shape(int64_t vectors, int most = 2) {
 }
 
 // The backward pass's: one load a thread where fp32 or unaligned rows would leave no
-// registers for the next row's.
+// registers for the next row's.  (The forward pass's too for unaligned rows: 1021 x 1001
+// 6.9 -> 6.3 us.)
 Shape choose_grad_shape(int64_t cols, int elem_bytes, bool aligned) {
     return choose_shape((cols + 7) / 8, elem_bytes == 2 && aligned ? 2 : 1);
 }
@@ -655,7 +660,7 @@ int ss_rms_norm_backward(const ss_norm_grad* n, ss_stream_t stream) {
     a.d_h = n->d_h, a.d_h_stride = n->d_h_stride, a.d_x = n->d_x, a.d_x_stride = n->d_x_stride;
     const int teams = s.threads / s.team;
     // Few rows (up to 4 in turn for each team of 8 CTAs) are one cluster's, which joins d_weight in
-    // its shared memory: one launch for two (50 x 64: 3.4 us where this takes 2.7).
+    // its shared memory: one launch for two (50 x 64, calls back to back: 12.5 -> 8.0 us).
     const bool cluster = n->d_weight && s.vecs <= 2 && n->rows <= 32 * teams;
     if (cluster) {
         grid = std::min<int64_t>((n->rows + teams - 1) / teams, 8);
