@@ -211,9 +211,12 @@ __device__ __forceinline__ void store_mx8(const NormArgs& a, int64_t row, int co
     if ((threadIdx.x & 3) == 0) a.mx_scales[ss::mx_scale_at(row, col >> 5, a.mx_tiles)] = (unsigned char)byte;
 }
 
+constexpr int kMostThreads = 512;  // of a row: two or three rows fit an SM's registers
+
 // VECS loads of 8 elements a thread, `team` threads a row, blockDim / team rows a CTA.
-template <class T, int VECS, bool ALIGNED>
-__global__ void __launch_bounds__(VECS > 2 ? 512 : 256) norm_kernel(const __grid_constant__ NormArgs a) {
+// WIDE: of more than 256 threads.
+template <class T, int VECS, bool ALIGNED, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? kMostThreads : 256) norm_kernel(const __grid_constant__ NormArgs a) {
     constexpr bool kWeightAhead = VECS <= 4;  // asked for with the row
     __shared__ float lane_sums[16];
     launch_after();
@@ -292,17 +295,24 @@ __global__ void __launch_bounds__(VECS > 2 ? 512 : 256) norm_kernel(const __grid
     }
 }
 
+constexpr int kCluster = 8;  // CTAs of a backward pass that joins d_weight itself, at the most
+
 // The rows of a backward pass in turn, each CTA its own; the next row's elements are
 // on their way while one is worked on, where the registers hold both.
 template <class T, int VECS, bool ALIGNED>
 __host__ __device__ constexpr bool loads_ahead() { return VECS * sizeof(T) <= (ALIGNED ? 4 : 2) || VECS == 1; }
 
+// Rows too long for the registers are read twice, the second time from L2.
+template <int VECS, bool ALIGNED>
+__host__ __device__ constexpr bool holds_row() { return VECS < (ALIGNED ? 8 : 4); }
+
 template <class T, int VECS, bool ALIGNED>
-__global__ void __launch_bounds__(VECS > 2 ? 512 : 256, VECS > 2 ? 1 : 2)
+__global__ void __launch_bounds__(kMostThreads)
 norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
     extern __shared__ float joined[];  // [rows at a time][cols], where that is more than one
     __shared__ float lane_sums[2][16];
-    constexpr bool kAhead = loads_ahead<T, VECS, ALIGNED>();
+    constexpr bool kAhead = loads_ahead<T, VECS, ALIGNED>(), kHold = holds_row<VECS, ALIGNED>();
+    constexpr int kHeld = kHold ? VECS : 1;
     launch_after();
     const int mine = threadIdx.x % a.team, teams = blockDim.x / a.team, team = threadIdx.x / a.team;
     const int lane = threadIdx.x & 31;
@@ -314,36 +324,46 @@ norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
         for (int k = 0; k < 8; ++k) dw[i][k] = 0.f;
     auto run = [&](int64_t row, int col) { return Run(row < a.rows ? a.cols - col : 0, lane == 0, lane == 31); };
     struct Row {
-        Vec8<T> dy[VECS], h[VECS], ds[VECS];
-        uint4 dy_tail[VECS], h_tail[VECS], ds_tail[VECS];
+        Vec8<T> dy[kHeld], h[kHeld], ds[kHeld];
+        uint4 dy_tail[kHeld], h_tail[kHeld], ds_tail[kHeld];
         float rstd;
     };
+    // Loads i of a row, or one of them, into place `to`.
+    auto fetch_one = [&](Row& x, int to, int64_t row, int i) {
+        const int col = 8 * (mine + i * a.team);
+        x.dy_tail[to] = x.h_tail[to] = x.ds_tail[to] = make_uint4(0, 0, 0, 0);
+        x.dy[to].template fetch<ALIGNED>(static_cast<const T*>(a.d_out) + row * a.d_out_stride + col, run(row, col), x.dy_tail[to]);
+        x.h[to].template fetch<ALIGNED>(static_cast<const T*>(a.h) + row * a.h_stride + col, run(row, col), x.h_tail[to]);
+        x.ds[to].clear();
+        if (a.d_sum)
+            x.ds[to].template fetch<ALIGNED>(static_cast<const T*>(a.d_sum) + row * a.d_sum_stride + col, run(row, col), x.ds_tail[to]);
+    };
+    auto settle_one = [&](Row& x, int to, int64_t row, int i) {
+        const int col = 8 * (mine + i * a.team);
+        x.dy[to].template settle<ALIGNED>(static_cast<const T*>(a.d_out) + row * a.d_out_stride + col, run(row, col), x.dy_tail[to]);
+        x.h[to].template settle<ALIGNED>(static_cast<const T*>(a.h) + row * a.h_stride + col, run(row, col), x.h_tail[to]);
+        if (a.d_sum)
+            x.ds[to].template settle<ALIGNED>(static_cast<const T*>(a.d_sum) + row * a.d_sum_stride + col, run(row, col), x.ds_tail[to]);
+    };
     auto fetch = [&](Row& x, int64_t row) {
-        const T* dy = static_cast<const T*>(a.d_out) + row * a.d_out_stride;
-        const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
-        const T* ds = static_cast<const T*>(a.d_sum) + row * a.d_sum_stride;
+        if (kHold) {
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) {
-            const int col = 8 * (mine + i * a.team);
-            x.dy_tail[i] = x.h_tail[i] = x.ds_tail[i] = make_uint4(0, 0, 0, 0);
-            x.dy[i].template fetch<ALIGNED>(dy + col, run(row, col), x.dy_tail[i]);
-            x.h[i].template fetch<ALIGNED>(h + col, run(row, col), x.h_tail[i]);
-            x.ds[i].clear();
-            if (a.d_sum) x.ds[i].template fetch<ALIGNED>(ds + col, run(row, col), x.ds_tail[i]);
+            for (int i = 0; i < VECS; ++i) fetch_one(x, kHold ? i : 0, row, i);
         }
         x.rstd = row < a.rows ? a.rstd[row] : 0.f;
     };
     auto settle = [&](Row& x, int64_t row) {
-        const T* dy = static_cast<const T*>(a.d_out) + row * a.d_out_stride;
-        const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
-        const T* ds = static_cast<const T*>(a.d_sum) + row * a.d_sum_stride;
+        if (kHold) {
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) {
-            const int col = 8 * (mine + i * a.team);
-            x.dy[i].template settle<ALIGNED>(dy + col, run(row, col), x.dy_tail[i]);
-            x.h[i].template settle<ALIGNED>(h + col, run(row, col), x.h_tail[i]);
-            if (a.d_sum) x.ds[i].template settle<ALIGNED>(ds + col, run(row, col), x.ds_tail[i]);
+            for (int i = 0; i < VECS; ++i) settle_one(x, kHold ? i : 0, row, i);
         }
+    };
+    // The place of loads i of a row that may have to be read again.
+    auto place = [&](Row& x, int64_t row, int i) {
+        if (kHold) return i;
+        fetch_one(x, 0, row, i);
+        settle_one(x, 0, row, i);
+        return 0;
     };
     int parity = 0;
     const int64_t step = (int64_t)gridDim.x * teams;
@@ -378,9 +398,10 @@ norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
 #pragma unroll
         for (int i = 0; i < VECS; ++i) {
             float f[8], q[8], g[8];
+            const int at = place(x, row, i);
             weight(i, g);
-            x.dy[i].get(f);
-            x.h[i].get(q);
+            x.dy[at].get(f);
+            x.h[at].get(q);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {  // zeros behind the row's end
                 const float t = f[k] * (q[k] * rstd);
@@ -393,10 +414,11 @@ norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
         for (int i = 0; i < VECS; ++i) {
             const int col = 8 * (mine + i * a.team);
             float f[8], q[8], g[8], d[8];
+            const int at = place(x, row, i);
             weight(i, g);
-            x.dy[i].get(f);
-            x.h[i].get(q);
-            x.ds[i].get(d);
+            x.dy[at].get(f);
+            x.h[at].get(q);
+            x.ds[at].get(d);
 #pragma unroll
             for (int k = 0; k < 8; ++k) f[k] = fmaf(rstd, fmaf(-q[k] * rstd, s, f[k] * g[k]), d[k]);
             Vec8<T> v;
@@ -434,15 +456,15 @@ norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
     tc::cluster_sync();
     const int ctas = gridDim.x, share = (a.cols + ctas - 1) / ctas, c0 = blockIdx.x * share;
     for (int c = c0 + threadIdx.x; c < min(c0 + share, a.cols); c += blockDim.x) {
-        float s = 0.f;
-        for (int q = 0; q < ctas; ++q) {
-            float v;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                         : "=f"(v)
-                         : "r"(tc::map_to_rank(tc::smem_addr(joined + c), q))
-                         : "memory");
-            s += v;
+        float v[kCluster], s = 0.f;
+#pragma unroll
+        for (int q = 0; q < kCluster; ++q) {
+            v[q] = 0.f;
+            if (q < ctas)
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[q]) : "r"(tc::map_to_rank(tc::smem_addr(joined + c), q)));
         }
+#pragma unroll
+        for (int q = 0; q < kCluster; ++q) s += v[q];
         store_weight(static_cast<T*>(a.d_weight) + c, s);
     }
     tc::cluster_sync();
@@ -475,37 +497,38 @@ __global__ void __launch_bounds__(32 * kJoinRows) norm_join_kernel(const float* 
 // ---------------------------------------------------------------------------
 
 constexpr int64_t kMaxRows = INT32_MAX;
-constexpr int64_t kMaxCols = 32768;  // 512 threads hold a row in registers
+constexpr int64_t kMaxCols = 32768;  // 512 threads hold a row, 8 loads each
 constexpr int64_t kMaxFlat = (int64_t)1 << 33;  // columns of dropout: groups count in 32 bits
 
-// Threads of a row and of a CTA, and loads of 8 elements a thread, `most` of them where 256
-// threads suffice.  Two: 2048 x 2048 forward 8.2 us where one takes 9.1 and four 9.7.
+// Threads of a row and of a CTA, and loads of 8 elements a thread.
 struct Shape {
     int vecs, team, threads;
 };
 
-Shape choose_shape(int64_t vectors, int most = 2) {
-    if (vectors <= 512) {
-        int team = 32;
-        while (team < 256 && team * most < vectors) team *= 2;
-        return {vectors <= team ? 1 : 2, team, 256};
-    }
-    const int vecs = vectors <= 2048 ? 4 : 8;
-    const int team = (int)((vectors + vecs - 1) / vecs + 31) / 32 * 32;
+// `most` loads a thread (1 or 2) as long as that many threads may take a row, then as few
+// as do.  Two, 2048 x 2048 forward: 8.2 us where one takes 9.1 and four 9.7.
+Shape choose_shape(int64_t vectors, int most) {
+    int team = 32;
+    while (team < 256 && team * most < vectors) team *= 2;
+    if (team * most >= vectors) return {vectors <= team ? 1 : 2, team, 256};
+    int vecs = most;
+    while (vecs * kMostThreads < vectors) vecs *= 2;
+    team = (int)((vectors + vecs - 1) / vecs + 31) / 32 * 32;
     return {vecs, team, team};
 }
 
-// The backward pass's: one load a thread where fp32 or unaligned rows would leave no
-// registers for the next row's.  (The forward pass's too for unaligned rows: 1021 x 1001
-// 6.9 -> 6.3 us.)
+// The forward pass's, and the backward pass's: one load a thread for unaligned rows (1021
+// x 1001 forward: 6.9 -> 6.3 us), and where fp32 rows would leave the backward pass no
+// registers for the next row's.
+Shape choose_norm_shape(int64_t vectors, bool aligned) { return choose_shape(vectors, aligned ? 2 : 1); }
 Shape choose_grad_shape(int64_t cols, int elem_bytes, bool aligned) {
     return choose_shape((cols + 7) / 8, elem_bytes == 2 && aligned ? 2 : 1);
 }
 
-// CTAs that take the rows of a backward pass in turn.
+// CTAs that take the rows of a backward pass in turn, as many as the registers hold.
 int64_t grad_grid(int64_t rows, const Shape& s) {
     const int64_t teams = s.threads / s.team, need = (rows + teams - 1) / teams;
-    return std::min(need, (int64_t)ss::num_sms() * 2);
+    return std::min(need, (int64_t)ss::num_sms() * (s.threads > 256 ? 1 : 2));
 }
 
 template <class F>
@@ -618,19 +641,21 @@ int ss_rms_norm(const ss_norm* n, ss_stream_t stream) {
     a.mx_tiles = (int)((n->cols + ss::kMxTile - 1) / ss::kMxTile);
     // the weight is one row: its own stride does not matter
     const bool al = rows_on_16(n->elem_bytes, {x, res, sum, out}) && ss::aligned(n->weight, 16);
-    const Shape s = choose_shape(n->mx_data ? (int64_t)a.mx_tiles * (ss::kMxTile / 8) : (n->cols + 7) / 8, al ? 2 : 1);
+    const Shape s = choose_norm_shape(n->mx_data ? (int64_t)a.mx_tiles * (ss::kMxTile / 8) : (n->cols + 7) / 8, al);
     a.team = s.team;
     const int64_t teams = s.threads / s.team, grid = (n->rows + teams - 1) / teams;
     return with_shape(n->elem_bytes, s.vecs, al, [&](auto t, auto v, auto aligned) {
-        return ss::launch(norm_kernel<decltype(t), decltype(v)::value, decltype(aligned)::value>, grid, s.threads, 0, 0,
-                          true, reinterpret_cast<cudaStream_t>(stream), a);
+        constexpr int V = decltype(v)::value;
+        constexpr bool A = decltype(aligned)::value;
+        const auto kernel = s.threads > 256 ? norm_kernel<decltype(t), V, A, true> : norm_kernel<decltype(t), V, A, (V > 2)>;
+        return ss::launch(kernel, grid, s.threads, 0, 0, true, reinterpret_cast<cudaStream_t>(stream), a);
     });
 }
 
 int ss_rms_norm_workspace(int64_t rows, int64_t cols, size_t* bytes_out) {
     if (rows < 0 || cols < 1 || !bytes_out) return SS_EINVAL;
     if (rows > kMaxRows || cols > kMaxCols) return SS_EOVERFLOW;
-    *bytes_out = (size_t)(std::max<int64_t>(grad_grid(rows, choose_grad_shape(cols, 4, false)), 1) * cols * 4);
+    *bytes_out = (size_t)(std::max<int64_t>(std::min(rows, (int64_t)ss::num_sms() * 2), 1) * cols * 4);
     return SS_OK;
 }
 
@@ -661,15 +686,15 @@ int ss_rms_norm_backward(const ss_norm_grad* n, ss_stream_t stream) {
     const int teams = s.threads / s.team;
     // Few rows (up to 4 in turn for each team of 8 CTAs) are one cluster's, which joins d_weight in
     // its shared memory: one launch for two (50 x 64, calls back to back: 12.5 -> 8.0 us).
-    const bool cluster = n->d_weight && s.vecs <= 2 && n->rows <= 32 * teams;
+    const bool cluster = n->d_weight && teams * a.cols * 4 <= 48 * 1024 - 512 && n->rows <= 32 * teams;
     if (cluster) {
-        grid = std::min<int64_t>((n->rows + teams - 1) / teams, 8);
+        grid = std::min<int64_t>((n->rows + teams - 1) / teams, kCluster);
         grid = std::max<int64_t>(grid, 1);
         a.d_weight = n->d_weight;
     } else if (n->d_weight) {
         a.part = static_cast<float*>(n->workspace);
     }
-    // with several teams at most 8 x 512 floats, 4 x 1024 or 2 x 2048; 4096 in a cluster
+    // with several teams at most 8 x 512 floats, 4 x 1024 or 2 x 2048
     const int smem = teams > 1 || cluster ? teams * a.cols * 4 : 0;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (int rc = with_shape(n->elem_bytes, s.vecs, al, [&](auto t, auto v, auto aligned) {
