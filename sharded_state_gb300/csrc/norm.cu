@@ -213,10 +213,18 @@ __device__ __forceinline__ void store_mx8(const NormArgs& a, int64_t row, int co
 
 constexpr int kMostThreads = 512;  // of a row: two or three rows fit an SM's registers
 
+// Rows of more than 256 threads and two loads of bf16 each are held to 56 registers, so
+// that three rows of 352 threads fit an SM (8192 x 5632 with dropout, forward: 76 us, where
+// 58 registers and two rows take 91).
+template <class T, int VECS, bool ALIGNED>
+constexpr bool three_rows() { return ALIGNED && VECS <= 2 && sizeof(T) == 2; }
+
 // VECS loads of 8 elements a thread, `team` threads a row, blockDim / team rows a CTA.
 // WIDE: of more than 256 threads.
 template <class T, int VECS, bool ALIGNED, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kMostThreads : 256) norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(!WIDE ? 256 : three_rows<T, VECS, ALIGNED>() ? 576 : kMostThreads,
+                                  WIDE && three_rows<T, VECS, ALIGNED>() ? 2 : 0)
+norm_kernel(const __grid_constant__ NormArgs a) {
     constexpr bool kWeightAhead = VECS <= 4;  // asked for with the row
     __shared__ float lane_sums[16];
     launch_after();
@@ -304,7 +312,7 @@ __host__ __device__ constexpr bool loads_ahead() { return VECS * sizeof(T) <= (A
 
 // Rows too long for the registers are read twice, the second time from L2.
 template <int VECS, bool ALIGNED>
-__host__ __device__ constexpr bool holds_row() { return VECS < (ALIGNED ? 8 : 4); }
+__host__ __device__ constexpr bool holds_row() { return VECS < 8; }
 
 template <class T, int VECS, bool ALIGNED>
 __global__ void __launch_bounds__(kMostThreads)
