@@ -310,16 +310,19 @@ constexpr int kCluster = 8;  // CTAs of a backward pass that joins d_weight itse
 template <class T, int VECS, bool ALIGNED>
 __host__ __device__ constexpr bool loads_ahead() { return VECS * sizeof(T) <= (ALIGNED ? 4 : 2) || VECS == 1; }
 
-// Rows too long for the registers are read twice, the second time from L2.
-template <int VECS, bool ALIGNED>
-__host__ __device__ constexpr bool holds_row() { return VECS < 8; }
+// Rows too long for the registers are read twice, the second time from L2: those of eight
+// loads a thread, but for aligned ones of bf16 (backward of 1000 x 20000, held 92 us and
+// read twice 136; of 1000 x 20001 772 and 231, of 500 x 32768 fp32 278 and 99: what is
+// held there spills; of four loads, 1801 x 9589 held 140 and read twice 179).
+template <class T, int VECS, bool ALIGNED>
+__host__ __device__ constexpr bool holds_row() { return VECS < 8 || (ALIGNED && sizeof(T) == 2); }
 
 template <class T, int VECS, bool ALIGNED>
 __global__ void __launch_bounds__(kMostThreads)
 norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
     extern __shared__ float joined[];  // [rows at a time][cols], where that is more than one
     __shared__ float lane_sums[2][16];
-    constexpr bool kAhead = loads_ahead<T, VECS, ALIGNED>(), kHold = holds_row<VECS, ALIGNED>();
+    constexpr bool kAhead = loads_ahead<T, VECS, ALIGNED>(), kHold = holds_row<T, VECS, ALIGNED>();
     constexpr int kHeld = kHold ? VECS : 1;
     launch_after();
     const int mine = threadIdx.x % a.team, teams = blockDim.x / a.team, team = threadIdx.x / a.team;
@@ -692,9 +695,12 @@ int ss_rms_norm_backward(const ss_norm_grad* n, ss_stream_t stream) {
     a.inv_cols = 1.f / (float)n->cols, a.rng = n->rng;
     a.d_h = n->d_h, a.d_h_stride = n->d_h_stride, a.d_x = n->d_x, a.d_x_stride = n->d_x_stride;
     const int teams = s.threads / s.team;
-    // Few rows (up to 4 in turn for each team of 8 CTAs) are one cluster's, which joins d_weight in
-    // its shared memory: one launch for two (50 x 64, calls back to back: 12.5 -> 8.0 us).
-    const bool cluster = n->d_weight && teams * a.cols * 4 <= 48 * 1024 - 512 && n->rows <= 32 * teams;
+    // Few rows, one for each team of 8 CTAs, are one cluster's, which joins d_weight in its
+    // shared memory: one launch for two (50 x 64, calls back to back: 12.5 -> 8.0 us).  With
+    // rows in turn the two launches are as short or shorter (32 x 4096 in a graph: 9.1 us in
+    // a cluster, 6.2 in two launches), and with four loads a thread even for one row (1 x
+    // 8976: 14.4, 9.5).
+    const bool cluster = n->d_weight && s.vecs <= 2 && teams * a.cols * 4 <= 48 * 1024 - 512 && n->rows <= kCluster * teams;
     if (cluster) {
         grid = std::min<int64_t>((n->rows + teams - 1) / teams, kCluster);
         grid = std::max<int64_t>(grid, 1);
