@@ -699,7 +699,6 @@ def _device() -> int:
 _get_device = None
 
 
-
 def _row_dtype(fn: str, t, what: str):
     """The type and shape of the bf16 or fp32 matrix that gives a call its sizes."""
     dtype, shape = t.dtype, t.shape
