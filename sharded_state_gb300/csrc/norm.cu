@@ -211,7 +211,15 @@ __device__ __forceinline__ void store_mx8(const NormArgs& a, int64_t row, int co
     if ((threadIdx.x & 3) == 0) a.mx_scales[ss::mx_scale_at(row, col >> 5, a.mx_tiles)] = (unsigned char)byte;
 }
 
-constexpr int kMostThreads = 512;  // of a row: two or three rows fit an SM's registers
+// Most threads of a row: two or three rows of 512 fit an SM's registers.  At any alignment
+// a load takes a block more, and fewer loads of more threads are better.
+constexpr int kMostThreads = 512;
+constexpr int norm_threads(int vecs, bool aligned, int elem_bytes) {
+    return aligned || vecs * elem_bytes > 4 ? kMostThreads : vecs == 1 ? 1024 : 768;
+}
+constexpr int grad_threads(int vecs, bool aligned, int elem_bytes) {
+    return aligned || elem_bytes > 2 || vecs > 2 ? kMostThreads : vecs == 1 ? 768 : 640;
+}
 
 // Rows of more than 256 threads and two loads of bf16 each are held to 56 registers, so
 // that three rows of 352 threads fit an SM (8192 x 5632 with dropout, forward: 76 us, where
@@ -222,11 +230,11 @@ constexpr bool three_rows() { return ALIGNED && VECS <= 2 && sizeof(T) == 2; }
 // VECS loads of 8 elements a thread, `team` threads a row, blockDim / team rows a CTA.
 // WIDE: of more than 256 threads.
 template <class T, int VECS, bool ALIGNED, bool WIDE>
-__global__ void __launch_bounds__(!WIDE ? 256 : three_rows<T, VECS, ALIGNED>() ? 576 : kMostThreads,
+__global__ void __launch_bounds__(!WIDE ? 256 : three_rows<T, VECS, ALIGNED>() ? 576 : norm_threads(VECS, ALIGNED, sizeof(T)),
                                   WIDE && three_rows<T, VECS, ALIGNED>() ? 2 : 0)
 norm_kernel(const __grid_constant__ NormArgs a) {
     constexpr bool kWeightAhead = VECS <= 4;  // asked for with the row
-    __shared__ float lane_sums[16];
+    __shared__ float lane_sums[32];
     launch_after();
     const int mine = threadIdx.x % a.team, lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / a.team) + threadIdx.x / a.team;
@@ -317,12 +325,12 @@ __host__ __device__ constexpr bool loads_ahead() { return VECS * sizeof(T) <= (A
 template <class T, int VECS, bool ALIGNED>
 __host__ __device__ constexpr bool holds_row() { return VECS < 8 || (ALIGNED && sizeof(T) == 2); }
 
-template <class T, int VECS, bool ALIGNED>
-__global__ void __launch_bounds__(kMostThreads)
+template <class T, int VECS, bool ALIGNED, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? grad_threads(VECS, ALIGNED, sizeof(T)) : kMostThreads)
 norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
     extern __shared__ float joined[];  // [rows at a time][cols], where that is more than one
-    __shared__ float lane_sums[2][16];
-    constexpr bool kAhead = loads_ahead<T, VECS, ALIGNED>(), kHold = holds_row<T, VECS, ALIGNED>();
+    __shared__ float lane_sums[2][32];
+    constexpr bool kAhead = !WIDE && loads_ahead<T, VECS, ALIGNED>(), kHold = holds_row<T, VECS, ALIGNED>();
     constexpr int kHeld = kHold ? VECS : 1;
     launch_after();
     const int mine = threadIdx.x % a.team, teams = blockDim.x / a.team, team = threadIdx.x / a.team;
@@ -518,12 +526,13 @@ struct Shape {
 
 // `most` loads a thread (1 or 2) as long as that many threads may take a row, then as few
 // as do.  Two, 2048 x 2048 forward: 8.2 us where one takes 9.1 and four 9.7.
-Shape choose_shape(int64_t vectors, int most) {
+template <class F>
+Shape choose_shape(int64_t vectors, int most, F&& most_threads) {
     int team = 32;
     while (team < 256 && team * most < vectors) team *= 2;
     if (team * most >= vectors) return {vectors <= team ? 1 : 2, team, 256};
     int vecs = most;
-    while (vecs * kMostThreads < vectors) vecs *= 2;
+    while (vecs * most_threads(vecs) < vectors) vecs *= 2;
     team = (int)((vectors + vecs - 1) / vecs + 31) / 32 * 32;
     return {vecs, team, team};
 }
@@ -531,9 +540,12 @@ Shape choose_shape(int64_t vectors, int most) {
 // The forward pass's, and the backward pass's: one load a thread for unaligned rows (1021
 // x 1001 forward: 6.9 -> 6.3 us), and where fp32 rows would leave the backward pass no
 // registers for the next row's.
-Shape choose_norm_shape(int64_t vectors, bool aligned) { return choose_shape(vectors, aligned ? 2 : 1); }
+Shape choose_norm_shape(int64_t vectors, int elem_bytes, bool aligned) {
+    return choose_shape(vectors, aligned ? 2 : 1, [&](int vecs) { return norm_threads(vecs, aligned, elem_bytes); });
+}
 Shape choose_grad_shape(int64_t cols, int elem_bytes, bool aligned) {
-    return choose_shape((cols + 7) / 8, elem_bytes == 2 && aligned ? 2 : 1);
+    return choose_shape((cols + 7) / 8, elem_bytes == 2 && aligned ? 2 : 1,
+                        [&](int vecs) { return grad_threads(vecs, aligned, elem_bytes); });
 }
 
 // CTAs that take the rows of a backward pass in turn, as many as the registers hold.
@@ -652,7 +664,7 @@ int ss_rms_norm(const ss_norm* n, ss_stream_t stream) {
     a.mx_tiles = (int)((n->cols + ss::kMxTile - 1) / ss::kMxTile);
     // the weight is one row: its own stride does not matter
     const bool al = rows_on_16(n->elem_bytes, {x, res, sum, out}) && ss::aligned(n->weight, 16);
-    const Shape s = choose_norm_shape(n->mx_data ? (int64_t)a.mx_tiles * (ss::kMxTile / 8) : (n->cols + 7) / 8, al);
+    const Shape s = choose_norm_shape(n->mx_data ? (int64_t)a.mx_tiles * (ss::kMxTile / 8) : (n->cols + 7) / 8, n->elem_bytes, al);
     a.team = s.team;
     const int64_t teams = s.threads / s.team, grid = (n->rows + teams - 1) / teams;
     return with_shape(n->elem_bytes, s.vecs, al, [&](auto t, auto v, auto aligned) {
@@ -712,8 +724,13 @@ int ss_rms_norm_backward(const ss_norm_grad* n, ss_stream_t stream) {
     const int smem = teams > 1 || cluster ? teams * a.cols * 4 : 0;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (int rc = with_shape(n->elem_bytes, s.vecs, al, [&](auto t, auto v, auto aligned) {
-            return ss::launch(norm_grad_kernel<decltype(t), decltype(v)::value, decltype(aligned)::value>, grid,
-                              s.threads, smem, cluster ? (int)grid : 0, true, st, a);
+            using T = decltype(t);
+            constexpr int V = decltype(v)::value;
+            constexpr bool A = decltype(aligned)::value;
+            const auto kernel = s.threads > kMostThreads
+                                    ? norm_grad_kernel<T, V, A, (grad_threads(V, A, sizeof(T)) > kMostThreads)>
+                                    : norm_grad_kernel<T, V, A, false>;
+            return ss::launch(kernel, grid, s.threads, smem, cluster ? (int)grid : 0, true, st, a);
         }))
         return rc;
     if (cluster) return SS_OK;
