@@ -211,11 +211,15 @@ __device__ __forceinline__ void store_mx8(const NormArgs& a, int64_t row, int co
     if ((threadIdx.x & 3) == 0) a.mx_scales[ss::mx_scale_at(row, col >> 5, a.mx_tiles)] = (unsigned char)byte;
 }
 
-// Most threads of a row: two or three rows of 512 fit an SM's registers.  At any alignment
-// a load takes a block more, and fewer loads of more threads are better.
+// Most threads of a row, for one, two and more loads a thread; two or three rows of 512 fit
+// an SM's registers.  At any alignment a load holds a block more, and where 512 threads
+// would take four loads each, one row an SM: more threads of fewer loads (1801 x 9589,
+// forward 86 -> 68 us, backward 141 -> 86; 13018 x 5155 backward in one load of 672 threads
+// 353, two of 352 446; forward in one 330, in two 236; 2000 x 6001 fp32 forward in one load
+// of 768 63, two of 384 66).
 constexpr int kMostThreads = 512;
 constexpr int norm_threads(int vecs, bool aligned, int elem_bytes) {
-    return aligned || vecs * elem_bytes > 4 ? kMostThreads : vecs == 1 ? 1024 : 768;
+    return aligned || vecs * elem_bytes != 4 ? kMostThreads : elem_bytes == 2 ? 768 : 1024;
 }
 constexpr int grad_threads(int vecs, bool aligned, int elem_bytes) {
     return aligned || elem_bytes > 2 || vecs > 2 ? kMostThreads : vecs == 1 ? 768 : 640;

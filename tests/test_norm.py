@@ -255,7 +255,8 @@ class Norm:
 
 SIZES = [(1, 1), (1, 2048), (3, 7), (50, 64), (700, 17), (33, 513), (5, 1001), (301, 2048), (2, 4095), (9, 4096),
          (700, 1030), (7, 5632), (5, 11008), (3, 16384), (2, 16391), (2, 32768),
-         (40, 5632), (20, 8192), (9, 9589), (11, 20000)]
+         (40, 5632), (20, 8192), (9, 9589), (11, 20000),
+         (20, 5155), (9, 6001)]
 
 
 @gpu
