@@ -674,7 +674,8 @@ int ss_rms_norm(const ss_norm* n, ss_stream_t stream) {
     return with_shape(n->elem_bytes, s.vecs, al, [&](auto t, auto v, auto aligned) {
         constexpr int V = decltype(v)::value;
         constexpr bool A = decltype(aligned)::value;
-        const auto kernel = s.threads > 256 ? norm_kernel<decltype(t), V, A, true> : norm_kernel<decltype(t), V, A, (V > 2)>;
+        constexpr bool kNarrow = V == 1 || (V == 2 && A), kWide = V > 1 || !A;  // what choose_norm_shape gives
+        const auto kernel = s.threads > 256 ? norm_kernel<decltype(t), V, A, kWide> : norm_kernel<decltype(t), V, A, !kNarrow>;
         return ss::launch(kernel, grid, s.threads, 0, 0, true, reinterpret_cast<cudaStream_t>(stream), a);
     });
 }
