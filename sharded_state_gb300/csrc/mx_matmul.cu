@@ -217,8 +217,9 @@ __device__ __forceinline__ void write_turned(const PairArgs& g, const uint32_t* 
 // load would allow 8.9; 8192 x 5632 x 2048 37 us, 5.1; 2048 x 5632 x 2048 in 8 bits 21 us,
 // 2.2 (2.3 rounds of tiles take 3).  What made it: the second accumulator (180 -> 165 us),
 // operands in uniform registers (-> 118), accumulators given back without a release (->
-// 105).  Handing B on to a second pair in clusters of 4 was 5 % slower: L2 is busy 28 % of
-// the time, and the device holds 36 such clusters, 144 SMs of 152.
+// 105).  Each CTA loads the scales of all of B's rows, 1 KB (4 bits) more a stage than its
+// half: no load is multicast, because a map may be of any address a caller gives (105 us
+// either way, 37 and 21 too).
 template <int FORMAT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairArgs g) {
@@ -277,8 +278,8 @@ mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairAr
                 tc::tma_load_2d(a, &maps.a, k * kRowBytes, a_row, bar);
                 tc::tma_load_2d(sa, &maps.a_scales, k * (kScales / 4), m * 2 + (int)rank, bar);
                 tc::tma_load_2d(b, &maps.b, k * kRowBytes, b_row, bar);
-                // the scales of all of B's rows, which both CTAs multiply with: half from either
-                tc::tma_load_2d_multicast(sb + rank * kScales, &maps.b_scales, k * (kScales / 4), n * 2 + (int)rank, bar, 3);
+                // the scales of all of B's rows, two rows of tiles: each CTA multiplies with both
+                tc::tma_load_2d(sb, &maps.b_scales, k * (kScales / 4), n * 2, bar);
             }
         }
     } else if (warp == 1 && rank == 0) {
@@ -574,14 +575,14 @@ int data_map(CUtensorMap* map, const void* data, int64_t rows, int64_t K, int fo
     return r == CUDA_SUCCESS ? SS_OK : ss::cuda_fail(cudaErrorInvalidValue);
 }
 
-// Its scales, as words, in boxes of a stage's tiles for 128 rows; zeros, which are the
-// lowest scale, outside.
-int scale_map(CUtensorMap* map, const void* scales, int64_t rows, int64_t K, int format) {
+// Its scales, as words, in boxes of a stage's tiles for box_tiles times 128 rows; zeros,
+// which are the lowest scale, outside.
+int scale_map(CUtensorMap* map, const void* scales, int64_t rows, int64_t K, int format, int box_tiles) {
     const ss::EncodeTiled fn = ss::tensor_map_encoder();
     if (!fn) return ss::cuda_fail(cudaErrorNotSupported);
     const cuuint64_t pitch = (cuuint64_t)div_up(K, ss::kMxTile) * ss::kMxTileBytes;
     const cuuint64_t dims[2] = {pitch / 4, (cuuint64_t)div_up(rows, ss::kMxTile)}, strides[1] = {pitch};
-    const cuuint32_t box[2] = {(cuuint32_t)scale_bytes(format) / 4, 1}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)scale_bytes(format) / 4, (cuuint32_t)box_tiles}, step[2] = {1, 1};
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void*>(scales), dims, strides, box, step,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -593,11 +594,12 @@ struct Operand {
     int64_t rows;
 };
 
-int make_maps(Maps* maps, const Operand& a, const Operand& b, int64_t K, int format, int b_rows) {
+// b_rows: of a box of B; b_tiles: rows of tiles in one of its scales.
+int make_maps(Maps* maps, const Operand& a, const Operand& b, int64_t K, int format, int b_rows, int b_tiles) {
     if (int rc = data_map(&maps->a, a.data, a.rows, K, format, kHalf)) return rc;
     if (int rc = data_map(&maps->b, b.data, b.rows, K, format, b_rows)) return rc;
-    if (int rc = scale_map(&maps->a_scales, a.scales, a.rows, K, format)) return rc;
-    return scale_map(&maps->b_scales, b.scales, b.rows, K, format);
+    if (int rc = scale_map(&maps->a_scales, a.scales, a.rows, K, format, 1)) return rc;
+    return scale_map(&maps->b_scales, b.scales, b.rows, K, format, b_tiles);
 }
 
 template <int FORMAT>
@@ -607,7 +609,7 @@ int launch_pair(const ss_mx_product* p, int64_t k_blocks, cudaStream_t st) {
     constexpr int smem = pair_smem(FORMAT);
     if (int rc = ss::allow_smem(ready, reinterpret_cast<const void*>(kernel), smem)) return rc;
     Maps maps;
-    if (int rc = make_maps(&maps, {p->a_data, p->a_scales, p->M}, {p->b_data, p->b_scales, p->N}, p->K, FORMAT, kHalf))
+    if (int rc = make_maps(&maps, {p->a_data, p->a_scales, p->M}, {p->b_data, p->b_scales, p->N}, p->K, FORMAT, kHalf, 2))
         return rc;
     const int64_t m_tiles = div_up(p->M, kTile), n_tiles = div_up(p->N, kTile), pairs = ss::num_sms() / 2;
     const PairArgs g = {p->M, p->N, p->out_stride, (int)m_tiles, (int)n_tiles, (int)k_blocks, p->out, p->elem_bytes,
@@ -644,7 +646,7 @@ int launch_few(const ss_mx_product* p, int64_t k_blocks, bool swap, cudaStream_t
     Operand a = {p->b_data, p->b_scales, p->N}, b = {p->a_data, p->a_scales, p->M};
     if (swap) std::swap(a, b);
     Maps maps;
-    if (int rc = make_maps(&maps, a, b, p->K, FORMAT, FEW)) return rc;
+    if (int rc = make_maps(&maps, a, b, p->K, FORMAT, FEW, 1)) return rc;
     const int64_t row_tiles = div_up(a.rows, kHalf), few_tiles = div_up(b.rows, FEW), tiles = row_tiles * few_tiles;
     const int splits = choose_splits(tiles, k_blocks, FEW, smem);
     const FewArgs g = {a.rows, b.rows, swap ? p->out_stride : 1, swap ? 1 : p->out_stride, (int)row_tiles, (int)k_blocks,

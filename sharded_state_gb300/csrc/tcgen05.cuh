@@ -157,17 +157,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// The same box to the same place in every CTA of `mask`; its bytes count in each of
-// their pairs' first CTA, at the offset of `bar` (an address in a pair's first CTA).
-__device__ __forceinline__ void tma_load_2d_multicast(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
-                                                      uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        ".cta_group::2 [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
-        "l"(map), "r"(bar), "r"(x), "r"(y), "h"(mask)
-        : "memory");
-}
-
 // The same for a CTA on its own barrier.
 __device__ __forceinline__ void tma_load_2d_one(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     asm volatile(
