@@ -19,7 +19,10 @@ struct Philox {
 
     Philox() = default;
 
-    // rng: {seed, offset} on the device.
+    // rng: {seed, offset} on the device.  Every lane keeps them as values of its own: put
+    // through a warp reduction first (one value for all lanes, in uniform registers), wrong
+    // masks came out of the norm's unaligned forward instances that spill registers, of no
+    // other, and it was no faster.
     __device__ __forceinline__ explicit Philox(const int64_t* rng) {
         const uint64_t seed = (uint64_t)rng[0], offset = (uint64_t)rng[1];
         key0 = (uint32_t)seed, key1 = (uint32_t)(seed >> 32);
