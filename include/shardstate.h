@@ -785,6 +785,11 @@ uint64_t ss_launch_count(void);
  * Everything else of the launch runs as always.  Errors: SS_EINVAL. */
 int ss_linear_ce_expire_wait(int launch);
 
+/* The same for this process's next ss_mx_matmul call that launches (on 1; 0: none):
+ * the first CTA, or pair of CTAs, waits before its products for what never comes, and
+ * the tiles of out that are its own are NaN.  Errors: SS_EINVAL. */
+int ss_mx_expire_wait(int on);
+
 #ifdef __cplusplus
 }
 #endif

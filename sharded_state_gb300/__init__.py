@@ -53,7 +53,7 @@ EXPORTED = ("fsdp_plan_create", "fsdp_plan_layout", "fsdp_plan_info", "fsdp_plan
             "fsdp_reduce_scatter_norm", "fsdp_clip_adamw", "ss_linear_ce_workspace",
             "ss_linear_cross_entropy", "ss_linear_ce_expire_wait", "ss_dropout", "ss_rms_norm",
             "ss_rms_norm_workspace", "ss_rms_norm_backward", "ss_mx_bytes", "ss_mx_quantize", "ss_mx_dequantize",
-            "ss_mx_matmul")
+            "ss_mx_matmul", "ss_mx_expire_wait")
 
 
 class ShardStateError(RuntimeError):
@@ -162,6 +162,7 @@ def _load() -> ctypes.CDLL:
         "ss_mx_quantize": ([ctypes.c_char_p, vp], i32),
         "ss_mx_dequantize": ([i64, i64, i32, vp, vp, vp, i64, i32, vp], i32),
         "ss_mx_matmul": ([ctypes.c_char_p, vp], i32),
+        "ss_mx_expire_wait": ([i32], i32),
         "ss_strerror": ([i32], ctypes.c_char_p),
         "ss_last_cuda_error": ([], i32),
         "ss_version": ([], ctypes.c_char_p),
@@ -864,6 +865,11 @@ def ss_mx_dequantize(data, scales, format: int, out, stream=None) -> None:
     status = _lib.ss_mx_dequantize(rows, cols, format, d, s, ao, ldo, dtype.itemsize, _stream(stream))
     if status != SS_OK:
         _check(fn, status)
+
+
+def ss_mx_expire_wait(on: bool) -> None:
+    """Diagnostics: a wait of the next ss_mx_matmul call that launches runs out."""
+    _check("ss_mx_expire_wait", _lib.ss_mx_expire_wait(int(on)))
 
 
 def ss_mx_matmul(a_data, a_scales, b_data, b_scales, K: int, format: int, out, stream=None) -> None:

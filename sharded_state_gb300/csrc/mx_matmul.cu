@@ -140,6 +140,7 @@ struct PairArgs {
     void* out;
     int elem_bytes;
     int vector;  // rows of out on 16 bytes
+    int expire;  // diagnostics: the first pair gets a wait that nothing ends
 };
 
 // 32 columns of this lane's row as bf16 words (or fp32 ones) in its warp's shared memory:
@@ -224,7 +225,7 @@ template <int FORMAT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairArgs g) {
     extern __shared__ unsigned char raw[];
-    __shared__ uint64_t bars[2 * kStages + 5];
+    __shared__ uint64_t bars[2 * kStages + 6];
     __shared__ uint32_t tmem_base;
     constexpr int kStage = pair_stage(FORMAT), kScales = scale_bytes(FORMAT);
 
@@ -234,6 +235,7 @@ mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairAr
     const uint32_t smem = (tc::smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
     const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, shared_read = acc_empty + 16;
+    const uint32_t never = shared_read + 8;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             tc::mbar_init(full + 8 * i, 1);
@@ -244,6 +246,7 @@ mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairAr
             tc::mbar_init(acc_empty + 8 * i, 2 * kEpilogueWarps);
         }
         tc::mbar_init(shared_read, kEpilogueWarps);
+        tc::mbar_init(never, 1);
         tc::mbar_init_fence();
         tc::prefetch_map(&maps.a);
         tc::prefetch_map(&maps.b);
@@ -285,7 +288,8 @@ mx_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ PairAr
     } else if (warp == 1 && rank == 0) {
         const uint32_t idesc = tc::scaled_desc(FORMAT == SS_MXFP4, kTile, kTile);
         int it = 0, j = 0;
-        for (int64_t id = first; id < tiles; id += pairs, ++j) {
+        if (g.expire && first == 0) ok = tc::mbar_wait_warp(never, 0);
+        for (int64_t id = first; id < tiles && ok; id += pairs, ++j) {
             ok = tc::mbar_wait_warp(acc_empty + 8 * (j & 1), ((j >> 1) & 1) ^ 1) &&
                  (j == 0 || tc::mbar_wait_warp(shared_read, (j - 1) & 1));
             if (!ok) break;
@@ -388,13 +392,14 @@ struct FewArgs {
     void* out;
     int elem_bytes;
     int vector;  // out's four neighbouring elements lie on their size
+    int expire;  // diagnostics: the first CTA gets a wait that nothing ends
 };
 
 template <int FORMAT, int FEW>
 __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_constant__ Maps maps,
                                                             const __grid_constant__ FewArgs g) {
     extern __shared__ unsigned char raw[];
-    __shared__ uint64_t bars[2 * kFewStages + 1];
+    __shared__ uint64_t bars[2 * kFewStages + 2];
     __shared__ uint32_t tmem_base;
     constexpr int kStage = few_stage(FORMAT, FEW), kScales = scale_bytes(FORMAT);
     static_assert(kStage % 1024 == 0 && (FEW + 8 * kFewThreads / 32) * kHalf * 4 <= kFewStages * kStage, "shared memory");
@@ -403,12 +408,14 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t smem = (tc::smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kFewStages, done = empty + 8 * kFewStages;
+    const uint32_t never = done + 8;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kFewStages; ++i) {
             tc::mbar_init(full + 8 * i, 1);
             tc::mbar_init(empty + 8 * i, 1);
         }
         tc::mbar_init(done, 1);
+        tc::mbar_init(never, 1);
         tc::mbar_init_fence();
         tc::prefetch_map(&maps.a);
         tc::prefetch_map(&maps.b);
@@ -444,7 +451,8 @@ __global__ void __launch_bounds__(kFewThreads) mx_few_kernel(const __grid_consta
         }
     } else if (warp == 1) {
         const uint32_t idesc = tc::scaled_desc(FORMAT == SS_MXFP4, kHalf, FEW);
-        for (int k = kb; k < ke; ++k) {
+        if (g.expire && blockIdx.x == 0) ok = tc::mbar_wait_warp(never, 0);
+        for (int k = kb; k < ke && ok; ++k) {
             const int it = k - kb, st = it % kFewStages;
             const uint32_t a = smem + st * kStage, b = a + kOperand, sa = b + FEW * kRowBytes, sb = sa + kScales;
             ok = tc::mbar_wait_warp(full + 8 * st, (it / kFewStages) & 1);
@@ -603,7 +611,7 @@ int make_maps(Maps* maps, const Operand& a, const Operand& b, int64_t K, int for
 }
 
 template <int FORMAT>
-int launch_pair(const ss_mx_product* p, int64_t k_blocks, cudaStream_t st) {
+int launch_pair(const ss_mx_product* p, int64_t k_blocks, bool expire, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
     const auto kernel = mx_pair_kernel<FORMAT>;
     constexpr int smem = pair_smem(FORMAT);
@@ -613,7 +621,7 @@ int launch_pair(const ss_mx_product* p, int64_t k_blocks, cudaStream_t st) {
         return rc;
     const int64_t m_tiles = div_up(p->M, kTile), n_tiles = div_up(p->N, kTile), pairs = ss::num_sms() / 2;
     const PairArgs g = {p->M, p->N, p->out_stride, (int)m_tiles, (int)n_tiles, (int)k_blocks, p->out, p->elem_bytes,
-                        ss::aligned(p->out, 16) && p->out_stride * p->elem_bytes % 16 == 0};
+                        ss::aligned(p->out, 16) && p->out_stride * p->elem_bytes % 16 == 0, expire};
     return ss::launch(kernel, 2 * std::min(m_tiles * n_tiles, pairs), kPairThreads, smem, 0, true, st, maps, g);
 }
 
@@ -638,7 +646,7 @@ int choose_splits(int64_t tiles, int64_t k_blocks, int few, int smem) {
 }
 
 template <int FORMAT, int FEW>
-int launch_few(const ss_mx_product* p, int64_t k_blocks, bool swap, cudaStream_t st) {
+int launch_few(const ss_mx_product* p, int64_t k_blocks, bool swap, bool expire, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
     const auto kernel = mx_few_kernel<FORMAT, FEW>;
     constexpr int smem = few_smem(FORMAT, FEW);
@@ -651,30 +659,40 @@ int launch_few(const ss_mx_product* p, int64_t k_blocks, bool swap, cudaStream_t
     const int splits = choose_splits(tiles, k_blocks, FEW, smem);
     const FewArgs g = {a.rows, b.rows, swap ? p->out_stride : 1, swap ? 1 : p->out_stride, (int)row_tiles, (int)k_blocks,
                        splits, p->out, p->elem_bytes,
-                       ss::aligned(p->out, 4 * p->elem_bytes) && p->out_stride % 4 == 0};
+                       ss::aligned(p->out, 4 * p->elem_bytes) && p->out_stride % 4 == 0, expire};
     if (tiles * splits > INT32_MAX) return SS_EOVERFLOW;
     return ss::launch(kernel, tiles * splits, kFewThreads, smem, splits > 1 ? splits : 0, true, st, maps, g);
 }
 
+// The next call gets a wait which nothing ends.
+std::atomic<bool> g_expire{false};
+
 template <int FORMAT>
 int launch_product(const ss_mx_product* p, cudaStream_t st) {
+    const bool expire = g_expire.exchange(false, std::memory_order_relaxed);
     const int64_t k_blocks = div_up(div_up(p->K, ss::kMxTile), scale_tiles(FORMAT));
     const int64_t big = div_up(p->M, kTile) * div_up(p->N, kTile);
     // half a round of tiles: 36 of them take the same either way (1536 x 1536 x 4096: 8.4 and 8.6 us),
     // 16 are faster as the few (1021 x 777 x 4096: 7.0 and 10.1), 44 as pairs (512 x 5632 x 4096: 16 and 9.2)
-    if (2 * big >= ss::num_sms() / 2 && p->M > kHalf && p->N > kHalf) return launch_pair<FORMAT>(p, k_blocks, st);
+    if (2 * big >= ss::num_sms() / 2 && p->M > kHalf && p->N > kHalf) return launch_pair<FORMAT>(p, k_blocks, expire, st);
     // the few are A's rows, or B's where those are no more than a tile (5003 x 72 x 2688: 7.4 us as A's,
     // 6.8 as B's; 2000 x 100 x 4096 in 8 bits 9.0 and 6.6, in 4 bits 7.0 and 7.3); with more of them a row
     // of out in one thread's hands costs more (1021 x 777 x 1024: 5.7 and 17)
     const bool swap = p->N < p->M && p->N <= kHalf;
     const int64_t few = swap ? p->N : p->M;
-    if (few <= 16) return launch_few<FORMAT, 16>(p, k_blocks, swap, st);
-    if (few <= 32) return launch_few<FORMAT, 32>(p, k_blocks, swap, st);
-    if (few <= 64) return launch_few<FORMAT, 64>(p, k_blocks, swap, st);
-    return launch_few<FORMAT, 128>(p, k_blocks, swap, st);
+    if (few <= 16) return launch_few<FORMAT, 16>(p, k_blocks, swap, expire, st);
+    if (few <= 32) return launch_few<FORMAT, 32>(p, k_blocks, swap, expire, st);
+    if (few <= 64) return launch_few<FORMAT, 64>(p, k_blocks, swap, expire, st);
+    return launch_few<FORMAT, 128>(p, k_blocks, swap, expire, st);
 }
 
 }  // namespace
+
+extern "C" int ss_mx_expire_wait(int on) {
+    if (on != 0 && on != 1) return SS_EINVAL;
+    g_expire.store(on != 0, std::memory_order_relaxed);
+    return SS_OK;
+}
 
 extern "C" int ss_mx_matmul(const ss_mx_product* p, ss_stream_t stream) {
     if (!p || p->M < 0 || p->N < 0 || p->K < 1 || (p->format != SS_MXFP4 && p->format != SS_MXFP8) ||
