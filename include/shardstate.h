@@ -629,7 +629,9 @@ int ss_mx_bytes(int64_t rows, int64_t cols, int format, size_t* data_bytes, size
  * nearest (ties to even), or, with rng, to one of the two neighbours: up, away from
  * zero, where the part cut off and u / 65536 make 1, u being the 16 bits that
  * ss_dropout takes for the element's place in x (the same for the transpose).  With
- * bf16 inputs the expected value is then the input up to 2^-16 of a step.
+ * bf16 inputs the expected value is then the input up to 2^-16 of a step; not so for
+ * elements beyond the format's largest (between 6 and 8, or 448 and 512, times the
+ * scale), which are cut to it every time, by up to a quarter or an eighth.
  */
 typedef struct {
     int64_t rows;

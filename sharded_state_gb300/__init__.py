@@ -839,7 +839,8 @@ def ss_mx_quantize(x, format: int, data=None, scales=None, t_data=None, t_scales
     """Quantise a bf16 or fp32 matrix x [R, C] (rows may be strided) to SS_MXFP4 or
     SS_MXFP8: along its rows into data and scales, along its columns (x.T, [C, R]) into
     t_data and t_scales, either or both from one read; uint8 buffers of ss_mx_bytes.  To
-    the nearest, or stochastically with rng (2 int64 on the device: seed, offset)."""
+    the nearest, or stochastically with rng (2 int64 on the device: seed, offset); elements
+    beyond the format's largest are cut to it either way."""
     fn = "ss_mx_quantize"
     (dtype, shape), dev = _row_dtype(fn, x, "x"), _device()
     _mx_format(fn, format)
