@@ -526,7 +526,10 @@ int ss_dropout(int64_t rows, int64_t cols, int elem_bytes, const void* x, int64_
  * it is NULL; the dropout is ss_dropout's of a [rows, cols] matrix.  Sums and
  * statistics are fp32 (a square passes it from |h| = 1.8e19 on), out is rounded
  * once.  A row that holds a NaN is NaN; beside an infinity, which is NaN itself,
- * the row is 0.  The same inputs give the same bits.
+ * the row is 0.  The order of a row's sum, and so the last bits, depends on the
+ * sizes, the type, whether mx_data is given, whether every address and row stride is
+ * a multiple of 16 bytes, and the device; with these alike, the same inputs give the
+ * same bits.
  *
  * All matrices are of the type elem_bytes says (2: bf16, 4: fp32), row-major with
  * a row stride in elements and any element alignment.  sum_out may be x or the
@@ -565,7 +568,8 @@ int ss_rms_norm(const ss_norm* args, ss_stream_t stream);
  *   d_x      = dropout(d_h), with the mask of the forward pass
  *   d_weight = sum over the rows of d_out * n
  * d_sum (nullable) is the gradient that reaches h from elsewhere.  Sums are fp32,
- * in an order that depends on the sizes and the device alone.  d_h may be d_out
+ * in an order that depends on the sizes, the type, whether every address and row
+ * stride is a multiple of 16 bytes, and the device.  d_h may be d_out
  * or d_sum (with its stride); outputs overlap no input and no other output
  * otherwise.
  */

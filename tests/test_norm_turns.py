@@ -62,3 +62,14 @@ def test_dropout_in_turn(ss, rows, cols, extra, offset, out_extra, out_offset, d
     assert bool(((out.double() - want).abs() <= (half_step(dtype) + 3 * W) * want.abs()).all())
     assert bool(((out == 0) == (want == 0)).all())
     assert outside_kept(buf, out, 5.0)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols,here,there", [(1024, (0, 0), (24, 8)), (5632, (8, 0), (32, 16)), (1024, (1, 0), (3, 5)),
+                                             (5155, (0, 0), (2, 1)), (9589, (0, 3), (7, 0))])
+def test_the_same_bits_elsewhere(ss, cols, here, there, dtype):  # noqa: F811
+    """Other addresses and strides give the same bits, as long as they are multiples of 16 bytes, or are not, alike."""
+    a, b = (Norm(ss, 310, cols, dtype, p=0.1, extra=e, offset=o).backward(ss) for e, o in (here, there))
+    for name in ("x", "dy", "h", "out", "rstd", "dh", "dx", "dw"):
+        assert torch.equal(getattr(a, name), getattr(b, name)), name
