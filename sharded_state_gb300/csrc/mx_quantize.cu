@@ -14,13 +14,12 @@
 // is 15, rounding at random rather than to the nearest 22).
 #include <cuda_runtime.h>
 
-#include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "launch.cuh"
 #include "mx.cuh"
 #include "philox.cuh"
-#include "tma_host.h"
 #include "vec8.cuh"
 
 namespace {
@@ -302,11 +301,9 @@ int launch_quantize(const QuantArgs& a, bool transpose, bool random, bool aligne
         });
     return with_flags(transpose, random, [&](auto t, auto r) {
         constexpr bool TR = decltype(t)::value, RA = decltype(r)::value;
-        static std::atomic<uint64_t> ready[2]{};
-        const int smem = TR ? tile_bytes<T, RA>() : 0;
+        constexpr int smem = TR ? tile_bytes<T, RA>() : 0;
+        static_assert(smem <= 48 * 1024, "more shared memory has to be asked for");
         const auto kernel = aligned ? quantize_kernel<T, FORMAT, kRounds, TR, RA, true> : quantize_kernel<T, FORMAT, kRounds, TR, RA, false>;
-        if (smem > 48 * 1024)
-            if (int rc = ss::allow_smem(ready[aligned], reinterpret_cast<const void*>(kernel), smem)) return rc;
         // the transpose's rows go on to a multiple of 128: parts of whole tiles
         const int64_t by_rows = TR ? a.row_tiles * (kMxTile / kRows) : parts(a.rows, kRounds);
         return ss::launch(kernel, by_rows * a.col_tiles, kThreads, smem, 0, true, st, a);

@@ -674,9 +674,14 @@ int ss_rms_norm(const ss_norm* n, ss_stream_t stream) {
     return with_shape(n->elem_bytes, s.vecs, al, [&](auto t, auto v, auto aligned) {
         constexpr int V = decltype(v)::value;
         constexpr bool A = decltype(aligned)::value;
-        constexpr bool kNarrow = V == 1 || (V == 2 && A), kWide = V > 1 || !A;  // what choose_norm_shape gives
-        const auto kernel = s.threads > 256 ? norm_kernel<decltype(t), V, A, kWide> : norm_kernel<decltype(t), V, A, !kNarrow>;
-        return ss::launch(kernel, grid, s.threads, 0, 0, true, reinterpret_cast<cudaStream_t>(stream), a);
+        // what choose_norm_shape gives: of unaligned fp32 rows one load by up to 1024 threads, then four
+        constexpr bool kNarrow = V == 1 || (V == 2 && A), kWide = V > 1 || !A, kNever = V == 2 && !A && sizeof(t) == 4;
+        if constexpr (kNever) {
+            return SS_EINVAL;
+        } else {
+            const auto kernel = s.threads > 256 ? norm_kernel<decltype(t), V, A, kWide> : norm_kernel<decltype(t), V, A, !kNarrow>;
+            return ss::launch(kernel, grid, s.threads, 0, 0, true, reinterpret_cast<cudaStream_t>(stream), a);
+        }
     });
 }
 
