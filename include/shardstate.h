@@ -524,7 +524,8 @@ int ss_dropout(int64_t rows, int64_t cols, int elem_bytes, const void* x, int64_
  *   out  = h * rstd * weight
  * without the dropout where its probability is 0 and without the residual where
  * it is NULL; the dropout is ss_dropout's of a [rows, cols] matrix.  Sums and
- * statistics are fp32 (a square passes it from |h| = 1.8e19 on), out is rounded
+ * statistics are fp32: a row whose sum of squares passes that (the root of the sum is
+ * 1.8e19 or more) is 0, and rstd too; one of zeros is NaN with eps 0.  out is rounded
  * once.  A row that holds a NaN is NaN; beside an infinity, which is NaN itself,
  * the row is 0.  The order of a row's sum, and so the last bits, depends on the
  * sizes, the type, whether mx_data is given, whether every address and row stride is
