@@ -8,10 +8,11 @@
 // (MXFP4) or 1.03 (MXFP8) written for each element and orientation.
 //
 // To the nearest along the rows the memory bounds it (32000 x 2048 bf16 to MXFP4: 28 us,
-// 6.0 TB/s; back 26 us, 6.4 TB/s), both ways the instructions begin to (18 an element;
-// 8192 x 2048 12.4 us, 4.1 TB/s), and at random they do: 41 an element both ways, the
-// integer pipe busy three quarters of the time (8192 x 5632 65 us, of which the generator
-// is 15, rounding at random rather than to the nearest 22).
+// 6.0 TB/s; back 26 us, 6.4 TB/s).  Both ways nothing is full (18 instructions an element
+// on 65 % of the issue slots, the integer pipe 61 %; 8192 x 2048 12.4 us, 4.1 TB/s).  At
+// random it is 41 instructions an element both ways, the integer pipe busy three quarters
+// of the time (8192 x 5632 65 us, of which the generator is 15, rounding at random rather
+// than to the nearest 22).
 #include <cuda_runtime.h>
 
 #include <type_traits>

@@ -18,8 +18,11 @@
 // registers (8 elements a load, up to 8 loads a thread) between the sum over it and the
 // outputs.  16384 x 4096 bf16, 537 MB either way: forward 81 us (6.6 TB/s, where a copy
 // makes 6.8), backward with d_weight 93 us (5.8 TB/s; 169 us without the next row on its
-// way).  Dropout is bound by the generator's instructions instead: 8192 x 11008 67 us,
-// 5.4 TB/s.
+// way).  With dropout the generator's instructions come on top: 100 us and, with d_x
+// written too, 119; by itself, 8192 x 11008, dropout takes 67 us, 5.4 TB/s, two thirds of
+// the issue slots.  Four and eight loads a thread, of more than 8192 columns, spill
+// registers (all but the forward pass of bf16 rows on 16 bytes or of four loads, and of
+// fp32 rows of four on 16 bytes): 2000 x 16384 bf16 forward 58, backward 102 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -1,9 +1,9 @@
 """Dropout and the residual stream's norm against the formulas in 64 bits.
 
 Tolerances.  u is half a step of the type (bf16 2^-8, fp32 2^-24, relative), w = 2^-24.  Sums over a row are taken
-by at most 512 threads, 64 elements each in turn, then 5 adds in the warp and 16 over the warps: a term passes at most
-64 + 5 + 16 adds, and its product's rounding, so the sum is off by at most SUM = 90 w times the sum of the terms'
-magnitudes (their sum itself for squares).
+by at most 512 threads, 64 elements each in turn, then 5 adds in the warp and 16 over the warps, or by up to 1024 of at
+most 16 elements and 32 warps: a term passes at most 64 + 5 + 16 adds, and its product's rounding, so the sum is off by at
+most SUM = 90 w times the sum of the terms' magnitudes (their sum itself for squares).
 """
 import math
 
